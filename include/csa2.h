@@ -77,6 +77,10 @@ typedef struct CUstream_st *csa2_stream_t; /* same object as cudaStream_t */
 #define CSA2_DERR_RANGE_ROW 256   /* a row index past the rows of a gather source / scatter target */
 #define CSA2_DERR_NONFINITE 512   /* a NaN or infinity in a group being quantised */
 
+/* element types of the dense-cache calls */
+#define CSA2_DT_BF16 1
+#define CSA2_DT_F16 2
+
 /* storage formats of csa2_quantize_rows */
 #define CSA2_FMT_FP8_B32 1        /* E4M3 codes + fp32 scale per 32 */
 #define CSA2_FMT_FP4KV 2          /* E2M1 codes + E4M3 scale per 16 */
@@ -466,6 +470,167 @@ CSA2_API int csa2_index_k_project(int64_t n, const void *x_bf16, int32_t dim_in,
 CSA2_API int csa2_quantize_rows(int32_t format, int64_t n, const float *src, int32_t dim,
                          const int64_t *dst_row, uint8_t *codes, void *scales,
                          int64_t rows, int32_t *d_err, csa2_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense caches: attention over every cached row, and eviction
+ *
+ * Beside the sparse attention over the latent pool, a stack needs attention
+ * that reads every row of a plain K/V cache: for layers without compression,
+ * for a drafter, and as the dense form a sparse layer is measured against.
+ * These calls take bf16 or f16 rows (`dtype`), n_heads query heads that share
+ * n_kv_heads key heads (head h reads key head h / G, G = n_heads /
+ * n_kv_heads), and requests that are runs of rows in one pool, as above.
+ *
+ *   num_q       rows of q and of the outputs
+ *   num_req     requests
+ *   cu_q[R+1]   request r holds query rows cu_q[r] .. cu_q[r+1]-1, ascending;
+ *               rows in front of cu_q[0] and behind cu_q[R] are not touched
+ *   kv_start[R] first row of the request in the K and V pools
+ *   kv_len[R]   rows of the request in the pools, m_r, the new ones included:
+ *               query i of n_r is at position m_r - n_r + i and sees the rows
+ *               0 .. m_r - n_r + i.  n_r = 1 is a decode step, n_r = m_r a
+ *               whole prompt, anything between an extend over a cached prefix.
+ *               A query at a negative position (n_r > m_r) sees nothing.
+ * All three are read on the device.  A request whose rows leave the pool of
+ * kv_rows rows has no keys (CSA2_DERR_RANGE_ROW); one whose query rows are not
+ * a range within num_q is skipped (CSA2_DERR_BAD_EXTEND).
+ *
+ *   q   [num_q, n_heads, dim]        rows `ldq` elements apart
+ *   k,v [kv_rows, n_kv_heads, dim]   rows `ldk`, `ldv` elements apart (heads
+ *       and channels contiguous), so that fused projections and interleaved
+ *       caches are read where they are
+ * Rows of k and v that no request of the call names may hold anything.  The
+ * rows that a request names must be finite: a NaN or infinity in a row that
+ * some query of a tile sees reaches the queries in front of it too.
+ * Supported: dim in {64, 128}, n_heads / n_kv_heads <= 128, n_kv_heads <=
+ * 1024, kv_rows < 2^31 - 256, 0 < sm_scale < inf (CSA2_ERR_INVALID_ARG);
+ * bases and outputs 16-byte aligned, row distances multiples of 8 elements
+ * (CSA2_ERR_UNSUPPORTED otherwise).
+ * ------------------------------------------------------------------------- */
+typedef struct csa2_packed {
+  int32_t num_q;
+  int32_t num_req;
+  const int32_t *cu_q;
+  const int64_t *kv_start;
+  const int64_t *kv_len;
+} csa2_packed;
+
+/* Causal attention over whole prompts and extends, packed.
+ *   l_j = sm_scale * <q[i,h], k[kv_start+j, h/G]>,  j = 0 .. m - n + i
+ *   out[i,h,:] = sum_j e^{l_j} v[kv_start+j, h/G, :] / sum_j e^{l_j}
+ *   lse[i,h]   = ln sum_j e^{l_j}
+ * A query that sees nothing gets out = 0, lse = -inf.
+ *   out [num_q, n_heads, dim] of the inputs' type, contiguous
+ *   lse [num_q, n_heads] fp32 or NULL
+ * The weights e^{l_j} are rounded to the inputs' type for the product with v
+ * (their sum is not); products accumulate in fp32.  For single tokens over
+ * long caches csa2_prefix_attn without groups splits the cache among CTAs. */
+CSA2_API int csa2_prompt_attn(const csa2_packed *b, int32_t n_heads, int32_t n_kv_heads,
+                              int32_t dim, int32_t dtype, const void *q, int64_t ldq,
+                              const void *k, int64_t ldk, const void *v, int64_t ldv,
+                              int64_t kv_rows, float sm_scale, void *out, float *lse,
+                              int32_t *d_err, csa2_stream_t stream);
+
+/* Requests that share prefixes.  Host struct; the arrays are device memory.
+ * Group g holds the requests cu_group[g] .. cu_group[g+1]-1, and every query
+ * of theirs sees the pool rows prefix_start[g] .. +prefix_len[g]-1 in front of
+ * its request's own rows.  Groups are disjoint; a request in no group has its
+ * own rows alone.  max_prefix is the longest prefix, for the choice of splits
+ * only. */
+typedef struct csa2_prefix_groups {
+  int32_t num_groups;
+  int32_t reserved;
+  const int32_t *cu_group;      /* [num_groups + 1] */
+  const int64_t *prefix_start;  /* [num_groups] */
+  const int64_t *prefix_len;    /* [num_groups] */
+  int64_t max_prefix;
+} csa2_prefix_groups;
+
+/* Attention of a batch whose requests share prefixes: the prefix rows are read
+ * once for all the queries of a group, the requests' own rows (causal, as in
+ * csa2_prompt_attn) apart, and both join in one softmax.  `groups` NULL or
+ * without groups: own rows alone, split over the cache (the form for single
+ * tokens).  max_kv is the longest kv_len, for the choice of splits only.
+ *   workspace  device scratch of at least csa2_prefix_attn_workspace bytes,
+ *              256-byte aligned, owned by the caller; its contents do not
+ *              matter and are undefined after the call.  Calls sharing one
+ *              workspace must not overlap (two captured graphs that may run at
+ *              the same time need one each).
+ * Other arguments, outputs and errors as csa2_prompt_attn; a prefix that
+ * leaves the pool counts as empty (CSA2_DERR_RANGE_ROW), and a group that is
+ * not a range of requests is skipped, its requests keeping their own rows
+ * (CSA2_DERR_BAD_EXTEND). */
+CSA2_API int csa2_prefix_attn_workspace(int32_t num_q, int32_t num_req, int32_t num_groups,
+                                        int32_t n_heads, int32_t n_kv_heads, int32_t dim,
+                                        int64_t max_prefix, int64_t max_kv, int64_t *bytes);
+CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix_groups *groups,
+                              int32_t n_heads, int32_t n_kv_heads, int32_t dim, int32_t dtype,
+                              const void *q, int64_t ldq, const void *k, int64_t ldk,
+                              const void *v, int64_t ldv, int64_t kv_rows, int64_t max_kv,
+                              float sm_scale, void *out, float *lse, void *workspace,
+                              int64_t workspace_bytes, int32_t *d_err, csa2_stream_t stream);
+
+/* Attention weight that a call's queries put on each cached row, added up:
+ *   mass_out[g, kv_start+j] = mass_in[g, kv_start+j]
+ *       + sum over queries i that see row j, heads h = gG .. gG+G-1, of
+ *         exp(sm_scale * <q[i,h], k[kv_start+j, g]> - lse[i,h])
+ *   lse      [num_q, n_heads] fp32 of the attention these queries ran (of the
+ *            joint softmax where they also saw a prefix); a query with lse =
+ *            -inf adds nothing
+ *   mass_in  [n_kv_heads, kv_rows] fp32, or NULL for zeros; mass_out the same
+ *            shape, and may be mass_in itself
+ * Only rows of the call's requests are written; no two requests may name the
+ * same row.  The queries are those the caller passes: a whole prompt, its last
+ * window (the rows csa2_tail_layout lists), or a decode step.  The sums are
+ * fp32, in a fixed order: the same call gives the same bits.
+ * max_kv is the longest kv_len, for the size of the grid only; num_req <= 8192
+ * (CSA2_ERR_UNSUPPORTED).  Other arguments as csa2_prompt_attn. */
+CSA2_API int csa2_attn_mass(const csa2_packed *b, int32_t n_heads, int32_t n_kv_heads,
+                            int32_t dim, int32_t dtype, const void *q, int64_t ldq,
+                            const void *k, int64_t ldk, int64_t kv_rows, const float *lse,
+                            int64_t max_kv, float sm_scale, const float *mass_in,
+                            float *mass_out, int32_t *d_err, csa2_stream_t stream);
+
+/* Rows to keep.  For each request and head, of its m = kv_len[r] rows: all of
+ * them if m <= keep, else the first `sink`, the last `recent`, and of the rest
+ * the keep - sink - recent of largest mass; equal masses (-0 equals 0): the
+ * lower row first; a NaN is below every number.
+ *   mass    [n_heads, kv_rows] fp32
+ *   idx     [num_req, n_heads, keep] rows kept, as offsets from kv_start[r],
+ *           ascending; -1 behind the last
+ *   new_len [num_req] = min(m, keep)
+ * sink, recent >= 0, keep >= 1, sink + recent <= keep (CSA2_ERR_INVALID_ARG).
+ * A request whose rows leave the pool keeps nothing (CSA2_DERR_RANGE_ROW). */
+CSA2_API int csa2_evict_select(int32_t num_req, int32_t n_heads, const int64_t *kv_start,
+                               const int64_t *kv_len, const float *mass, int64_t kv_rows,
+                               int32_t keep, int32_t sink, int32_t recent, int32_t *idx,
+                               int64_t *new_len, int32_t *d_err, csa2_stream_t stream);
+
+/* One per-head buffer of a cache: element (row, head) is elem_bytes bytes (a
+ * multiple of 4) at row * row_stride + head * head_stride bytes. */
+typedef struct csa2_evict_buf {
+  const void *src;
+  void *dst;
+  int64_t src_rows, dst_rows;
+  int64_t src_row_stride, src_head_stride;
+  int64_t dst_row_stride, dst_head_stride;
+  int64_t elem_bytes;
+} csa2_evict_buf;
+
+/* Moves the rows kept, in up to 8 buffers at once (K, V, their scales, the
+ * mass): for i < new_len[r]
+ *   dst row dst_start[r] + i, head h  =  src row src_start[r] + idx[r, h, i], head h
+ * dst may be src when dst_start is src_start: the rows close up in place
+ * (ascending idx, as csa2_evict_select writes them).  Otherwise source and
+ * destination rows must not overlap.  Rows of dst that are not named keep
+ * their bytes.  A negative idx is skipped; a row outside src_rows or dst_rows
+ * is skipped (CSA2_DERR_RANGE_ROW).  Host structs, read during the call only.
+ * Pointers and strides multiples of 4 bytes; copies are widest where they are
+ * all multiples of 16. */
+CSA2_API int csa2_evict_rows(int32_t num_req, int32_t n_heads, const int32_t *idx, int32_t keep,
+                             const int64_t *new_len, const int64_t *src_start,
+                             const int64_t *dst_start, int32_t n_bufs,
+                             const csa2_evict_buf *bufs, int32_t *d_err, csa2_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -25,13 +25,16 @@ DERR_RANGE_IDX, DERR_RANGE_WINDOW, DERR_RANGE_CTX = 1, 2, 4
 DERR_SCALE, DERR_LD, DERR_CAPACITY, DERR_BAD_EXTEND = 8, 16, 32, 64
 DERR_TIMEOUT, DERR_RANGE_ROW, DERR_NONFINITE = 128, 256, 512
 FMT_FP8_B32, FMT_FP4KV, FMT_MXFP4 = 1, 2, 3
+DT_BF16, DT_F16 = 1, 2
 
 EXPORTED = ("csa2_status_string", "csa2_tail_layout", "csa2_index_score", "csa2_topk",
             "csa2_topk_candidates", "csa2_sparse_swa_attn", "csa2_sparse_swa_attn_fp4kv",
             "csa2_encoder_replay_layout", "csa2_rows_gather", "csa2_rows_scatter",
             "csa2_quantize_rows", "csa2_set_wait_limit_ns", "csa2_index_topk_workspace",
             "csa2_index_topk", "csa2_index_k_project", "csa2_index_topk_static_capacity",
-            "csa2_index_topk_static")
+            "csa2_index_topk_static", "csa2_prompt_attn", "csa2_prefix_attn_workspace",
+            "csa2_prefix_attn", "csa2_attn_mass", "csa2_evict_select", "csa2_evict_rows")
+EVICT_MAX_BUFS = 8
 
 
 class Csa2Error(RuntimeError):
@@ -44,6 +47,24 @@ class CBatch(C.Structure):
                 ("q_req", C.c_void_p), ("q_pos", C.c_void_p),
                 ("kv_start", C.c_void_p), ("kv_len", C.c_void_p),
                 ("swa_start", C.c_void_p), ("swa_pos0", C.c_void_p), ("swa_len", C.c_void_p)]
+
+
+class CPacked(C.Structure):
+    _fields_ = [("num_q", C.c_int32), ("num_req", C.c_int32), ("cu_q", C.c_void_p),
+                ("kv_start", C.c_void_p), ("kv_len", C.c_void_p)]
+
+
+class CPrefixGroups(C.Structure):
+    _fields_ = [("num_groups", C.c_int32), ("reserved", C.c_int32), ("cu_group", C.c_void_p),
+                ("prefix_start", C.c_void_p), ("prefix_len", C.c_void_p),
+                ("max_prefix", C.c_int64)]
+
+
+class CEvictBuf(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("src_rows", C.c_int64),
+                ("dst_rows", C.c_int64), ("src_row_stride", C.c_int64),
+                ("src_head_stride", C.c_int64), ("dst_row_stride", C.c_int64),
+                ("dst_head_stride", C.c_int64), ("elem_bytes", C.c_int64)]
 
 
 _lib = None
@@ -83,6 +104,15 @@ def load(path: Optional[str] = None):
                                            vp, vp]
     lib.csa2_index_topk.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, i64, i32, vp, vp, vp, i64,
                                     vp, vp]
+    lib.csa2_prompt_attn.argtypes = [vp, i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, i64, f32,
+                                     vp, vp, vp, vp]
+    lib.csa2_prefix_attn_workspace.argtypes = [i32, i32, i32, i32, i32, i32, i64, i64, vp]
+    lib.csa2_prefix_attn.argtypes = [vp, vp, i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, i64,
+                                     i64, f32, vp, vp, vp, i64, vp, vp]
+    lib.csa2_attn_mass.argtypes = [vp, i32, i32, i32, i32, vp, i64, vp, i64, i64, vp, i64, f32,
+                                   vp, vp, vp, vp]
+    lib.csa2_evict_select.argtypes = [i32, i32, vp, vp, vp, i64, i32, i32, i32, vp, vp, vp, vp]
+    lib.csa2_evict_rows.argtypes = [i32, i32, vp, i32, vp, vp, vp, i32, vp, vp, vp]
     for name in EXPORTED[1:]:
         getattr(lib, name).restype = C.c_int
     _lib = lib
@@ -438,3 +468,292 @@ def sparse_swa_attn_fp4kv(batch, q, kv_fp4, kv_sf, idx, swa_fp8, swa_scale, win_
                                       swa_scale, win_lo, window, sm_scale, sink, out, lse, d_err,
                                       stream), "csa2_sparse_swa_attn_fp4kv")
     return out, lse
+
+
+# ---------------------------------------------------------------------------
+# dense caches: prompt and shared-prefix attention, attention weight, eviction.
+# ``packed`` is a dict like ``batch``: num_q, num_req and the device tensors
+# cu_q (int32 [R+1]), kv_start and kv_len (int64 [R]); ``groups`` a dict of
+# num_groups, cu_group (int32 [G+1]), prefix_start, prefix_len (int64 [G]) and
+# max_prefix.  q, k and v are [rows, heads, dim] of one 16-bit type, heads and
+# channels contiguous, rows any distance apart that is a multiple of 8.
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+
+
+def _typed(t, dtype, name, numel=0, device=None):
+    """Device pointer of a contiguous tensor of a given type (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise Csa2Error("%s: expected %s, got %s" % (name, dtype, t.dtype))
+    if t.numel() < numel:
+        raise Csa2Error("%s: expected at least %d values, got %d" % (name, numel, t.numel()))
+    if device is not None and t.device != device:
+        raise Csa2Error("%s is on %s, not on %s" % (name, t.device, device))
+    return _ptr(t)
+
+
+def _rows3(t, name, like=None):
+    """(pointer, row distance) of a [rows, heads, dim] tensor."""
+    if not t.is_cuda:
+        raise Csa2Error("libcsa2 takes device tensors; got a %s tensor" % t.device)
+    if t.dim() != 3 or t.dtype not in _DTYPES:
+        raise Csa2Error("%s: expected [rows, heads, dim] of bf16 or f16" % name)
+    if like is not None and (t.dtype != like.dtype or t.device != like.device
+                             or t.shape[2] != like.shape[2]):
+        raise Csa2Error("%s: expected the type, device and head size of q" % name)
+    n, h, d = t.shape
+    s = t.stride()
+    if (s[2] != 1 and d > 1) or (s[1] != d and h > 1):
+        raise Csa2Error("%s: heads and channels must be contiguous" % name)
+    return C.c_void_p(t.data_ptr()), max(s[0], h * d) if n <= 1 else s[0]
+
+
+def make_packed(b, device=None):
+    """Host struct for a packed dict of device tensors."""
+    r = int(b["num_req"])
+    return CPacked(int(b["num_q"]), r, _typed(b["cu_q"], torch.int32, "cu_q", r + 1, device),
+                   _typed(b["kv_start"], torch.int64, "kv_start", r, device),
+                   _typed(b["kv_len"], torch.int64, "kv_len", r, device))
+
+
+def make_groups(g, device=None):
+    """Host struct for a groups dict of device tensors (None: no groups)."""
+    if g is None:
+        return None
+    n = int(g["num_groups"])
+    return CPrefixGroups(n, 0, _typed(g["cu_group"], torch.int32, "cu_group", n + 1, device),
+                         _typed(g["prefix_start"], torch.int64, "prefix_start", n, device),
+                         _typed(g["prefix_len"], torch.int64, "prefix_len", n, device),
+                         int(g["max_prefix"]))
+
+
+class _on:
+    """Makes a tensor's device the current one for a call's launches."""
+
+    __slots__ = ("back", "to")
+
+    def __init__(self, t):
+        self.to = t.device.index
+        self.back = None
+
+    def __enter__(self):
+        if self.to is not None:
+            cur = torch.cuda.current_device()
+            if cur != self.to:
+                self.back = cur
+                torch.cuda.set_device(self.to)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _same_kv(k, v):
+    if k.shape != v.shape:
+        raise Csa2Error("k and v: expected the same shape, got %s and %s"
+                        % (tuple(k.shape), tuple(v.shape)))
+
+
+def _check_q(packed, q, k):
+    if int(packed["num_q"]) > q.shape[0]:
+        raise Csa2Error("q has %d rows, the batch names %d" % (q.shape[0], packed["num_q"]))
+    if k.shape[1] < 1 or q.shape[1] % k.shape[1]:
+        raise Csa2Error("%d query heads do not share %d key heads" % (q.shape[1], k.shape[1]))
+
+
+def csa2_prompt_attn(packed, q, k, v, sm_scale, out, lse, d_err, stream=None) -> int:
+    st = make_packed(packed, q.device)
+    _check_q(packed, q, k)
+    _same_kv(k, v)
+    (qp, ldq), (kp, ldk), (vp, ldv) = _rows3(q, "q"), _rows3(k, "k", q), _rows3(v, "v", q)
+    n = st.num_q * q.shape[1]
+    with _on(q):
+        return load().csa2_prompt_attn(
+            C.byref(st), q.shape[1], k.shape[1], q.shape[2], _DTYPES[q.dtype], qp, ldq, kp, ldk,
+            vp, ldv, k.shape[0], float(sm_scale),
+            _typed(out, q.dtype, "out", n * q.shape[2], q.device),
+            _typed(lse, torch.float32, "lse", n, q.device),
+            _typed(d_err, torch.int32, "d_err", 1, q.device), _stream(stream))
+
+
+def csa2_prefix_attn_workspace(num_q, num_req, num_groups, n_heads, n_kv_heads, dim, max_prefix,
+                               max_kv) -> int:
+    """Workspace bytes csa2_prefix_attn needs for these sizes."""
+    out = C.c_int64(0)
+    _check(load().csa2_prefix_attn_workspace(int(num_q), int(num_req), int(num_groups),
+                                             int(n_heads), int(n_kv_heads), int(dim),
+                                             int(max_prefix), int(max_kv), C.byref(out)),
+           "csa2_prefix_attn_workspace")
+    return int(out.value)
+
+
+def csa2_prefix_attn(packed, groups, q, k, v, max_kv, sm_scale, out, lse, workspace,
+                     workspace_bytes, d_err, stream=None) -> int:
+    st = make_packed(packed, q.device)
+    gr = make_groups(groups, q.device)
+    _check_q(packed, q, k)
+    _same_kv(k, v)
+    (qp, ldq), (kp, ldk), (vp, ldv) = _rows3(q, "q"), _rows3(k, "k", q), _rows3(v, "v", q)
+    n = st.num_q * q.shape[1]
+    with _on(q):
+        return load().csa2_prefix_attn(
+            C.byref(st), None if gr is None else C.byref(gr), q.shape[1], k.shape[1], q.shape[2],
+            _DTYPES[q.dtype], qp, ldq, kp, ldk, vp, ldv, k.shape[0], int(max_kv),
+            float(sm_scale), _typed(out, q.dtype, "out", n * q.shape[2], q.device),
+            _typed(lse, torch.float32, "lse", n, q.device),
+            _typed(workspace, torch.uint8, "workspace", workspace_bytes, q.device),
+            int(workspace_bytes), _typed(d_err, torch.int32, "d_err", 1, q.device),
+            _stream(stream))
+
+
+def csa2_attn_mass(packed, q, k, lse, max_kv, sm_scale, mass_in, mass_out, d_err,
+                   stream=None) -> int:
+    st = make_packed(packed, q.device)
+    _check_q(packed, q, k)
+    (qp, ldq), (kp, ldk) = _rows3(q, "q"), _rows3(k, "k", q)
+    n = k.shape[0] * k.shape[1]
+    with _on(q):
+        return load().csa2_attn_mass(
+            C.byref(st), q.shape[1], k.shape[1], q.shape[2], _DTYPES[q.dtype], qp, ldq, kp, ldk,
+            k.shape[0], _typed(lse, torch.float32, "lse", st.num_q * q.shape[1], q.device),
+            int(max_kv), float(sm_scale), _typed(mass_in, torch.float32, "mass_in", n, q.device),
+            _typed(mass_out, torch.float32, "mass_out", n, q.device),
+            _typed(d_err, torch.int32, "d_err", 1, q.device), _stream(stream))
+
+
+def csa2_evict_select(num_req, kv_start, kv_len, mass, keep, sink, recent, idx, new_len, d_err,
+                      stream=None) -> int:
+    h, rows = mass.shape
+    dev = mass.device
+    with _on(mass):
+        return load().csa2_evict_select(
+            int(num_req), h, _typed(kv_start, torch.int64, "kv_start", num_req, dev),
+            _typed(kv_len, torch.int64, "kv_len", num_req, dev),
+            _typed(mass, torch.float32, "mass"), rows, int(keep), int(sink), int(recent),
+            _typed(idx, torch.int32, "idx", num_req * h * keep, dev),
+            _typed(new_len, torch.int64, "new_len", num_req, dev),
+            _typed(d_err, torch.int32, "d_err", 1, dev), _stream(stream))
+
+
+def _evict_buf(src, dst, heads):
+    """Layout of a (source, destination) pair of [rows, heads, ...] tensors
+    whose elements (the dimensions behind heads) are contiguous."""
+    if not (src.is_cuda and dst.is_cuda):
+        raise Csa2Error("libcsa2 takes device tensors")
+    if src.dtype != dst.dtype or src.dim() < 2 or src.shape[1:] != dst.shape[1:] \
+            or src.shape[1] != heads:
+        raise Csa2Error("a buffer's source and destination are [rows, %d, ...] of one type and "
+                        "element shape" % heads)
+    e = src.element_size()
+    n = 1
+    for t in (src, dst):
+        n = 1
+        for i in range(t.dim() - 1, 1, -1):
+            if t.stride(i) != n and t.shape[i] > 1:
+                raise Csa2Error("a buffer's elements must be contiguous")
+            n *= t.shape[i]
+    return CEvictBuf(src.data_ptr(), dst.data_ptr(), src.shape[0], dst.shape[0],
+                     src.stride(0) * e, src.stride(1) * e, dst.stride(0) * e, dst.stride(1) * e,
+                     n * e)
+
+
+def csa2_evict_rows(num_req, n_heads, idx, keep, new_len, src_start, dst_start, bufs, d_err,
+                    stream=None) -> int:
+    """bufs: (source, destination) pairs of [rows, heads, ...] tensors (a
+    transposed view for head-major ones)."""
+    dev = idx.device
+    for s, d in bufs:
+        if s.device != dev or d.device != dev:
+            raise Csa2Error("the buffers must be on idx's device")
+    arr = (CEvictBuf * max(1, len(bufs)))(*[_evict_buf(s, d, n_heads) for s, d in bufs])
+    with _on(idx):
+        return load().csa2_evict_rows(
+            int(num_req), int(n_heads),
+            _typed(idx, torch.int32, "idx", num_req * n_heads * keep), int(keep),
+            _typed(new_len, torch.int64, "new_len", num_req, dev),
+            _typed(src_start, torch.int64, "src_start", num_req, dev),
+            _typed(dst_start, torch.int64, "dst_start", num_req, dev), len(bufs), arr,
+            _typed(d_err, torch.int32, "d_err", 1, dev), _stream(stream))
+
+
+def _attn_out(q, out, lse, want_lse):
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    return out, lse
+
+
+def prompt_attn(packed, q, k, v, sm_scale=None, out=None, lse=None, want_lse=True, d_err=None,
+                stream=None):
+    """Causal attention of packed prompts and extends with grouped heads.
+    Rows that no request holds are left as they were in ``out`` and ``lse``
+    (unset, where these are allocated here)."""
+    out, lse = _attn_out(q, out, lse, want_lse)
+    if sm_scale is None:
+        sm_scale = q.shape[2] ** -0.5
+    _check(csa2_prompt_attn(packed, q, k, v, sm_scale, out, lse, d_err, stream),
+           "csa2_prompt_attn")
+    return out, lse
+
+
+def prefix_attn(packed, groups, q, k, v, max_kv, sm_scale=None, out=None, lse=None,
+                want_lse=True, workspace=None, d_err=None, stream=None):
+    """Attention of requests that share prefixes, each prefix read once for its
+    group; without groups, split-cache attention for single tokens.  Allocates
+    the workspace (uint8, csa2_prefix_attn_workspace bytes) if none is given."""
+    out, lse = _attn_out(q, out, lse, want_lse)
+    if sm_scale is None:
+        sm_scale = q.shape[2] ** -0.5
+    need = csa2_prefix_attn_workspace(packed["num_q"], packed["num_req"],
+                                      groups["num_groups"] if groups else 0, q.shape[1],
+                                      k.shape[1], q.shape[2],
+                                      groups["max_prefix"] if groups else 0, max_kv)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    _check(csa2_prefix_attn(packed, groups, q, k, v, max_kv, sm_scale, out, lse, workspace,
+                            workspace.numel(), d_err, stream), "csa2_prefix_attn")
+    return out, lse
+
+
+def attn_mass(packed, q, k, lse, max_kv, sm_scale=None, mass_in=None, mass=None, d_err=None,
+              stream=None):
+    """Attention weight of the queries on each cached row, fp32 [kv heads,
+    rows], added to ``mass_in`` if given.  ``mass`` may be ``mass_in``; rows of
+    no request keep their values (zeros, where it is allocated here)."""
+    if mass is None:
+        mass = torch.zeros((k.shape[1], k.shape[0]), dtype=torch.float32, device=q.device)
+    if sm_scale is None:
+        sm_scale = q.shape[2] ** -0.5
+    _check(csa2_attn_mass(packed, q, k, lse, max_kv, sm_scale, mass_in, mass, d_err, stream),
+           "csa2_attn_mass")
+    return mass
+
+
+def evict_select(kv_start, kv_len, mass, keep, sink=0, recent=0, idx=None, new_len=None,
+                 d_err=None, stream=None):
+    """The rows of each request and head that stay: the first ``sink``, the
+    last ``recent`` and those of largest mass, ``keep`` in all, ascending.
+    mass is [heads, rows]; returns (idx [R, heads, keep], new_len [R])."""
+    r, h = int(kv_len.shape[0]), int(mass.shape[0])
+    if idx is None:
+        idx = torch.empty((r, h, int(keep)), dtype=torch.int32, device=mass.device)
+    if new_len is None:
+        new_len = torch.empty(r, dtype=torch.int64, device=mass.device)
+    _check(csa2_evict_select(r, kv_start, kv_len, mass, keep, sink, recent, idx, new_len, d_err,
+                             stream), "csa2_evict_select")
+    return idx, new_len
+
+
+def evict_rows(idx, new_len, src_start, dst_start, bufs, d_err=None, stream=None):
+    """Moves the rows ``evict_select`` kept in every (source, destination)
+    pair of [rows, heads, ...] tensors; the two may be one tensor where
+    dst_start is src_start."""
+    r, h, keep = idx.shape
+    _check(csa2_evict_rows(r, h, idx, keep, new_len, src_start, dst_start, bufs, d_err, stream),
+           "csa2_evict_rows")

@@ -1,0 +1,199 @@
+// What the dense-cache kernels share (prompt and shared-prefix attention,
+// accumulated attention weight): the packed batch on the device, the tensor
+// maps of Q, K and V, and bounded waits.
+//
+// Packed rows.  n_heads query heads share n_kv_heads key heads, G = n_heads /
+// n_kv_heads to each.  A query tile holds the rows (token, head of the group)
+// of one key head, token-major: row x is token x / G, head h * G + x % G, so
+// that short extends and decode steps fill a tile with heads, and the causal
+// edge crosses few tiles.  A tile has tpt tokens (tpt * G <= 128 rows); TMA
+// fetches it as one box (64 channels, G heads, tpt tokens) per 64 channels,
+// which lands as consecutive 128-byte rows.
+#pragma once
+#include "common.cuh"
+#include "tcgen05.cuh"
+#include "tma.cuh"
+
+namespace csa2 {
+namespace dense {
+
+using namespace tc;
+
+constexpr int kTile = 128;            // rows of a query tile, keys of a key tile
+constexpr uint32_t kBlk = 128 * 128;  // bytes of a 128-row, 64-channel operand block
+constexpr int kSms = 152;             // GB300: split plans are made for this count
+constexpr uint64_t kDrainNs = 2000000000ull;
+
+// ---------------------------------------------------------------------------
+// waits: bounded, and left early once another role has given up
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t gtimer() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+
+struct Bound {
+  uint64_t wait_ns;
+  int abort;
+};
+
+static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, Bound *bd) {
+  const uint64_t t0 = gtimer();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*(volatile int *)&bd->abort) return false;
+    if (gtimer() - t0 > bd->wait_ns) {
+      atomicExch(&bd->abort, 1);
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Bound *bd) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, bd);
+}
+
+// wait that ignores the abort flag, for work that has to land before the CTA
+// leaves
+__device__ __forceinline__ void drain_bar(uint64_t *bar, uint32_t parity) {
+  const uint64_t t0 = gtimer();
+  while (!mbar_try_wait(bar, parity) && gtimer() - t0 < kDrainNs) {
+  }
+}
+
+// 2^x on the special-function unit (ex2.approx: relative error ~2^-22)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A operand in TMEM (16-bit elements, two per 32-bit column), B in shared memory
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <typename T> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+  static constexpr bool kBf16 = true;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+  }
+};
+template <> struct Elem<__half> {
+  static constexpr bool kBf16 = false;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+  }
+};
+
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_of(uint32_t m, uint32_t n, bool b_mn) {
+  return make_idesc_f16(m, n, false, b_mn) | (Elem<T>::kBf16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+// ---------------------------------------------------------------------------
+// sequences on the device: `count` runs of query rows, each with its run of
+// cache rows.  With cu_group set, run i is a group of requests: its query
+// rows are those of the requests cu_group[i] .. cu_group[i+1] - 1.
+// ---------------------------------------------------------------------------
+struct Seqs {
+  int count, num_q, num_req;
+  const int32_t *cu_q;
+  const int32_t *cu_group;
+  const int64_t *kv_start, *kv_len;
+  int64_t kv_rows;
+};
+
+__device__ __forceinline__ void seq_rows(const Seqs &S, int i, int &q0, int &n, int &err) {
+  int a = i, b = i + 1;
+  if (S.cu_group) {
+    a = S.cu_group[i];
+    b = S.cu_group[i + 1];
+    if (a < 0 || b < a || b > S.num_req) {
+      q0 = n = 0;
+      err |= CSA2_DERR_BAD_EXTEND;
+      return;
+    }
+  }
+  const int lo = S.cu_q[a], hi = S.cu_q[b];
+  if (lo < 0 || hi < lo || hi > S.num_q) {
+    q0 = n = 0;
+    err |= CSA2_DERR_BAD_EXTEND;
+    return;
+  }
+  q0 = lo;
+  n = hi - lo;
+}
+
+__device__ __forceinline__ void seq_keys(const Seqs &S, int i, int64_t &start, int64_t &m,
+                                         int &err) {
+  start = S.kv_start[i];
+  m = S.kv_len[i];
+  if (m < 0 || start < 0 || start > S.kv_rows || m > S.kv_rows - start) {
+    start = m = 0;
+    err |= CSA2_DERR_RANGE_ROW;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// tensor maps (host)
+// ---------------------------------------------------------------------------
+// [rows, heads, dim] with `ld` elements between rows, as boxes of 64 channels
+// x box_heads heads x box_rows rows in the 128-byte swizzle
+inline bool make_rows_map(CUtensorMap *map, bool bf16, const void *base, int64_t rows, int heads,
+                          int dim, int64_t ld, int box_heads, int box_rows) {
+  EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)ld * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ---------------------------------------------------------------------------
+// host checks shared by the entry points
+// ---------------------------------------------------------------------------
+struct Shape {
+  int n_heads, n_kv, dim, group;
+  bool bf16;
+};
+
+inline int check_packed(const csa2_packed *b, int32_t n_heads, int32_t n_kv_heads, int32_t dim,
+                        int32_t dtype, int64_t kv_rows, float sm_scale, Shape *s) {
+  if (!b || b->num_q < 0 || b->num_req < 0 || kv_rows < 0) return CSA2_ERR_INVALID_ARG;
+  if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads) return CSA2_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || !(sm_scale <= 3.402823466e38f)) return CSA2_ERR_INVALID_ARG;
+  if (dtype != CSA2_DT_BF16 && dtype != CSA2_DT_F16) return CSA2_ERR_UNSUPPORTED;
+  if (dim != 64 && dim != 128) return CSA2_ERR_UNSUPPORTED;
+  if (n_heads / n_kv_heads > kTile || n_kv_heads > 1024) return CSA2_ERR_UNSUPPORTED;
+  if (kv_rows > 0x7fffffffll - 2 * kTile) return CSA2_ERR_UNSUPPORTED;
+  if (b->num_q > 0 && b->num_req > 0 && (!b->cu_q || !b->kv_start || !b->kv_len))
+    return CSA2_ERR_INVALID_ARG;
+  *s = Shape{n_heads, n_kv_heads, dim, n_heads / n_kv_heads, dtype == CSA2_DT_BF16};
+  return CSA2_OK;
+}
+
+// rows with `ld` elements between them: TMA wants 16-byte rows and bases
+inline int check_rows(const void *p, int64_t ld, int heads, int dim) {
+  if (!p || ld < (int64_t)heads * dim) return CSA2_ERR_INVALID_ARG;
+  if (((uintptr_t)p & 15u) || (ld & 7) || ld > (1ll << 31)) return CSA2_ERR_UNSUPPORTED;
+  return CSA2_OK;
+}
+
+}  // namespace dense
+}  // namespace csa2
