@@ -17,7 +17,7 @@
 // Roles (12 warps, one CTA per SM, persistent over items):
 //   warps 0-7  weights: warp w reads TMEM sub-partition w % 4 (keys 32(w % 4)
 //              .. + 31), the 16-column chunks of parity w / 4
-//   warp 8     TMEM; lane 0 issues the products
+//   warp 8     TMEM; issues the products
 //   warp 9     K and Q tiles by TMA
 //   warp 10    looks items up a few ahead
 //   warp 11    -lse of the query tiles
@@ -67,11 +67,6 @@ struct MassMisc {
   alignas(16) float nl[kBufs][kTile];    // -lse in log2 units, by query row
   float red[2][kTile];
 };
-
-// warp-uniform wait
-__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, Bound *bd) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, bd));
-}
 
 __device__ void schedule_role(const MassParams &P, uint8_t *smem, MassMisc *ms) {
   const int lane = threadIdx.x & 31;
@@ -186,31 +181,39 @@ template <typename T, int D>
 __device__ void product_role(const MassParams &P, uint8_t *smem, MassMisc *ms) {
   constexpr uint32_t kKStage = (D / 64) * kBlk;
   const uint32_t idesc = idesc_of<T>(kTile, P.ncol, false);
-  const uint32_t base = smem_u32(smem), qblk = P.ncol * 128;
-  uint32_t gk = 0, gq = 0;
-  for_items<false>(ms, [&](const MassItem &it) {
-    if (it.nq == 0) return true;
-    const uint32_t sk = gk % P.kst;
-    if (!wait_bar(&ms->k_full[sk], (gk / P.kst) & 1, &ms->bd)) return false;
-    const uint64_t a = make_desc_sw128(base + sk * kKStage, 16, 1024);
-    for (int t = 0; t < it.nq; ++t, ++gq) {
-      const uint32_t sq = gq % P.qst, sb = gq % kBufs;
-      if (!wait_bar(&ms->s_empty[sb], ((gq / kBufs) & 1) ^ 1, &ms->bd)) return false;
-      if (!wait_bar(&ms->q_full[sq], (gq / P.qst) & 1, &ms->bd)) return false;
+  const uint32_t tmem = uniform(ms->tmem), qblk = P.ncol * 128;
+  const uint64_t kd = make_desc_sw128(smem_u32(smem), 16, 1024);
+  const uint64_t qd = make_desc_sw128(smem_u32(smem + P.off_q), 16, 1024);
+  uint32_t sk = 0, pk = 0, sq = 0, pq = 0, g = 0;     // ring stages and phases
+  for_items<true>(ms, [&](const MassItem &it) {
+    const int nq = uniform(it.nq);
+    if (nq == 0) return true;
+    if (!wait_all(&ms->k_full[sk], pk, &ms->bd)) return false;
+    const uint64_t a = desc_add(kd, sk * kKStage);
+    for (int t = 0; t < nq; ++t, ++g) {
+      const uint32_t sb = g % kBufs;
+      if (!wait_all(&ms->s_empty[sb], ((g / kBufs) & 1) ^ 1, &ms->bd)) return false;
+      if (!wait_all(&ms->q_full[sq], pq, &ms->bd)) return false;
       fence_after_sync();
-      const uint64_t b = make_desc_sw128(base + P.off_q + sq * P.q_stage, 16, 1024);
+      const uint64_t b = desc_add(qd, sq * P.q_stage);
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_f16(ms->tmem + sb * kTile, desc_add(a, (k >> 2) * kBlk + (k & 3) * 32),
-                desc_add(b, (k >> 2) * qblk + (k & 3) * 32), idesc, k > 0);
-      mma_commit(&ms->s_full[sb]);
-      mma_commit(&ms->q_empty[sq]);
+        for (int k = 0; k < D / 16; ++k)
+          mma_f16(tmem + sb * kTile, desc_add(a, (k >> 2) * kBlk + (k & 3) * 32),
+                  desc_add(b, (k >> 2) * qblk + (k & 3) * 32), idesc, k > 0);
+        mma_commit(&ms->s_full[sb]);
+        mma_commit(&ms->q_empty[sq]);
+      }
+      __syncwarp();
+      if (++sq == (uint32_t)P.qst) sq = 0, pq ^= 1;
     }
-    mma_commit(&ms->k_empty[sk]);
-    ++gk;
+    if (elect_one()) mma_commit(&ms->k_empty[sk]);
+    __syncwarp();
+    if (++sk == (uint32_t)P.kst) sk = 0, pk ^= 1;
     return true;
   });
-  mma_commit(&ms->done);
+  if (elect_one()) mma_commit(&ms->done);
+  __syncwarp();
   drain_bar(&ms->done, 0);
 }
 
@@ -345,8 +348,7 @@ attn_mass_kernel(MassParams P, const __grid_constant__ CUtensorMap mq,
   if (warp < kEpiWarps) {
     weight_role(P, ms);
   } else if (warp == 8) {
-    if ((threadIdx.x & 31) == 0) product_role<T, D>(P, smem, ms);
-    __syncwarp();
+    product_role<T, D>(P, smem, ms);
   } else if (warp == 9) {
     if ((threadIdx.x & 31) == 0) load_role<D>(P, smem, ms, &mq, &mk);
     __syncwarp();

@@ -38,11 +38,25 @@ struct Bound {
   int abort;
 };
 
+// poll without suspending
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, Bound *bd) {
-  const uint64_t t0 = gtimer();
-  while (!mbar_try_wait(bar, parity)) {
+  // the hardware suspends a try_wait for some microseconds: a bound shorter
+  // than that is polled for
+  const uint64_t t0 = gtimer(), limit = bd->wait_ns;
+  while (limit < 100000 ? !mbar_test(bar, parity) : !mbar_try_wait(bar, parity)) {
     if (*(volatile int *)&bd->abort) return false;
-    if (gtimer() - t0 > bd->wait_ns) {
+    if (gtimer() - t0 > limit) {
       atomicExch(&bd->abort, 1);
       return false;
     }
@@ -51,8 +65,34 @@ static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, Bo
 }
 
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Bound *bd) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_test(bar, parity)) return true;
   return wait_slow(bar, parity, bd);
+}
+
+// the same by a whole warp, which goes on or gives up together
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, Bound *bd) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, bd));
+}
+
+// One lane of a converged warp (the same one every time).  Products are issued
+// by the elected lane of a warp that runs its whole loop together: operands of
+// an MMA live in uniform registers, which only warp-uniform code computes in
+// place.  From a lane-0 branch each is moved over first, which holds the
+// tensor pipe at 70 cycles for an M = N = 128, K = 16 product with both
+// operands in shared memory and 107 with A in TMEM; issued this way it runs
+// at its own 64.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// the value of lane 0, known to be the same in every lane
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xffffffffu, v, 0);
 }
 
 // wait that ignores the abort flag, for work that has to land before the CTA
@@ -68,6 +108,33 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// two fp32 operations in one instruction, on register pairs
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // A operand in TMEM (16-bit elements, two per 32-bit column), B in shared memory

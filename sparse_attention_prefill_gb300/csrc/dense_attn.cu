@@ -16,7 +16,7 @@
 // then, since S of this step was issued after them), and writes P rounded to
 // the inputs' type.  Row sums are taken of the unrounded P in fp32.
 //
-// The MMA thread issues, for each key tile j and query tile t, O[t](j) and
+// The MMA warp issues, for each key tile j and query tile t, O[t](j) and
 // then S[t](j+1): while one tile's softmax runs, the other tile's products
 // keep the tensor pipe busy (kNT = 2), or those of the second CTA of the SM
 // do (kNT = 1).
@@ -80,15 +80,15 @@ struct Item {
 template <int kStages>
 struct Misc {
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full, aux, s_full[2], p_full[2], o_full[2], done;
+  uint64_t q_full, aux, s_full[2], p_full[2][2], o_full[2], done;
   Bound bd;
   uint32_t tmem;
   Item item;
 };
 
-// Run and tile of this CTA, by one warp.  False if the CTA has no work.
-__device__ bool find_item(const AttnParams &P, int slot, int split, int tok_cta, int nt,
-                          Item &it) {
+// Run and tile of this CTA, by one warp; run = -1 if the CTA has no work.
+template <int NT>
+__device__ void find_item(const AttnParams &P, int slot, int split, int tok_cta, Item &it) {
   const int lane = threadIdx.x & 31;
   int base = 0, err = 0, run = -1, tile = 0, q0 = 0, n = 0;
   for (int i0 = 0; i0 < P.seqs.count; i0 += 32) {
@@ -121,12 +121,13 @@ __device__ bool find_item(const AttnParams &P, int slot, int split, int tok_cta,
     seq_keys(P.seqs, run, it.start, it.m, err);
     const int ntok = min(tok_cta, n - it.tok0);
     it.ntile = (ntok + P.tpt - 1) / P.tpt;
-    for (int t = 0; t < nt; ++t) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
       const int last_tok = min(it.tok0 + (t + 1) * P.tpt, n) - 1;
       const int64_t last = P.causal ? it.m - n + last_tok : it.m - 1;
       it.nkt[t] = t < it.ntile && last >= 0 ? (int)(last / kTile) + 1 : 0;
     }
-    const int total = it.nkt[it.ntile - 1];
+    const int total = NT == 2 ? max(it.nkt[0], it.nkt[NT - 1]) : it.nkt[0];
     if (P.splits > 0) {
       const int per = (total + P.splits - 1) / P.splits;
       it.kt0 = min(total, split * per);
@@ -135,7 +136,8 @@ __device__ bool find_item(const AttnParams &P, int slot, int split, int tok_cta,
       it.kt0 = 0;
       it.kt1 = total;
     }
-    for (int t = 0; t < nt; ++t) it.nkt[t] = min(it.nkt[t], it.kt1);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) it.nkt[t] = min(it.nkt[t], it.kt1);
     it.uncovered = 0;
     if (P.cover) {
       bool mine = false;
@@ -147,7 +149,6 @@ __device__ bool find_item(const AttnParams &P, int slot, int split, int tok_cta,
   }
   err = __reduce_or_sync(0xffffffffu, err);
   if (lane == 0) raise_err(P.d_err, err);
-  return run >= 0;
 }
 
 // Producer warp: Q once, then K and V tiles through the ring.
@@ -212,59 +213,82 @@ __device__ void producer_role(const AttnParams &P, uint8_t *smem, M *ms, int h,
   __syncwarp();
 }
 
-// One thread issues every product.
+// One warp issues every product.
 template <typename T, int D, int NT, typename M>
 __device__ void mma_role(uint8_t *smem, M *ms) {
   using C = Cfg<D, NT>;
-  const Item &it = ms->item;
-  const uint32_t tmem = ms->tmem;
-  const uint32_t id_s = idesc_of<T>(kTile, kTile, false);
-  const uint32_t id_o = idesc_of<T>(kTile, D, true);
-  const uint32_t ring = smem_u32(smem + C::kOffRing), q0 = smem_u32(smem);
-  const int nk = it.kt1 - it.kt0;
-  auto issue_s = [&](int t, uint32_t stage) {
-    const uint64_t a = make_desc_sw128(q0 + t * C::kQTile, 16, 1024);
-    const uint64_t b = make_desc_sw128(ring + stage * C::kStage, 16, 1024);
+  constexpr uint32_t kIdS = idesc_of<T>(kTile, kTile, false);
+  constexpr uint32_t kIdO = idesc_of<T>(kTile, D, true);
+  const uint32_t tmem = uniform(ms->tmem);
+  const int kt0 = uniform(ms->item.kt0), nk = uniform(ms->item.kt1) - kt0;
+  int end[NT];                     // key tiles of query tile t, counted from kt0
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (k >> 2) * kBlk + (k & 3) * 32;
-      mma_f16(tmem + t * 128, desc_add(a, off), desc_add(b, off), id_s, k > 0);
+  for (int t = 0; t < NT; ++t) end[t] = uniform(ms->item.nkt[t]) - kt0;
+  const uint64_t ring_k = make_desc_sw128(smem_u32(smem + C::kOffRing), 16, 1024);
+  const uint64_t ring_v = make_desc_sw128(smem_u32(smem + C::kOffRing), kBlk, 1024);
+  const uint64_t qd = make_desc_sw128(smem_u32(smem), 16, 1024);
+  auto issue_s = [&](int t, uint32_t stage) {
+    const uint64_t b = desc_add(ring_k, stage * C::kStage);
+    if (elect_one()) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (k >> 2) * kBlk + (k & 3) * 32;
+        mma_f16(tmem + t * 128, desc_add(qd, t * C::kQTile + off), desc_add(b, off), kIdS, k > 0);
+      }
+      mma_commit(&ms->s_full[t]);
     }
-    mma_commit(&ms->s_full[t]);
+    __syncwarp();
   };
-  bool ok = wait_bar(&ms->q_full, 0, &ms->bd) && wait_bar(&ms->full[0], 0, &ms->bd);
+  auto commit = [&](uint64_t *bar) {
+    if (elect_one()) mma_commit(bar);
+    __syncwarp();
+  };
+  bool ok = wait_all(&ms->q_full, 0, &ms->bd) && wait_all(&ms->full[0], 0, &ms->bd);
   if (ok) {
     fence_after_sync();
-    for (int t = 0; t < it.ntile; ++t)
-      if (it.kt0 < it.nkt[t]) issue_s(t, 0);
-    mma_commit(&ms->empty[0]);
-  }
-  for (int j = 0; j < nk && ok; ++j) {
-    const uint32_t gv = 2 * j + 1, sv = gv % C::kStages;
-    const uint32_t gk = 2 * j + 2, sk = gk % C::kStages;
-    if (!(ok = wait_bar(&ms->full[sv], (gv / C::kStages) & 1, &ms->bd))) break;
-    bool next = false;                      // the next K tile has arrived
-    for (int t = 0; t < it.ntile; ++t) {
-      if (it.kt0 + j >= it.nkt[t]) continue;
-      if (!(ok = wait_bar(&ms->p_full[t], j & 1, &ms->bd))) break;
-      fence_after_sync();
-      const uint64_t b = make_desc_sw128(ring + sv * C::kStage, kBlk, 1024);
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        mma_f16_ts(tmem + C::kColO + t * D, tmem + t * 128 + k * 8, desc_add(b, k * 2048), id_o,
-                   j > 0 || k > 0);
-      if (it.kt0 + j + 1 < it.nkt[t]) {
-        if (!next && !(ok = wait_bar(&ms->full[sk], (gk / C::kStages) & 1, &ms->bd))) break;
+    for (int t = 0; t < NT; ++t)
+      if (end[t] > 0) issue_s(t, 0);
+    commit(&ms->empty[0]);
+  }
+  uint32_t sv = 1, pv = 0;         // ring stage and phase of V(j)
+  for (int j = 0; j < nk && ok; ++j) {
+    uint32_t sk = sv + 1, pk = pv;                 // K(j + 1)
+    if (sk == C::kStages) sk = 0, pk ^= 1;
+    if (!(ok = wait_all(&ms->full[sv], pv, &ms->bd))) break;
+    bool next = false;                             // K(j + 1) has arrived
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (j >= end[t] || !ok) continue;
+      const uint64_t b = desc_add(ring_v, sv * C::kStage);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {       // P arrives in halves of 64 keys
+        if (ok && (ok = wait_all(&ms->p_full[t][half], j & 1, &ms->bd))) {
+          fence_after_sync();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              mma_f16_ts(tmem + C::kColO + t * D, tmem + t * 128 + k * 8, desc_add(b, k * 2048),
+                         kIdO, j > 0 || k > 0);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) continue;
+      if (j + 1 < end[t]) {
+        if (!next && !(ok = wait_all(&ms->full[sk], pk, &ms->bd))) continue;
         next = true;
         issue_s(t, sk);
       } else {
-        mma_commit(&ms->o_full[t]);
+        commit(&ms->o_full[t]);
       }
     }
-    mma_commit(&ms->empty[sv]);
-    if (j + 1 < nk) mma_commit(&ms->empty[sk]);
+    commit(&ms->empty[sv]);
+    if (j + 1 < nk) commit(&ms->empty[sk]);
+    sv = sk + 1, pv = pk;
+    if (sv == C::kStages) sv = 0, pv ^= 1;
   }
-  mma_commit(&ms->done);      // TMEM is not freed under a running product
+  commit(&ms->done);               // TMEM is not freed under a running product
   drain_bar(&ms->done, 0);
 }
 
@@ -289,6 +313,7 @@ __device__ void softmax_role(const AttnParams &P, M *ms, int h, int split) {
   // largest keep full precision and the largest stays below 2^16
   constexpr float kLift = Elem<T>::kBf16 ? 0.f : 8.f;
   constexpr float kMargin = Elem<T>::kBf16 ? 8.f : 7.f;
+  const uint64_t scale2 = pack2(P.scale_log2, P.scale_log2);
   float ref = -INFINITY, sum = 0.f;
   bool ok = true;
   const int kt_end = it.nkt[t];
@@ -308,12 +333,15 @@ __device__ void softmax_role(const AttnParams &P, M *ms, int h, int split) {
         for (int e = 0; e < 32; ++e)
           if (32 * c + e > vis) s[c][e] = 0xff800000u;
     }
-    float mx = -INFINITY;
+    float m4[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < 4; ++c) {
+      m4[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-      for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[c][e]));
-    mx *= P.scale_log2;
+      for (int e = 2; e < 32; e += 2)
+        m4[c] = max3(m4[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+    }
+    const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * P.scale_log2;
     const bool move = mx > ref + (kLift + kMargin);
     if (__any_sync(0xffffffffu, move)) {
       const float nref = move ? mx - kLift : ref;
@@ -333,24 +361,29 @@ __device__ void softmax_role(const AttnParams &P, M *ms, int h, int split) {
       }
     }
     const float sub = ref == -INFINITY ? 0.f : ref;
-    float part = 0.f;
+    const uint64_t sub2 = pack2(-sub, -sub);
+    uint64_t part[2] = {pack2(sum, 0.f), 0};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t p[32];
 #pragma unroll
       for (int e = 0; e < 32; e += 2) {
-        const float a = ex2(fmaf(__uint_as_float(s[c][e]), P.scale_log2, -sub));
-        const float b = ex2(fmaf(__uint_as_float(s[c][e + 1]), P.scale_log2, -sub));
-        part += a + b;
+        const float2 x = unpack2(fma2(pack2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                      scale2, sub2));
+        const float a = ex2(x.x), b = ex2(x.y);
+        part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], pack2(a, b));
         p[e / 2] = Elem<T>::pack(a, b);
       }
       tmem_st32x32b_x16(ts + 16 * c, p);
+      if (c & 1) {                 // 64 keys written: their product may start
+        tmem_wait_st();
+        fence_before_sync();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->p_full[t][c >> 1]);
+      }
     }
-    sum += part;
-    tmem_wait_st();
-    fence_before_sync();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->p_full[t]);
+    const float2 part2 = unpack2(add2(part[0], part[1]));
+    sum = part2.x + part2.y;
   }
   const bool any = it.kt0 < kt_end;
   if (ok && any) ok = wait_bar(&ms->o_full[t], 0, &ms->bd);
@@ -422,7 +455,7 @@ dense_attn_kernel(AttnParams P, const __grid_constant__ CUtensorMap mq,
   const int slot = blockIdx.x / ns / P.n_kv;
   if (warp == 4 * NT + 1) {
     Item it;
-    find_item(P, slot, split, NT * P.tpt, NT, it);
+    find_item<NT>(P, slot, split, NT * P.tpt, it);
     if ((threadIdx.x & 31) == 0) ms->item = it;
   } else if (warp == 4 * NT) {
     tmem_alloc(&ms->tmem, C::kTmemCols);
@@ -437,7 +470,8 @@ dense_attn_kernel(AttnParams P, const __grid_constant__ CUtensorMap mq,
     mbar_init(&ms->done, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&ms->s_full[t], 1);
-      mbar_init(&ms->p_full[t], 4);
+      mbar_init(&ms->p_full[t][0], 4);
+      mbar_init(&ms->p_full[t][1], 4);
       mbar_init(&ms->o_full[t], 1);
     }
     ms->bd.abort = 0;
@@ -451,7 +485,7 @@ dense_attn_kernel(AttnParams P, const __grid_constant__ CUtensorMap mq,
     if (warp == 4 * NT + 1) {
       producer_role<D, NT>(P, smem, ms, h, &mq, &mk, &mv);
     } else if (warp == 4 * NT) {
-      if ((threadIdx.x & 31) == 0 && ms->item.kt0 < ms->item.kt1) mma_role<T, D, NT>(smem, ms);
+      if (ms->item.kt0 < ms->item.kt1) mma_role<T, D, NT>(smem, ms);
       __syncwarp();
     } else {
       softmax_role<T, D, NT>(P, ms, h, split);
