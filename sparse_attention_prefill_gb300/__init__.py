@@ -480,103 +480,119 @@ def sparse_swa_attn_fp4kv(batch, q, kv_fp4, kv_sf, idx, swa_fp8, swa_scale, win_
 # ---------------------------------------------------------------------------
 
 _DTYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
-def _typed(t, dtype, name, numel=0, device=None):
-    """Device pointer of a contiguous tensor of a given type (None: NULL)."""
+def _arg(t, dtype, name, numel, dev):
+    """Address of a contiguous tensor of a type, with at least numel values, on
+    CUDA device dev (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise Csa2Error("%s: expected %s, got %s" % (name, dtype, t.dtype))
-    if t.numel() < numel:
-        raise Csa2Error("%s: expected at least %d values, got %d" % (name, numel, t.numel()))
-    if device is not None and t.device != device:
-        raise Csa2Error("%s is on %s, not on %s" % (name, t.device, device))
-    return _ptr(t)
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < numel \
+            or not t.is_contiguous():
+        if t.get_device() < 0:
+            raise Csa2Error("libcsa2 takes device tensors; %s is a %s tensor" % (name, t.device))
+        if not t.is_contiguous():
+            raise Csa2Error("libcsa2 takes contiguous tensors; %s is not" % name)
+        raise Csa2Error("%s: expected at least %d values of %s on cuda:%d, got %d of %s on %s"
+                        % (name, numel, dtype, dev, t.numel(), t.dtype, t.device))
+    return t.data_ptr()
 
 
-def _rows3(t, name, like=None):
-    """(pointer, row distance) of a [rows, heads, dim] tensor."""
-    if not t.is_cuda:
-        raise Csa2Error("libcsa2 takes device tensors; got a %s tensor" % t.device)
-    if t.dim() != 3 or t.dtype not in _DTYPES:
+def _rows3(t, name, dtype, dev, dim):
+    """(address, row distance, rows, heads) of a [rows, heads, dim] tensor."""
+    if t.dim() != 3 or dtype not in _DTYPES:
         raise Csa2Error("%s: expected [rows, heads, dim] of bf16 or f16" % name)
-    if like is not None and (t.dtype != like.dtype or t.device != like.device
-                             or t.shape[2] != like.shape[2]):
-        raise Csa2Error("%s: expected the type, device and head size of q" % name)
     n, h, d = t.shape
-    s = t.stride()
-    if (s[2] != 1 and d > 1) or (s[1] != d and h > 1):
-        raise Csa2Error("%s: heads and channels must be contiguous" % name)
-    return C.c_void_p(t.data_ptr()), max(s[0], h * d) if n <= 1 else s[0]
+    s0, s1, s2 = t.stride()
+    if t.dtype is not dtype or t.get_device() != dev or d != dim or s1 != d or s2 != 1:
+        if t.get_device() < 0:
+            raise Csa2Error("libcsa2 takes device tensors; %s is a %s tensor" % (name, t.device))
+        if t.dtype is not dtype or t.get_device() != dev or d != dim:
+            raise Csa2Error("%s: expected the type, device and head size of q" % name)
+        if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+            raise Csa2Error("%s: heads and channels must be contiguous" % name)
+    return t.data_ptr(), s0 if n > 1 else max(s0, h * d), n, h
 
 
-def make_packed(b, device=None):
-    """Host struct for a packed dict of device tensors."""
+def make_packed(b, dev):
+    """Host struct for a packed dict of tensors on CUDA device dev."""
     r = int(b["num_req"])
-    return CPacked(int(b["num_q"]), r, _typed(b["cu_q"], torch.int32, "cu_q", r + 1, device),
-                   _typed(b["kv_start"], torch.int64, "kv_start", r, device),
-                   _typed(b["kv_len"], torch.int64, "kv_len", r, device))
+    return CPacked(int(b["num_q"]), r, _arg(b["cu_q"], _I32, "cu_q", r + 1, dev),
+                   _arg(b["kv_start"], _I64, "kv_start", r, dev),
+                   _arg(b["kv_len"], _I64, "kv_len", r, dev))
 
 
-def make_groups(g, device=None):
-    """Host struct for a groups dict of device tensors (None: no groups)."""
-    if g is None:
-        return None
+def make_groups(g, dev):
+    """Host struct for a groups dict of tensors on CUDA device dev."""
     n = int(g["num_groups"])
-    return CPrefixGroups(n, 0, _typed(g["cu_group"], torch.int32, "cu_group", n + 1, device),
-                         _typed(g["prefix_start"], torch.int64, "prefix_start", n, device),
-                         _typed(g["prefix_len"], torch.int64, "prefix_len", n, device),
+    return CPrefixGroups(n, 0, _arg(g["cu_group"], _I32, "cu_group", n + 1, dev),
+                         _arg(g["prefix_start"], _I64, "prefix_start", n, dev),
+                         _arg(g["prefix_len"], _I64, "prefix_len", n, dev),
                          int(g["max_prefix"]))
 
 
-class _on:
-    """Makes a tensor's device the current one for a call's launches."""
-
-    __slots__ = ("back", "to")
-
-    def __init__(self, t):
-        self.to = t.device.index
-        self.back = None
-
-    def __enter__(self):
-        if self.to is not None:
-            cur = torch.cuda.current_device()
-            if cur != self.to:
-                self.back = cur
-                torch.cuda.set_device(self.to)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _call(dev, fn, args, stream):
+    """fn(*args, stream) with device dev current; its current stream by default."""
+    if dev < 0:
+        raise Csa2Error("libcsa2 takes device tensors")
+    if torch._C._cuda_getDevice() == dev:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                  else stream.cuda_stream)
+    with torch.cuda.device(dev):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                  else stream.cuda_stream)
 
 
-def _same_kv(k, v):
-    if k.shape != v.shape:
+def _packed_args(packed, q, k):
+    """What the calls on a packed batch begin with: the host struct (kept alive
+    by the caller), the device, q's type, and the shape arguments with q and k."""
+    dt, dev = q.dtype, q.get_device()
+    d = q.shape[-1]
+    if dev < 0:
+        raise Csa2Error("libcsa2 takes device tensors; q is a %s tensor" % q.device)
+    qp, ldq, nq, h = _rows3(q, "q", dt, dev, d)
+    kp, ldk, rows, kv = _rows3(k, "k", dt, dev, d)
+    st = make_packed(packed, dev)
+    if st.num_q > nq:
+        raise Csa2Error("q has %d rows, the batch names %d" % (nq, st.num_q))
+    return st, dev, dt, rows, (h, kv, d, _DTYPES[dt], qp, ldq, kp, ldk)
+
+
+def _attn_args(packed, q, k, v, out, lse, want_lse, d_err):
+    """The attention calls' arguments; allocates the outputs that are None."""
+    st, dev, dt, rows, shape = _packed_args(packed, q, k)
+    vp, ldv, vrows, vh = _rows3(v, "v", dt, dev, shape[2])
+    if vrows != rows or vh != shape[1]:
         raise Csa2Error("k and v: expected the same shape, got %s and %s"
                         % (tuple(k.shape), tuple(v.shape)))
+    n = st.num_q * shape[0]
+    if out is None:
+        out = torch.empty(q.shape, dtype=dt, device=q.device)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, dt, "out", n * shape[2], dev)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+        lp = lse.data_ptr()
+    else:
+        lp = _arg(lse, _F32, "lse", n, dev)
+    return (st, dev, shape + (vp, ldv, rows), (op, lp), _arg(d_err, _I32, "d_err", 1, dev),
+            out, lse)
 
 
-def _check_q(packed, q, k):
-    if int(packed["num_q"]) > q.shape[0]:
-        raise Csa2Error("q has %d rows, the batch names %d" % (q.shape[0], packed["num_q"]))
-    if k.shape[1] < 1 or q.shape[1] % k.shape[1]:
-        raise Csa2Error("%d query heads do not share %d key heads" % (q.shape[1], k.shape[1]))
+def _prompt(packed, q, k, v, sm_scale, out, lse, want_lse, d_err, stream):
+    st, dev, shape, outs, err, out, lse = _attn_args(packed, q, k, v, out, lse, want_lse, d_err)
+    if sm_scale is None:
+        sm_scale = shape[2] ** -0.5
+    return _call(dev, load().csa2_prompt_attn,
+                 (C.byref(st), *shape, float(sm_scale), *outs, err), stream), out, lse
 
 
 def csa2_prompt_attn(packed, q, k, v, sm_scale, out, lse, d_err, stream=None) -> int:
-    st = make_packed(packed, q.device)
-    _check_q(packed, q, k)
-    _same_kv(k, v)
-    (qp, ldq), (kp, ldk), (vp, ldv) = _rows3(q, "q"), _rows3(k, "k", q), _rows3(v, "v", q)
-    n = st.num_q * q.shape[1]
-    with _on(q):
-        return load().csa2_prompt_attn(
-            C.byref(st), q.shape[1], k.shape[1], q.shape[2], _DTYPES[q.dtype], qp, ldq, kp, ldk,
-            vp, ldv, k.shape[0], float(sm_scale),
-            _typed(out, q.dtype, "out", n * q.shape[2], q.device),
-            _typed(lse, torch.float32, "lse", n, q.device),
-            _typed(d_err, torch.int32, "d_err", 1, q.device), _stream(stream))
+    if out is None:
+        raise Csa2Error("csa2_prompt_attn: out is missing")
+    return _prompt(packed, q, k, v, sm_scale, out, lse, False, d_err, stream)[0]
 
 
 def csa2_prefix_attn_workspace(num_q, num_req, num_groups, n_heads, n_kv_heads, dim, max_prefix,
@@ -587,104 +603,98 @@ def csa2_prefix_attn_workspace(num_q, num_req, num_groups, n_heads, n_kv_heads, 
                                              int(n_heads), int(n_kv_heads), int(dim),
                                              int(max_prefix), int(max_kv), C.byref(out)),
            "csa2_prefix_attn_workspace")
-    return int(out.value)
+    return out.value
+
+
+def _prefix(packed, groups, q, k, v, max_kv, sm_scale, out, lse, want_lse, workspace, nbytes,
+            d_err, stream):
+    st, dev, shape, outs, err, out, lse = _attn_args(packed, q, k, v, out, lse, want_lse, d_err)
+    if sm_scale is None:
+        sm_scale = shape[2] ** -0.5
+    gr = None if groups is None else make_groups(groups, dev)
+    if nbytes is None:
+        nbytes = csa2_prefix_attn_workspace(st.num_q, st.num_req, 0 if gr is None else
+                                            gr.num_groups, *shape[:3], 0 if gr is None else
+                                            gr.max_prefix, max_kv)
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            if stream is not None:
+                workspace.record_stream(stream)
+        else:
+            nbytes = max(nbytes, workspace.numel())
+    return _call(dev, load().csa2_prefix_attn,
+                 (C.byref(st), None if gr is None else C.byref(gr), *shape, int(max_kv),
+                  float(sm_scale), *outs, _arg(workspace, torch.uint8, "workspace", nbytes, dev),
+                  nbytes, err), stream), out, lse
 
 
 def csa2_prefix_attn(packed, groups, q, k, v, max_kv, sm_scale, out, lse, workspace,
                      workspace_bytes, d_err, stream=None) -> int:
-    st = make_packed(packed, q.device)
-    gr = make_groups(groups, q.device)
-    _check_q(packed, q, k)
-    _same_kv(k, v)
-    (qp, ldq), (kp, ldk), (vp, ldv) = _rows3(q, "q"), _rows3(k, "k", q), _rows3(v, "v", q)
-    n = st.num_q * q.shape[1]
-    with _on(q):
-        return load().csa2_prefix_attn(
-            C.byref(st), None if gr is None else C.byref(gr), q.shape[1], k.shape[1], q.shape[2],
-            _DTYPES[q.dtype], qp, ldq, kp, ldk, vp, ldv, k.shape[0], int(max_kv),
-            float(sm_scale), _typed(out, q.dtype, "out", n * q.shape[2], q.device),
-            _typed(lse, torch.float32, "lse", n, q.device),
-            _typed(workspace, torch.uint8, "workspace", workspace_bytes, q.device),
-            int(workspace_bytes), _typed(d_err, torch.int32, "d_err", 1, q.device),
-            _stream(stream))
+    if out is None:
+        raise Csa2Error("csa2_prefix_attn: out is missing")
+    return _prefix(packed, groups, q, k, v, max_kv, sm_scale, out, lse, False, workspace,
+                   int(workspace_bytes), d_err, stream)[0]
 
 
 def csa2_attn_mass(packed, q, k, lse, max_kv, sm_scale, mass_in, mass_out, d_err,
                    stream=None) -> int:
-    st = make_packed(packed, q.device)
-    _check_q(packed, q, k)
-    (qp, ldq), (kp, ldk) = _rows3(q, "q"), _rows3(k, "k", q)
-    n = k.shape[0] * k.shape[1]
-    with _on(q):
-        return load().csa2_attn_mass(
-            C.byref(st), q.shape[1], k.shape[1], q.shape[2], _DTYPES[q.dtype], qp, ldq, kp, ldk,
-            k.shape[0], _typed(lse, torch.float32, "lse", st.num_q * q.shape[1], q.device),
-            int(max_kv), float(sm_scale), _typed(mass_in, torch.float32, "mass_in", n, q.device),
-            _typed(mass_out, torch.float32, "mass_out", n, q.device),
-            _typed(d_err, torch.int32, "d_err", 1, q.device), _stream(stream))
+    st, dev, _, rows, shape = _packed_args(packed, q, k)
+    n = rows * shape[1]
+    return _call(dev, load().csa2_attn_mass,
+                 (C.byref(st), *shape, rows, _arg(lse, _F32, "lse", st.num_q * shape[0], dev),
+                  int(max_kv), float(sm_scale), _arg(mass_in, _F32, "mass_in", n, dev),
+                  _arg(mass_out, _F32, "mass_out", n, dev),
+                  _arg(d_err, _I32, "d_err", 1, dev)), stream)
 
 
 def csa2_evict_select(num_req, kv_start, kv_len, mass, keep, sink, recent, idx, new_len, d_err,
                       stream=None) -> int:
+    num_req, keep, dev = int(num_req), int(keep), mass.get_device()
     h, rows = mass.shape
-    dev = mass.device
-    with _on(mass):
-        return load().csa2_evict_select(
-            int(num_req), h, _typed(kv_start, torch.int64, "kv_start", num_req, dev),
-            _typed(kv_len, torch.int64, "kv_len", num_req, dev),
-            _typed(mass, torch.float32, "mass"), rows, int(keep), int(sink), int(recent),
-            _typed(idx, torch.int32, "idx", num_req * h * keep, dev),
-            _typed(new_len, torch.int64, "new_len", num_req, dev),
-            _typed(d_err, torch.int32, "d_err", 1, dev), _stream(stream))
+    return _call(dev, load().csa2_evict_select,
+                 (num_req, h, _arg(kv_start, _I64, "kv_start", num_req, dev),
+                  _arg(kv_len, _I64, "kv_len", num_req, dev), _arg(mass, _F32, "mass", 0, dev),
+                  rows, keep, int(sink), int(recent),
+                  _arg(idx, _I32, "idx", num_req * h * keep, dev),
+                  _arg(new_len, _I64, "new_len", num_req, dev),
+                  _arg(d_err, _I32, "d_err", 1, dev)), stream)
 
 
-def _evict_buf(src, dst, heads):
-    """Layout of a (source, destination) pair of [rows, heads, ...] tensors
-    whose elements (the dimensions behind heads) are contiguous."""
-    if not (src.is_cuda and dst.is_cuda):
-        raise Csa2Error("libcsa2 takes device tensors")
-    if src.dtype != dst.dtype or src.dim() < 2 or src.shape[1:] != dst.shape[1:] \
-            or src.shape[1] != heads:
+def _evict_buf(src, dst, heads, dev):
+    """Fields of csa2_evict_buf for a (source, destination) pair of [rows,
+    heads, ...] tensors whose elements (the dimensions behind heads) are
+    contiguous."""
+    if src.get_device() != dev or dst.get_device() != dev:
+        raise Csa2Error("the buffers must be on idx's device")
+    a, b = src.shape, dst.shape
+    if src.dtype is not dst.dtype or len(a) < 2 or a[1:] != b[1:] or a[1] != heads:
         raise Csa2Error("a buffer's source and destination are [rows, %d, ...] of one type and "
                         "element shape" % heads)
-    e = src.element_size()
+    s, d = src.stride(), dst.stride()
     n = 1
-    for t in (src, dst):
-        n = 1
-        for i in range(t.dim() - 1, 1, -1):
-            if t.stride(i) != n and t.shape[i] > 1:
-                raise Csa2Error("a buffer's elements must be contiguous")
-            n *= t.shape[i]
-    return CEvictBuf(src.data_ptr(), dst.data_ptr(), src.shape[0], dst.shape[0],
-                     src.stride(0) * e, src.stride(1) * e, dst.stride(0) * e, dst.stride(1) * e,
-                     n * e)
+    for i in range(len(a) - 1, 1, -1):
+        if (s[i] != n or d[i] != n) and a[i] > 1:
+            raise Csa2Error("a buffer's elements must be contiguous")
+        n *= a[i]
+    e = src.element_size()
+    return (src.data_ptr(), dst.data_ptr(), a[0], b[0], s[0] * e, s[1] * e, d[0] * e, d[1] * e,
+            n * e)
 
 
 def csa2_evict_rows(num_req, n_heads, idx, keep, new_len, src_start, dst_start, bufs, d_err,
                     stream=None) -> int:
-    """bufs: (source, destination) pairs of [rows, heads, ...] tensors (a
+    """``bufs``: (source, destination) pairs of [rows, heads, ...] tensors (a
     transposed view for head-major ones)."""
-    dev = idx.device
-    for s, d in bufs:
-        if s.device != dev or d.device != dev:
-            raise Csa2Error("the buffers must be on idx's device")
-    arr = (CEvictBuf * max(1, len(bufs)))(*[_evict_buf(s, d, n_heads) for s, d in bufs])
-    with _on(idx):
-        return load().csa2_evict_rows(
-            int(num_req), int(n_heads),
-            _typed(idx, torch.int32, "idx", num_req * n_heads * keep), int(keep),
-            _typed(new_len, torch.int64, "new_len", num_req, dev),
-            _typed(src_start, torch.int64, "src_start", num_req, dev),
-            _typed(dst_start, torch.int64, "dst_start", num_req, dev), len(bufs), arr,
-            _typed(d_err, torch.int32, "d_err", 1, dev), _stream(stream))
-
-
-def _attn_out(q, out, lse, want_lse):
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    return out, lse
+    num_req, keep, dev = int(num_req), int(keep), idx.get_device()
+    ip = _arg(idx, _I32, "idx", num_req * n_heads * keep, dev)
+    # csa2_evict_buf is nine 64-bit fields
+    arr = (C.c_int64 * (9 * max(1, len(bufs))))(*[x for s, d in bufs
+                                                  for x in _evict_buf(s, d, n_heads, dev)])
+    return _call(dev, load().csa2_evict_rows,
+                 (num_req, int(n_heads), ip, keep, _arg(new_len, _I64, "new_len", num_req, dev),
+                  _arg(src_start, _I64, "src_start", num_req, dev),
+                  _arg(dst_start, _I64, "dst_start", num_req, dev), len(bufs), arr,
+                  _arg(d_err, _I32, "d_err", 1, dev)), stream)
 
 
 def prompt_attn(packed, q, k, v, sm_scale=None, out=None, lse=None, want_lse=True, d_err=None,
@@ -692,11 +702,8 @@ def prompt_attn(packed, q, k, v, sm_scale=None, out=None, lse=None, want_lse=Tru
     """Causal attention of packed prompts and extends with grouped heads.
     Rows that no request holds are left as they were in ``out`` and ``lse``
     (unset, where these are allocated here)."""
-    out, lse = _attn_out(q, out, lse, want_lse)
-    if sm_scale is None:
-        sm_scale = q.shape[2] ** -0.5
-    _check(csa2_prompt_attn(packed, q, k, v, sm_scale, out, lse, d_err, stream),
-           "csa2_prompt_attn")
+    st, out, lse = _prompt(packed, q, k, v, sm_scale, out, lse, want_lse, d_err, stream)
+    _check(st, "csa2_prompt_attn")
     return out, lse
 
 
@@ -705,19 +712,9 @@ def prefix_attn(packed, groups, q, k, v, max_kv, sm_scale=None, out=None, lse=No
     """Attention of requests that share prefixes, each prefix read once for its
     group; without groups, split-cache attention for single tokens.  Allocates
     the workspace (uint8, csa2_prefix_attn_workspace bytes) if none is given."""
-    out, lse = _attn_out(q, out, lse, want_lse)
-    if sm_scale is None:
-        sm_scale = q.shape[2] ** -0.5
-    need = csa2_prefix_attn_workspace(packed["num_q"], packed["num_req"],
-                                      groups["num_groups"] if groups else 0, q.shape[1],
-                                      k.shape[1], q.shape[2],
-                                      groups["max_prefix"] if groups else 0, max_kv)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)
-    _check(csa2_prefix_attn(packed, groups, q, k, v, max_kv, sm_scale, out, lse, workspace,
-                            workspace.numel(), d_err, stream), "csa2_prefix_attn")
+    st, out, lse = _prefix(packed, groups, q, k, v, max_kv, sm_scale, out, lse, want_lse,
+                           workspace, None, d_err, stream)
+    _check(st, "csa2_prefix_attn")
     return out, lse
 
 

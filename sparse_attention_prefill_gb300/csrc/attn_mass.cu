@@ -382,7 +382,7 @@ int mass_launch(MassParams &P, int64_t items, const CUtensorMap &mq, const CUten
   P.off_cum = P.off_q + P.qst * P.q_stage;
   P.off_misc = P.off_cum + cum;
   const int smem = (int)(P.off_misc + sizeof(MassMisc));
-  cudaFuncSetAttribute(attn_mass_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  allow_smem<attn_mass_kernel<T, D>>((int)kMost);
   const int grid = (int)(items < sm_count() ? items : sm_count());
   attn_mass_kernel<T, D><<<grid, kMassThreads, smem, st>>>(P, mq, mk);
   return launch_status();

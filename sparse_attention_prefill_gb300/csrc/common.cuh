@@ -41,6 +41,19 @@ static inline int sm_count() {
   return c;
 }
 
+// Raises kernel K's dynamic shared memory limit on the current device, once
+// (concurrent first calls set the same value).
+template <auto *K>
+static inline void allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return;
+  if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess)
+    done.fetch_or(bit, std::memory_order_relaxed);
+}
+
 // Bound on the pipeline waits of the tensor-core kernels (ns of %globaltimer),
 // read when a launch is issued; set by csa2_set_wait_limit_ns.
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;

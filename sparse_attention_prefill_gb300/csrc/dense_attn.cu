@@ -558,8 +558,7 @@ int launch(const AttnParams &P, int slots, const CUtensorMap &mq, const CUtensor
   using C = Cfg<D, NT>;
   const int64_t grid = (int64_t)slots * P.n_kv * (P.splits > 0 ? P.splits : 1);
   if (grid > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
-  cudaFuncSetAttribute(dense_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)C::kSmem);
+  allow_smem<dense_attn_kernel<T, D, NT>>((int)C::kSmem);
   dense_attn_kernel<T, D, NT><<<(int)grid, C::kThreads, C::kSmem, st>>>(P, mq, mk, mv);
   return launch_status();
 }

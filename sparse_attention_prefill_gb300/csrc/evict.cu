@@ -281,7 +281,7 @@ extern "C" CSA2_API int csa2_evict_select(int32_t num_req, int32_t n_heads,
   SelParams P{num_req, n_heads, kv_start, kv_len, mass, kv_rows, keep,
               sink,    recent,  idx,      new_len, d_err};
   constexpr int kSmem = kHeld * 4;
-  cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  allow_smem<evict_select_kernel>(kSmem);
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
