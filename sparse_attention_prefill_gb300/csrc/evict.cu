@@ -13,15 +13,29 @@ namespace cg = cooperative_groups;
 // Selection.  One cluster of CTAs per (request, head); each CTA holds a
 // contiguous slice of the rows between the sink and the recent ones as
 // order-preserving 32-bit keys in shared memory (what does not fit is read
-// again from L2).  Three histogram passes of 11, 11 and 10 bits, added up over
-// the cluster through distributed shared memory, give the key T of the last
-// row kept; rows above T stay, and of those equal to T the first in row order.
-// The masses are read from memory once; the passes and the ordered write run
-// on shared memory.
+// again from L2).  Histograms of 11, 11 and 10 bits, added up over the cluster
+// through distributed shared memory, give the key T of the last row kept;
+// rows above T stay, and of those equal to T the first in row order.
+//
+// The masses are read from memory once, and the slice is walked three times
+// more, four keys a lane: the first histogram is taken while loading; the keys
+// in its chosen bin are listed (they are few, and the other two histograms are
+// taken of the list; a list that overflows is replaced by the slice); the rows
+// that stay are counted by warp, each warp having a contiguous part; and they
+// are written in row order, a warp at a time without further barriers.  With
+// the digits taken of whole slices and a block-wide scan every 2048 rows the
+// kernel was bound by its instructions (170 to 32 rows, 50 us for 24 x 8 rows
+// of 26,000 on average, now 38 us; what is left is each step's fixed cost to a
+// warp).
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 512;
-constexpr int kHeld = 20480;          // keys of a slice in shared memory (80 KB)
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kHeld = 10240;          // keys of a slice in shared memory (40 KB)
+constexpr int kLoads = 8;             // masses in flight a thread
+constexpr int kMinSlice = 4096;
+constexpr int kSelPlaces = 3 * 152;     // CTAs the GPU holds at a time
 constexpr int kBins = 2048;
+constexpr int kList = 1024;           // listed keys
 
 struct SelParams {
   int num_req, n_heads;
@@ -36,13 +50,16 @@ struct SelParams {
 
 struct SelShared {
   uint32_t hist[kBins];
-  uint32_t scan[kSelThreads / 32];
-  uint32_t digit, above;          // the pass's answer
+  uint32_t list[kList];
+  uint32_t listed;                // keys offered to the list
+  uint32_t scan[kSelWarps];
+  uint32_t digit, above;          // a histogram's answer
+  uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
   uint32_t gt, eq;                // this CTA's rows above T, and equal to it
 };
 
-// exclusive prefix sum over the block in thread order; `total` gets the sum
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *tmp, uint32_t &total) {
+// exclusive prefix sum over the block in thread order
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *tmp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t inc = v;
 #pragma unroll
@@ -50,24 +67,199 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *tmp, uint32
     const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
-  __syncthreads();               // tmp may still be read from the last call
   if (lane == 31) tmp[warp] = inc;
   __syncthreads();
-  uint32_t base = 0, all = 0;
+  const uint32_t before = lane < warp ? tmp[lane] : 0u;     // warps in front
+  return __reduce_add_sync(0xffffffffu, before) + inc - v;
+}
+
+// One CTA's slice: `len` candidate rows from src on, `lo` rows behind the
+// request's first; kAll: the slices of the cluster fit into shared memory.
+template <bool kAll>
+__device__ void select_slice(const SelParams &P, SelShared &sh, uint32_t *held,
+                             const float *__restrict__ src, int32_t *__restrict__ idx, int lo,
+                             uint32_t len, int room, int nc, int rank) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // clusters of one CTA need the block's barrier only
+  auto sync = [&]() {
+    if (nc == 1) __syncthreads(); else cluster.sync();
+  };
+  for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+  if (threadIdx.x == 0) sh.listed = 0;
+  __syncthreads();
+  for (uint32_t i0 = threadIdx.x; i0 < len; i0 += kLoads * kSelThreads) {
+    float m[kLoads];
+    if (i0 - threadIdx.x + kLoads * kSelThreads <= len) {     // a whole step
 #pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) {
-    const uint32_t t = tmp[w];
-    if (w < warp) base += t;
-    all += t;
+      for (int u = 0; u < kLoads; ++u) m[u] = __ldg(src + i0 + u * kSelThreads);
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const uint32_t k = float_key(m[u]);
+        if (kAll || i0 + u * kSelThreads < kHeld) held[i0 + u * kSelThreads] = k;
+        atomicAdd(&sh.hist[k >> 21], 1u);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+        m[u] = i0 + u * kSelThreads < len ? __ldg(src + i0 + u * kSelThreads) : 0.f;
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const uint32_t i = i0 + u * kSelThreads;
+        if (i >= len) break;
+        const uint32_t k = float_key(m[u]);
+        if (kAll || i < kHeld) held[i] = k;
+        atomicAdd(&sh.hist[k >> 21], 1u);
+      }
+    }
   }
-  total = all;
-  return base + inc - v;
+  // four keys from i on (a multiple of 4), and how many of them there are
+  auto keys_at = [&](uint32_t i, uint32_t (&k)[4]) {
+    if (kAll || i < kHeld) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(held + i);
+      k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = i + e < len ? float_key(__ldg(src + i + e)) : 0u;
+    }
+    return (int)min(4u, len - i);
+  };
+  // the digit of the histograms' sum whose bin holds the row that is number
+  // `room` from above; keys above the digits fixed so far number `above`
+  uint32_t fixed = 0, above = 0;
+  auto choose = [&](int shift) {
+    sync();
+    // thread t holds the four bins 2048 - 4t - 4 .., highest first
+    const int b0 = kBins - 4 - 4 * threadIdx.x;
+    uint4 sum = make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < nc; ++c) {
+      const uint32_t *hist = nc == 1 ? sh.hist : cluster.map_shared_rank(sh.hist, c);
+      const uint4 v = *reinterpret_cast<const uint4 *>(hist + b0);
+      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+    uint32_t at = above + block_scan(sum.x + sum.y + sum.z + sum.w, sh.scan);
+    const uint32_t v[4] = {sum.w, sum.z, sum.y, sum.x};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (at < (uint32_t)room && at + v[e] >= (uint32_t)room) {
+        sh.digit = b0 + 3 - e;
+        sh.above = at;
+      }
+      at += v[e];
+    }
+    sync();                       // and no histogram is cleared while it is read
+    fixed |= sh.digit << shift;
+    above = sh.above;
+  };
+  choose(21);
+  for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+  for (uint32_t i = 4 * threadIdx.x; i < len; i += 4 * kSelThreads) {
+    uint32_t k[4];
+    const int c = keys_at(i, k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e < c && ((k[e] ^ fixed) >> 21) == 0) {
+        const uint32_t at = atomicAdd(&sh.listed, 1u);
+        if (at < kList) sh.list[at] = k[e];
+      }
+    }
+  }
+  __syncthreads();
+  const bool whole = sh.listed > kList;
+#pragma unroll 1
+  for (int pass = 1; pass < 3; ++pass) {
+    const int shift = pass == 1 ? 10 : 0;
+    const uint32_t mask = pass == 1 ? 2047u : 1023u;
+    const int top = pass == 1 ? 21 : 10;
+    if (pass == 2) {
+      for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+      __syncthreads();
+    }
+    auto count = [&](uint32_t k) {
+      if (((k ^ fixed) >> top) == 0) atomicAdd(&sh.hist[(k >> shift) & mask], 1u);
+    };
+    if (whole) {
+      for (uint32_t i = 4 * threadIdx.x; i < len; i += 4 * kSelThreads) {
+        uint32_t k[4];
+        const int c = keys_at(i, k);
+        for (int e = 0; e < c; ++e) count(k[e]);
+      }
+    } else {
+      for (uint32_t i = threadIdx.x; i < sh.listed; i += kSelThreads) count(sh.list[i]);
+    }
+    choose(shift);
+  }
+  const uint32_t T = fixed, ties = room - above;
+  // each warp has a contiguous part of the slice: rows above T and equal to it
+  const uint32_t part = ((len + kSelWarps - 1) / kSelWarps + 3) & ~3u;
+  const uint32_t p0 = min(len, warp * part), p1 = min(len, p0 + part);
+  uint32_t gt = 0, eq = 0;
+  for (uint32_t i = p0 + 4 * lane; i < p1; i += 128) {
+    uint32_t k[4];
+    const int c = keys_at(i, k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      gt += e < c && k[e] > T;
+      eq += e < c && k[e] == T;
+    }
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) sh.warp_gt[warp] = gt, sh.warp_eq[warp] = eq;
+  __syncthreads();
+  // rows in front of this warp's: those of the warps and the CTAs in front
+  uint32_t g0 = 0, q0 = 0;
+  for (int w = 0; w < kSelWarps; ++w) {
+    if (w == warp) gt = g0, eq = q0;
+    g0 += sh.warp_gt[w];
+    q0 += sh.warp_eq[w];
+  }
+  if (nc > 1) {
+    if (threadIdx.x == 0) sh.gt = g0, sh.eq = q0;
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) {
+      gt += *cluster.map_shared_rank(&sh.gt, c);
+      eq += *cluster.map_shared_rank(&sh.eq, c);
+    }
+  }
+  for (uint32_t i0 = p0; i0 < p1; i0 += 128) {
+    const uint32_t i = i0 + 4 * lane;
+    uint32_t k[4] = {0, 0, 0, 0}, v = 0;
+    int c = 0;
+    if (i < p1) c = keys_at(i, k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v += e < c && k[e] > T;
+      v += (uint32_t)(e < c && k[e] == T) << 16;
+    }
+    uint32_t inc = v;             // at most 128 in either half
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);
+    uint32_t g = gt + ((inc - v) & 0xffffu), q = eq + ((inc - v) >> 16);
+    if (v) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool up = e < c && k[e] > T, tie = e < c && k[e] == T;
+        if (up || (tie && q < ties))
+          idx[P.sink + g + min(q, ties)] = (int32_t)(P.sink + lo + i + e);
+        g += up;
+        q += tie;
+      }
+    }
+    gt += all & 0xffffu;
+    eq += all >> 16;
+  }
+  if (nc > 1) cluster.sync();     // no CTA leaves while its counts are read
 }
 
 __global__ void __launch_bounds__(kSelThreads)
 evict_select_kernel(SelParams P) {
-  extern __shared__ uint32_t held[];
-  __shared__ SelShared sh;
+  extern __shared__ __align__(16) uint32_t held[];
+  __shared__ __align__(16) SelShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int64_t pair = blockIdx.x / nc;
@@ -91,95 +283,14 @@ evict_select_kernel(SelParams P) {
   const int room = P.keep - P.sink - P.recent;
   if (room == 0) return;
   const int cand = (int)(n - P.sink - P.recent);       // > room
-  const int per = (cand + nc - 1) / nc;
-  const int lo = min(cand, rank * per), len = min(cand, lo + per) - lo;
+  const int per = (int)(((int64_t)cand + nc - 1) / nc);
+  const int lo = (int)min((int64_t)cand, (int64_t)rank * per);
+  const uint32_t len = (uint32_t)min((int64_t)cand, (int64_t)lo + per) - lo;
   const float *src = P.mass + (int64_t)h * P.kv_rows + start + P.sink + lo;
-  auto key_at = [&](int i) { return i < kHeld ? held[i] : float_key(__ldg(src + i)); };
-  for (int i = threadIdx.x; i < len && i < kHeld; i += kSelThreads)
-    held[i] = float_key(__ldg(src + i));
-  // T, digit by digit: keys above the digits fixed so far are counted in `above`
-  uint32_t fixed = 0, above = 0;
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const uint32_t mask = pass == 2 ? 1023u : 2047u;
-    const uint32_t high = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
-    for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.hist[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < len; i += kSelThreads) {
-      const uint32_t k = key_at(i);
-      if ((k & high) == fixed) atomicAdd(&sh.hist[(k >> shift) & mask], 1u);
-    }
-    cluster.sync();
-    // thread t holds bins 4 t' .. 4 t' + 3 of the cluster's sum, highest first
-    const int b0 = kBins - 4 - 4 * threadIdx.x;
-    uint4 sum = make_uint4(0, 0, 0, 0);
-    for (int c = 0; c < nc; ++c) {
-      const uint4 v = *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(sh.hist, c) + b0);
-      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-    }
-    uint32_t total;
-    uint32_t at = above + block_scan(sum.x + sum.y + sum.z + sum.w, sh.scan, total);
-    const uint32_t v[4] = {sum.w, sum.z, sum.y, sum.x};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (at < (uint32_t)room && at + v[e] >= (uint32_t)room) {
-        sh.digit = b0 + 3 - e;
-        sh.above = at;
-      }
-      at += v[e];
-    }
-    cluster.sync();               // and no histogram is cleared while it is read
-    fixed |= sh.digit << shift;
-    above = sh.above;
-  }
-  const uint32_t T = fixed, ties = room - above;
-  // rows above T and equal to it in the slices in front of this one
-  uint32_t gt = 0, eq = 0;
-  for (int i = threadIdx.x; i < len; i += kSelThreads) {
-    const uint32_t k = key_at(i);
-    gt += k > T;
-    eq += k == T;
-  }
-  {
-    uint32_t tg, te;
-    block_scan(gt, sh.scan, tg);
-    block_scan(eq, sh.scan, te);
-    if (threadIdx.x == 0) sh.gt = tg, sh.eq = te;
-  }
-  cluster.sync();
-  uint32_t gt0 = 0, eq0 = 0;
-  for (int c = 0; c < rank; ++c) {
-    gt0 += *cluster.map_shared_rank(&sh.gt, c);
-    eq0 += *cluster.map_shared_rank(&sh.eq, c);
-  }
-  // in row order, 4 rows to a thread
-  for (int i0 = 0; i0 < len; i0 += 4 * kSelThreads) {
-    uint32_t k[4], g4 = 0, e4 = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + 4 * threadIdx.x + e;
-      k[e] = i < len ? key_at(i) : 0u;
-      g4 += i < len && k[e] > T;
-      e4 += i < len && k[e] == T;
-    }
-    uint32_t tot;
-    const uint32_t before = block_scan(g4 | (e4 << 16), sh.scan, tot);   // at most 2048 each
-    uint32_t g = gt0 + (before & 0xffffu), q = eq0 + (before >> 16);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + 4 * threadIdx.x + e;
-      if (i >= len) break;
-      const bool is_eq = k[e] == T;
-      if (k[e] > T || (is_eq && q < ties))
-        idx[P.sink + g + min(q, ties)] = P.sink + lo + i;
-      g += k[e] > T;
-      q += is_eq;
-    }
-    gt0 += tot & 0xffffu;
-    eq0 += tot >> 16;
-  }
-  cluster.sync();                 // no CTA leaves while its counts are read
+  if (per <= kHeld)               // the same for the whole cluster
+    select_slice<true>(P, sh, held, src, idx, lo, len, room, nc, rank);
+  else
+    select_slice<false>(P, sh, held, src, idx, lo, len, room, nc, rank);
 }
 
 // ---------------------------------------------------------------------------
@@ -198,59 +309,70 @@ constexpr int kUnroll = 8;
 struct MoveParams {
   csa2_evict_buf buf[kMaxBufs];
   int vec[kMaxBufs];              // bytes of a lane's piece: 16 or 4
+  int shift[kMaxBufs];            // log2 of the pieces of an element, or -1
   int n_heads, keep;
   const int32_t *idx;
   const int64_t *new_len, *src_start, *dst_start;
   int32_t *d_err;
 };
 
-template <typename V>
-__device__ void move_rows(const MoveParams &P, const csa2_evict_buf &b, int64_t pair, int64_t s0,
-                          int64_t d0, int n, int64_t h, int part, int parts, int &err) {
+template <typename V, bool kInPlace>
+__device__ void move_rows(const MoveParams &P, const csa2_evict_buf &b, int shift, int64_t pair,
+                          int64_t s0, int64_t d0, int n, int64_t h, int part, int parts,
+                          int &err) {
   const int32_t *idx = P.idx + pair * P.keep;
-  const int pieces = (int)(b.elem_bytes / sizeof(V));
+  const int64_t pieces = b.elem_bytes / (int64_t)sizeof(V);
   const uint8_t *src = static_cast<const uint8_t *>(b.src) + h * b.src_head_stride;
   uint8_t *dst = static_cast<uint8_t *>(b.dst) + h * b.dst_head_stride;
-  const int64_t total = (int64_t)n * pieces, batch = (int64_t)kMoveThreads * kUnroll;
+  const int64_t total = n * pieces, batch = (int64_t)kMoveThreads * kUnroll;
   for (int64_t w0 = part * batch; w0 < total; w0 += parts * batch) {
     V v[kUnroll];
-    int64_t to[kUnroll];
+    int j[kUnroll];
+    int64_t to[kUnroll], p[kUnroll];
+    // the rows, then their bytes: each step's loads are all in flight together
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t w = w0 + u * kMoveThreads + threadIdx.x;
-      to[u] = -1;
-      if (w >= total) continue;
-      const int64_t i = w / pieces, p = w - i * pieces;
-      const int64_t j = idx[i];
-      if (j < 0) continue;
-      if (s0 + j >= b.src_rows || d0 + i >= b.dst_rows) {
-        err |= CSA2_DERR_RANGE_ROW;
-        continue;
-      }
-      v[u] = *reinterpret_cast<const V *>(src + (s0 + j) * b.src_row_stride + p * sizeof(V));
-      to[u] = (d0 + i) * b.dst_row_stride + p * sizeof(V);
+      const int64_t i = shift >= 0 ? w >> shift : w / pieces;
+      p[u] = (w - i * pieces) * (int64_t)sizeof(V);
+      to[u] = d0 + i;
+      j[u] = w < total ? __ldg(idx + i) : -1;
     }
-    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (j[u] >= 0 && (s0 + j[u] >= b.src_rows || to[u] >= b.dst_rows)) {
+        err |= CSA2_DERR_RANGE_ROW;
+        j[u] = -1;
+      }
+      to[u] = to[u] * b.dst_row_stride + p[u];
+      if (j[u] >= 0)
+        v[u] = *reinterpret_cast<const V *>(src + (s0 + j[u]) * b.src_row_stride + p[u]);
+    }
+    if (kInPlace) __syncthreads();
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (to[u] >= 0) *reinterpret_cast<V *>(dst + to[u]) = v[u];
+      if (j[u] >= 0) *reinterpret_cast<V *>(dst + to[u]) = v[u];
   }
 }
 
+template <bool kInPlace>
 __global__ void __launch_bounds__(kMoveThreads)
-evict_rows_kernel(MoveParams P) {
+evict_rows_kernel(const __grid_constant__ MoveParams P) {
   const int64_t pair = blockIdx.x;
   const int r = (int)(pair / P.n_heads);
   const csa2_evict_buf &b = P.buf[blockIdx.y];
   const int64_t len = P.new_len[r], s0 = P.src_start[r], d0 = P.dst_start[r];
   const int n = (int)(len < 0 ? 0 : len < P.keep ? len : P.keep);
+  const int shift = P.shift[blockIdx.y];
   int err = 0;
   if (s0 < 0 || d0 < 0) {
     err = n > 0 ? CSA2_DERR_RANGE_ROW : 0;
   } else if (P.vec[blockIdx.y] == 16) {
-    move_rows<uint4>(P, b, pair, s0, d0, n, pair % P.n_heads, blockIdx.z, gridDim.z, err);
+    move_rows<uint4, kInPlace>(P, b, shift, pair, s0, d0, n, pair % P.n_heads, blockIdx.z,
+                               gridDim.z, err);
   } else {
-    move_rows<uint32_t>(P, b, pair, s0, d0, n, pair % P.n_heads, blockIdx.z, gridDim.z, err);
+    move_rows<uint32_t, kInPlace>(P, b, shift, pair, s0, d0, n, pair % P.n_heads, blockIdx.z,
+                                  gridDim.z, err);
   }
   if (err) raise_err(P.d_err, err);
 }
@@ -275,9 +397,14 @@ extern "C" CSA2_API int csa2_evict_select(int32_t num_req, int32_t n_heads,
   if ((uintptr_t)mass & 3u) return CSA2_ERR_UNSUPPORTED;
   const int64_t pairs = (int64_t)num_req * n_heads;
   if (pairs > 0x7fffffffll / 8) return CSA2_ERR_UNSUPPORTED;
-  // as many CTAs to a row as keep the GPU's places filled
-  int nc = 1;
-  while (nc < 8 && pairs * nc * 2 <= 2 * 152) nc *= 2;
+  // CTAs to a (request, head): as many as the GPU holds at a time, but no fewer
+  // than kMinSlice rows to each on average (8 x 8 rows of 5200: 10.9 us at
+  // 4096 a slice, 11.9 at 2048, 16.8 at 1024; 24 x 8 rows of 26,000: 37.6 us
+  // with two CTAs, 43 with three, 56 with one)
+  const int64_t by_rows = kv_rows / num_req / kMinSlice;
+  int64_t nc = kSelPlaces / pairs;
+  nc = nc < by_rows ? nc : by_rows;
+  nc = nc < 1 ? 1 : nc > 8 ? 8 : nc;
   SelParams P{num_req, n_heads, kv_start, kv_len, mass, kv_rows, keep,
               sink,    recent,  idx,      new_len, d_err};
   constexpr int kSmem = kHeld * 4;
@@ -330,6 +457,9 @@ extern "C" CSA2_API int csa2_evict_rows(int32_t num_req, int32_t n_heads, const 
     in_place |= b.src == b.dst;
     const int64_t pieces = b.elem_bytes / P.vec[i];
     if (pieces > most) most = pieces;
+    P.shift[i] = -1;
+    for (int s = 0; s < 24; ++s)
+      if (pieces == (1ll << s)) P.shift[i] = s;
   }
   P.n_heads = n_heads;
   P.keep = keep;
@@ -344,11 +474,14 @@ extern "C" CSA2_API int csa2_evict_rows(int32_t num_req, int32_t n_heads, const 
   if (!in_place) {
     const int64_t batches =
         (most * keep + kMoveThreads * kUnroll - 1) / (kMoveThreads * kUnroll);
-    parts = (152 * 8 * 4 + pairs * n_bufs - 1) / (pairs * n_bufs);
+    parts = (152 * 8 * 8 + pairs * n_bufs - 1) / (pairs * n_bufs);
     if (parts > batches) parts = batches;
     if (parts < 1) parts = 1;
   }
-  evict_rows_kernel<<<dim3((unsigned)pairs, (unsigned)n_bufs, (unsigned)parts), kMoveThreads, 0,
-                      as_stream(stream)>>>(P);
+  const dim3 grid((unsigned)pairs, (unsigned)n_bufs, (unsigned)parts);
+  if (in_place)
+    evict_rows_kernel<true><<<grid, kMoveThreads, 0, as_stream(stream)>>>(P);
+  else
+    evict_rows_kernel<false><<<grid, kMoveThreads, 0, as_stream(stream)>>>(P);
   return launch_status();
 }
