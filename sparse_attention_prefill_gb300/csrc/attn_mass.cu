@@ -2,26 +2,36 @@
 // head (csa2_attn_mass):
 //   mass[g, j] (+)= sum_{i sees j, h in group g} exp(c <q[i,h], k[j,g]> - lse[i,h])
 //
-// Keys are stationary: a work item is 128 keys of one request and key head.
-// Its K tile is the A operand, the packed query tiles (dense.cuh) that see it
-// pass as B operands, so S^T[key, query row] has a key to a TMEM lane and the
-// sum over queries stays in one thread's register: no atomics, a fixed order.
-// The exponent needs no maximum (lse is given): exp2(c' s - lse'), one fused
-// multiply-add and one exponential to a score, with -lse' read from shared
-// memory (one value per column, the same for all lanes).
+// Keys are stationary: a work item is up to `span` tiles of 128 keys of one
+// request and key head.  Each K tile is an A operand, the packed query tiles
+// (dense.cuh) that see it pass as B operands, so S^T[key, query row] has a key
+// to a TMEM lane and the sum over queries stays in one thread's register: no
+// atomics, a fixed order.  The exponent needs no maximum (lse is given):
+// exp2(c' s - lse'), one fused multiply-add and one exponential to a score,
+// with -lse' read from shared memory (one value per column, the same for all
+// lanes).
 //
-// Per item the kernel reads the K tile once and every query tile once (from
-// L2, where a request's queries stay); a decode step is bound by the K rows,
-// a window of queries by the products and exponentials.
+// Per item the kernel reads its K tiles once and every query tile once (from
+// L2, where a request's queries stay).  A decode step is bound by the K rows,
+// a window of queries by the exponentials (512 cycles of the special-function
+// units to a 128 x 128 tile, as long as its product takes).  Products and
+// weights rotate over four S^T buffers and four warpgroups: product number x
+// of an item (query tile by query tile, the item's key tiles within) goes to
+// buffer and warpgroup x % 4.  With four key tiles to an item a warpgroup has
+// a key tile to itself; with two or one (few items) 2 or 4 warpgroups share
+// one and add up at its end.  Different warpgroups are at different places of
+// their tiles, which keeps the exponential units busy: with all four on
+// quarters of one tile they idled during its barrier and TMEM load (1400
+// cycles a tile).
 //
-// Roles (12 warps, one CTA per SM, persistent over items):
-//   warps 0-7  weights: warp w reads TMEM sub-partition w % 4 (keys 32(w % 4)
-//              .. + 31), the 16-column chunks of parity w / 4
-//   warp 8     TMEM; issues the products
-//   warp 9     K and Q tiles by TMA
-//   warp 10    looks items up a few ahead
-//   warp 11    -lse of the query tiles
-// S^T has four TMEM buffers, so products run up to four query tiles ahead.
+// Roles (23 warps, one CTA per SM, persistent over items):
+//   0-15       weights: warp w reads TMEM sub-partition w % 4 (keys 32(w % 4)
+//              .. + 31 of a tile) of buffer w / 4
+//   16         TMEM; issues the products
+//   17         K and Q tiles by TMA
+//   18         looks items up, 32 at a time, and publishes them a few ahead
+//   19-22      -lse of the query tiles, a warp to a buffer, so that four tiles'
+//              loads are under way
 // Every wait is bounded, as in the attention.
 #include "dense.cuh"
 
@@ -31,14 +41,16 @@ namespace {
 
 constexpr int kMaxReq = 8192;
 constexpr int kBufs = 4;            // S^T buffers (128 TMEM columns each)
-constexpr int kItems = 4;           // items looked up ahead
+constexpr int kItems = 8;           // items published ahead
 constexpr int kMaxK = 6, kMaxQ = 4; // ring stages at most
-constexpr int kEpiWarps = 8;
-constexpr int kMassThreads = 12 * 32;
+constexpr int kEpiWarps = 4 * kBufs;    // a warpgroup to a buffer
+constexpr int kLseWarps = kBufs;    // a warp to a buffer
+constexpr int kMassThreads = (kEpiWarps + 3 + kLseWarps) * 32;
 
 struct MassParams {
   Seqs seqs;
-  int n_heads, n_kv, group, tpt, ncol;   // ncol: tpt * group, rounded up to 16
+  int n_heads, n_kv, group, tpt, ncol;   // ncol: tpt * group, rounded up to 32
+  int span;                              // key tiles of an item: 1, 2 or 4
   int kst, qst;                          // ring stages
   uint32_t q_stage, off_q, off_cum, off_misc;
   float scale_log2;
@@ -51,10 +63,10 @@ struct MassParams {
 
 struct MassItem {
   int q0, n;          // the request's query rows
-  int h, keys;        // key head; keys of the tile (-1: no more items)
-  int qt0, nq;        // first query tile that sees the tile, and how many
+  int h, keys;        // key head; keys of the item (-1: no more items)
+  int qt0, nq;        // first query tile that sees it, and how many
   int64_t row;        // first pool row
-  int64_t shift;      // query i sees the tile's key x if x <= shift + i
+  int64_t shift;      // query i sees the item's key x if x <= shift + i
 };
 
 struct MassMisc {
@@ -65,7 +77,7 @@ struct MassMisc {
   uint32_t tmem;
   MassItem item[kItems];
   alignas(16) float nl[kBufs][kTile];    // -lse in log2 units, by query row
-  float red[2][kTile];
+  float red[2][kBufs][kTile];            // partial sums by item parity and warpgroup
 };
 
 __device__ void schedule_role(const MassParams &P, uint8_t *smem, MassMisc *ms) {
@@ -78,7 +90,7 @@ __device__ void schedule_role(const MassParams &P, uint8_t *smem, MassMisc *ms) 
     if (i0 + lane < P.seqs.count) {
       int64_t start, m;
       seq_keys(P.seqs, i0 + lane, start, m, err);
-      nt = (uint32_t)((m + kTile - 1) / kTile);
+      nt = (uint32_t)((m + P.span * kTile - 1) / (P.span * kTile));
     }
     uint32_t inc = nt;
 #pragma unroll
@@ -91,10 +103,11 @@ __device__ void schedule_role(const MassParams &P, uint8_t *smem, MassMisc *ms) 
   }
   __syncwarp();
   const int64_t total = (int64_t)base * P.n_kv;
+  // a lane to an item: 32 are looked up together, so that their loads overlap
   uint32_t u = 0;
-  for (int64_t id = blockIdx.x;; id += gridDim.x, ++u) {
-    const uint32_t s = u % kItems;
-    if (!wait_all(&ms->item_empty[s], ((u / kItems) & 1) ^ 1, &ms->bd)) break;
+  bool more = true;
+  for (int64_t id0 = blockIdx.x; more; id0 += 32 * (int64_t)gridDim.x) {
+    const int64_t id = id0 + lane * (int64_t)gridDim.x;
     MassItem it{};
     it.keys = -1;
     if (id < total) {
@@ -109,21 +122,28 @@ __device__ void schedule_role(const MassParams &P, uint8_t *smem, MassMisc *ms) 
       int64_t start, m;
       seq_rows(P.seqs, lo, it.q0, it.n, err);
       seq_keys(P.seqs, lo, start, m, err);
-      const int64_t left = m - (int64_t)kt * kTile;
-      it.keys = left < 0 ? 0 : left < kTile ? (int)left : kTile;
-      it.row = start + (int64_t)kt * kTile;
-      it.shift = m - it.n - (int64_t)kt * kTile;
+      const int64_t k0 = (int64_t)kt * P.span * kTile, left = m - k0;
+      it.keys = left < 0 ? 0 : left < P.span * kTile ? (int)left : P.span * kTile;
+      it.row = start + k0;
+      it.shift = m - it.n - k0;
       const int64_t first = it.shift >= 0 ? 0 : -it.shift;      // first query that sees key 0
       const int tiles = (it.n + P.tpt - 1) / P.tpt;
       it.qt0 = first < it.n ? (int)(first / P.tpt) : tiles;
       it.nq = it.keys > 0 ? tiles - it.qt0 : 0;
     }
-    if (lane == 0) {
-      ms->item[s] = it;
-      mbar_arrive(&ms->item_full[s]);
+    for (int l = 0; l < 32 && more; ++l, ++u) {
+      const uint32_t s = u % kItems;
+      if (!wait_all(&ms->item_empty[s], ((u / kItems) & 1) ^ 1, &ms->bd)) {
+        more = false;
+        break;
+      }
+      if (lane == l) {
+        ms->item[s] = it;
+        mbar_arrive(&ms->item_full[s]);
+      }
+      __syncwarp();
+      more = __shfl_sync(0xffffffffu, it.keys, l) >= 0;
     }
-    __syncwarp();
-    if (it.keys < 0) break;
   }
   err = __reduce_or_sync(0xffffffffu, err);
   if (lane == 0) raise_err(P.d_err, err);
@@ -138,8 +158,13 @@ __device__ __forceinline__ bool for_items(MassMisc *ms, F f) {
     bool ok = wait_bar(&ms->item_full[s], (u / kItems) & 1, &ms->bd);
     if (kWarp) ok = __all_sync(0xffffffffu, ok);
     if (!ok) return false;
-    const MassItem it = ms->item[s];
-    if (kWarp) __syncwarp();
+    MassItem it = ms->item[s];
+    if (kWarp) {
+      // known to be the same in every lane, or the loop counts as divergent
+      it.keys = uniform(it.keys);
+      it.nq = uniform(it.nq);
+      __syncwarp();
+    }
     if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&ms->item_empty[s]);
     if (it.keys < 0) return true;
     if (!f(it)) return false;
@@ -154,12 +179,14 @@ __device__ void load_role(const MassParams &P, uint8_t *smem, MassMisc *ms,
   uint32_t gk = 0, gq = 0;
   for_items<false>(ms, [&](const MassItem &it) {
     if (it.nq == 0) return true;
-    const uint32_t sk = gk % P.kst;
-    if (!wait_bar(&ms->k_empty[sk], ((gk / P.kst) & 1) ^ 1, &ms->bd)) return false;
-    mbar_arrive_expect_tx(&ms->k_full[sk], kKStage);
-    for (int c = 0; c < D / 64; ++c)
-      tma_load_3d(smem + sk * kKStage + c * kBlk, mk, c * 64, it.h, (int)it.row, &ms->k_full[sk]);
-    ++gk;
+    for (int k = 0; k < it.keys; k += kTile, ++gk) {
+      const uint32_t sk = gk % P.kst;
+      if (!wait_bar(&ms->k_empty[sk], ((gk / P.kst) & 1) ^ 1, &ms->bd)) return false;
+      mbar_arrive_expect_tx(&ms->k_full[sk], kKStage);
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_3d(smem + sk * kKStage + c * kBlk, mk, c * 64, it.h, (int)it.row + k,
+                    &ms->k_full[sk]);
+    }
     for (int t = 0; t < it.nq; ++t, ++gq) {
       const uint32_t sq = gq % P.qst;
       if (!wait_bar(&ms->q_empty[sq], ((gq / P.qst) & 1) ^ 1, &ms->bd)) return false;
@@ -184,120 +211,174 @@ __device__ void product_role(const MassParams &P, uint8_t *smem, MassMisc *ms) {
   const uint32_t tmem = uniform(ms->tmem), qblk = P.ncol * 128;
   const uint64_t kd = make_desc_sw128(smem_u32(smem), 16, 1024);
   const uint64_t qd = make_desc_sw128(smem_u32(smem + P.off_q), 16, 1024);
-  uint32_t sk = 0, pk = 0, sq = 0, pq = 0, g = 0;     // ring stages and phases
-  for_items<true>(ms, [&](const MassItem &it) {
-    const int nq = uniform(it.nq);
-    if (nq == 0) return true;
-    if (!wait_all(&ms->k_full[sk], pk, &ms->bd)) return false;
-    const uint64_t a = desc_add(kd, sk * kKStage);
-    for (int t = 0; t < nq; ++t, ++g) {
-      const uint32_t sb = g % kBufs;
-      if (!wait_all(&ms->s_empty[sb], ((g / kBufs) & 1) ^ 1, &ms->bd)) return false;
-      if (!wait_all(&ms->q_full[sq], pq, &ms->bd)) return false;
-      fence_after_sync();
+  uint32_t sk = 0, pk = 0, sq = 0, pq = 0;     // ring stages and phases
+  uint32_t uses = 0;                           // parity of each S^T buffer's uses
+  bool ok = true;
+  for (uint32_t u = 0; ok; ++u) {
+    const uint32_t si = u % kItems;
+    if (!(ok = wait_all(&ms->item_full[si], (u / kItems) & 1, &ms->bd))) break;
+    const int keys = uniform(ms->item[si].keys), nq = uniform(ms->item[si].nq);
+    if (elect_one()) mbar_arrive(&ms->item_empty[si]);
+    __syncwarp();
+    if (keys < 0) break;
+    const int nk = (keys + kTile - 1) / kTile;
+    uint32_t ks = sk, kp = pk;                 // the item's K tiles
+    for (int t = 0; t < nq && ok; ++t) {
+      ks = sk, kp = pk;
+      ok = wait_all(&ms->q_full[sq], pq, &ms->bd);
       const uint64_t b = desc_add(qd, sq * P.q_stage);
-      if (elect_one()) {
+      for (int i = 0; i < nk && ok; ++i) {
+        const uint32_t sb = (t * P.span + i) % kBufs;
+        if (t == 0) ok = wait_all(&ms->k_full[ks], kp, &ms->bd);
+        ok = ok && wait_all(&ms->s_empty[sb], ((uses >> sb) & 1) ^ 1, &ms->bd);
+        uses ^= 1u << sb;
+        if (ok) {
+          fence_after_sync();
+          const uint64_t a = desc_add(kd, ks * kKStage);
+          if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_f16(tmem + sb * kTile, desc_add(a, (k >> 2) * kBlk + (k & 3) * 32),
-                  desc_add(b, (k >> 2) * qblk + (k & 3) * 32), idesc, k > 0);
-        mma_commit(&ms->s_full[sb]);
-        mma_commit(&ms->q_empty[sq]);
+            for (int k = 0; k < D / 16; ++k)
+              mma_f16(tmem + sb * kTile, desc_add(a, (k >> 2) * kBlk + (k & 3) * 32),
+                      desc_add(b, (k >> 2) * qblk + (k & 3) * 32), idesc, k > 0);
+            mma_commit(&ms->s_full[sb]);
+            if (t == nq - 1) mma_commit(&ms->k_empty[ks]);
+            if (i == nk - 1) mma_commit(&ms->q_empty[sq]);
+          }
+          __syncwarp();
+        }
+        if (++ks == (uint32_t)P.kst) ks = 0, kp ^= 1;
       }
-      __syncwarp();
       if (++sq == (uint32_t)P.qst) sq = 0, pq ^= 1;
     }
-    if (elect_one()) mma_commit(&ms->k_empty[sk]);
-    __syncwarp();
-    if (++sk == (uint32_t)P.kst) sk = 0, pk ^= 1;
-    return true;
-  });
+    sk = ks, pk = kp;
+  }
   if (elect_one()) mma_commit(&ms->done);
   __syncwarp();
   drain_bar(&ms->done, 0);
 }
 
-__device__ void lse_role(const MassParams &P, MassMisc *ms) {
+// The query tiles of an item that buffer (and warpgroup) `which` gets, t0, t0 +
+// step, .. below t1, and the key tile they meet there: product t * span + i
+// goes to buffer (t * span + i) % 4.
+struct Turns {
+  int tile, t0, t1, step;
+  __device__ __forceinline__ Turns(const MassParams &P, const MassItem &it, int which) {
+    tile = which & (P.span - 1);
+    step = kBufs / P.span;
+    t0 = which / P.span;
+    t1 = tile * kTile < it.keys ? it.nq : 0;
+  }
+};
+
+// -lse of the query tiles of one S^T buffer
+__device__ void lse_role(const MassParams &P, MassMisc *ms, uint32_t which) {
   const int lane = threadIdx.x & 31;
-  uint32_t g = 0;
+  int tok[4], off[4];              // this lane's rows: token of the tile, head of the group
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    tok[u] = (u * 32 + lane) / P.group;
+    off[u] = tok[u] * P.n_heads + (u * 32 + lane) % P.group;
+    if (tok[u] >= P.tpt) tok[u] = 0x7fffffff;
+  }
+  uint32_t uses = 0;
   for_items<true>(ms, [&](const MassItem &it) {
-    for (int t = 0; t < it.nq; ++t, ++g) {
-      const uint32_t sb = g % kBufs;
+    const Turns w(P, it, which);
+    for (int t = w.t0; t < w.t1; t += w.step, ++uses) {
       const int tok0 = (it.qt0 + t) * P.tpt;
+      const float *src = P.lse + (int64_t)(it.q0 + tok0) * P.n_heads + it.h * P.group;
       float v[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int x = u * 32 + lane, tok = tok0 + x / P.group;
-        v[u] = -INFINITY;
-        if (x < P.tpt * P.group && tok < it.n)
-          v[u] = __ldg(P.lse + (int64_t)(it.q0 + tok) * P.n_heads + it.h * P.group + x % P.group);
-      }
-      if (!wait_all(&ms->s_empty[sb], ((g / kBufs) & 1) ^ 1, &ms->bd)) return false;
+      for (int u = 0; u < 4; ++u)
+        v[u] = tok[u] < it.n - tok0 ? __ldg(src + off[u]) : -INFINITY;
+      if (!wait_all(&ms->s_empty[which], (uses & 1) ^ 1, &ms->bd)) return false;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const bool none = v[u] == -INFINITY;      // adds nothing
-        ms->nl[sb][u * 32 + lane] = none ? -INFINITY : -v[u] * 1.4426950408889634f;
+        ms->nl[which][u * 32 + lane] = none ? -INFINITY : -v[u] * 1.4426950408889634f;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->l_full[sb]);
+      if (lane == 0) mbar_arrive(&ms->l_full[which]);
     }
     return true;
   });
 }
 
+// 32 columns from c0 on of a row of S^T: the weights, added to acc
+template <bool kEdge>
+__device__ __forceinline__ void weigh(uint32_t tmem, const float *nl, uint64_t c2, int lo, int hi,
+                                      int c0, uint64_t (&acc)[2]) {
+  uint32_t s[32];
+  tmem_ld32x32b_x32(tmem + c0, s);
+  tmem_wait_ld();
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const ulonglong2 n4 = *reinterpret_cast<const ulonglong2 *>(nl + c0 + e);
+    const float2 a = unpack2(
+        fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, n4.x));
+    const float2 b = unpack2(
+        fma2(pack2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, n4.y));
+    float w[4] = {ex2(a.x), ex2(a.y), ex2(b.x), ex2(b.y)};
+    if (kEdge) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c0 + e + k < lo || c0 + e + k >= hi) w[k] = 0.f;
+    }
+    acc[0] = add2(acc[0], pack2(w[0], w[1]));
+    acc[1] = add2(acc[1], pack2(w[2], w[3]));
+  }
+}
+
 __device__ void weight_role(const MassParams &P, MassMisc *ms) {
-  const int warp = threadIdx.x >> 5, half = warp >> 2, x = (warp & 3) * 32 + (threadIdx.x & 31);
-  const uint32_t lane_addr = (uint32_t)(32 * (warp & 3)) << 16;
-  const float c = P.scale_log2;
-  uint32_t g = 0, u = 0;
+  const int warp = threadIdx.x >> 5, wg = warp >> 2, x = (warp & 3) * 32 + (threadIdx.x & 31);
+  const uint32_t tmem = ms->tmem + wg * kTile + ((uint32_t)(32 * (warp & 3)) << 16);
+  const uint64_t c2 = pack2(P.scale_log2, P.scale_log2);
+  const float *nl = ms->nl[wg];
+  uint32_t uses = 0, u = 0;
   for_items<true>(ms, [&](const MassItem &it) {
-    float *out = P.mass_out + (int64_t)it.h * P.seqs.kv_rows + it.row + x;
-    const bool mine = half == 0 && x < it.keys;
+    const Turns w(P, it, wg);
+    const int key = w.tile * kTile + x;            // of the item
+    // the first of the key tile's warpgroups stores its masses
+    const bool mine = wg < P.span && key < it.keys;
+    const int64_t at = (int64_t)it.h * P.seqs.kv_rows + it.row + key;
     float old = 0.f;
-    if (mine && P.mass_in) old = P.mass_in[(int64_t)it.h * P.seqs.kv_rows + it.row + x];
-    float acc0 = 0.f, acc1 = 0.f;
-    for (int t = 0; t < it.nq; ++t, ++g) {
-      const uint32_t sb = g % kBufs, ph = (g / kBufs) & 1;
-      bool ok = wait_bar(&ms->l_full[sb], ph, &ms->bd) && wait_bar(&ms->s_full[sb], ph, &ms->bd);
+    if (mine && P.mass_in) old = P.mass_in[at];
+    uint64_t acc[2] = {0, 0};
+    for (int t = w.t0; t < w.t1; t += w.step, ++uses) {
+      const int tok0 = (it.qt0 + t) * P.tpt;
+      const bool ok = wait_bar(&ms->l_full[wg], uses & 1, &ms->bd) &&
+                      wait_bar(&ms->s_full[wg], uses & 1, &ms->bd);
       if (!__all_sync(0xffffffffu, ok)) return false;
       fence_after_sync();
-      const int tok0 = (it.qt0 + t) * P.tpt;
-      // columns [lo, hi) see this key
-      const int hi = min(P.tpt, it.n - tok0) * P.group;
-      const int64_t first = x - it.shift - tok0;
-      const int lo = first <= 0 ? 0 : first > kTile ? kTile : (int)first * P.group;
-      const bool edge = hi < P.tpt * P.group || kTile - 1 - it.shift - tok0 > 0;
-      for (int c0 = 16 * half; c0 < P.ncol; c0 += 32) {
-        uint32_t s[32];
-        tmem_ld32x32b_x16(ms->tmem + sb * kTile + c0 + lane_addr, s);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const float4 nl = *reinterpret_cast<const float4 *>(&ms->nl[sb][c0 + e]);
-          float w[4] = {ex2(fmaf(__uint_as_float(s[e]), c, nl.x)),
-                        ex2(fmaf(__uint_as_float(s[e + 1]), c, nl.y)),
-                        ex2(fmaf(__uint_as_float(s[e + 2]), c, nl.z)),
-                        ex2(fmaf(__uint_as_float(s[e + 3]), c, nl.w))};
-          if (edge) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (c0 + e + k < lo || c0 + e + k >= hi) w[k] = 0.f;
-          }
-          acc0 += w[0] + w[1];
-          acc1 += w[2] + w[3];
-        }
+      const int64_t shift = it.shift - w.tile * kTile;
+      const bool edge = (it.n - tok0) < P.tpt || kTile - 1 - shift - tok0 > 0;
+      if (!edge) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < P.ncol; c0 += 32) weigh<false>(tmem, nl, c2, 0, 0, c0, acc);
+      } else {
+        // columns [lo, hi) see this key
+        const int hi = min(P.tpt, it.n - tok0) * P.group;
+        const int64_t first = x - shift - tok0;
+        const int lo = first <= 0 ? 0 : first > kTile ? kTile : (int)first * P.group;
+#pragma unroll 1
+        for (int c0 = 0; c0 < P.ncol; c0 += 32) weigh<true>(tmem, nl, c2, lo, hi, c0, acc);
       }
       fence_before_sync();
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->s_empty[sb]);
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->s_empty[wg]);
     }
-    const float acc = acc0 + acc1;
-    if (half == 1) ms->red[u & 1][x] = acc;
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->grp);
-    if (!wait_all(&ms->grp, u & 1, &ms->bd)) return false;
-    if (mine) *out = old + (acc + ms->red[u & 1][x]);
-    ++u;
+    const float2 sum2 = unpack2(add2(acc[0], acc[1]));
+    float sum = sum2.x + sum2.y;
+    if (P.span < kBufs) {          // other warpgroups had query tiles of these keys
+      ms->red[u & 1][wg][x] = sum;
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->grp);
+      if (!wait_all(&ms->grp, u & 1, &ms->bd)) return false;
+      const float(*r)[kTile] = ms->red[u & 1];
+      if (mine)
+        sum = P.span == 2 ? r[wg][x] + r[wg + 2][x] : (r[0][x] + r[1][x]) + (r[2][x] + r[3][x]);
+      ++u;
+    }
+    if (mine) P.mass_out[at] = old + sum;
     return true;
   });
 }
@@ -314,12 +395,12 @@ attn_mass_kernel(MassParams P, const __grid_constant__ CUtensorMap mq,
     for (int i = 0; i < kMaxQ; ++i) mbar_init(&ms->q_full[i], 1), mbar_init(&ms->q_empty[i], 1);
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&ms->s_full[i], 1);
-      mbar_init(&ms->s_empty[i], kEpiWarps);
+      mbar_init(&ms->s_empty[i], 4);
       mbar_init(&ms->l_full[i], 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&ms->item_full[i], 1);
-      mbar_init(&ms->item_empty[i], kEpiWarps + 3);   // weights, products, loads, lse
+      mbar_init(&ms->item_empty[i], kEpiWarps + 2 + kLseWarps);
     }
     mbar_init(&ms->grp, kEpiWarps);
     mbar_init(&ms->done, 1);
@@ -327,7 +408,7 @@ attn_mass_kernel(MassParams P, const __grid_constant__ CUtensorMap mq,
     ms->bd.wait_ns = P.wait_ns;
     mbar_fence_init();
   }
-  // query rows that pad a tile to 16 columns are never fetched: zeros, so that
+  // query rows that pad a tile to 32 columns are never fetched: zeros, so that
   // their scores are finite (their -lse is -inf)
   {
     const int pad0 = P.tpt * P.group, pad = (P.ncol - pad0) * 8;   // 16-byte pieces a block
@@ -338,7 +419,7 @@ attn_mass_kernel(MassParams P, const __grid_constant__ CUtensorMap mq,
     }
     fence_proxy_async_smem();
   }
-  if (warp == 8) {
+  if (warp == kEpiWarps) {
     tmem_alloc(&ms->tmem, 512);
     tmem_relinquish();
   }
@@ -347,20 +428,20 @@ attn_mass_kernel(MassParams P, const __grid_constant__ CUtensorMap mq,
   fence_after_sync();
   if (warp < kEpiWarps) {
     weight_role(P, ms);
-  } else if (warp == 8) {
+  } else if (warp == kEpiWarps) {
     product_role<T, D>(P, smem, ms);
-  } else if (warp == 9) {
+  } else if (warp == kEpiWarps + 1) {
     if ((threadIdx.x & 31) == 0) load_role<D>(P, smem, ms, &mq, &mk);
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == kEpiWarps + 2) {
     schedule_role(P, smem, ms);
   } else {
-    lse_role(P, ms);
+    lse_role(P, ms, warp - kEpiWarps - 3);
   }
   fence_before_sync();
   __syncthreads();
   if (threadIdx.x == 0 && ms->bd.abort) raise_err(P.d_err, CSA2_DERR_TIMEOUT);
-  if (warp == 8) {
+  if (warp == kEpiWarps) {
     fence_after_sync();
     tmem_dealloc(ms->tmem, 512);
   }
@@ -372,12 +453,13 @@ int mass_launch(MassParams &P, int64_t items, const CUtensorMap &mq, const CUten
   constexpr uint32_t kKStage = (D / 64) * kBlk;
   constexpr uint32_t kMost = 232448;
   P.q_stage = (uint32_t)P.ncol * 128u * (D / 64);
-  P.qst = P.ncol > 64 ? 3 : 4;
+  P.qst = P.q_stage > 16384 ? 2 : 4;      // query tiles serve several key tiles each
   const uint32_t cum = ((uint32_t)P.seqs.count * 4u + 15u) & ~15u;
   const uint32_t rest = P.qst * P.q_stage + cum + (uint32_t)sizeof(MassMisc);
-  int kst = (int)((kMost - rest) / kKStage);
+  const int kst = (int)((kMost - rest) / kKStage);
   P.kst = kst > kMaxK ? kMaxK : kst;
   if (P.kst < 2) return CSA2_ERR_UNSUPPORTED;
+  while (P.span > P.kst) P.span /= 2;
   P.off_q = P.kst * kKStage;
   P.off_cum = P.off_q + P.qst * P.q_stage;
   P.off_misc = P.off_cum + cum;
@@ -422,7 +504,7 @@ extern "C" CSA2_API int csa2_attn_mass(const csa2_packed *b, int32_t n_heads, in
   int tpt = 1;      // a tile no longer than the requests' queries on average
   while (tpt < most && (int64_t)tpt * b->num_req < b->num_q) tpt *= 2;
   P.tpt = tpt < most ? tpt : most;
-  P.ncol = (P.tpt * P.group + 15) & ~15;
+  P.ncol = (P.tpt * P.group + 31) & ~31;
   P.scale_log2 = sm_scale * 1.4426950408889634f;
   P.lse = lse;
   P.mass_in = mass_in;
@@ -436,12 +518,14 @@ extern "C" CSA2_API int csa2_attn_mass(const csa2_packed *b, int32_t n_heads, in
                      none ? s.n_kv : s.n_heads, s.dim, none ? ldk : ldq, none ? 1 : s.group,
                      P.tpt))
     return CSA2_ERR_UNSUPPORTED;
-  const int64_t tiles = (max_kv + kTile - 1) / kTile;
-  const int64_t items = (tiles > 0 ? tiles : 1) * b->num_req * s.n_kv;
+  // key tiles of an item: as many as leave every SM several items
+  const int64_t most_kv = max_kv < kv_rows ? max_kv : kv_rows, all_kv = most_kv * b->num_req;
+  const int64_t tiles = ((all_kv < kv_rows ? all_kv : kv_rows) / kTile + b->num_req) * s.n_kv;
+  P.span = tiles >= 4 * 6 * kSms ? 4 : tiles >= 2 * 4 * kSms ? 2 : 1;
   const cudaStream_t cs = csa2::as_stream(stream);
   if (s.bf16)
-    return s.dim == 128 ? mass_launch<__nv_bfloat16, 128>(P, items, mq, mk, cs)
-                        : mass_launch<__nv_bfloat16, 64>(P, items, mq, mk, cs);
-  return s.dim == 128 ? mass_launch<__half, 128>(P, items, mq, mk, cs)
-                      : mass_launch<__half, 64>(P, items, mq, mk, cs);
+    return s.dim == 128 ? mass_launch<__nv_bfloat16, 128>(P, tiles, mq, mk, cs)
+                        : mass_launch<__nv_bfloat16, 64>(P, tiles, mq, mk, cs);
+  return s.dim == 128 ? mass_launch<__half, 128>(P, tiles, mq, mk, cs)
+                      : mass_launch<__half, 64>(P, tiles, mq, mk, cs);
 }

@@ -69,6 +69,19 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Bound *
   return wait_slow(bar, parity, bd);
 }
 
+// the same without a call, for the elected lane between its products
+__device__ __forceinline__ void wait_inline(uint64_t *bar, uint32_t parity, Bound *bd) {
+  if (mbar_test(bar, parity)) return;
+  const uint64_t t0 = gtimer(), limit = bd->wait_ns;
+  while (!mbar_test(bar, parity)) {
+    if (*(volatile int *)&bd->abort) return;
+    if (gtimer() - t0 > limit) {
+      atomicExch(&bd->abort, 1);
+      return;
+    }
+  }
+}
+
 // the same by a whole warp, which goes on or gives up together
 __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, Bound *bd) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, bd));

@@ -227,68 +227,70 @@ __device__ void mma_role(uint8_t *smem, M *ms) {
   const uint64_t ring_k = make_desc_sw128(smem_u32(smem + C::kOffRing), 16, 1024);
   const uint64_t ring_v = make_desc_sw128(smem_u32(smem + C::kOffRing), kBlk, 1024);
   const uint64_t qd = make_desc_sw128(smem_u32(smem), 16, 1024);
+  // products of S[t] with the K tile of a ring stage, by the elected lane
   auto issue_s = [&](int t, uint32_t stage) {
     const uint64_t b = desc_add(ring_k, stage * C::kStage);
-    if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k >> 2) * kBlk + (k & 3) * 32;
-        mma_f16(tmem + t * 128, desc_add(qd, t * C::kQTile + off), desc_add(b, off), kIdS, k > 0);
-      }
-      mma_commit(&ms->s_full[t]);
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t off = (k >> 2) * kBlk + (k & 3) * 32;
+      mma_f16(tmem + t * 128, desc_add(qd, t * C::kQTile + off), desc_add(b, off), kIdS, k > 0);
     }
-    __syncwarp();
+    mma_commit(&ms->s_full[t]);
   };
-  auto commit = [&](uint64_t *bar) {
-    if (elect_one()) mma_commit(bar);
-    __syncwarp();
-  };
-  bool ok = wait_all(&ms->q_full, 0, &ms->bd) && wait_all(&ms->full[0], 0, &ms->bd);
-  if (ok) {
+  if (elect_one()) {
+    wait_inline(&ms->q_full, 0, &ms->bd);
+    wait_inline(&ms->full[0], 0, &ms->bd);
     fence_after_sync();
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       if (end[t] > 0) issue_s(t, 0);
-    commit(&ms->empty[0]);
+    mma_commit(&ms->empty[0]);
   }
+  __syncwarp();
   uint32_t sv = 1, pv = 0;         // ring stage and phase of V(j)
-  for (int j = 0; j < nk && ok; ++j) {
+  for (int j = 0; j < nk; ++j) {
+    // once a wait has run out nothing waits any more, and the products of the
+    // step at hand read whatever is there
+    if (uniform(*(volatile int *)&ms->bd.abort)) break;
     uint32_t sk = sv + 1, pk = pv;                 // K(j + 1)
     if (sk == C::kStages) sk = 0, pk ^= 1;
-    if (!(ok = wait_all(&ms->full[sv], pv, &ms->bd))) break;
-    bool next = false;                             // K(j + 1) has arrived
+    const bool more = j + 1 < nk;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      if (j >= end[t] || !ok) continue;
-      const uint64_t b = desc_add(ring_v, sv * C::kStage);
+      if (j < end[t]) {
+        const uint64_t b = desc_add(ring_v, sv * C::kStage);
+        // The waits lie between the products that they hold back: the tensor
+        // pipe has some four products queued meanwhile.
+        if (elect_one()) {
+          wait_inline(&ms->full[sv], pv, &ms->bd);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {       // P arrives in halves of 64 keys
-        if (ok && (ok = wait_all(&ms->p_full[t][half], j & 1, &ms->bd))) {
-          fence_after_sync();
-          if (elect_one()) {
+          for (int half = 0; half < 2; ++half) {   // P arrives in halves of 64 keys
+            wait_inline(&ms->p_full[t][half], j & 1, &ms->bd);
+            fence_after_sync();
 #pragma unroll
             for (int k = 4 * half; k < 4 * half + 4; ++k)
               mma_f16_ts(tmem + C::kColO + t * D, tmem + t * 128 + k * 8, desc_add(b, k * 2048),
                          kIdO, j > 0 || k > 0);
           }
-          __syncwarp();
+          if (j + 1 < end[t]) {
+            wait_inline(&ms->full[sk], pk, &ms->bd);
+            issue_s(t, sk);
+          } else {
+            mma_commit(&ms->o_full[t]);
+          }
+          if (t == NT - 1 || j >= end[NT - 1]) {
+            mma_commit(&ms->empty[sv]);
+            if (more) mma_commit(&ms->empty[sk]);
+          }
         }
-      }
-      if (!ok) continue;
-      if (j + 1 < end[t]) {
-        if (!next && !(ok = wait_all(&ms->full[sk], pk, &ms->bd))) continue;
-        next = true;
-        issue_s(t, sk);
-      } else {
-        commit(&ms->o_full[t]);
+        __syncwarp();
       }
     }
-    commit(&ms->empty[sv]);
-    if (j + 1 < nk) commit(&ms->empty[sk]);
     sv = sk + 1, pv = pk;
     if (sv == C::kStages) sv = 0, pv ^= 1;
   }
-  commit(&ms->done);               // TMEM is not freed under a running product
+  if (elect_one()) mma_commit(&ms->done);          // TMEM is not freed under a running product
+  __syncwarp();
   drain_bar(&ms->done, 0);
 }
 
