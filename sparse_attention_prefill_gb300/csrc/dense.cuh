@@ -50,7 +50,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, Bound *bd) {
+__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, Bound *bd) {
   // the hardware suspends a try_wait for some microseconds: a bound shorter
   // than that is polled for
   const uint64_t t0 = gtimer(), limit = bd->wait_ns;
@@ -100,6 +100,29 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
+}
+
+// Cluster launch control: asks for the index of a CTA of this grid that has not
+// started, which then does not start; the answer (16 bytes) completes on `bar`.
+__device__ __forceinline__ void ask_next(uint64_t *answer, uint64_t *bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The answer: false if no CTA is left (no further request may be made then).
+__device__ __forceinline__ bool next_cta(const uint64_t *answer, uint32_t &cta) {
+  uint32_t got;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+      "mov.b128 a, {%2, %3};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(got), "=r"(cta)
+      : "l"(((const volatile uint64_t *)answer)[0]), "l"(((const volatile uint64_t *)answer)[1]));
+  return got != 0;
 }
 
 // the value of lane 0, known to be the same in every lane

@@ -6,8 +6,8 @@
 //   l_j = c <q_x, k_j>,  out = sum_j e^{l_j} v_j / sum_j e^{l_j},
 //   lse = ln sum_j e^{l_j}.
 //
-// One CTA handles kNT query tiles of 128 packed rows (dense.cuh) of one key
-// head and walks over key tiles of 128 keys:
+// An item is kNT query tiles of 128 packed rows (dense.cuh) of one key head,
+// walked over in key tiles of 128 keys:
 //   S[t] = Q[t] K^T     (both operands in shared memory, S in TMEM)
 //   O[t] += P[t] V      (P in TMEM over S's columns, V in shared memory)
 // The softmax holds one row to a thread: it reads its row of S, keeps a
@@ -19,7 +19,9 @@
 // The MMA warp issues, for each key tile j and query tile t, O[t](j) and
 // then S[t](j+1): while one tile's softmax runs, the other tile's products
 // keep the tensor pipe busy (kNT = 2), or those of the second CTA of the SM
-// do (kNT = 1).
+// do (kNT = 1).  The grid has a CTA to an item, but a CTA that runs takes the
+// items of CTAs that have not started, so that an item's output overlaps the
+// loads and first products of the next.
 //
 // Rows of K and V outside a request's run never matter: scores past the last
 // key are replaced before use, and the rows of the last V tile past the end
@@ -34,6 +36,7 @@ namespace dense {
 namespace {
 
 constexpr int kMaxSplits = 16;
+constexpr uint32_t kMiscBytes = 640;   // barriers and items, behind the tiles
 
 struct AttnParams {
   Seqs seqs;
@@ -59,8 +62,14 @@ struct Cfg {
   static constexpr uint32_t kStage = (D / 64) * kBlk;
   static constexpr uint32_t kOffRing = NT * kQTile;
   static constexpr uint32_t kOffMisc = kOffRing + kStages * kStage;
-  static constexpr uint32_t kSmem = kOffMisc + 512;
-  static constexpr int kThreads = (4 * NT + 2) * 32;
+  static constexpr uint32_t kSmem = kOffMisc + kMiscBytes;
+  // one warpgroup of softmax to a query tile; MMA and producer warp in a third
+  // (second) one, which gives most of its registers to them: 168 to a thread
+  // at launch (NT = 2) or 128 (NT = 1), the sum stays
+  static constexpr int kThreads = (NT + 1) * 128;
+  static constexpr int kRegsSoftmax = NT == 2 ? 224 : 208;
+  static constexpr int kRegsRest = NT == 2 ? 56 : 48;
+  static_assert(NT * kRegsSoftmax + kRegsRest <= (NT + 1) * (NT == 2 ? 168 : 128), "registers");
   static constexpr uint32_t kTmemCols = NT == 2 ? 512 : 256;
   // columns: S tiles (128 each; P over the first 64), then O tiles (D each)
   static constexpr uint32_t kColO = NT * 128;
@@ -68,10 +77,12 @@ struct Cfg {
 };
 
 struct Item {
-  int run, q0, n, tok0;      // run, its first query row and rows, first token of this CTA
+  int run, q0, n, tok0;      // run (-1: no work, -2: no more items), its first query row and
+                             // rows, first token of the item
+  int h, split;
   int64_t start;             // first cache row
   int64_t m;                 // cache rows
-  int kt0, kt1;              // key tiles of this CTA
+  int kt0, kt1;              // key tiles
   int nkt[2];                // key tiles that query tile t needs (end, <= kt1)
   int ntile;                 // query tiles with tokens
   int uncovered;             // a request in no group (own part of a shared-prefix call)
@@ -80,15 +91,20 @@ struct Item {
 template <int kStages>
 struct Misc {
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full, aux, s_full[2], p_full[2][2], o_full[2], done;
+  uint64_t q_full, q_empty, aux, s_full[2], p_full[2][2], o_full[2], done, clc;
+  uint64_t item_full[2], item_empty[2];
   Bound bd;
   uint32_t tmem;
-  Item item;
+  alignas(16) uint64_t next[2];      // answer to the request for another CTA's work
+  Item item[2];
 };
-
-// Run and tile of this CTA, by one warp; run = -1 if the CTA has no work.
+// The item of CTA `cta` of the grid, by one warp; run = -1 if it has no work.
 template <int NT>
-__device__ void find_item(const AttnParams &P, int slot, int split, int tok_cta, Item &it) {
+__device__ void find_item(const AttnParams &P, uint32_t cta, Item &it) {
+  const int ns = P.splits > 0 ? P.splits : 1, tok_cta = NT * P.tpt;
+  const int split = it.split = (int)(cta % ns);
+  it.h = (int)(cta / ns % P.n_kv);
+  const int slot = (int)(cta / ns / P.n_kv);
   const int lane = threadIdx.x & 31;
   int base = 0, err = 0, run = -1, tile = 0, q0 = 0, n = 0;
   for (int i0 = 0; i0 < P.seqs.count; i0 += 32) {
@@ -151,62 +167,109 @@ __device__ void find_item(const AttnParams &P, int slot, int split, int tok_cta,
   if (lane == 0) raise_err(P.d_err, err);
 }
 
-// Producer warp: Q once, then K and V tiles through the ring.
+// Producer warp.  Takes this CTA's item, then those of CTAs of the grid that
+// have not started (cluster launch control: the hardware hands out their
+// indices), looks each up while the loads of the item in front are under way,
+// and publishes it; then Q, and K and V tiles through the ring.
 template <int D, int NT, typename M>
-__device__ void producer_role(const AttnParams &P, uint8_t *smem, M *ms, int h,
+__device__ void producer_role(const AttnParams &P, uint8_t *smem, M *ms, Item cur,
                               const CUtensorMap *mq, const CUtensorMap *mk,
                               const CUtensorMap *mv) {
   using C = Cfg<D, NT>;
   const int lane = threadIdx.x & 31;
-  const Item &it = ms->item;
-  if (it.kt0 >= it.kt1) return;
-  if (lane == 0) {
-    const uint32_t box = (uint32_t)P.tpt * P.group * 128u;
-    mbar_arrive_expect_tx(&ms->q_full, box * (D / 64) * it.ntile);
-    for (int t = 0; t < it.ntile; ++t)
-      for (int c = 0; c < D / 64; ++c)
-        tma_load_3d(smem + t * C::kQTile + c * kBlk, mq, c * 64, h * P.group,
-                    it.q0 + it.tok0 + t * P.tpt, &ms->q_full);
-  }
-  uint32_t g = 0;
-  bool ok = true, aux = false;
-  for (int kt = it.kt0; kt < it.kt1 && ok; ++kt) {
-    const int row = (int)(it.start + (int64_t)kt * kTile);
-    const int64_t left = it.m - (int64_t)kt * kTile;    // keys of this tile
-    for (int kv = 0; kv < 2; ++kv, ++g) {
-      const uint32_t s = g % C::kStages, ph = (g / C::kStages) & 1;
-      uint8_t *st = smem + C::kOffRing + s * C::kStage;
-      ok = wait_bar(&ms->empty[s], ph ^ 1, &ms->bd);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const bool tail = kv == 1 && left < kTile;
-      if (lane == 0) {
-        uint64_t *bar = tail ? &ms->aux : &ms->full[s];
-        mbar_arrive_expect_tx(bar, C::kStage);
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(st + c * kBlk, kv ? mv : mk, c * 64, h, row, bar);
-      }
-      if (tail) {
-        // rows past the end are zeroed once the copy has landed
-        aux = true;
-        __syncwarp();
-        ok = wait_bar(&ms->aux, 0, &ms->bd);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        for (int i = (int)left * 8 + lane; i < kTile * 8; i += 32)
+  uint32_t g = 0, nq = 0, naux = 0, nclc = 0, items = 0;     // uses so far
+  bool ok = true, asked = false, tail_open = false;
+  auto publish = [&](const Item &it) {
+    const uint32_t s = items & 1;
+    ok = wait_all(&ms->item_empty[s], ((items >> 1) & 1) ^ 1, &ms->bd);
+    if (ok && lane == 0) {
+      ms->item[s] = it;
+      mbar_arrive(&ms->item_full[s]);
+    }
+    __syncwarp();
+    ++items;
+  };
+  bool more = true;
+  while (ok && more) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&ms->clc, 16);
+      ask_next(ms->next, &ms->clc);
+    }
+    asked = true;
+    Item nxt;
+    bool looked = false;
+    auto look_ahead = [&]() {
+      looked = true;
+      ok = wait_all(&ms->clc, nclc & 1, &ms->bd);
+      if (!ok) return;
+      ++nclc;
+      asked = false;
+      uint32_t cta;
+      more = next_cta(ms->next, cta);
+      fence_proxy_async_smem();      // the next answer is written by the async proxy
+      __syncwarp();
+      if (more) find_item<NT>(P, cta, nxt);
+    };
+    if (cur.run >= 0) publish(cur);
+    if (ok && cur.run >= 0 && cur.kt0 < cur.kt1) {
+      ok = wait_all(&ms->q_empty, (nq & 1) ^ 1, &ms->bd);
+      if (ok && lane == 0) {
+        const uint32_t box = (uint32_t)P.tpt * P.group * 128u;
+        mbar_arrive_expect_tx(&ms->q_full, box * (D / 64) * cur.ntile);
+        for (int t = 0; t < cur.ntile; ++t)
           for (int c = 0; c < D / 64; ++c)
-            *reinterpret_cast<uint4 *>(st + c * kBlk + i * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->full[s]);
+            tma_load_3d(smem + t * C::kQTile + c * kBlk, mq, c * 64, cur.h * P.group,
+                        cur.q0 + cur.tok0 + t * P.tpt, &ms->q_full);
+      }
+      if (ok) ++nq;
+      int loads = 0;
+      for (int kt = cur.kt0; kt < cur.kt1 && ok; ++kt) {
+        const int row = (int)(cur.start + (int64_t)kt * kTile);
+        const int64_t left = cur.m - (int64_t)kt * kTile;    // keys of this tile
+        for (int kv = 0; kv < 2; ++kv, ++g) {
+          if (loads++ == C::kStages) look_ahead();           // the ring is full
+          if (!ok) break;
+          const uint32_t s = g % C::kStages, ph = (g / C::kStages) & 1;
+          uint8_t *st = smem + C::kOffRing + s * C::kStage;
+          if (!(ok = wait_all(&ms->empty[s], ph ^ 1, &ms->bd))) break;
+          const bool tail = kv == 1 && left < kTile;
+          if (lane == 0) {
+            uint64_t *bar = tail ? &ms->aux : &ms->full[s];
+            mbar_arrive_expect_tx(bar, C::kStage);
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(st + c * kBlk, kv ? mv : mk, c * 64, cur.h, row, bar);
+          }
+          if (tail) {
+            // rows past the end are zeroed once the copy has landed
+            __syncwarp();
+            tail_open = true;
+            if (!(ok = wait_all(&ms->aux, naux & 1, &ms->bd))) break;
+            tail_open = false;
+            ++naux;
+            for (int i = (int)left * 8 + lane; i < kTile * 8; i += 32)
+              for (int c = 0; c < D / 64; ++c)
+                *reinterpret_cast<uint4 *>(st + c * kBlk + i * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms->full[s]);
+          }
+        }
       }
     }
+    if (ok && !looked) look_ahead();
+    if (ok && more) cur = nxt;
+  }
+  if (ok) {
+    Item end{};
+    end.run = -2;
+    publish(end);
   }
   // every copy has to land before the CTA leaves (the products wait for all
   // of them, but not once a wait has run out)
   if (lane == 0) {
-    drain_bar(&ms->q_full, 0);
-    if (aux) drain_bar(&ms->aux, 0);
+    if (asked) drain_bar(&ms->clc, nclc & 1);
+    if (nq) drain_bar(&ms->q_full, (nq - 1) & 1);
+    if (tail_open) drain_bar(&ms->aux, naux & 1);
     for (uint32_t i = g > (uint32_t)C::kStages ? g - C::kStages : 0; i < g; ++i)
       drain_bar(&ms->full[i % C::kStages], (i / C::kStages) & 1);
   }
@@ -220,10 +283,6 @@ __device__ void mma_role(uint8_t *smem, M *ms) {
   constexpr uint32_t kIdS = idesc_of<T>(kTile, kTile, false);
   constexpr uint32_t kIdO = idesc_of<T>(kTile, D, true);
   const uint32_t tmem = uniform(ms->tmem);
-  const int kt0 = uniform(ms->item.kt0), nk = uniform(ms->item.kt1) - kt0;
-  int end[NT];                     // key tiles of query tile t, counted from kt0
-#pragma unroll
-  for (int t = 0; t < NT; ++t) end[t] = uniform(ms->item.nkt[t]) - kt0;
   const uint64_t ring_k = make_desc_sw128(smem_u32(smem + C::kOffRing), 16, 1024);
   const uint64_t ring_v = make_desc_sw128(smem_u32(smem + C::kOffRing), kBlk, 1024);
   const uint64_t qd = make_desc_sw128(smem_u32(smem), 16, 1024);
@@ -237,69 +296,95 @@ __device__ void mma_role(uint8_t *smem, M *ms) {
     }
     mma_commit(&ms->s_full[t]);
   };
-  if (elect_one()) {
-    wait_inline(&ms->q_full, 0, &ms->bd);
-    wait_inline(&ms->full[0], 0, &ms->bd);
-    fence_after_sync();
+  uint32_t s0 = 0, p0 = 0;          // ring stage and phase of the next tile to take
+  uint32_t pq = 0, pp = 0;          // phases of Q, and of P by query tile (a bit each)
+  for (uint32_t u = 0;; ++u) {
+    if (!wait_all(&ms->item_full[u & 1], (u >> 1) & 1, &ms->bd)) break;
+    const Item &it = ms->item[u & 1];
+    const int run = uniform(it.run), kt0 = uniform(it.kt0), nk = uniform(it.kt1) - kt0;
+    int end[NT];                    // key tiles of query tile t, counted from kt0
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-      if (end[t] > 0) issue_s(t, 0);
-    mma_commit(&ms->empty[0]);
-  }
-  __syncwarp();
-  uint32_t sv = 1, pv = 0;         // ring stage and phase of V(j)
-  for (int j = 0; j < nk; ++j) {
-    // once a wait has run out nothing waits any more, and the products of the
-    // step at hand read whatever is there
-    if (uniform(*(volatile int *)&ms->bd.abort)) break;
-    uint32_t sk = sv + 1, pk = pv;                 // K(j + 1)
-    if (sk == C::kStages) sk = 0, pk ^= 1;
-    const bool more = j + 1 < nk;
+    for (int t = 0; t < NT; ++t) end[t] = uniform(it.nkt[t]) - kt0;
+    if (elect_one()) mbar_arrive(&ms->item_empty[u & 1]);
+    __syncwarp();
+    if (run < 0) break;
+    if (nk <= 0) continue;
+    if (elect_one()) {
+      wait_inline(&ms->q_full, pq, &ms->bd);
+      wait_inline(&ms->full[s0], p0, &ms->bd);
+      fence_after_sync();
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (j < end[t]) {
-        const uint64_t b = desc_add(ring_v, sv * C::kStage);
-        // The waits lie between the products that they hold back: the tensor
-        // pipe has some four products queued meanwhile.
-        if (elect_one()) {
-          wait_inline(&ms->full[sv], pv, &ms->bd);
+      for (int t = 0; t < NT; ++t)
+        if (end[t] > 0) issue_s(t, s0);
+      mma_commit(&ms->empty[s0]);
+      if (nk == 1) mma_commit(&ms->q_empty);
+    }
+    __syncwarp();
+    pq ^= 1;
+    uint32_t sv = s0 + 1, pv = p0;  // V(j)
+    if (sv == C::kStages) sv = 0, pv ^= 1;
+    bool ok = true;
+    for (int j = 0; j < nk && ok; ++j) {
+      // once a wait has run out nothing waits any more, and the products of
+      // the step at hand read whatever is there
+      ok = uniform(*(volatile int *)&ms->bd.abort) == 0;
+      uint32_t sk = sv + 1, pk = pv;                 // K(j + 1)
+      if (sk == C::kStages) sk = 0, pk ^= 1;
+      const bool more = j + 1 < nk;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {   // P arrives in halves of 64 keys
-            wait_inline(&ms->p_full[t][half], j & 1, &ms->bd);
-            fence_after_sync();
+      for (int t = 0; t < NT; ++t) {
+        if (ok && j < end[t]) {
+          const uint64_t b = desc_add(ring_v, sv * C::kStage);
+          // The waits lie between the products that they hold back: the
+          // tensor pipe has some four products queued meanwhile.
+          if (elect_one()) {
+            wait_inline(&ms->full[sv], pv, &ms->bd);
 #pragma unroll
-            for (int k = 4 * half; k < 4 * half + 4; ++k)
-              mma_f16_ts(tmem + C::kColO + t * D, tmem + t * 128 + k * 8, desc_add(b, k * 2048),
-                         kIdO, j > 0 || k > 0);
+            for (int half = 0; half < 2; ++half) {   // P arrives in halves of 64 keys
+              wait_inline(&ms->p_full[t][half], (pp >> t) & 1, &ms->bd);
+              fence_after_sync();
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; ++k)
+                mma_f16_ts(tmem + C::kColO + t * D, tmem + t * 128 + k * 8, desc_add(b, k * 2048),
+                           kIdO, j > 0 || k > 0);
+            }
+            if (j + 1 < end[t]) {
+              wait_inline(&ms->full[sk], pk, &ms->bd);
+              issue_s(t, sk);
+            } else {
+              mma_commit(&ms->o_full[t]);
+            }
+            if (t == NT - 1 || j >= end[NT - 1]) {
+              mma_commit(&ms->empty[sv]);
+              if (more) mma_commit(&ms->empty[sk]);
+              if (j + 2 == nk) mma_commit(&ms->q_empty);   // the item's last S
+            }
           }
-          if (j + 1 < end[t]) {
-            wait_inline(&ms->full[sk], pk, &ms->bd);
-            issue_s(t, sk);
-          } else {
-            mma_commit(&ms->o_full[t]);
-          }
-          if (t == NT - 1 || j >= end[NT - 1]) {
-            mma_commit(&ms->empty[sv]);
-            if (more) mma_commit(&ms->empty[sk]);
-          }
+          __syncwarp();
+          pp ^= 1u << t;
         }
-        __syncwarp();
+      }
+      if (more) {
+        sv = sk + 1, pv = pk;
+        if (sv == C::kStages) sv = 0, pv ^= 1;
       }
     }
-    sv = sk + 1, pv = pk;
-    if (sv == C::kStages) sv = 0, pv ^= 1;
+    if (!ok) break;
+    s0 = sv + 1, p0 = pv;
+    if (s0 == C::kStages) s0 = 0, p0 ^= 1;
   }
   if (elect_one()) mma_commit(&ms->done);          // TMEM is not freed under a running product
   __syncwarp();
   drain_bar(&ms->done, 0);
 }
 
-// Softmax of query tile t and its output; one row to a thread.
+// Softmax of one item's query tile t and its output; one row to a thread.
+// False if a wait ran out.
 template <typename T, int D, int NT, typename M>
-__device__ void softmax_role(const AttnParams &P, M *ms, int h, int split) {
+__device__ bool softmax_item(const AttnParams &P, M *ms, const Item &it, int t, uint32_t &ps,
+                             uint32_t &po) {
   using C = Cfg<D, NT>;
-  const Item &it = ms->item;
-  const int t = threadIdx.x >> 7, x = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
+  const int x = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
   const int tok = x / P.group;
   const int i = it.tok0 + t * P.tpt + tok;                 // token of the run
   const bool valid = tok < P.tpt && i < it.n;
@@ -321,7 +406,8 @@ __device__ void softmax_role(const AttnParams &P, M *ms, int h, int split) {
   const int kt_end = it.nkt[t];
   int j = 0;
   for (int kt = it.kt0; kt < kt_end; ++kt, ++j) {
-    if (!(ok = wait_bar(&ms->s_full[t], j & 1, &ms->bd))) break;
+    if (!(ok = wait_bar(&ms->s_full[t], ps, &ms->bd))) break;
+    ps ^= 1;
     fence_after_sync();
     uint32_t s[4][32];
 #pragma unroll
@@ -388,20 +474,21 @@ __device__ void softmax_role(const AttnParams &P, M *ms, int h, int split) {
     sum = part2.x + part2.y;
   }
   const bool any = it.kt0 < kt_end;
-  if (ok && any) ok = wait_bar(&ms->o_full[t], 0, &ms->bd);
+  if (ok && any) ok = wait_bar(&ms->o_full[t], po, &ms->bd);
   ok = __all_sync(0xffffffffu, ok);
-  if (!ok || t >= it.ntile) return;
+  if (!ok) return false;
+  if (any) po ^= 1;
   fence_after_sync();
   const bool seen = any && !(sum == 0.f);       // a NaN sum stays a NaN
   const float inv = seen ? 1.f / sum : 0.f;
   const float lse =
       seen ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-  const int64_t row = (int64_t)(it.q0 + i) * P.n_heads + h * P.group + x % P.group;
+  const int64_t row = (int64_t)(it.q0 + i) * P.n_heads + it.h * P.group + x % P.group;
   const int64_t rows = (int64_t)P.seqs.num_q * P.n_heads;
   if (valid) {
     if (P.splits > 0) {
-      P.part_lse[split * rows + row] = lse;
-      if (it.uncovered && split == 0)
+      P.part_lse[it.split * rows + row] = lse;
+      if (it.uncovered && it.split == 0)
         for (int s = 0; s < P.cover_splits; ++s) P.cover_lse[s * rows + row] = -INFINITY;
     } else if (P.lse) {
       P.lse[row] = lse;
@@ -420,7 +507,7 @@ __device__ void softmax_role(const AttnParams &P, M *ms, int h, int split) {
     if (!valid) continue;
     if (P.splits > 0) {
       if (!seen) continue;
-      float4 *dst = reinterpret_cast<float4 *>(P.part_o + (split * rows + row) * D + 32 * c);
+      float4 *dst = reinterpret_cast<float4 *>(P.part_o + (it.split * rows + row) * D + 32 * c);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
@@ -439,6 +526,25 @@ __device__ void softmax_role(const AttnParams &P, M *ms, int h, int split) {
       }
     }
   }
+  fence_before_sync();      // O is read: the next item's first product may overwrite it
+  return true;
+}
+
+// Items one after another, as the producer publishes them.
+template <typename T, int D, int NT, typename M>
+__device__ void softmax_role(const AttnParams &P, M *ms) {
+  const int t = threadIdx.x >> 7;
+  uint32_t ps = 0, po = 0;          // phases of S and O
+  for (uint32_t u = 0;; ++u) {
+    if (!wait_all(&ms->item_full[u & 1], (u >> 1) & 1, &ms->bd)) return;
+    // the item stays in shared memory until its output is written: registers
+    // are short
+    const Item &it = ms->item[u & 1];
+    if (it.run < 0) return;
+    if (t < it.ntile && !softmax_item<T, D, NT>(P, ms, it, t, ps, po)) return;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->item_empty[u & 1]);
+  }
 }
 
 template <typename T, int D, int NT>
@@ -447,18 +553,13 @@ dense_attn_kernel(AttnParams P, const __grid_constant__ CUtensorMap mq,
                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using C = Cfg<D, NT>;
   using M = Misc<C::kStages>;
-  static_assert(sizeof(M) <= 512, "misc region");
+  static_assert(sizeof(M) <= kMiscBytes, "misc region");
   extern __shared__ __align__(1024) uint8_t smem[];
   M *ms = reinterpret_cast<M *>(smem + C::kOffMisc);
   const int warp = threadIdx.x >> 5;
-  const int ns = P.splits > 0 ? P.splits : 1;
-  const int split = blockIdx.x % ns;
-  const int h = (blockIdx.x / ns) % P.n_kv;
-  const int slot = blockIdx.x / ns / P.n_kv;
+  Item first;
   if (warp == 4 * NT + 1) {
-    Item it;
-    find_item<NT>(P, slot, split, NT * P.tpt, it);
-    if ((threadIdx.x & 31) == 0) ms->item = it;
+    find_item<NT>(P, blockIdx.x, first);
   } else if (warp == 4 * NT) {
     tmem_alloc(&ms->tmem, C::kTmemCols);
     tmem_relinquish();
@@ -468,13 +569,17 @@ dense_attn_kernel(AttnParams P, const __grid_constant__ CUtensorMap mq,
       mbar_init(&ms->empty[i], 1);
     }
     mbar_init(&ms->q_full, 1);
+    mbar_init(&ms->q_empty, 1);
     mbar_init(&ms->aux, 1);
     mbar_init(&ms->done, 1);
+    mbar_init(&ms->clc, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&ms->s_full[t], 1);
       mbar_init(&ms->p_full[t][0], 4);
       mbar_init(&ms->p_full[t][1], 4);
       mbar_init(&ms->o_full[t], 1);
+      mbar_init(&ms->item_full[t], 1);
+      mbar_init(&ms->item_empty[t], 4 * NT + 1);     // softmax warps, MMA warp
     }
     ms->bd.abort = 0;
     ms->bd.wait_ns = P.wait_ns;
@@ -483,15 +588,15 @@ dense_attn_kernel(AttnParams P, const __grid_constant__ CUtensorMap mq,
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  if (ms->item.run >= 0) {
-    if (warp == 4 * NT + 1) {
-      producer_role<D, NT>(P, smem, ms, h, &mq, &mk, &mv);
-    } else if (warp == 4 * NT) {
-      if (ms->item.kt0 < ms->item.kt1) mma_role<T, D, NT>(smem, ms);
-      __syncwarp();
-    } else {
-      softmax_role<T, D, NT>(P, ms, h, split);
-    }
+  if (warp >= 4 * NT) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
+    if (warp == 4 * NT + 1)
+      producer_role<D, NT>(P, smem, ms, first, &mq, &mk, &mv);
+    else if (warp == 4 * NT)
+      mma_role<T, D, NT>(smem, ms);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+    softmax_role<T, D, NT>(P, ms);
   }
   fence_before_sync();
   __syncthreads();
