@@ -249,6 +249,17 @@ __device__ __forceinline__ void seq_keys(const Seqs &S, int i, int64_t &start, i
   }
 }
 
+// Whether request r lies in one of the groups, by one warp.
+__device__ __forceinline__ bool in_groups(const int32_t *cu_group, int groups, int r,
+                                          int num_req) {
+  bool mine = false;
+  for (int g = threadIdx.x & 31; g < groups; g += 32) {
+    const int lo = cu_group[g], hi = cu_group[g + 1];
+    mine |= lo >= 0 && lo <= r && r < hi && hi <= num_req;
+  }
+  return __any_sync(0xffffffffu, mine);
+}
+
 // ---------------------------------------------------------------------------
 // tensor maps (host)
 // ---------------------------------------------------------------------------

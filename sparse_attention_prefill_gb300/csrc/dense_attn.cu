@@ -6,22 +6,31 @@
 //   l_j = c <q_x, k_j>,  out = sum_j e^{l_j} v_j / sum_j e^{l_j},
 //   lse = ln sum_j e^{l_j}.
 //
-// An item is kNT query tiles of 128 packed rows (dense.cuh) of one key head,
-// walked over in key tiles of 128 keys:
+// An item is walked over in key tiles of 128 keys by two streams, each with a
+// query tile of 128 packed rows (dense.cuh) of one key head:
 //   S[t] = Q[t] K^T     (both operands in shared memory, S in TMEM)
 //   O[t] += P[t] V      (P in TMEM over S's columns, V in shared memory)
+// Wide items (prompts, shared prefixes) have two neighbouring query tiles that
+// share the key tiles; narrow ones (decode steps, short extends: requests whose
+// rows fill one tile) have one query tile, and its streams take the even and
+// the odd key tiles and join their sums in the end.
+//
 // The softmax holds one row to a thread: it reads its row of S, keeps a
 // reference maximum that moves only when a logit passes it by a margin (then
 // the thread rescales its row of O; the products of that row are complete by
 // then, since S of this step was issued after them), and writes P rounded to
-// the inputs' type.  Row sums are taken of the unrounded P in fp32.
+// the inputs' type.  Row sums are taken of the unrounded P in fp32.  Warps
+// without a query row leave their P as it is: rows do not mix.
 //
-// The MMA warp issues, for each key tile j and query tile t, O[t](j) and
-// then S[t](j+1): while one tile's softmax runs, the other tile's products
-// keep the tensor pipe busy (kNT = 2), or those of the second CTA of the SM
-// do (kNT = 1).  The grid has a CTA to an item, but a CTA that runs takes the
-// items of CTAs that have not started, so that an item's output overlaps the
-// loads and first products of the next.
+// The MMA warp issues, step by step and stream by stream, O[t](j) and then
+// S[t](j+1): while one stream's softmax runs, the other's products keep the
+// tensor pipe busy.  The grid has a CTA to an item, but a CTA that runs takes
+// the items of CTAs that have not started, so that an item's output overlaps
+// the loads and first products of the next.
+//
+// A shared-prefix call runs the prefixes (wide items where a group's rows fill
+// more than one query tile) and the requests' own rows (decode_attn.cu where a
+// request has 16 rows at most) into partial results, which a last kernel joins.
 //
 // Rows of K and V outside a request's run never matter: scores past the last
 // key are replaced before use, and the rows of the last V tile past the end
@@ -36,18 +45,19 @@ namespace dense {
 namespace {
 
 constexpr int kMaxSplits = 16;
-constexpr uint32_t kMiscBytes = 640;   // barriers and items, behind the tiles
+constexpr uint32_t kMiscBytes = 1792;  // barriers and items, behind the tiles
 
 struct AttnParams {
   Seqs seqs;
-  int n_heads, n_kv, group, tpt, causal, splits;
-  float scale_log2;
-  void *out;         // [num_q, n_heads, D]  (splits == 0)
-  float *lse;        // [num_q, n_heads] or null
-  float *part_o;     // [splits, num_q, n_heads, D]  (splits > 0)
+  int n_heads, n_kv, group, tpt, causal;
+  int splits;        // of the key range; 0: the output itself is written
+  float *part_o;     // [splits, num_q, n_heads, D]
   float *part_lse;   // [splits, num_q, n_heads]
-  // own part of a shared-prefix call: rows of requests in no group get -inf
-  // in the prefix part's statistics
+  float scale_log2;
+  void *out;         // [num_q, n_heads, D]
+  float *lse;        // [num_q, n_heads] or null
+  // shared-prefix call: rows of requests in no group get -inf in the prefix
+  // part's statistics
   const int32_t *cover;
   int n_cover, cover_splits;
   float *cover_lse;
@@ -55,26 +65,28 @@ struct AttnParams {
   uint64_t wait_ns;
 };
 
-template <int D, int NT>
+template <int D>
 struct Cfg {
-  static constexpr int kStages = D == 128 ? (NT == 2 ? 5 : 2) : (NT == 2 ? 8 : 5);
+  static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr uint32_t kQTile = (D / 64) * kBlk;
   static constexpr uint32_t kStage = (D / 64) * kBlk;
-  static constexpr uint32_t kOffRing = NT * kQTile;
+  static constexpr uint32_t kOffRing = 2 * kQTile;
   static constexpr uint32_t kOffMisc = kOffRing + kStages * kStage;
   static constexpr uint32_t kSmem = kOffMisc + kMiscBytes;
-  // one warpgroup of softmax to a query tile; MMA and producer warp in a third
-  // (second) one, which gives most of its registers to them: 168 to a thread
-  // at launch (NT = 2) or 128 (NT = 1), the sum stays
-  static constexpr int kThreads = (NT + 1) * 128;
-  static constexpr int kRegsSoftmax = NT == 2 ? 224 : 208;
-  static constexpr int kRegsRest = NT == 2 ? 56 : 48;
-  static_assert(NT * kRegsSoftmax + kRegsRest <= (NT + 1) * (NT == 2 ? 168 : 128), "registers");
-  static constexpr uint32_t kTmemCols = NT == 2 ? 512 : 256;
+  // two warpgroups of softmax; MMA, producer and item warp in a third one, which
+  // gives most of its registers to them: 168 to a thread at launch, and the
+  // sum stays
+  static constexpr int kThreads = 3 * 128;
+  static constexpr int kRegsSoftmax = 224;
+  static constexpr int kRegsRest = 56;
+  static_assert(2 * kRegsSoftmax + kRegsRest <= 3 * 168, "registers");
+  static constexpr uint32_t kTmemCols = 512;
   // columns: S tiles (128 each; P over the first 64), then O tiles (D each)
-  static constexpr uint32_t kColO = NT * 128;
+  static constexpr uint32_t kColO = 2 * 128;
   static_assert(kSmem <= 232448, "shared memory");
 };
+constexpr int kMmaWarp = 8, kProducerWarp = 9, kItemWarp = 10;
+constexpr int kItems = 3;            // items published at a time
 
 struct Item {
   int run, q0, n, tok0;      // run (-1: no work, -2: no more items), its first query row and
@@ -82,8 +94,8 @@ struct Item {
   int h, split;
   int64_t start;             // first cache row
   int64_t m;                 // cache rows
-  int kt0, kt1;              // key tiles
-  int nkt[2];                // key tiles that query tile t needs (end, <= kt1)
+  int kt0, nk;               // key tiles
+  int steps[2];              // of each stream
   int ntile;                 // query tiles with tokens
   int uncovered;             // a request in no group (own part of a shared-prefix call)
 };
@@ -92,182 +104,221 @@ template <int kStages>
 struct Misc {
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full, q_empty, aux, s_full[2], p_full[2][2], o_full[2], done, clc;
-  uint64_t item_full[2], item_empty[2];
+  uint64_t item_full[kItems], item_empty[kItems];
   Bound bd;
   uint32_t tmem;
+  uint64_t stat_full, stat_empty;
   alignas(16) uint64_t next[2];      // answer to the request for another CTA's work
-  Item item[2];
+  Item item[kItems];
+  float2 stat[kTile];                // narrow items: reference and sum of stream 1's rows
 };
+// Items of a part's runs, as a warp holds them: lane l has those of an equal
+// share of the runs, and the sum up to and with its share.
+struct Shares {
+  int own, upto;
+};
+
+__device__ __forceinline__ int lane_scan(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+__device__ Shares count_items(const AttnParams &P, int tok, int &err) {
+  const int lane = threadIdx.x & 31, per = (P.seqs.count + 31) / 32;
+  Shares s{0, 0};
+#pragma unroll 4
+  for (int i = lane * per; i < min(P.seqs.count, (lane + 1) * per); ++i) {
+    int a, c;
+    seq_rows(P.seqs, i, a, c, err);
+    s.own += (c + tok - 1) / tok;
+  }
+  s.upto = lane_scan(s.own);
+  return s;
+}
+
 // The item of CTA `cta` of the grid, by one warp; run = -1 if it has no work.
-template <int NT>
-__device__ void find_item(const AttnParams &P, uint32_t cta, Item &it) {
-  const int ns = P.splits > 0 ? P.splits : 1, tok_cta = NT * P.tpt;
-  const int split = it.split = (int)(cta % ns);
+template <bool kNarrow>
+__device__ void find_item(const AttnParams &P, uint32_t cta, const Shares &s, Item &it,
+                          int &err) {
+  const int lane = threadIdx.x & 31;
+  const int ns = P.splits > 0 ? P.splits : 1, tok = kNarrow ? P.tpt : 2 * P.tpt;
+  const int per = (P.seqs.count + 31) / 32;
+  it.split = (int)(cta % ns);
   it.h = (int)(cta / ns % P.n_kv);
   const int slot = (int)(cta / ns / P.n_kv);
-  const int lane = threadIdx.x & 31;
-  int base = 0, err = 0, run = -1, tile = 0, q0 = 0, n = 0;
-  for (int i0 = 0; i0 < P.seqs.count; i0 += 32) {
+  it.run = -1;
+  const uint32_t share = __ballot_sync(0xffffffffu, slot < s.upto);
+  if (!share) return;
+  const int l = __ffs(share) - 1;
+  int base = __shfl_sync(0xffffffffu, s.upto - s.own, l);
+  const int end = min(P.seqs.count, (l + 1) * per);
+  for (int i0 = l * per; i0 < end && it.run < 0; i0 += 32) {
+    // everything of a lane's run at once
     int a = 0, c = 0;
-    if (i0 + lane < P.seqs.count) seq_rows(P.seqs, i0 + lane, a, c, err);
-    const int nt_i = (c + tok_cta - 1) / tok_cta;
-    int inc = nt_i;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+    int64_t start = 0, m = 0;
+    if (i0 + lane < end) {
+      seq_rows(P.seqs, i0 + lane, a, c, err);
+      seq_keys(P.seqs, i0 + lane, start, m, err);
     }
+    const int inc = lane_scan((c + tok - 1) / tok);
     const uint32_t hit = __ballot_sync(0xffffffffu, slot < base + inc);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      run = i0 + src;
+      it.run = i0 + src;
       // the longest key ranges first
-      tile = __shfl_sync(0xffffffffu, base + inc, src) - 1 - slot;
-      q0 = __shfl_sync(0xffffffffu, a, src);
-      n = __shfl_sync(0xffffffffu, c, src);
-      break;
+      it.tok0 = (__shfl_sync(0xffffffffu, base + inc, src) - 1 - slot) * tok;
+      it.q0 = __shfl_sync(0xffffffffu, a, src);
+      it.n = __shfl_sync(0xffffffffu, c, src);
+      it.start = __shfl_sync(0xffffffffu, start, src);
+      it.m = __shfl_sync(0xffffffffu, m, src);
     }
     base += __shfl_sync(0xffffffffu, inc, 31);
   }
-  it.run = run;
-  if (run >= 0) {
-    it.q0 = q0;
-    it.n = n;
-    it.tok0 = tile * tok_cta;
-    seq_keys(P.seqs, run, it.start, it.m, err);
-    const int ntok = min(tok_cta, n - it.tok0);
-    it.ntile = (ntok + P.tpt - 1) / P.tpt;
+  if (it.run < 0) return;
+  it.uncovered = P.cover && !in_groups(P.cover, P.n_cover, it.run, P.seqs.num_req);
+  it.ntile = min(tok, it.n - it.tok0) > P.tpt ? 2 : 1;
+  int nkt[2];                      // key tiles that each query tile needs
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int last_tok = min(it.tok0 + (t + 1) * P.tpt, n) - 1;
-      const int64_t last = P.causal ? it.m - n + last_tok : it.m - 1;
-      it.nkt[t] = t < it.ntile && last >= 0 ? (int)(last / kTile) + 1 : 0;
-    }
-    const int total = NT == 2 ? max(it.nkt[0], it.nkt[NT - 1]) : it.nkt[0];
-    if (P.splits > 0) {
-      const int per = (total + P.splits - 1) / P.splits;
-      it.kt0 = min(total, split * per);
-      it.kt1 = min(total, it.kt0 + per);
-    } else {
-      it.kt0 = 0;
-      it.kt1 = total;
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) it.nkt[t] = min(it.nkt[t], it.kt1);
-    it.uncovered = 0;
-    if (P.cover) {
-      bool mine = false;
-      for (int g = lane; g < P.n_cover; g += 32)
-        mine |= P.cover[g] >= 0 && P.cover[g] <= run && run < P.cover[g + 1] &&
-                P.cover[g + 1] <= P.seqs.num_req;
-      it.uncovered = !__any_sync(0xffffffffu, mine);
-    }
+  for (int t = 0; t < 2; ++t) {
+    const int last_tok = min(it.tok0 + (t + 1) * P.tpt, it.n) - 1;
+    const int64_t last = P.causal ? it.m - it.n + last_tok : it.m - 1;
+    nkt[t] = t < it.ntile && last >= 0 ? (int)(last / kTile) + 1 : 0;
   }
-  err = __reduce_or_sync(0xffffffffu, err);
-  if (lane == 0) raise_err(P.d_err, err);
+  const int total = max(nkt[0], nkt[1]);
+  it.kt0 = 0;
+  it.nk = total;
+  if (P.splits > 0) {
+    const int each = (total + P.splits - 1) / P.splits;
+    it.kt0 = min(total, it.split * each);
+    it.nk = min(total, it.kt0 + each) - it.kt0;
+  }
+  if (kNarrow) {
+    it.steps[0] = (it.nk + 1) / 2;
+    it.steps[1] = it.nk / 2;
+  } else {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) it.steps[t] = max(0, min(nkt[t] - it.kt0, it.nk));
+  }
 }
 
-// Producer warp.  Takes this CTA's item, then those of CTAs of the grid that
-// have not started (cluster launch control: the hardware hands out their
-// indices), looks each up while the loads of the item in front are under way,
-// and publishes it; then Q, and K and V tiles through the ring.
-template <int D, int NT, typename M>
-__device__ void producer_role(const AttnParams &P, uint8_t *smem, M *ms, Item cur,
-                              const CUtensorMap *mq, const CUtensorMap *mk,
-                              const CUtensorMap *mv) {
-  using C = Cfg<D, NT>;
+// Publishes items: this CTA's, then those of CTAs of the grid that have not
+// started (cluster launch control: the hardware hands out their indices).  The
+// next index is asked for while an item is looked up, and a few items wait
+// for the other warps.
+template <bool kNarrow, typename M>
+__device__ void item_role(const AttnParams &P, M *ms) {
   const int lane = threadIdx.x & 31;
-  uint32_t g = 0, nq = 0, naux = 0, nclc = 0, items = 0;     // uses so far
-  bool ok = true, asked = false, tail_open = false;
-  auto publish = [&](const Item &it) {
-    const uint32_t s = items & 1;
-    ok = wait_all(&ms->item_empty[s], ((items >> 1) & 1) ^ 1, &ms->bd);
-    if (ok && lane == 0) {
-      ms->item[s] = it;
-      mbar_arrive(&ms->item_full[s]);
-    }
-    __syncwarp();
-    ++items;
-  };
-  bool more = true;
+  uint32_t nclc = 0, items = 0;
+  bool ok = true, more = true, asked = false;
+  int err = 0;
+  const Shares shares = count_items(P, kNarrow ? P.tpt : 2 * P.tpt, err);
+  uint32_t cta = blockIdx.x;
+  Item it;
   while (ok && more) {
     if (lane == 0) {
       mbar_arrive_expect_tx(&ms->clc, 16);
       ask_next(ms->next, &ms->clc);
     }
     asked = true;
-    Item nxt;
-    bool looked = false;
-    auto look_ahead = [&]() {
-      looked = true;
-      ok = wait_all(&ms->clc, nclc & 1, &ms->bd);
-      if (!ok) return;
-      ++nclc;
-      asked = false;
-      uint32_t cta;
-      more = next_cta(ms->next, cta);
-      fence_proxy_async_smem();      // the next answer is written by the async proxy
-      __syncwarp();
-      if (more) find_item<NT>(P, cta, nxt);
-    };
-    if (cur.run >= 0) publish(cur);
-    if (ok && cur.run >= 0 && cur.kt0 < cur.kt1) {
-      ok = wait_all(&ms->q_empty, (nq & 1) ^ 1, &ms->bd);
+    find_item<kNarrow>(P, cta, shares, it, err);
+    if (it.run >= 0) {
+      const uint32_t s = items % kItems;
+      ok = wait_all(&ms->item_empty[s], ((items / kItems) & 1) ^ 1, &ms->bd);
       if (ok && lane == 0) {
-        const uint32_t box = (uint32_t)P.tpt * P.group * 128u;
-        mbar_arrive_expect_tx(&ms->q_full, box * (D / 64) * cur.ntile);
-        for (int t = 0; t < cur.ntile; ++t)
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(smem + t * C::kQTile + c * kBlk, mq, c * 64, cur.h * P.group,
-                        cur.q0 + cur.tok0 + t * P.tpt, &ms->q_full);
+        ms->item[s] = it;
+        mbar_arrive(&ms->item_full[s]);
       }
-      if (ok) ++nq;
-      int loads = 0;
-      for (int kt = cur.kt0; kt < cur.kt1 && ok; ++kt) {
-        const int row = (int)(cur.start + (int64_t)kt * kTile);
-        const int64_t left = cur.m - (int64_t)kt * kTile;    // keys of this tile
-        for (int kv = 0; kv < 2; ++kv, ++g) {
-          if (loads++ == C::kStages) look_ahead();           // the ring is full
-          if (!ok) break;
-          const uint32_t s = g % C::kStages, ph = (g / C::kStages) & 1;
-          uint8_t *st = smem + C::kOffRing + s * C::kStage;
-          if (!(ok = wait_all(&ms->empty[s], ph ^ 1, &ms->bd))) break;
-          const bool tail = kv == 1 && left < kTile;
-          if (lane == 0) {
-            uint64_t *bar = tail ? &ms->aux : &ms->full[s];
-            mbar_arrive_expect_tx(bar, C::kStage);
+      __syncwarp();
+      ++items;
+    }
+    if (!ok || !(ok = wait_all(&ms->clc, nclc & 1, &ms->bd))) break;
+    ++nclc;
+    asked = false;
+    more = next_cta(ms->next, cta);
+    fence_proxy_async_smem();      // the next answer is written by the async proxy
+    __syncwarp();
+  }
+  if (ok) {
+    const uint32_t s = items % kItems;
+    ok = wait_all(&ms->item_empty[s], ((items / kItems) & 1) ^ 1, &ms->bd);
+    if (ok && lane == 0) {
+      ms->item[s].run = -2;
+      mbar_arrive(&ms->item_full[s]);
+    }
+  }
+  if (asked && lane == 0) drain_bar(&ms->clc, nclc & 1);
+  err = __reduce_or_sync(0xffffffffu, err);
+  if (lane == 0) raise_err(P.d_err, err);
+}
+
+// Producer warp: an item's Q, then its K and V tiles through the ring.
+template <int D, bool kNarrow, typename M>
+__device__ void producer_role(const AttnParams &P, uint8_t *smem, M *ms, const CUtensorMap *mq,
+                              const CUtensorMap *mk, const CUtensorMap *mv) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  uint32_t g = 0, nq = 0, naux = 0;     // uses so far
+  bool ok = true, tail_open = false;
+  for (uint32_t u = 0; ok; ++u) {
+    if (!(ok = wait_all(&ms->item_full[u % kItems], (u / kItems) & 1, &ms->bd))) break;
+    const Item cur = ms->item[u % kItems];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ms->item_empty[u % kItems]);
+    if (cur.run < 0) break;
+    if (cur.nk <= 0) continue;
+    if (!(ok = wait_all(&ms->q_empty, (nq & 1) ^ 1, &ms->bd))) break;
+    if (lane == 0) {
+      const uint32_t box = (uint32_t)P.tpt * P.group * 128u;
+      mbar_arrive_expect_tx(&ms->q_full, box * (D / 64) * cur.ntile);
+      for (int t = 0; t < cur.ntile; ++t)
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(smem + t * C::kQTile + c * kBlk, mq, c * 64, cur.h * P.group,
+                      cur.q0 + cur.tok0 + t * P.tpt, &ms->q_full);
+    }
+    ++nq;
+    // narrow items take their key tiles in pairs: K, K, V, V
+    constexpr int pair = kNarrow ? 2 : 1;
+    for (int k0 = 0; k0 < cur.nk && ok; k0 += pair) {
+      const int both = min(pair, cur.nk - k0);
+      for (int x = 0; x < 2 * both; ++x, ++g) {
+        const int kv = x >= both, kt = cur.kt0 + k0 + (kv ? x - both : x);
+        const int64_t left = cur.m - (int64_t)kt * kTile;  // keys of this tile
+        const uint32_t s = g % C::kStages, ph = (g / C::kStages) & 1;
+        uint8_t *st = smem + C::kOffRing + s * C::kStage;
+        if (!(ok = wait_all(&ms->empty[s], ph ^ 1, &ms->bd))) break;
+        const bool tail = kv == 1 && left < kTile;
+        if (lane == 0) {
+          uint64_t *bar = tail ? &ms->aux : &ms->full[s];
+          mbar_arrive_expect_tx(bar, C::kStage);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(st + c * kBlk, kv ? mv : mk, c * 64, cur.h,
+                        (int)(cur.start + (int64_t)kt * kTile), bar);
+        }
+        if (tail) {
+          // rows past the end are zeroed once the copy has landed
+          __syncwarp();
+          tail_open = true;
+          if (!(ok = wait_all(&ms->aux, naux & 1, &ms->bd))) break;
+          tail_open = false;
+          ++naux;
+          for (int i = (int)left * 8 + lane; i < kTile * 8; i += 32)
             for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(st + c * kBlk, kv ? mv : mk, c * 64, cur.h, row, bar);
-          }
-          if (tail) {
-            // rows past the end are zeroed once the copy has landed
-            __syncwarp();
-            tail_open = true;
-            if (!(ok = wait_all(&ms->aux, naux & 1, &ms->bd))) break;
-            tail_open = false;
-            ++naux;
-            for (int i = (int)left * 8 + lane; i < kTile * 8; i += 32)
-              for (int c = 0; c < D / 64; ++c)
-                *reinterpret_cast<uint4 *>(st + c * kBlk + i * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ms->full[s]);
-          }
+              *reinterpret_cast<uint4 *>(st + c * kBlk + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms->full[s]);
         }
       }
     }
-    if (ok && !looked) look_ahead();
-    if (ok && more) cur = nxt;
-  }
-  if (ok) {
-    Item end{};
-    end.run = -2;
-    publish(end);
   }
   // every copy has to land before the CTA leaves (the products wait for all
   // of them, but not once a wait has run out)
   if (lane == 0) {
-    if (asked) drain_bar(&ms->clc, nclc & 1);
     if (nq) drain_bar(&ms->q_full, (nq - 1) & 1);
     if (tail_open) drain_bar(&ms->aux, naux & 1);
     for (uint32_t i = g > (uint32_t)C::kStages ? g - C::kStages : 0; i < g; ++i)
@@ -277,117 +328,138 @@ __device__ void producer_role(const AttnParams &P, uint8_t *smem, M *ms, Item cu
 }
 
 // One warp issues every product.
-template <typename T, int D, int NT, typename M>
+template <typename T, int D, bool kNarrow, typename M>
 __device__ void mma_role(uint8_t *smem, M *ms) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D>;
   constexpr uint32_t kIdS = idesc_of<T>(kTile, kTile, false);
   constexpr uint32_t kIdO = idesc_of<T>(kTile, D, true);
   const uint32_t tmem = uniform(ms->tmem);
   const uint64_t ring_k = make_desc_sw128(smem_u32(smem + C::kOffRing), 16, 1024);
   const uint64_t ring_v = make_desc_sw128(smem_u32(smem + C::kOffRing), kBlk, 1024);
   const uint64_t qd = make_desc_sw128(smem_u32(smem), 16, 1024);
-  // products of S[t] with the K tile of a ring stage, by the elected lane
-  auto issue_s = [&](int t, uint32_t stage) {
-    const uint64_t b = desc_add(ring_k, stage * C::kStage);
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (k >> 2) * kBlk + (k & 3) * 32;
-      mma_f16(tmem + t * 128, desc_add(qd, t * C::kQTile + off), desc_add(b, off), kIdS, k > 0);
-    }
-    mma_commit(&ms->s_full[t]);
-  };
   uint32_t s0 = 0, p0 = 0;          // ring stage and phase of the next tile to take
-  uint32_t pq = 0, pp = 0;          // phases of Q, and of P by query tile (a bit each)
+  uint32_t pq = 0, pp = 0;          // phases of Q, and of P by stream (a bit each)
+  // ring stage (low bits) and phase (bit 8) of the tile `n` further on
+  auto at = [&](uint32_t s, uint32_t p, uint32_t n) {
+    s += n;
+    return s >= C::kStages ? (s - C::kStages) | ((p ^ 1) << 8) : s | (p << 8);
+  };
   for (uint32_t u = 0;; ++u) {
-    if (!wait_all(&ms->item_full[u & 1], (u >> 1) & 1, &ms->bd)) break;
-    const Item &it = ms->item[u & 1];
-    const int run = uniform(it.run), kt0 = uniform(it.kt0), nk = uniform(it.kt1) - kt0;
-    int end[NT];                    // key tiles of query tile t, counted from kt0
-#pragma unroll
-    for (int t = 0; t < NT; ++t) end[t] = uniform(it.nkt[t]) - kt0;
-    if (elect_one()) mbar_arrive(&ms->item_empty[u & 1]);
+    const uint32_t slot = u % kItems;
+    if (!wait_all(&ms->item_full[slot], (u / kItems) & 1, &ms->bd)) break;
+    const Item &it = ms->item[slot];
+    const int run = uniform(it.run), nk = uniform(it.nk);
+    const int steps[2] = {uniform(it.steps[0]), uniform(it.steps[1])};
+    if (elect_one()) mbar_arrive(&ms->item_empty[slot]);
     __syncwarp();
     if (run < 0) break;
     if (nk <= 0) continue;
+    // products of S[t] with the K tile of a ring stage, by the elected lane
+    auto issue_s = [&](int t, uint32_t stage) {
+      const uint64_t a = desc_add(qd, kNarrow ? 0 : t * C::kQTile), b = desc_add(ring_k, stage * C::kStage);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (k >> 2) * kBlk + (k & 3) * 32;
+        mma_f16(tmem + t * 128, desc_add(a, off), desc_add(b, off), kIdS, k > 0);
+      }
+      mma_commit(&ms->s_full[t]);
+    };
+    const uint32_t second = at(s0, p0, 1);           // a narrow item's second K tile
+    const int first = kNarrow && nk > 1 ? 2 : 1;      // K tiles in front of the first V
     if (elect_one()) {
       wait_inline(&ms->q_full, pq, &ms->bd);
       wait_inline(&ms->full[s0], p0, &ms->bd);
       fence_after_sync();
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (end[t] > 0) issue_s(t, s0);
+      if (steps[0] > 0) issue_s(0, s0);
+      if (steps[1] > 0) {
+        if (kNarrow) {
+          wait_inline(&ms->full[second & 255], second >> 8, &ms->bd);
+          fence_after_sync();
+          issue_s(1, second & 255);
+          mma_commit(&ms->empty[second & 255]);
+        } else {
+          issue_s(1, s0);
+        }
+      }
       mma_commit(&ms->empty[s0]);
-      if (nk == 1) mma_commit(&ms->q_empty);
+      if (nk <= first) mma_commit(&ms->q_empty);
     }
     __syncwarp();
     pq ^= 1;
-    uint32_t sv = s0 + 1, pv = p0;  // V(j)
-    if (sv == C::kStages) sv = 0, pv ^= 1;
+    const uint32_t v0 = at(s0, p0, first);
+    uint32_t sv = v0 & 255, pv = v0 >> 8;            // this step's first V tile
+    const int rounds = max(steps[0], steps[1]);
     bool ok = true;
-    for (int j = 0; j < nk && ok; ++j) {
+    for (int j = 0; j < rounds && ok; ++j) {
       // once a wait has run out nothing waits any more, and the products of
       // the step at hand read whatever is there
       ok = uniform(*(volatile int *)&ms->bd.abort) == 0;
-      uint32_t sk = sv + 1, pk = pv;                 // K(j + 1)
-      if (sk == C::kStages) sk = 0, pk ^= 1;
-      const bool more = j + 1 < nk;
+      // tiles of the ring: V of this step (two of a narrow item, unless its
+      // last pair is one tile), then K of the next step
+      const int here = kNarrow ? min(2, nk - 2 * j) : 1;
+      const int ahead = kNarrow ? max(0, min(2, nk - 2 * j - 2)) : (j + 1 < rounds ? 1 : 0);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (ok && j < end[t]) {
-          const uint64_t b = desc_add(ring_v, sv * C::kStage);
+      for (int t = 0; t < 2; ++t) {
+        if (ok && j < steps[t]) {
+          const uint32_t v = at(sv, pv, kNarrow ? t : 0);
+          const uint32_t k = at(sv, pv, kNarrow ? here + t : 1);
+          const uint64_t b = desc_add(ring_v, (v & 255) * C::kStage);
+          const bool next = j + 1 < steps[t];
+          // the last stream to use this step's tiles lets them go
+          const bool last = kNarrow || t == 1 || j >= steps[1];
           // The waits lie between the products that they hold back: the
           // tensor pipe has some four products queued meanwhile.
           if (elect_one()) {
-            wait_inline(&ms->full[sv], pv, &ms->bd);
+            wait_inline(&ms->full[v & 255], v >> 8, &ms->bd);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {   // P arrives in halves of 64 keys
               wait_inline(&ms->p_full[t][half], (pp >> t) & 1, &ms->bd);
               fence_after_sync();
 #pragma unroll
-              for (int k = 4 * half; k < 4 * half + 4; ++k)
-                mma_f16_ts(tmem + C::kColO + t * D, tmem + t * 128 + k * 8, desc_add(b, k * 2048),
-                           kIdO, j > 0 || k > 0);
+              for (int x = 4 * half; x < 4 * half + 4; ++x)
+                mma_f16_ts(tmem + C::kColO + t * D, tmem + t * 128 + x * 8, desc_add(b, x * 2048),
+                           kIdO, j > 0 || x > 0);
             }
-            if (j + 1 < end[t]) {
-              wait_inline(&ms->full[sk], pk, &ms->bd);
-              issue_s(t, sk);
+            if (next) {
+              wait_inline(&ms->full[k & 255], k >> 8, &ms->bd);
+              issue_s(t, k & 255);
             } else {
               mma_commit(&ms->o_full[t]);
             }
-            if (t == NT - 1 || j >= end[NT - 1]) {
-              mma_commit(&ms->empty[sv]);
-              if (more) mma_commit(&ms->empty[sk]);
-              if (j + 2 == nk) mma_commit(&ms->q_empty);   // the item's last S
+            if (last) {
+              mma_commit(&ms->empty[v & 255]);
+              if (kNarrow ? next : ahead > 0) mma_commit(&ms->empty[k & 255]);
+              // the item's last S releases Q
+              if (kNarrow ? next && 2 * (j + 1) + t == nk - 1 : j + 2 == rounds)
+                mma_commit(&ms->q_empty);
             }
           }
           __syncwarp();
           pp ^= 1u << t;
         }
       }
-      if (more) {
-        sv = sk + 1, pv = pk;
-        if (sv == C::kStages) sv = 0, pv ^= 1;
-      }
+      const uint32_t v1 = at(sv, pv, here + ahead);
+      sv = v1 & 255, pv = v1 >> 8;
     }
     if (!ok) break;
-    s0 = sv + 1, p0 = pv;
-    if (s0 == C::kStages) s0 = 0, p0 ^= 1;
+    s0 = sv, p0 = pv;
   }
   if (elect_one()) mma_commit(&ms->done);          // TMEM is not freed under a running product
   __syncwarp();
   drain_bar(&ms->done, 0);
 }
 
-// Softmax of one item's query tile t and its output; one row to a thread.
-// False if a wait ran out.
-template <typename T, int D, int NT, typename M>
+// Softmax of one item's stream t and its output; one row to a thread.  False if
+// a wait ran out.
+template <typename T, int D, bool kNarrow, typename M>
 __device__ bool softmax_item(const AttnParams &P, M *ms, const Item &it, int t, uint32_t &ps,
-                             uint32_t &po) {
-  using C = Cfg<D, NT>;
+                             uint32_t &po, uint32_t &pst) {
+  using C = Cfg<D>;
   const int x = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
   const int tok = x / P.group;
-  const int i = it.tok0 + t * P.tpt + tok;                 // token of the run
+  const int i = it.tok0 + (kNarrow ? 0 : t * P.tpt) + tok;     // token of the run
   const bool valid = tok < P.tpt && i < it.n;
+  const bool rows_here = __any_sync(0xffffffffu, valid);
   const uint32_t lane_addr = (uint32_t)(32 * warp) << 16;
   const uint32_t ts = ms->tmem + t * 128 + lane_addr, to = ms->tmem + C::kColO + t * D + lane_addr;
   // keys this row sees: j <= last (rows without a token are never masked:
@@ -403,11 +475,19 @@ __device__ bool softmax_item(const AttnParams &P, M *ms, const Item &it, int t, 
   const uint64_t scale2 = pack2(P.scale_log2, P.scale_log2);
   float ref = -INFINITY, sum = 0.f;
   bool ok = true;
-  const int kt_end = it.nkt[t];
-  int j = 0;
-  for (int kt = it.kt0; kt < kt_end; ++kt, ++j) {
+  const int steps = it.steps[t], stride = kNarrow ? 2 : 1;
+  int kt = it.kt0 + (kNarrow ? t : 0);
+  for (int j = 0; j < steps; ++j, kt += stride) {
     if (!(ok = wait_bar(&ms->s_full[t], ps, &ms->bd))) break;
     ps ^= 1;
+    if (!rows_here) {
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) {
+        mbar_arrive(&ms->p_full[t][0]);
+        mbar_arrive(&ms->p_full[t][1]);
+      }
+      continue;
+    }
     fence_after_sync();
     uint32_t s[4][32];
 #pragma unroll
@@ -473,14 +553,40 @@ __device__ bool softmax_item(const AttnParams &P, M *ms, const Item &it, int t, 
     const float2 part2 = unpack2(add2(part[0], part[1]));
     sum = part2.x + part2.y;
   }
-  const bool any = it.kt0 < kt_end;
+  const bool any = steps > 0;
   if (ok && any) ok = wait_bar(&ms->o_full[t], po, &ms->bd);
   ok = __all_sync(0xffffffffu, ok);
   if (!ok) return false;
   if (any) po ^= 1;
   fence_after_sync();
+  // a narrow item's stream 1 hands its rows' statistics to stream 0, which
+  // reads both rows of O (they are in the same lanes) and writes the output
+  if (kNarrow && t == 1) {
+    ms->stat[x] = make_float2(ref, sum);
+    fence_before_sync();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->stat_full);
+    ok = wait_all(&ms->stat_empty, pst, &ms->bd);
+    pst ^= 1;
+    return ok;
+  }
+  float w0 = 1.f, w1 = 0.f;          // weights of the streams' rows
+  bool other = false;
+  if (kNarrow) {
+    if (!wait_all(&ms->stat_full, pst, &ms->bd)) return false;
+    pst ^= 1;
+    fence_after_sync();
+    other = it.steps[1] > 0;
+    const float2 st = ms->stat[x];
+    const float r = fmaxf(ref, st.x), base = r == -INFINITY ? 0.f : r;
+    w0 = ex2(ref - base);
+    w1 = ex2(st.x - base);
+    sum = sum * w0 + (other ? st.y * w1 : 0.f);
+    ref = r;
+  }
   const bool seen = any && !(sum == 0.f);       // a NaN sum stays a NaN
   const float inv = seen ? 1.f / sum : 0.f;
+  w0 *= inv, w1 *= inv;
   const float lse =
       seen ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
   const int64_t row = (int64_t)(it.q0 + i) * P.n_heads + it.h * P.group + x % P.group;
@@ -494,73 +600,82 @@ __device__ bool softmax_item(const AttnParams &P, M *ms, const Item &it, int t, 
       P.lse[row] = lse;
     }
   }
+  if (rows_here) {
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    uint32_t o[32];
-    if (any) {
-      tmem_ld32x32b_x32(to + 32 * c, o);
-      tmem_wait_ld();
-    }
-    if (!seen)
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      float f[32];
+      if (any) {
+        tmem_ld32x32b_x32(to + 32 * c, o);
+        tmem_wait_ld();
+      }
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = 0;
-    if (!valid) continue;
-    if (P.splits > 0) {
-      if (!seen) continue;
-      float4 *dst = reinterpret_cast<float4 *>(P.part_o + (it.split * rows + row) * D + 32 * c);
+      for (int e = 0; e < 32; ++e) f[e] = seen ? __uint_as_float(o[e]) * w0 : 0.f;
+      if (other) {
+        tmem_ld32x32b_x32(to + D + 32 * c, o);
+        tmem_wait_ld();
+        if (seen) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                             __uint_as_float(o[4 * e + 2]) * inv,
-                             __uint_as_float(o[4 * e + 3]) * inv);
-    } else {
-      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(P.out) + row * D + 32 * c);
+          for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
+        }
+      }
+      if (!valid) continue;
+      if (P.splits > 0) {
+        if (!seen) continue;
+        float4 *dst = reinterpret_cast<float4 *>(P.part_o + (it.split * rows + row) * D + 32 * c);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t w[4];
+        for (int e = 0; e < 8; ++e)
+          dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+      } else {
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(P.out) + row * D + 32 * c);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          w[u] = Elem<T>::pack(__uint_as_float(o[8 * e + 2 * u]) * inv,
-                               __uint_as_float(o[8 * e + 2 * u + 1]) * inv);
-        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < 4; ++e)
+          dst[e] = make_uint4(Elem<T>::pack(f[8 * e], f[8 * e + 1]),
+                              Elem<T>::pack(f[8 * e + 2], f[8 * e + 3]),
+                              Elem<T>::pack(f[8 * e + 4], f[8 * e + 5]),
+                              Elem<T>::pack(f[8 * e + 6], f[8 * e + 7]));
       }
     }
+  }
+  if (kNarrow) {
+    fence_before_sync();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->stat_empty);
   }
   fence_before_sync();      // O is read: the next item's first product may overwrite it
   return true;
 }
 
 // Items one after another, as the producer publishes them.
-template <typename T, int D, int NT, typename M>
+template <typename T, int D, bool kNarrow, typename M>
 __device__ void softmax_role(const AttnParams &P, M *ms) {
   const int t = threadIdx.x >> 7;
-  uint32_t ps = 0, po = 0;          // phases of S and O
+  uint32_t ps = 0, po = 0, pst = 0;      // phases of S, O and the statistics
   for (uint32_t u = 0;; ++u) {
-    if (!wait_all(&ms->item_full[u & 1], (u >> 1) & 1, &ms->bd)) return;
+    const uint32_t slot = u % kItems;
+    if (!wait_all(&ms->item_full[slot], (u / kItems) & 1, &ms->bd)) return;
     // the item stays in shared memory until its output is written: registers
     // are short
-    const Item &it = ms->item[u & 1];
+    const Item &it = ms->item[slot];
     if (it.run < 0) return;
-    if (t < it.ntile && !softmax_item<T, D, NT>(P, ms, it, t, ps, po)) return;
+    if ((kNarrow || t < it.ntile) && !softmax_item<T, D, kNarrow>(P, ms, it, t, ps, po, pst))
+      return;
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->item_empty[u & 1]);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->item_empty[slot]);
   }
 }
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, NT == 1 ? 2 : 1)
-dense_attn_kernel(AttnParams P, const __grid_constant__ CUtensorMap mq,
+template <typename T, int D, bool kNarrow>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+dense_attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ CUtensorMap mq,
                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D>;
   using M = Misc<C::kStages>;
   static_assert(sizeof(M) <= kMiscBytes, "misc region");
   extern __shared__ __align__(1024) uint8_t smem[];
   M *ms = reinterpret_cast<M *>(smem + C::kOffMisc);
   const int warp = threadIdx.x >> 5;
-  Item first;
-  if (warp == 4 * NT + 1) {
-    find_item<NT>(P, blockIdx.x, first);
-  } else if (warp == 4 * NT) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&ms->tmem, C::kTmemCols);
     tmem_relinquish();
   } else if (threadIdx.x == 0) {
@@ -573,13 +688,17 @@ dense_attn_kernel(AttnParams P, const __grid_constant__ CUtensorMap mq,
     mbar_init(&ms->aux, 1);
     mbar_init(&ms->done, 1);
     mbar_init(&ms->clc, 1);
+    mbar_init(&ms->stat_full, 4);
+    mbar_init(&ms->stat_empty, 4);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&ms->s_full[t], 1);
       mbar_init(&ms->p_full[t][0], 4);
       mbar_init(&ms->p_full[t][1], 4);
       mbar_init(&ms->o_full[t], 1);
-      mbar_init(&ms->item_full[t], 1);
-      mbar_init(&ms->item_empty[t], 4 * NT + 1);     // softmax warps, MMA warp
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&ms->item_full[i], 1);
+      mbar_init(&ms->item_empty[i], 8 + 2);          // softmax, MMA and producer warps
     }
     ms->bd.abort = 0;
     ms->bd.wait_ns = P.wait_ns;
@@ -588,20 +707,22 @@ dense_attn_kernel(AttnParams P, const __grid_constant__ CUtensorMap mq,
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  if (warp >= 4 * NT) {
+  if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
-    if (warp == 4 * NT + 1)
-      producer_role<D, NT>(P, smem, ms, first, &mq, &mk, &mv);
-    else if (warp == 4 * NT)
-      mma_role<T, D, NT>(smem, ms);
+    if (warp == kProducerWarp)
+      producer_role<D, kNarrow>(P, smem, ms, &mq, &mk, &mv);
+    else if (warp == kMmaWarp)
+      mma_role<T, D, kNarrow>(smem, ms);
+    else if (warp == kItemWarp)
+      item_role<kNarrow>(P, ms);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
-    softmax_role<T, D, NT>(P, ms);
+    softmax_role<T, D, kNarrow>(P, ms);
   }
   fence_before_sync();
   __syncthreads();
   if (threadIdx.x == 0 && ms->bd.abort) raise_err(P.d_err, CSA2_DERR_TIMEOUT);
-  if (warp == 4 * NT) {
+  if (warp == kMmaWarp) {
     fence_after_sync();
     tmem_dealloc(ms->tmem, C::kTmemCols);
   }
@@ -636,20 +757,29 @@ merge_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ls
   w *= inv;
   constexpr int V = D / 32;
   float acc[V] = {};
-  for (int s = 0; s < parts; ++s) {
-    const float ws = __shfl_sync(0xffffffffu, w, s);
-    if (__shfl_sync(0xffffffffu, l, s) == -INFINITY) continue;
-    const float *src = part_o + (s * rows + row) * D + lane * V;
-    float v[V];
-    if (V == 4) {
-      const float4 f = *reinterpret_cast<const float4 *>(src);
-      v[0] = f.x, v[1] = f.y, v[V - 2] = f.z, v[V - 1] = f.w;
-    } else {
-      const float2 f = *reinterpret_cast<const float2 *>(src);
-      v[0] = f.x, v[1] = f.y;
+  for (int s0 = 0; s0 < parts; s0 += 4) {       // four parts' loads in flight
+    float v[4][V];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool use = s0 + u < parts &&
+                       __shfl_sync(0xffffffffu, l, (s0 + u) & 31) != -INFINITY;
+      const float *src = part_o + ((s0 + u) * rows + row) * D + lane * V;
+      if (V == 4) {
+        const float4 f = use ? *reinterpret_cast<const float4 *>(src) : make_float4(0, 0, 0, 0);
+        v[u][0] = f.x, v[u][1] = f.y, v[u][V - 2] = f.z, v[u][V - 1] = f.w;
+      } else {
+        const float2 f = use ? *reinterpret_cast<const float2 *>(src) : make_float2(0, 0);
+        v[u][0] = f.x, v[u][1] = f.y;
+      }
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = fmaf(ws, v[e], acc[e]);
+    for (int u = 0; u < 4; ++u) {
+      const float ws = __shfl_sync(0xffffffffu, w, (s0 + u) & 31);
+      if (s0 + u < parts) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(ws, v[u][e], acc[e]);
+      }
+    }
   }
   T *dst = out + row * D + lane * V;
 #pragma unroll
@@ -659,25 +789,20 @@ merge_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ls
     lse[row] = tot > 0.f || nan ? (ref + log2f(tot) * 0.6931471805599453f) : -INFINITY;
 }
 
-template <typename T, int D, int NT>
-int launch(const AttnParams &P, int slots, const CUtensorMap &mq, const CUtensorMap &mk,
-           const CUtensorMap &mv, cudaStream_t st) {
-  using C = Cfg<D, NT>;
-  const int64_t grid = (int64_t)slots * P.n_kv * (P.splits > 0 ? P.splits : 1);
-  if (grid > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
-  allow_smem<dense_attn_kernel<T, D, NT>>((int)C::kSmem);
-  dense_attn_kernel<T, D, NT><<<(int)grid, C::kThreads, C::kSmem, st>>>(P, mq, mk, mv);
+template <typename T, int D, bool kNarrow>
+int launch(const AttnParams &P, int items, const CUtensorMap (&m)[3], cudaStream_t st) {
+  using C = Cfg<D>;
+  allow_smem<dense_attn_kernel<T, D, kNarrow>>((int)C::kSmem);
+  dense_attn_kernel<T, D, kNarrow><<<items, C::kThreads, C::kSmem, st>>>(P, m[0], m[1], m[2]);
   return launch_status();
 }
 
-template <int NT>
-int launch_any(const Shape &s, const AttnParams &P, int slots, const CUtensorMap &mq,
-               const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
-  if (s.bf16)
-    return s.dim == 128 ? launch<__nv_bfloat16, 128, NT>(P, slots, mq, mk, mv, st)
-                        : launch<__nv_bfloat16, 64, NT>(P, slots, mq, mk, mv, st);
-  return s.dim == 128 ? launch<__half, 128, NT>(P, slots, mq, mk, mv, st)
-                      : launch<__half, 64, NT>(P, slots, mq, mk, mv, st);
+template <typename T>
+int launch_any(const Shape &s, const AttnParams &P, bool narrow, int items,
+               const CUtensorMap (&m)[3], cudaStream_t st) {
+  if (s.dim == 128)
+    return narrow ? launch<T, 128, true>(P, items, m, st) : launch<T, 128, false>(P, items, m, st);
+  return narrow ? launch<T, 64, true>(P, items, m, st) : launch<T, 64, false>(P, items, m, st);
 }
 
 struct Cache {
@@ -694,20 +819,22 @@ int tile_tokens(int64_t num_q, int64_t runs, int group) {
   return t < most ? t : most;
 }
 
-int run_attn(const Shape &s, const Cache &c, AttnParams &P, bool two, cudaStream_t st) {
-  const int tok = P.tpt * (two ? 2 : 1);
-  const int64_t slots = P.seqs.num_q / tok + P.seqs.count;
-  if (slots > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
-  CUtensorMap mq, mk, mv;
+int run_attn(const Shape &s, const Cache &c, const AttnParams &P, bool narrow, cudaStream_t st) {
+  // an upper bound of the items, since the lengths are on the device
+  const int64_t tok = narrow ? P.tpt : 2 * P.tpt;
+  const int64_t items =
+      (P.seqs.num_q / tok + P.seqs.count) * s.n_kv * (P.splits > 0 ? P.splits : 1);
+  if (items > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
+  CUtensorMap m[3];
   const bool none = c.kv_rows == 0;   // no key row is ever fetched then
-  if (!make_rows_map(&mq, s.bf16, c.q, P.seqs.num_q, s.n_heads, s.dim, c.ldq, s.group, P.tpt) ||
-      !make_rows_map(&mk, s.bf16, none ? c.q : c.k, none ? 1 : c.kv_rows, s.n_kv, s.dim,
+  if (!make_rows_map(&m[0], s.bf16, c.q, P.seqs.num_q, s.n_heads, s.dim, c.ldq, s.group, P.tpt) ||
+      !make_rows_map(&m[1], s.bf16, none ? c.q : c.k, none ? 1 : c.kv_rows, s.n_kv, s.dim,
                      none ? c.ldq : c.ldk, 1, kTile) ||
-      !make_rows_map(&mv, s.bf16, none ? c.q : c.v, none ? 1 : c.kv_rows, s.n_kv, s.dim,
+      !make_rows_map(&m[2], s.bf16, none ? c.q : c.v, none ? 1 : c.kv_rows, s.n_kv, s.dim,
                      none ? c.ldq : c.ldv, 1, kTile))
     return CSA2_ERR_UNSUPPORTED;
-  return two ? launch_any<2>(s, P, (int)slots, mq, mk, mv, st)
-             : launch_any<1>(s, P, (int)slots, mq, mk, mv, st);
+  return s.bf16 ? launch_any<__nv_bfloat16>(s, P, narrow, (int)items, m, st)
+                : launch_any<__half>(s, P, narrow, (int)items, m, st);
 }
 
 int check_cache(const csa2_packed *b, const Shape &s, const Cache &c) {
@@ -717,41 +844,41 @@ int check_cache(const csa2_packed *b, const Shape &s, const Cache &c) {
   return st;
 }
 
-// Splits of a part with `items` CTAs unsplit on `slots` places and `tiles`
-// key tiles each: the waves' length in key tiles, 3 tiles of fixed cost to a
-// CTA, and half a tile to a split for the join.
-int plan_splits(int64_t items, int slots, int64_t tiles) {
+// Splits of a part with `items` items unsplit of `tiles` key tile steps each: the
+// waves' length in steps, 3 steps of fixed cost to an item, and half a step to
+// a split for the join.
+int plan_splits(int64_t items, int64_t tiles) {
   int best = 1;
   double cost = 1e30;
   for (int s = 1; s <= kMaxSplits && s <= (tiles > 0 ? tiles : 1); ++s) {
-    const int64_t waves = (items * s + slots - 1) / slots;
+    const int64_t waves = (items * s + kSms - 1) / kSms;
     const double c = (double)waves * ((double)((tiles + s - 1) / s) + 3.0) + 0.5 * s;
     if (c < cost) cost = c, best = s;
   }
   return best;
 }
 
+// Narrow items where a run's rows fill no more than one query tile.
 struct PrefixPlan {
-  int tpt_pre, tpt_own, splits_pre, splits_own;
-  bool two_pre;
+  int tpt_pre, tpt_own, narrow_pre, narrow_own, splits_pre, splits_own;
 };
+
+void plan_part(const Shape &s, int64_t num_q, int64_t runs, int64_t most, int &tpt, int &narrow,
+               int &splits) {
+  tpt = tile_tokens(num_q, runs, s.group);
+  narrow = num_q <= runs * tpt;
+  const int64_t tok = narrow ? tpt : 2 * tpt;
+  const int64_t items = (num_q / tok > runs ? num_q / tok : runs) * s.n_kv;
+  const int64_t tiles = most / kTile + (most % kTile != 0);
+  splits = plan_splits(items, narrow ? (tiles + 1) / 2 : tiles);
+}
 
 PrefixPlan plan_prefix(const Shape &s, int64_t num_q, int64_t num_req, int64_t num_groups,
                        int64_t max_prefix, int64_t max_kv) {
   PrefixPlan p{};
-  p.tpt_own = tile_tokens(num_q, num_req > 0 ? num_req : 1, s.group);
-  const int64_t own_items = (num_q / p.tpt_own > num_req ? num_q / p.tpt_own : num_req) * s.n_kv;
-  p.splits_own = plan_splits(own_items, 2 * kSms, (max_kv + kTile - 1) / kTile);
-  if (num_groups > 0) {
-    p.tpt_pre = tile_tokens(num_q, num_groups, s.group);
-    const int64_t tiles = num_q / p.tpt_pre > num_groups ? num_q / p.tpt_pre : num_groups;
-    // two query tiles to a CTA halve the traffic of the shared keys; with a
-    // single tile to a group the second would be empty
-    p.two_pre = num_q > num_groups * p.tpt_pre;
-    const int64_t items = (p.two_pre ? (tiles + 1) / 2 : tiles) * s.n_kv;
-    p.splits_pre = plan_splits(items, p.two_pre ? kSms : 2 * kSms,
-                               (max_prefix + kTile - 1) / kTile);
-  }
+  plan_part(s, num_q, num_req > 0 ? num_req : 1, max_kv, p.tpt_own, p.narrow_own, p.splits_own);
+  if (num_groups > 0)
+    plan_part(s, num_q, num_groups, max_prefix, p.tpt_pre, p.narrow_pre, p.splits_pre);
   return p;
 }
 
@@ -792,9 +919,7 @@ extern "C" CSA2_API int csa2_prompt_attn(const csa2_packed *b, int32_t n_heads,
   P.lse = lse;
   P.d_err = d_err;
   P.wait_ns = csa2::wait_limit_ns();
-  // one tile to a CTA where a request's rows fill no more than one
-  const bool two = (int64_t)b->num_req * P.tpt < b->num_q;
-  return run_attn(s, c, P, two, csa2::as_stream(stream));
+  return run_attn(s, c, P, b->num_q <= (int64_t)b->num_req * P.tpt, csa2::as_stream(stream));
 }
 
 extern "C" CSA2_API int csa2_prefix_attn_workspace(int32_t num_q, int32_t num_req,
@@ -855,7 +980,7 @@ extern "C" CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix
     P.splits = p.splits_pre;
     P.part_o = part_o;
     P.part_lse = part_lse;
-    if ((st = run_attn(s, c, P, p.two_pre, cs)) != CSA2_OK) return st;
+    if ((st = run_attn(s, c, P, p.narrow_pre, cs)) != CSA2_OK) return st;
     P.cover = g->cu_group;
     P.n_cover = ng;
     P.cover_splits = p.splits_pre;
@@ -868,7 +993,7 @@ extern "C" CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix
   P.splits = p.splits_own;
   P.part_o = part_o + p.splits_pre * rows * s.dim;
   P.part_lse = part_lse + p.splits_pre * rows;
-  if ((st = run_attn(s, c, P, false, cs)) != CSA2_OK) return st;
+  if ((st = run_attn(s, c, P, p.narrow_own, cs)) != CSA2_OK) return st;
   const int64_t grid = (rows + 7) / 8;
   if (grid > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
   auto merge = [&](auto *o, auto dim_c) {
