@@ -302,6 +302,25 @@ inline int check_packed(const csa2_packed *b, int32_t n_heads, int32_t n_kv_head
   return CSA2_OK;
 }
 
+// Single tokens over their own rows (decode_attn.cu): groups of at most
+// kDecodeGroup heads; results or partial results as in dense_attn.cu.
+constexpr int kDecodeGroup = 16;
+struct DecodeParams {
+  Seqs seqs;
+  const void *q, *k, *v;
+  int64_t ldq, ldk, ldv;
+  int n_heads, n_kv, group;
+  int splits;
+  float scale_log2;
+  void *out;
+  float *lse, *part_o, *part_lse;
+  const int32_t *cover;
+  int n_cover, cover_splits;
+  float *cover_lse;
+  int32_t *d_err;
+};
+int decode_attn(const Shape &s, const DecodeParams &P, cudaStream_t st);
+
 // rows with `ld` elements between them: TMA wants 16-byte rows and bases
 inline int check_rows(const void *p, int64_t ld, int heads, int dim) {
   if (!p || ld < (int64_t)heads * dim) return CSA2_ERR_INVALID_ARG;

@@ -107,7 +107,7 @@ struct Misc {
   uint64_t item_full[kItems], item_empty[kItems];
   Bound bd;
   uint32_t tmem;
-  uint64_t stat_full, stat_empty;
+  uint64_t loaded, stat_full, stat_empty;
   alignas(16) uint64_t next[2];      // answer to the request for another CTA's work
   Item item[kItems];
   float2 stat[kTile];                // narrow items: reference and sum of stream 1's rows
@@ -208,23 +208,19 @@ __device__ void find_item(const AttnParams &P, uint32_t cta, const Shares &s, It
 
 // Publishes items: this CTA's, then those of CTAs of the grid that have not
 // started (cluster launch control: the hardware hands out their indices).  The
-// next index is asked for while an item is looked up, and a few items wait
-// for the other warps.
+// next one is asked for once all loads of the last are issued: earlier, and a
+// CTA would sit on items that an idle one could take (448 items of 37 steps:
+// 194 us with up to four items ahead); later, and the loads would pause.
 template <bool kNarrow, typename M>
 __device__ void item_role(const AttnParams &P, M *ms) {
   const int lane = threadIdx.x & 31;
-  uint32_t nclc = 0, items = 0;
-  bool ok = true, more = true, asked = false;
+  uint32_t asked = 0, items = 0;
+  bool ok = true, more = true, waiting = false;
   int err = 0;
   const Shares shares = count_items(P, kNarrow ? P.tpt : 2 * P.tpt, err);
   uint32_t cta = blockIdx.x;
   Item it;
   while (ok && more) {
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&ms->clc, 16);
-      ask_next(ms->next, &ms->clc);
-    }
-    asked = true;
     find_item<kNarrow>(P, cta, shares, it, err);
     if (it.run >= 0) {
       const uint32_t s = items % kItems;
@@ -234,11 +230,18 @@ __device__ void item_role(const AttnParams &P, M *ms) {
         mbar_arrive(&ms->item_full[s]);
       }
       __syncwarp();
+      ok = ok && wait_all(&ms->loaded, items & 1, &ms->bd);
       ++items;
     }
-    if (!ok || !(ok = wait_all(&ms->clc, nclc & 1, &ms->bd))) break;
-    ++nclc;
-    asked = false;
+    if (!ok) break;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&ms->clc, 16);
+      ask_next(ms->next, &ms->clc);
+    }
+    waiting = true;
+    if (!(ok = wait_all(&ms->clc, asked & 1, &ms->bd))) break;
+    waiting = false;
+    ++asked;
     more = next_cta(ms->next, cta);
     fence_proxy_async_smem();      // the next answer is written by the async proxy
     __syncwarp();
@@ -251,7 +254,7 @@ __device__ void item_role(const AttnParams &P, M *ms) {
       mbar_arrive(&ms->item_full[s]);
     }
   }
-  if (asked && lane == 0) drain_bar(&ms->clc, nclc & 1);
+  if (waiting && lane == 0) drain_bar(&ms->clc, asked & 1);
   err = __reduce_or_sync(0xffffffffu, err);
   if (lane == 0) raise_err(P.d_err, err);
 }
@@ -270,7 +273,10 @@ __device__ void producer_role(const AttnParams &P, uint8_t *smem, M *ms, const C
     __syncwarp();
     if (lane == 0) mbar_arrive(&ms->item_empty[u % kItems]);
     if (cur.run < 0) break;
-    if (cur.nk <= 0) continue;
+    if (cur.nk <= 0) {
+      if (lane == 0) mbar_arrive(&ms->loaded);
+      continue;
+    }
     if (!(ok = wait_all(&ms->q_empty, (nq & 1) ^ 1, &ms->bd))) break;
     if (lane == 0) {
       const uint32_t box = (uint32_t)P.tpt * P.group * 128u;
@@ -315,6 +321,7 @@ __device__ void producer_role(const AttnParams &P, uint8_t *smem, M *ms, const C
         }
       }
     }
+    if (lane == 0) mbar_arrive(&ms->loaded);
   }
   // every copy has to land before the CTA leaves (the products wait for all
   // of them, but not once a wait has run out)
@@ -688,6 +695,7 @@ dense_attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ 
     mbar_init(&ms->aux, 1);
     mbar_init(&ms->done, 1);
     mbar_init(&ms->clc, 1);
+    mbar_init(&ms->loaded, 1);
     mbar_init(&ms->stat_full, 4);
     mbar_init(&ms->stat_empty, 4);
     for (int t = 0; t < 2; ++t) {
@@ -844,46 +852,73 @@ int check_cache(const csa2_packed *b, const Shape &s, const Cache &c) {
   return st;
 }
 
-// Splits of a part with `items` items unsplit of `tiles` key tile steps each: the
-// waves' length in steps, 3 steps of fixed cost to an item, and half a step to
-// a split for the join.
-int plan_splits(int64_t items, int64_t tiles) {
+// Single tokens of few heads go by decode_attn.cu; other runs whose rows fill no
+// more than one query tile are narrow items.
+enum Kind { kWideItems, kNarrowItems, kSingleTokens };
+
+Kind kind_of(int64_t num_q, int64_t runs, int tpt, int group, bool single) {
+  if (single && tpt == 1 && group <= kDecodeGroup) return kSingleTokens;
+  return num_q <= runs * tpt ? kNarrowItems : kWideItems;
+}
+
+// Splits of `items` items unsplit on `places` places, of `steps` steps each: the
+// waves' length in steps, `fixed` steps of fixed cost to an item, and half a
+// step to a split for the join.
+int plan_splits(int64_t items, int places, int64_t steps, double fixed) {
   int best = 1;
   double cost = 1e30;
-  for (int s = 1; s <= kMaxSplits && s <= (tiles > 0 ? tiles : 1); ++s) {
-    const int64_t waves = (items * s + kSms - 1) / kSms;
-    const double c = (double)waves * ((double)((tiles + s - 1) / s) + 3.0) + 0.5 * s;
+  for (int s = 1; s <= kMaxSplits && s <= (steps > 0 ? steps : 1); ++s) {
+    const int64_t waves = (items * s + places - 1) / places;
+    const double c = (double)waves * ((double)((steps + s - 1) / s) + fixed) + 0.5 * s;
     if (c < cost) cost = c, best = s;
   }
   return best;
 }
 
-// Narrow items where a run's rows fill no more than one query tile.
-struct PrefixPlan {
-  int tpt_pre, tpt_own, narrow_pre, narrow_own, splits_pre, splits_own;
+struct PartPlan {
+  int tpt, splits;
+  Kind kind;
 };
 
-void plan_part(const Shape &s, int64_t num_q, int64_t runs, int64_t most, int &tpt, int &narrow,
-               int &splits) {
-  tpt = tile_tokens(num_q, runs, s.group);
-  narrow = num_q <= runs * tpt;
-  const int64_t tok = narrow ? tpt : 2 * tpt;
+PartPlan plan_part(const Shape &s, int64_t num_q, int64_t runs, int64_t most, bool single) {
+  PartPlan p;
+  p.tpt = tile_tokens(num_q, runs, s.group);
+  p.kind = kind_of(num_q, runs, p.tpt, s.group, single);
+  const int64_t tok = p.kind == kWideItems ? 2 * p.tpt : p.tpt;
   const int64_t items = (num_q / tok > runs ? num_q / tok : runs) * s.n_kv;
   const int64_t tiles = most / kTile + (most % kTile != 0);
-  splits = plan_splits(items, narrow ? (tiles + 1) / 2 : tiles);
+  if (p.kind == kSingleTokens)       // three CTAs to an SM, 64 keys a step
+    p.splits = plan_splits(items, 3 * kSms, 2 * tiles, 4.0);
+  else
+    p.splits = plan_splits(items, kSms, p.kind == kNarrowItems ? (tiles + 1) / 2 : tiles, 3.0);
+  return p;
 }
+
+struct PrefixPlan {
+  PartPlan pre, own;
+};
 
 PrefixPlan plan_prefix(const Shape &s, int64_t num_q, int64_t num_req, int64_t num_groups,
                        int64_t max_prefix, int64_t max_kv) {
   PrefixPlan p{};
-  plan_part(s, num_q, num_req > 0 ? num_req : 1, max_kv, p.tpt_own, p.narrow_own, p.splits_own);
-  if (num_groups > 0)
-    plan_part(s, num_q, num_groups, max_prefix, p.tpt_pre, p.narrow_pre, p.splits_pre);
+  p.own = plan_part(s, num_q, num_req > 0 ? num_req : 1, max_kv, true);
+  if (num_groups > 0) p.pre = plan_part(s, num_q, num_groups, max_prefix, false);
   return p;
 }
 
+// One part of an attention call.
+int run_part(const Shape &s, const Cache &c, AttnParams &P, const PartPlan &p, cudaStream_t st) {
+  P.tpt = p.tpt;
+  if (p.kind != kSingleTokens) return run_attn(s, c, P, p.kind == kNarrowItems, st);
+  const DecodeParams D{P.seqs,   c.q,     c.k,      c.v,        c.ldq,       c.ldk,
+                       c.ldv,    P.n_heads, P.n_kv, P.group,    P.splits,    P.scale_log2,
+                       P.out,    P.lse,   P.part_o, P.part_lse, P.cover,     P.n_cover,
+                       P.cover_splits, P.cover_lse, P.d_err};
+  return decode_attn(s, D, st);
+}
+
 int64_t plan_bytes(const PrefixPlan &p, int64_t num_q, const Shape &s) {
-  return (int64_t)(p.splits_pre + p.splits_own) * num_q * s.n_heads * (s.dim + 4) * 4 + 256;
+  return (int64_t)(p.pre.splits + p.own.splits) * num_q * s.n_heads * (s.dim + 4) * 4 + 256;
 }
 
 }  // namespace
@@ -912,14 +947,13 @@ extern "C" CSA2_API int csa2_prompt_attn(const csa2_packed *b, int32_t n_heads,
   P.n_heads = s.n_heads;
   P.n_kv = s.n_kv;
   P.group = s.group;
-  P.tpt = tile_tokens(b->num_q, b->num_req, s.group);
   P.causal = 1;
   P.scale_log2 = sm_scale * 1.4426950408889634f;
   P.out = out;
   P.lse = lse;
   P.d_err = d_err;
   P.wait_ns = csa2::wait_limit_ns();
-  return run_attn(s, c, P, b->num_q <= (int64_t)b->num_req * P.tpt, csa2::as_stream(stream));
+  return run_part(s, c, P, plan_part(s, b->num_q, b->num_req, 0, true), csa2::as_stream(stream));
 }
 
 extern "C" CSA2_API int csa2_prefix_attn_workspace(int32_t num_q, int32_t num_req,
@@ -961,7 +995,7 @@ extern "C" CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix
   if (!workspace || workspace_bytes < plan_bytes(p, b->num_q, s)) return CSA2_ERR_INVALID_ARG;
   if ((uintptr_t)workspace & 255u) return CSA2_ERR_UNSUPPORTED;
   const cudaStream_t cs = csa2::as_stream(stream);
-  const int parts = p.splits_pre + p.splits_own;
+  const int parts = p.pre.splits + p.own.splits;
   const int64_t rows = (int64_t)b->num_q * s.n_heads;
   float *part_o = static_cast<float *>(workspace);
   float *part_lse = part_o + parts * rows * s.dim;
@@ -975,25 +1009,23 @@ extern "C" CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix
   if (ng > 0) {
     P.seqs = Seqs{ng, b->num_q, b->num_req, b->cu_q, g->cu_group, g->prefix_start, g->prefix_len,
                   kv_rows};
-    P.tpt = p.tpt_pre;
     P.causal = 0;
-    P.splits = p.splits_pre;
+    P.splits = p.pre.splits;
     P.part_o = part_o;
     P.part_lse = part_lse;
-    if ((st = run_attn(s, c, P, p.narrow_pre, cs)) != CSA2_OK) return st;
+    if ((st = run_part(s, c, P, p.pre, cs)) != CSA2_OK) return st;
     P.cover = g->cu_group;
     P.n_cover = ng;
-    P.cover_splits = p.splits_pre;
+    P.cover_splits = p.pre.splits;
     P.cover_lse = part_lse;
   }
   P.seqs = Seqs{b->num_req, b->num_q, b->num_req, b->cu_q, nullptr, b->kv_start, b->kv_len,
                 kv_rows};
-  P.tpt = p.tpt_own;
   P.causal = 1;
-  P.splits = p.splits_own;
-  P.part_o = part_o + p.splits_pre * rows * s.dim;
-  P.part_lse = part_lse + p.splits_pre * rows;
-  if ((st = run_attn(s, c, P, p.narrow_own, cs)) != CSA2_OK) return st;
+  P.splits = p.own.splits;
+  P.part_o = part_o + p.pre.splits * rows * s.dim;
+  P.part_lse = part_lse + p.pre.splits * rows;
+  if ((st = run_part(s, c, P, p.own, cs)) != CSA2_OK) return st;
   const int64_t grid = (rows + 7) / 8;
   if (grid > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
   auto merge = [&](auto *o, auto dim_c) {
