@@ -262,8 +262,11 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
   __syncthreads();
   const bool uncovered =
       P.cover && split == 0 && !in_groups(P.cover, P.n_cover, run, S.num_req);
-  constexpr int kTeam = kWarps * 32 / (8 * kN), kCh = D / kTeam;    // threads of a row
-  const int row = threadIdx.x / kTeam, d0 = (threadIdx.x % kTeam) * kCh;
+  // a result's rows are channel-innermost, a partial result's row-innermost
+  const bool part = P.splits > 0;
+  constexpr int kRows = 8 * kN, kTeam = kWarps * 32 / kRows;       // threads of a row
+  const int row = part ? threadIdx.x % kRows : threadIdx.x / kTeam;
+  const int col = part ? threadIdx.x / kRows : threadIdx.x % kTeam;
   if (row >= P.group) return;
   float top = -INFINITY, tot = 0.f, w[kWarps];
 #pragma unroll
@@ -276,35 +279,41 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
   }
   const bool seen = !(tot == 0.f);   // a NaN stays a NaN
   const float inv = seen ? 1.f / tot : 0.f;
-  const int64_t at = (int64_t)token * P.n_heads + h * P.group + row;
-  const int64_t rows = (int64_t)S.num_q * P.n_heads;
-  if (d0 == 0) {
-    const float lse = seen ? (base + log2f(tot)) * 0.6931471805599453f : -INFINITY;
-    if (P.splits > 0)
-      P.part_lse[split * rows + at] = lse;
-    else if (P.lse)
-      P.lse[at] = lse;
-    if (uncovered)
-      for (int i = 0; i < P.cover_splits; ++i) P.cover_lse[i * rows + at] = -INFINITY;
-  }
-  if (P.splits > 0 && !seen) return;
-#pragma unroll
-  for (int d = 0; d < kCh; d += 4) {
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const float4 v = *reinterpret_cast<const float4 *>(&sh.o[i][row][d0 + d]);
-      f[0] = fmaf(w[i], v.x, f[0]), f[1] = fmaf(w[i], v.y, f[1]);
-      f[2] = fmaf(w[i], v.z, f[2]), f[3] = fmaf(w[i], v.w, f[3]);
+  const float lse = seen ? (base + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+  if (part) {
+    const int64_t rows = (int64_t)S.num_q * P.group, at = (int64_t)token * P.group + row;
+    if (col == 0) {
+      P.part_lse[((int64_t)split * P.n_kv + h) * rows + at] = lse;
+      if (uncovered)
+        for (int i = 0; i < P.cover_splits; ++i)
+          P.cover_lse[((int64_t)i * P.n_kv + h) * rows + at] = -INFINITY;
     }
+    if (!seen) return;
+    float *dst = P.part_o + ((int64_t)split * P.n_kv + h) * D * rows + at;
+#pragma unroll 4
+    for (int d = col; d < D; d += kTeam) {
+      float f = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = seen ? f[e] * inv : 0.f;
-    if (P.splits > 0)
-      *reinterpret_cast<float4 *>(P.part_o + (split * rows + at) * D + d0 + d) =
-          make_float4(f[0], f[1], f[2], f[3]);
-    else
-      *reinterpret_cast<uint2 *>(static_cast<T *>(P.out) + at * D + d0 + d) =
+      for (int i = 0; i < kWarps; ++i) f = fmaf(w[i], sh.o[i][row][d], f);
+      dst[d * rows] = f * inv;
+    }
+  } else {
+    const int64_t at = (int64_t)token * P.n_heads + h * P.group + row;
+    if (col == 0 && P.lse) P.lse[at] = lse;
+#pragma unroll
+    for (int d = 4 * col; d < D; d += 4 * kTeam) {
+      float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const float4 v = *reinterpret_cast<const float4 *>(&sh.o[i][row][d]);
+        f[0] = fmaf(w[i], v.x, f[0]), f[1] = fmaf(w[i], v.y, f[1]);
+        f[2] = fmaf(w[i], v.z, f[2]), f[3] = fmaf(w[i], v.w, f[3]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = seen ? f[e] * inv : 0.f;
+      *reinterpret_cast<uint2 *>(static_cast<T *>(P.out) + at * D + d) =
           make_uint2(Elem<T>::pack(f[0], f[1]), Elem<T>::pack(f[2], f[3]));
+    }
   }
 }
 

@@ -51,8 +51,8 @@ struct AttnParams {
   Seqs seqs;
   int n_heads, n_kv, group, tpt, causal;
   int splits;        // of the key range; 0: the output itself is written
-  float *part_o;     // [splits, num_q, n_heads, D]
-  float *part_lse;   // [splits, num_q, n_heads]
+  float *part_o;     // [splits, n_kv, D, num_q * group]: packed rows innermost,
+  float *part_lse;   // [splits, n_kv, num_q * group]: so that lanes store neighbours
   float scale_log2;
   void *out;         // [num_q, n_heads, D]
   float *lse;        // [num_q, n_heads] or null
@@ -456,6 +456,70 @@ __device__ void mma_role(uint8_t *smem, M *ms) {
   drain_bar(&ms->done, 0);
 }
 
+// Normalises and stores a warp's 32 rows of O.  Read 16 lanes x 256 bits at a
+// time, a quad of threads has 8 neighbouring columns of a row; packed to 16
+// bits and transposed among the quad, each thread has 16 bytes and the quad
+// 64 of a row.  (Whole rows to a thread, 16 bytes a store, touched 32 lines an
+// instruction: 4000 cycles of the load/store pipe to an item, during which the
+// MMA warp's barrier polls waited too.)  `at`, `valid`, `seen`, w0 and w1 are
+// those of the lane's own row.
+template <typename T, int D>
+__device__ __forceinline__ void store_rows(const AttnParams &P, uint32_t to, int64_t at,
+                                           bool valid, bool seen, bool any, bool other, float w0,
+                                           float w1) {
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  const uint32_t ok = __ballot_sync(0xffffffffu, valid), has = __ballot_sync(0xffffffffu, seen);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float a[2], b[2];
+    T *dst[2];
+    int row[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      row[r] = 16 * half + 8 * r + (lane >> 2);
+      a[r] = __shfl_sync(0xffffffffu, w0, row[r]);
+      b[r] = __shfl_sync(0xffffffffu, w1, row[r]);
+      dst[r] = static_cast<T *>(P.out) + __shfl_sync(0xffffffffu, at, row[r]) * D + 8 * c;
+    }
+    const uint32_t base = to + ((uint32_t)(16 * half) << 16);
+#pragma unroll
+    for (int col = 0; col < D; col += 32) {
+      uint32_t o[16], o1[16];
+      if (any) tmem_ld16x256b_x4(base + col, o);
+      if (other) tmem_ld16x256b_x4(base + D + col, o1);
+      tmem_wait_ld();
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            f[e] = (has >> row[r]) & 1 ? __uint_as_float(o[4 * k + 2 * r + e]) * a[r] : 0.f;
+            if (other && ((has >> row[r]) & 1))
+              f[e] = fmaf(__uint_as_float(o1[4 * k + 2 * r + e]), b[r], f[e]);
+          }
+          w[k] = Elem<T>::pack(f[0], f[1]);
+        }
+        // word k of thread c to word c of thread k
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, c & 1 ? w[k] : w[k + 1], 1);
+          if (c & 1) w[k] = got; else w[k + 1] = got;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, c & 2 ? w[k] : w[k + 2], 2);
+          if (c & 2) w[k] = got; else w[k + 2] = got;
+        }
+        if ((ok >> row[r]) & 1)
+          *reinterpret_cast<uint4 *>(dst[r] + col) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+}
+
 // Softmax of one item's stream t and its output; one row to a thread.  False if
 // a wait ran out.
 template <typename T, int D, bool kNarrow, typename M>
@@ -596,53 +660,41 @@ __device__ bool softmax_item(const AttnParams &P, M *ms, const Item &it, int t, 
   w0 *= inv, w1 *= inv;
   const float lse =
       seen ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-  const int64_t row = (int64_t)(it.q0 + i) * P.n_heads + it.h * P.group + x % P.group;
-  const int64_t rows = (int64_t)P.seqs.num_q * P.n_heads;
-  if (valid) {
-    if (P.splits > 0) {
-      P.part_lse[it.split * rows + row] = lse;
+  if (P.splits > 0) {
+    const int64_t rows = (int64_t)P.seqs.num_q * P.group;
+    const int64_t at = (int64_t)(it.q0 + i) * P.group + x % P.group;
+    if (valid) {
+      P.part_lse[((int64_t)it.split * P.n_kv + it.h) * rows + at] = lse;
       if (it.uncovered && it.split == 0)
-        for (int s = 0; s < P.cover_splits; ++s) P.cover_lse[s * rows + row] = -INFINITY;
-    } else if (P.lse) {
-      P.lse[row] = lse;
+        for (int s = 0; s < P.cover_splits; ++s)
+          P.cover_lse[((int64_t)s * P.n_kv + it.h) * rows + at] = -INFINITY;
     }
-  }
-  if (rows_here) {
+    if (rows_here && any) {
+      float *dst = P.part_o + ((int64_t)it.split * P.n_kv + it.h) * D * rows + at;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      uint32_t o[32];
-      float f[32];
-      if (any) {
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        float f[32];
         tmem_ld32x32b_x32(to + 32 * c, o);
         tmem_wait_ld();
-      }
 #pragma unroll
-      for (int e = 0; e < 32; ++e) f[e] = seen ? __uint_as_float(o[e]) * w0 : 0.f;
-      if (other) {
-        tmem_ld32x32b_x32(to + D + 32 * c, o);
-        tmem_wait_ld();
-        if (seen) {
+        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * w0;
+        if (other) {
+          tmem_ld32x32b_x32(to + D + 32 * c, o);
+          tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
         }
-      }
-      if (!valid) continue;
-      if (P.splits > 0) {
-        if (!seen) continue;
-        float4 *dst = reinterpret_cast<float4 *>(P.part_o + (it.split * rows + row) * D + 32 * c);
+        if (valid && seen) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-      } else {
-        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(P.out) + row * D + 32 * c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          dst[e] = make_uint4(Elem<T>::pack(f[8 * e], f[8 * e + 1]),
-                              Elem<T>::pack(f[8 * e + 2], f[8 * e + 3]),
-                              Elem<T>::pack(f[8 * e + 4], f[8 * e + 5]),
-                              Elem<T>::pack(f[8 * e + 6], f[8 * e + 7]));
+          for (int e = 0; e < 32; ++e) dst[(32 * c + e) * rows] = f[e];
+        }
       }
     }
+  } else {
+    const int64_t at = (int64_t)(it.q0 + i) * P.n_heads + it.h * P.group + x % P.group;
+    if (valid && P.lse) P.lse[at] = lse;
+    if (rows_here) store_rows<T, D>(P, to, at, valid, seen, any, other, w0, w1);
   }
   if (kNarrow) {
     fence_before_sync();
@@ -737,64 +789,70 @@ dense_attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ 
 }
 
 // Joins the parts of a row: lse = ln sum_s e^{lse_s}, out = sum_s
-// e^{lse_s - lse} out_s.  One warp per (query row, head); parts without keys
-// (-inf) are not read.  Rows in front of or behind the sequences are left.
+// e^{lse_s - lse} out_s.  A block has 32 packed rows of a key head, a lane to a
+// row, a warp to an eighth of the channels; parts without keys (-inf) are not
+// read.  Rows in front of or behind the sequences are left.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
 merge_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse, int parts,
-             int num_q, int n_heads, const int32_t *__restrict__ cu_q, int num_req,
+             int num_q, int n_kv, int group, const int32_t *__restrict__ cu_q, int num_req,
              T *__restrict__ out, float *__restrict__ lse) {
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)num_q * n_heads;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  const int q = (int)(row / n_heads);
-  if (q < cu_q[0] || q >= cu_q[num_req]) return;
-  float mx = -INFINITY, l = lane < parts ? part_lse[lane * rows + row] : -INFINITY;
-  bool nan = l != l;
-  mx = l;
+  constexpr int kCh = D / 8;
+  constexpr int kBatch = 3;
+  __shared__ __align__(16) T tile[32][D + 8];
+  __shared__ float weight[2 * kMaxSplits][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
+  const int64_t rows = (int64_t)num_q * group, row0 = (int64_t)blockIdx.x * 32;
+  const int64_t lo = (int64_t)cu_q[0] * group, hi = min(rows, (int64_t)cu_q[num_req] * group);
+  const int64_t row = row0 + lane;
+  const bool mine = row >= lo && row < hi;
+  const float *po = part_o + ((int64_t)h * D + warp * kCh) * rows + row;
+  for (int s = warp; s < parts; s += 8)
+    weight[s][lane] = mine ? part_lse[((int64_t)s * n_kv + h) * rows + row] : -INFINITY;
+  __syncthreads();
+  float top = -INFINITY, tot = 0.f;
+  bool nan = false;
+  for (int s = 0; s < parts; ++s) {
+    const float l = weight[s][lane];
+    nan |= l != l;
+    top = fmaxf(top, l);
+  }
+  const float ref = top == -INFINITY ? 0.f : top;
+  float acc[kCh] = {};
+  for (int s0 = 0; s0 < parts; s0 += kBatch) {       // the batch's loads all in flight
+    float v[kBatch][kCh], w[kBatch];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  nan = __any_sync(0xffffffffu, nan);
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  float w = ex2((l - ref) * 1.4426950408889634f);
-  float tot = w;
+    for (int u = 0; u < kBatch; ++u) {
+      w[u] = s0 + u < parts ? ex2((weight[s0 + u][lane] - ref) * 1.4426950408889634f) : 0.f;
+      const float *src = po + (int64_t)(s0 + u) * n_kv * D * rows;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-  const float inv = tot > 0.f || nan ? 1.f / tot : 0.f;
-  w *= inv;
-  constexpr int V = D / 32;
-  float acc[V] = {};
-  for (int s0 = 0; s0 < parts; s0 += 4) {       // four parts' loads in flight
-    float v[4][V];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bool use = s0 + u < parts &&
-                       __shfl_sync(0xffffffffu, l, (s0 + u) & 31) != -INFINITY;
-      const float *src = part_o + ((s0 + u) * rows + row) * D + lane * V;
-      if (V == 4) {
-        const float4 f = use ? *reinterpret_cast<const float4 *>(src) : make_float4(0, 0, 0, 0);
-        v[u][0] = f.x, v[u][1] = f.y, v[u][V - 2] = f.z, v[u][V - 1] = f.w;
-      } else {
-        const float2 f = use ? *reinterpret_cast<const float2 *>(src) : make_float2(0, 0);
-        v[u][0] = f.x, v[u][1] = f.y;
-      }
+      for (int d = 0; d < kCh; ++d) v[u][d] = w[u] != 0.f ? src[d * rows] : 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float ws = __shfl_sync(0xffffffffu, w, (s0 + u) & 31);
-      if (s0 + u < parts) {
+    for (int u = 0; u < kBatch; ++u) {
+      tot += w[u];
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(ws, v[u][e], acc[e]);
-      }
+      for (int d = 0; d < kCh; ++d) acc[d] = fmaf(w[u], v[u][d], acc[d]);
     }
   }
-  T *dst = out + row * D + lane * V;
+  const float inv = tot > 0.f || nan ? 1.f / tot : 0.f;
 #pragma unroll
-  for (int e = 0; e < V; e += 2)
-    *reinterpret_cast<uint32_t *>(dst + e) = Elem<T>::pack(acc[e], acc[e + 1]);
-  if (lane == 0 && lse)
-    lse[row] = tot > 0.f || nan ? (ref + log2f(tot) * 0.6931471805599453f) : -INFINITY;
+  for (int d = 0; d < kCh; d += 2)
+    *reinterpret_cast<uint32_t *>(&tile[lane][warp * kCh + d]) =
+        Elem<T>::pack(acc[d] * inv, acc[d + 1] * inv);
+  const int64_t heads = (int64_t)n_kv * group;
+  if (warp == 0 && mine && lse)
+    lse[row / group * heads + (int64_t)h * group + row % group] =
+        tot > 0.f || nan ? ref + log2f(tot) * 0.6931471805599453f : -INFINITY;
+  __syncthreads();
+  constexpr int kVec = D / 8;            // 16-byte pieces of a row
+  for (int i = threadIdx.x; i < 32 * kVec; i += 256) {
+    const int64_t r = row0 + i / kVec;
+    if (r < lo || r >= hi) continue;
+    const int64_t at = r / group * heads + (int64_t)h * group + r % group;
+    *reinterpret_cast<uint4 *>(out + at * D + (i % kVec) * 8) =
+        *reinterpret_cast<const uint4 *>(&tile[i / kVec][(i % kVec) * 8]);
+  }
 }
 
 template <typename T, int D, bool kNarrow>
@@ -1026,12 +1084,12 @@ extern "C" CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix
   P.part_o = part_o + p.pre.splits * rows * s.dim;
   P.part_lse = part_lse + p.pre.splits * rows;
   if ((st = run_part(s, c, P, p.own, cs)) != CSA2_OK) return st;
-  const int64_t grid = (rows + 7) / 8;
-  if (grid > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
+  const int64_t blocks = ((int64_t)b->num_q * s.group + 31) / 32;
+  if (blocks > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
   auto merge = [&](auto *o, auto dim_c) {
     merge_kernel<std::remove_pointer_t<decltype(o)>, decltype(dim_c)::value>
-        <<<(int)grid, 256, 0, cs>>>(part_o, part_lse, parts, b->num_q, s.n_heads, b->cu_q,
-                                    b->num_req, o, lse);
+        <<<dim3((unsigned)blocks, (unsigned)s.n_kv), 256, 0, cs>>>(
+            part_o, part_lse, parts, b->num_q, s.n_kv, s.group, b->cu_q, b->num_req, o, lse);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
