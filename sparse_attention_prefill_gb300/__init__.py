@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -481,6 +482,7 @@ def sparse_swa_attn_fp4kv(batch, q, kv_fp4, kv_sf, idx, swa_fp8, swa_scale, win_
 
 _DTYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16}
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_EVICT_BUF = struct.Struct("=QQ7q")
 
 
 def _arg(t, dtype, name, numel, dev):
@@ -688,8 +690,7 @@ def csa2_evict_rows(num_req, n_heads, idx, keep, new_len, src_start, dst_start, 
     num_req, keep, dev = int(num_req), int(keep), idx.get_device()
     ip = _arg(idx, _I32, "idx", num_req * n_heads * keep, dev)
     # csa2_evict_buf is nine 64-bit fields
-    arr = (C.c_int64 * (9 * max(1, len(bufs))))(*[x for s, d in bufs
-                                                  for x in _evict_buf(s, d, n_heads, dev)])
+    arr = b"".join([_EVICT_BUF.pack(*_evict_buf(s, d, n_heads, dev)) for s, d in bufs])
     return _call(dev, load().csa2_evict_rows,
                  (num_req, int(n_heads), ip, keep, _arg(new_len, _I64, "new_len", num_req, dev),
                   _arg(src_start, _I64, "src_start", num_req, dev),

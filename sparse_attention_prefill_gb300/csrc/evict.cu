@@ -409,6 +409,10 @@ extern "C" CSA2_API int csa2_evict_select(int32_t num_req, int32_t n_heads,
               sink,    recent,  idx,      new_len, d_err};
   constexpr int kSmem = kHeld * 4;
   allow_smem<evict_select_kernel>(kSmem);
+  if (nc == 1) {                  // a plain launch costs the host less
+    evict_select_kernel<<<(unsigned)pairs, kSelThreads, kSmem, as_stream(stream)>>>(P);
+    return launch_status();
+  }
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
