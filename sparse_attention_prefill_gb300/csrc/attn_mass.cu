@@ -24,13 +24,13 @@
 // quarters of one tile they idled during its barrier and TMEM load (1400
 // cycles a tile).
 //
-// Roles (23 warps, one CTA per SM, persistent over items):
+// Roles (24 warps, one CTA per SM, persistent over items):
 //   0-15       weights: warp w reads TMEM sub-partition w % 4 (keys 32(w % 4)
 //              .. + 31 of a tile) of buffer w / 4
-//   16         TMEM; issues the products
-//   17         K and Q tiles by TMA
-//   18         looks items up, 32 at a time, and publishes them a few ahead
-//   19-22      -lse of the query tiles, a warp to a buffer, so that four tiles'
+//   16, 17     issue the products in turn (16: TMEM)
+//   18         K and Q tiles by TMA
+//   19         looks items up, 32 at a time, and publishes them a few ahead
+//   20-23      -lse of the query tiles, a warp to a buffer, so that four tiles'
 //              loads are under way
 // Every wait is bounded, as in the attention.
 #include "dense.cuh"
@@ -45,7 +45,8 @@ constexpr int kItems = 8;           // items published ahead
 constexpr int kMaxK = 6, kMaxQ = 4; // ring stages at most
 constexpr int kEpiWarps = 4 * kBufs;    // a warpgroup to a buffer
 constexpr int kLseWarps = kBufs;    // a warp to a buffer
-constexpr int kMassThreads = (kEpiWarps + 3 + kLseWarps) * 32;
+constexpr int kIssueWarps = 2;
+constexpr int kMassThreads = (kEpiWarps + kIssueWarps + 2 + kLseWarps) * 32;
 
 struct MassParams {
   Seqs seqs;
@@ -72,7 +73,7 @@ struct MassItem {
 struct MassMisc {
   uint64_t k_full[kMaxK], k_empty[kMaxK], q_full[kMaxQ], q_empty[kMaxQ];
   uint64_t s_full[kBufs], s_empty[kBufs], l_full[kBufs];
-  uint64_t item_full[kItems], item_empty[kItems], grp, done;
+  uint64_t item_full[kItems], item_empty[kItems], grp, done[kIssueWarps];
   Bound bd;
   uint32_t tmem;
   MassItem item[kItems];
@@ -204,8 +205,11 @@ __device__ void load_role(const MassParams &P, uint8_t *smem, MassMisc *ms,
     drain_bar(&ms->q_full[i % P.qst], (i / P.qst) & 1);
 }
 
+// Two warps issue the products in turn (product x by warp x % 2): what one spends
+// between its products, on barriers and commits, the other's cover.  One warp
+// alone kept the tensor pipe idle for half of every 1100 cycles.
 template <typename T, int D>
-__device__ void product_role(const MassParams &P, uint8_t *smem, MassMisc *ms) {
+__device__ void product_role(const MassParams &P, uint8_t *smem, MassMisc *ms, int which) {
   constexpr uint32_t kKStage = (D / 64) * kBlk;
   const uint32_t idesc = idesc_of<T>(kTile, P.ncol, false);
   const uint32_t tmem = uniform(ms->tmem), qblk = P.ncol * 128;
@@ -224,37 +228,43 @@ __device__ void product_role(const MassParams &P, uint8_t *smem, MassMisc *ms) {
     const int nk = (keys + kTile - 1) / kTile;
     uint32_t ks = sk, kp = pk;                 // the item's K tiles
     for (int t = 0; t < nq && ok; ++t) {
+      // once a wait has run out nothing waits any more
+      ok = uniform(*(volatile int *)&ms->bd.abort) == 0;
       ks = sk, kp = pk;
-      ok = wait_all(&ms->q_full[sq], pq, &ms->bd);
       const uint64_t b = desc_add(qd, sq * P.q_stage);
-      for (int i = 0; i < nk && ok; ++i) {
-        const uint32_t sb = (t * P.span + i) % kBufs;
-        if (t == 0) ok = wait_all(&ms->k_full[ks], kp, &ms->bd);
-        ok = ok && wait_all(&ms->s_empty[sb], ((uses >> sb) & 1) ^ 1, &ms->bd);
-        uses ^= 1u << sb;
-        if (ok) {
-          fence_after_sync();
-          const uint64_t a = desc_add(kd, ks * kKStage);
-          if (elect_one()) {
+      for (int i = 0; i < nk; ++i) {
+        const int x = t * P.span + i;
+        const uint32_t sb = x % kBufs;
+        const uint64_t a = desc_add(kd, ks * kKStage);
+        // The waits by the elected lane itself, between its products.  Both
+        // warps wait for every tile, with a product of theirs on it or not:
+        // they let it go together, and neither may do so a round early.
+        if (elect_one()) {
+          if (i == 0) wait_inline(&ms->q_full[sq], pq, &ms->bd);
+          if (t == 0) wait_inline(&ms->k_full[ks], kp, &ms->bd);
+          if ((x & 1) == which) {
+            wait_inline(&ms->s_empty[sb], ((uses >> sb) & 1) ^ 1, &ms->bd);
+            fence_after_sync();
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
               mma_f16(tmem + sb * kTile, desc_add(a, (k >> 2) * kBlk + (k & 3) * 32),
                       desc_add(b, (k >> 2) * qblk + (k & 3) * 32), idesc, k > 0);
             mma_commit(&ms->s_full[sb]);
-            if (t == nq - 1) mma_commit(&ms->k_empty[ks]);
-            if (i == nk - 1) mma_commit(&ms->q_empty[sq]);
           }
-          __syncwarp();
+          if (t == nq - 1) mma_commit(&ms->k_empty[ks]);
+          if (i == nk - 1) mma_commit(&ms->q_empty[sq]);
         }
+        __syncwarp();
+        uses ^= 1u << sb;
         if (++ks == (uint32_t)P.kst) ks = 0, kp ^= 1;
       }
       if (++sq == (uint32_t)P.qst) sq = 0, pq ^= 1;
     }
     sk = ks, pk = kp;
   }
-  if (elect_one()) mma_commit(&ms->done);
+  if (elect_one()) mma_commit(&ms->done[which]);
   __syncwarp();
-  drain_bar(&ms->done, 0);
+  drain_bar(&ms->done[which], 0);
 }
 
 // The query tiles of an item that buffer (and warpgroup) `which` gets, t0, t0 +
@@ -391,8 +401,8 @@ attn_mass_kernel(MassParams P, const __grid_constant__ CUtensorMap mq,
   MassMisc *ms = reinterpret_cast<MassMisc *>(smem + P.off_misc);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kMaxK; ++i) mbar_init(&ms->k_full[i], 1), mbar_init(&ms->k_empty[i], 1);
-    for (int i = 0; i < kMaxQ; ++i) mbar_init(&ms->q_full[i], 1), mbar_init(&ms->q_empty[i], 1);
+    for (int i = 0; i < kMaxK; ++i) mbar_init(&ms->k_full[i], 1), mbar_init(&ms->k_empty[i], kIssueWarps);
+    for (int i = 0; i < kMaxQ; ++i) mbar_init(&ms->q_full[i], 1), mbar_init(&ms->q_empty[i], kIssueWarps);
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&ms->s_full[i], 1);
       mbar_init(&ms->s_empty[i], 4);
@@ -400,10 +410,10 @@ attn_mass_kernel(MassParams P, const __grid_constant__ CUtensorMap mq,
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&ms->item_full[i], 1);
-      mbar_init(&ms->item_empty[i], kEpiWarps + 2 + kLseWarps);
+      mbar_init(&ms->item_empty[i], kEpiWarps + kIssueWarps + 1 + kLseWarps);
     }
     mbar_init(&ms->grp, kEpiWarps);
-    mbar_init(&ms->done, 1);
+    for (int i = 0; i < kIssueWarps; ++i) mbar_init(&ms->done[i], 1);
     ms->bd.abort = 0;
     ms->bd.wait_ns = P.wait_ns;
     mbar_fence_init();
@@ -426,17 +436,18 @@ attn_mass_kernel(MassParams P, const __grid_constant__ CUtensorMap mq,
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
+  constexpr int kLoad = kEpiWarps + kIssueWarps;
   if (warp < kEpiWarps) {
     weight_role(P, ms);
-  } else if (warp == kEpiWarps) {
-    product_role<T, D>(P, smem, ms);
-  } else if (warp == kEpiWarps + 1) {
+  } else if (warp < kLoad) {
+    product_role<T, D>(P, smem, ms, warp - kEpiWarps);
+  } else if (warp == kLoad) {
     if ((threadIdx.x & 31) == 0) load_role<D>(P, smem, ms, &mq, &mk);
     __syncwarp();
-  } else if (warp == kEpiWarps + 2) {
+  } else if (warp == kLoad + 1) {
     schedule_role(P, smem, ms);
   } else {
-    lse_role(P, ms, warp - kEpiWarps - 3);
+    lse_role(P, ms, warp - kLoad - 2);
   }
   fence_before_sync();
   __syncthreads();
