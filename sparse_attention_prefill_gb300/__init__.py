@@ -514,7 +514,7 @@ def _rows3(t, name, dtype, dev, dim):
             raise Csa2Error("%s: expected the type, device and head size of q" % name)
         if (s2 != 1 and d > 1) or (s1 != d and h > 1):
             raise Csa2Error("%s: heads and channels must be contiguous" % name)
-    return t.data_ptr(), s0 if n > 1 else max(s0, h * d), n, h
+    return t.data_ptr(), s0 if n > 1 else h * d, n, h
 
 
 def make_packed(b, dev):
@@ -561,7 +561,14 @@ def _packed_args(packed, q, k):
     return st, dev, dt, rows, (h, kv, d, _DTYPES[dt], qp, ldq, kp, ldk)
 
 
-def _attn_args(packed, q, k, v, out, lse, want_lse, d_err):
+def _used_on(t, stream):
+    """t, allocated for the current stream, also held for `stream`."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _attn_args(packed, q, k, v, out, lse, want_lse, d_err, stream):
     """The attention calls' arguments; allocates the outputs that are None."""
     st, dev, dt, rows, shape = _packed_args(packed, q, k)
     vp, ldv, vrows, vh = _rows3(v, "v", dt, dev, shape[2])
@@ -570,12 +577,12 @@ def _attn_args(packed, q, k, v, out, lse, want_lse, d_err):
                         % (tuple(k.shape), tuple(v.shape)))
     n = st.num_q * shape[0]
     if out is None:
-        out = torch.empty(q.shape, dtype=dt, device=q.device)
+        out = _used_on(torch.empty(q.shape, dtype=dt, device=q.device), stream)
         op = out.data_ptr()
     else:
         op = _arg(out, dt, "out", n * shape[2], dev)
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+        lse = _used_on(torch.empty(q.shape[:2], dtype=_F32, device=q.device), stream)
         lp = lse.data_ptr()
     else:
         lp = _arg(lse, _F32, "lse", n, dev)
@@ -584,7 +591,8 @@ def _attn_args(packed, q, k, v, out, lse, want_lse, d_err):
 
 
 def _prompt(packed, q, k, v, sm_scale, out, lse, want_lse, d_err, stream):
-    st, dev, shape, outs, err, out, lse = _attn_args(packed, q, k, v, out, lse, want_lse, d_err)
+    st, dev, shape, outs, err, out, lse = _attn_args(packed, q, k, v, out, lse, want_lse, d_err,
+                                                        stream)
     if sm_scale is None:
         sm_scale = shape[2] ** -0.5
     return _call(dev, load().csa2_prompt_attn,
@@ -610,7 +618,8 @@ def csa2_prefix_attn_workspace(num_q, num_req, num_groups, n_heads, n_kv_heads, 
 
 def _prefix(packed, groups, q, k, v, max_kv, sm_scale, out, lse, want_lse, workspace, nbytes,
             d_err, stream):
-    st, dev, shape, outs, err, out, lse = _attn_args(packed, q, k, v, out, lse, want_lse, d_err)
+    st, dev, shape, outs, err, out, lse = _attn_args(packed, q, k, v, out, lse, want_lse, d_err,
+                                                        stream)
     if sm_scale is None:
         sm_scale = shape[2] ** -0.5
     gr = None if groups is None else make_groups(groups, dev)
@@ -619,9 +628,7 @@ def _prefix(packed, groups, q, k, v, max_kv, sm_scale, out, lse, want_lse, works
                                             gr.num_groups, *shape[:3], 0 if gr is None else
                                             gr.max_prefix, max_kv)
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            workspace = _used_on(torch.empty(nbytes, dtype=torch.uint8, device=q.device), stream)
         else:
             nbytes = max(nbytes, workspace.numel())
     return _call(dev, load().csa2_prefix_attn,
@@ -725,7 +732,8 @@ def attn_mass(packed, q, k, lse, max_kv, sm_scale=None, mass_in=None, mass=None,
     rows], added to ``mass_in`` if given.  ``mass`` may be ``mass_in``; rows of
     no request keep their values (zeros, where it is allocated here)."""
     if mass is None:
-        mass = torch.zeros((k.shape[1], k.shape[0]), dtype=torch.float32, device=q.device)
+        with torch.cuda.stream(stream):       # zeroed in front of the call
+            mass = torch.zeros((k.shape[1], k.shape[0]), dtype=torch.float32, device=q.device)
     if sm_scale is None:
         sm_scale = q.shape[2] ** -0.5
     _check(csa2_attn_mass(packed, q, k, lse, max_kv, sm_scale, mass_in, mass, d_err, stream),
@@ -740,9 +748,10 @@ def evict_select(kv_start, kv_len, mass, keep, sink=0, recent=0, idx=None, new_l
     mass is [heads, rows]; returns (idx [R, heads, keep], new_len [R])."""
     r, h = int(kv_len.shape[0]), int(mass.shape[0])
     if idx is None:
-        idx = torch.empty((r, h, int(keep)), dtype=torch.int32, device=mass.device)
+        idx = _used_on(torch.empty((r, h, int(keep)), dtype=torch.int32, device=mass.device),
+                       stream)
     if new_len is None:
-        new_len = torch.empty(r, dtype=torch.int64, device=mass.device)
+        new_len = _used_on(torch.empty(r, dtype=torch.int64, device=mass.device), stream)
     _check(csa2_evict_select(r, kv_start, kv_len, mass, keep, sink, recent, idx, new_len, d_err,
                              stream), "csa2_evict_select")
     return idx, new_len

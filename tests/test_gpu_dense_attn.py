@@ -182,7 +182,9 @@ def test_prefix_groups(heads, kv, dim, dtype):
 
 @pytest.mark.parametrize("reqs,heads,kv,dim,prefix,hint", [
     (1, 8, 1, 128, 1, 1), (1, 8, 8, 64, 20000, 20000), (40, 16, 2, 128, 3001, 3001),
-    (300, 8, 8, 64, 130, 130), (9, 64, 8, 128, 5000, 10), (33, 5, 1, 64, 700, 100000)])
+    (300, 8, 8, 64, 130, 130), (9, 64, 8, 128, 5000, 10), (33, 5, 1, 64, 700, 100000),
+    (12, 16, 1, 128, 900, 900), (20, 24, 2, 64, 900, 900), (7, 34, 2, 128, 300, 300),
+    (6, 128, 1, 64, 500, 500)])
 def test_prefix_decode(reqs, heads, kv, dim, prefix, hint):
     """Decode batches of one group; max_prefix and max_kv only steer the splits."""
     rows = [1 + (37 * i) % 400 for i in range(reqs)]
@@ -206,6 +208,74 @@ def test_decode_without_groups(reqs, m):
     for r in range(0, reqs, max(1, reqs // 7)):
         ref, n = _ref(q, k, v, cu, start, [1] * reqs, rows, r, 128 ** -0.5)
         R.check_attention(out[r:r + 1], lse[r:r + 1], ref, HF, n)
+
+
+@pytest.mark.parametrize("heads,kv", [(8, 1), (12, 1), (40, 2)])
+def test_decode_strided_cache_and_uneven_tokens(heads, kv):
+    """An interleaved cache, requests of no, one, two and three tokens (not a
+    token each, though as many as requests), rows in front and behind."""
+    new, rows = [2, 0, 1, 0, 3, 0], [2, 40, 300, 7, 65, 1]
+    b, cu, start, q, k, v = _inputs(new, rows, heads, kv, 128, BF, seed=heads, lead=0, tail=0)
+    c = torch.stack([k, v], 1)
+    for call in (lambda k, v: S.prompt_attn(b, q, k, v),
+                 lambda k, v: S.prefix_attn(b, None, q, k, v, 300)):
+        out, lse = call(c[:, 0], c[:, 1])
+        for r in range(len(new)):
+            if new[r]:
+                ref, n = _ref(q, k, v, cu, start, new, rows, r, 128 ** -0.5)
+                R.check_attention(out[cu[r]:cu[r + 1]], lse[cu[r]:cu[r + 1]], ref, BF, n)
+
+
+@pytest.mark.parametrize("n", [1, 3, 300])
+def test_rows_past_two_to_the_32_bytes(n):
+    """Requests at the end of pools whose byte offsets pass 32 bits."""
+    kv, dim, m, pool = 8, 128, 333, (1 << 21) + 5000
+    k = torch.empty((pool, kv, dim), dtype=BF, device=DEV)
+    v = torch.empty((pool, kv, dim), dtype=BF, device=DEV)
+    start = pool - m
+    k[start:] = torch.randn((m, kv, dim), device=DEV).to(BF)
+    v[start:] = torch.randn((m, kv, dim), device=DEV).to(BF)
+    q = torch.randn((n, 16, dim), device=DEV).to(BF)
+    b, cu = R.batch([n], [m], [start], DEV)
+    ref, keys = _ref(q, k, v, cu, [start], [n], [m], 0, dim ** -0.5)
+    for out, lse in (S.prompt_attn(b, q, k, v), S.prefix_attn(b, None, q, k, v, m)):
+        R.check_attention(out, lse, ref, BF, keys)
+    mass = torch.zeros((kv, pool), device=DEV)
+    S.attn_mass(b, q, k, lse, m, mass=mass)
+    w, tol = R.mass(q, k[start:], lse, dim ** -0.5, m - n + torch.arange(n, device=DEV))
+    assert ((mass[:, start:].double() - w).abs() <= tol + w * 2.0 ** -22 + 1e-30).all()
+    assert (mass[:, :start] == 0).all()
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    """Two shared-prefix calls on two streams, replayed from one graph."""
+    args = []
+    for seed in (1, 2):
+        rows = [100 + 50 * seed] * 20
+        b, cu, start, q, k, v = _inputs([1] * 20, rows, 16, 2, 128, BF, seed=seed, extra=[2000])
+        gr = dict(num_groups=1, cu_group=torch.tensor([0, 20], dtype=torch.int32, device=DEV),
+                  prefix_start=torch.tensor(start[-1:], device=DEV),
+                  prefix_len=torch.tensor([2000], device=DEV), max_prefix=2000)
+        need = S.csa2_prefix_attn_workspace(20, 20, 1, 16, 2, 128, 2000, 200)
+        ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+        args.append((b, gr, q, k, v, 200, ws))
+    want = [S.prefix_attn(*a[:6], workspace=a[6]) for a in args]
+    got = [tuple(torch.empty_like(x) for x in w) for w in want]
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        S.prefix_attn(*args[0][:6], workspace=args[0][6], out=got[0][0], lse=got[0][1])
+        S.prefix_attn(*args[1][:6], workspace=args[1][6], out=got[1][0], lse=got[1][1],
+                      stream=side)
+        main.wait_stream(side)
+    for _ in range(3):
+        for g in got:
+            g[0].zero_(), g[1].zero_()
+        graph.replay()
+        for w, g in zip(want, got):
+            assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1])
 
 
 def test_prefix_bad_groups_are_flagged():

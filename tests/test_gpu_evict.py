@@ -66,6 +66,17 @@ def test_mass_decode(reqs, m, heads, kv):
     assert abs(float(mass.double().sum()) - reqs * heads) <= 1e-4 * reqs * heads
 
 
+@pytest.mark.parametrize("hint", [0, 40, 10 ** 9])
+def test_mass_hint_only_steers_the_grid(hint):
+    """Many rows and windows of queries, one, two and four key tiles an item."""
+    rows = [2000 + 700 * i for i in range(8)]
+    b, cu, start, q, k, v = _inputs([70] * 8, rows, 32, 8, 64, BF, seed=4)
+    _, lse = S.prompt_attn(b, q, k, v)
+    mass = S.attn_mass(b, q, k, lse, hint)
+    _check_mass(b, cu, start, q, k, [70] * 8, rows, 64 ** -0.5, lse, mass, None, 0.0)
+    assert torch.equal(mass, S.attn_mass(b, q, k, lse, hint))
+
+
 def test_mass_counts_lse_of_a_joint_softmax_and_skips_empty_rows():
     """lse from elsewhere; -inf adds nothing though the row sees keys."""
     b, cu, start, q, k, _ = _inputs([6], [200], 4, 2, 64, BF, seed=2)
@@ -208,6 +219,27 @@ def test_rows_move(dim, dtype, heads, in_place):
             for h in range(heads):
                 want[to[r]:to[r] + m, h] = x[start[r] + idx[r, h, :m].long(), h]
         assert torch.equal(y, want)
+
+
+def test_rows_interleaved_cache_in_place_on_a_side_stream():
+    """K and V as views of one buffer, closed up in place on another stream."""
+    rows, keep, heads = [900, 300], 128, 4
+    start, pool = R.starts(rows)
+    i64 = lambda x: torch.tensor(x, dtype=torch.int64, device=DEV)    # noqa: E731
+    c = torch.randn((pool, 2, heads, 64), device=DEV).to(BF)
+    c0 = c.clone()
+    mass = torch.rand((heads, pool), device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    st = i64(start)
+    idx, new_len = S.evict_select(st, i64(rows), mass, keep, 1, 1, stream=side)
+    S.evict_rows(idx, new_len, st, st, [(c[:, 0], c[:, 0]), (c[:, 1], c[:, 1])], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    want = c0.clone()
+    for r, s in enumerate(start):
+        for h in range(heads):
+            want[s:s + keep, :, h] = c0[s + idx[r, h].long(), :, h]
+    assert torch.equal(c, want)
 
 
 def test_rows_bad_indices_are_flagged():
