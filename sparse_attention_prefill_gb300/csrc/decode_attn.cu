@@ -78,10 +78,9 @@ struct Shared {
   float ref[kWarps][8 * kN], sum[kWarps][8 * kN];
 };
 
-// The run that holds query row `token`, by a warp: the guess if it does.
-__device__ int run_of(const Seqs &S, int token, int guess, int &err) {
+// The run that holds query row `token`, by a warp.
+__device__ int run_of(const Seqs &S, int token, int &err) {
   const int lane = threadIdx.x & 31;
-  if (guess < S.count && S.cu_q[guess] <= token && token < S.cu_q[guess + 1]) return guess;
   for (int i0 = 0; i0 < S.count; i0 += 32) {
     int q0 = 0, n = 0;
     if (i0 + lane < S.count) seq_rows(S, i0 + lane, q0, n, err);
@@ -101,22 +100,25 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
   const int ns = P.splits > 0 ? P.splits : 1;
   const int split = blockIdx.x % ns, h = blockIdx.x / ns % P.n_kv, slot = blockIdx.x / ns / P.n_kv;
   const Seqs &S = P.seqs;
-  // token `slot` of the sequences
+  // Token `slot` of the sequences and its run.  In a batch of single tokens that
+  // is run `slot`: everything of it is asked for at once.
   int err = 0;
-  const int first = S.cu_q[0], token = first + slot;
-  if (first < 0 || token >= S.num_q || token >= S.cu_q[S.count]) {
+  const int first = S.cu_q[0], behind = S.cu_q[S.count], token = first + slot;
+  int run = min(slot, S.count - 1);
+  int q0 = S.cu_q[run], n = S.cu_q[run + 1] - q0;
+  int64_t start = S.kv_start[run], m = S.kv_len[run];
+  if (first < 0 || token >= S.num_q || token >= behind) {
     if (first < 0 && threadIdx.x == 0) raise_err(P.d_err, CSA2_DERR_BAD_EXTEND);
     return;
   }
-  const int run = run_of(S, token, slot, err);
-  int q0 = 0, n = 0;
-  int64_t start = 0, m = 0;
-  if (run >= 0) {
-    seq_rows(S, run, q0, n, err);
-    seq_keys(S, run, start, m, err);
+  if (token < q0 || token - q0 >= n || q0 < 0 || n > S.num_q - q0) {
+    run = run_of(S, token, err);
+    if (run >= 0) seq_rows(S, run, q0, n, err);
   }
+  if (run >= 0) seq_keys(S, run, start, m, err);
+  err = __reduce_or_sync(0xffffffffu, err);
   if (err && lane == 0 && warp == 0) raise_err(P.d_err, err);
-  if (run < 0 || n == 0) return;
+  if (run < 0) return;
   const int64_t last = m - n + (token - q0);           // keys seen: 0 .. last
   const int keys = last < 0 ? 0 : (int)last + 1;
   // Q's fragments; rows past the group's heads are zeros
@@ -262,7 +264,7 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
   __syncthreads();
   const bool uncovered =
       P.cover && split == 0 && !in_groups(P.cover, P.n_cover, run, S.num_req);
-  // a result's rows are channel-innermost, a partial result's row-innermost
+  // a result's rows are channel-innermost, a partial result's blocks row-innermost
   const bool part = P.splits > 0;
   constexpr int kRows = 8 * kN, kTeam = kWarps * 32 / kRows;       // threads of a row
   const int row = part ? threadIdx.x % kRows : threadIdx.x / kTeam;
@@ -281,21 +283,21 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
   const float inv = seen ? 1.f / tot : 0.f;
   const float lse = seen ? (base + log2f(tot)) * 0.6931471805599453f : -INFINITY;
   if (part) {
-    const int64_t rows = (int64_t)S.num_q * P.group, at = (int64_t)token * P.group + row;
+    const int64_t rows = part_rows(S.num_q, P.group), at = (int64_t)token * P.group + row;
     if (col == 0) {
-      P.part_lse[((int64_t)split * P.n_kv + h) * rows + at] = lse;
+      P.part_lse[part_stat(rows, P.n_kv, split, h, at)] = lse;
       if (uncovered)
         for (int i = 0; i < P.cover_splits; ++i)
-          P.cover_lse[((int64_t)i * P.n_kv + h) * rows + at] = -INFINITY;
+          P.cover_lse[part_stat(rows, P.n_kv, i, h, at)] = -INFINITY;
     }
     if (!seen) return;
-    float *dst = P.part_o + ((int64_t)split * P.n_kv + h) * D * rows + at;
+    float *dst = P.part_o + part_elem(rows, P.n_kv, D, split, h, at);
 #pragma unroll 4
     for (int d = col; d < D; d += kTeam) {
       float f = 0.f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) f = fmaf(w[i], sh.o[i][row][d], f);
-      dst[d * rows] = f * inv;
+      dst[d * 32] = f * inv;
     }
   } else {
     const int64_t at = (int64_t)token * P.n_heads + h * P.group + row;

@@ -51,8 +51,7 @@ struct AttnParams {
   Seqs seqs;
   int n_heads, n_kv, group, tpt, causal;
   int splits;        // of the key range; 0: the output itself is written
-  float *part_o;     // [splits, n_kv, D, num_q * group]: packed rows innermost,
-  float *part_lse;   // [splits, n_kv, num_q * group]: so that lanes store neighbours
+  float *part_o, *part_lse;      // partial results (dense.cuh)
   float scale_log2;
   void *out;         // [num_q, n_heads, D]
   float *lse;        // [num_q, n_heads] or null
@@ -661,16 +660,16 @@ __device__ bool softmax_item(const AttnParams &P, M *ms, const Item &it, int t, 
   const float lse =
       seen ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
   if (P.splits > 0) {
-    const int64_t rows = (int64_t)P.seqs.num_q * P.group;
+    const int64_t rows = part_rows(P.seqs.num_q, P.group);
     const int64_t at = (int64_t)(it.q0 + i) * P.group + x % P.group;
     if (valid) {
-      P.part_lse[((int64_t)it.split * P.n_kv + it.h) * rows + at] = lse;
+      P.part_lse[part_stat(rows, P.n_kv, it.split, it.h, at)] = lse;
       if (it.uncovered && it.split == 0)
         for (int s = 0; s < P.cover_splits; ++s)
-          P.cover_lse[((int64_t)s * P.n_kv + it.h) * rows + at] = -INFINITY;
+          P.cover_lse[part_stat(rows, P.n_kv, s, it.h, at)] = -INFINITY;
     }
     if (rows_here && any) {
-      float *dst = P.part_o + ((int64_t)it.split * P.n_kv + it.h) * D * rows + at;
+      float *dst = P.part_o + part_elem(rows, P.n_kv, D, it.split, it.h, at);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -687,7 +686,7 @@ __device__ bool softmax_item(const AttnParams &P, M *ms, const Item &it, int t, 
         }
         if (valid && seen) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) dst[(32 * c + e) * rows] = f[e];
+          for (int e = 0; e < 32; ++e) dst[(32 * c + e) * 32] = f[e];
         }
       }
     }
@@ -790,25 +789,25 @@ dense_attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ 
 
 // Joins the parts of a row: lse = ln sum_s e^{lse_s}, out = sum_s
 // e^{lse_s - lse} out_s.  A block has 32 packed rows of a key head, a lane to a
-// row, a warp to an eighth of the channels; parts without keys (-inf) are not
+// row, a warp to a sixteenth of the channels; parts without keys (-inf) are not
 // read.  Rows in front of or behind the sequences are left.
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
 merge_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse, int parts,
              int num_q, int n_kv, int group, const int32_t *__restrict__ cu_q, int num_req,
              T *__restrict__ out, float *__restrict__ lse) {
-  constexpr int kCh = D / 8;
-  constexpr int kBatch = 3;
+  constexpr int kCh = D / 16, kBatch = 4;
   __shared__ __align__(16) T tile[32][D + 8];
   __shared__ float weight[2 * kMaxSplits][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
-  const int64_t rows = (int64_t)num_q * group, row0 = (int64_t)blockIdx.x * 32;
-  const int64_t lo = (int64_t)cu_q[0] * group, hi = min(rows, (int64_t)cu_q[num_req] * group);
+  const int64_t rows = part_rows(num_q, group), row0 = (int64_t)blockIdx.x * 32;
+  const int64_t lo = (int64_t)cu_q[0] * group;
+  const int64_t hi = (int64_t)min(num_q, cu_q[num_req]) * group;
   const int64_t row = row0 + lane;
   const bool mine = row >= lo && row < hi;
-  const float *po = part_o + ((int64_t)h * D + warp * kCh) * rows + row;
-  for (int s = warp; s < parts; s += 8)
-    weight[s][lane] = mine ? part_lse[((int64_t)s * n_kv + h) * rows + row] : -INFINITY;
+  const float *po = part_o + part_elem(rows, n_kv, D, 0, h, row) + warp * kCh * 32;
+  for (int s = warp; s < parts; s += 16)
+    weight[s][lane] = mine ? part_lse[part_stat(rows, n_kv, s, h, row)] : -INFINITY;
   __syncthreads();
   float top = -INFINITY, tot = 0.f;
   bool nan = false;
@@ -824,9 +823,9 @@ merge_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ls
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       w[u] = s0 + u < parts ? ex2((weight[s0 + u][lane] - ref) * 1.4426950408889634f) : 0.f;
-      const float *src = po + (int64_t)(s0 + u) * n_kv * D * rows;
+      const float *src = po + (int64_t)(s0 + u) * n_kv * rows * D;
 #pragma unroll
-      for (int d = 0; d < kCh; ++d) v[u][d] = w[u] != 0.f ? src[d * rows] : 0.f;
+      for (int d = 0; d < kCh; ++d) v[u][d] = w[u] != 0.f ? src[d * 32] : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -846,7 +845,7 @@ merge_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ls
         tot > 0.f || nan ? ref + log2f(tot) * 0.6931471805599453f : -INFINITY;
   __syncthreads();
   constexpr int kVec = D / 8;            // 16-byte pieces of a row
-  for (int i = threadIdx.x; i < 32 * kVec; i += 256) {
+  for (int i = threadIdx.x; i < 32 * kVec; i += 512) {
     const int64_t r = row0 + i / kVec;
     if (r < lo || r >= hi) continue;
     const int64_t at = r / group * heads + (int64_t)h * group + r % group;
@@ -976,7 +975,7 @@ int run_part(const Shape &s, const Cache &c, AttnParams &P, const PartPlan &p, c
 }
 
 int64_t plan_bytes(const PrefixPlan &p, int64_t num_q, const Shape &s) {
-  return (int64_t)(p.pre.splits + p.own.splits) * num_q * s.n_heads * (s.dim + 4) * 4 + 256;
+  return (p.pre.splits + p.own.splits) * part_rows(num_q, s.group) * s.n_kv * (s.dim + 1) * 4;
 }
 
 }  // namespace
@@ -1054,7 +1053,7 @@ extern "C" CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix
   if ((uintptr_t)workspace & 255u) return CSA2_ERR_UNSUPPORTED;
   const cudaStream_t cs = csa2::as_stream(stream);
   const int parts = p.pre.splits + p.own.splits;
-  const int64_t rows = (int64_t)b->num_q * s.n_heads;
+  const int64_t rows = part_rows(b->num_q, s.group) * s.n_kv;
   float *part_o = static_cast<float *>(workspace);
   float *part_lse = part_o + parts * rows * s.dim;
   AttnParams P{};
@@ -1084,11 +1083,11 @@ extern "C" CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix
   P.part_o = part_o + p.pre.splits * rows * s.dim;
   P.part_lse = part_lse + p.pre.splits * rows;
   if ((st = run_part(s, c, P, p.own, cs)) != CSA2_OK) return st;
-  const int64_t blocks = ((int64_t)b->num_q * s.group + 31) / 32;
+  const int64_t blocks = part_rows(b->num_q, s.group) / 32;
   if (blocks > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
   auto merge = [&](auto *o, auto dim_c) {
     merge_kernel<std::remove_pointer_t<decltype(o)>, decltype(dim_c)::value>
-        <<<dim3((unsigned)blocks, (unsigned)s.n_kv), 256, 0, cs>>>(
+        <<<dim3((unsigned)blocks, (unsigned)s.n_kv), 512, 0, cs>>>(
             part_o, part_lse, parts, b->num_q, s.n_kv, s.group, b->cu_q, b->num_req, o, lse);
   };
   using D64 = std::integral_constant<int, 64>;

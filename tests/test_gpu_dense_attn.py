@@ -247,6 +247,28 @@ def test_rows_past_two_to_the_32_bytes(n):
     assert (mass[:, :start] == 0).all()
 
 
+def test_decode_bad_requests_are_flagged():
+    rows = [20, 60, 25]
+    b, cu, start, q, k, v = _inputs([1, 1, 1], rows, 8, 2, 128, BF)
+    good, _ = S.prompt_attn(b, q, k, v)
+    i64 = lambda x: torch.tensor(x, dtype=torch.int64, device=DEV)    # noqa: E731
+    for bad in (dict(kv_start=b["kv_start"] + i64([0, 10 ** 9, 0])),
+                dict(kv_len=b["kv_len"] * i64([1, -1, 1]))):
+        for call in (lambda b, d: S.prompt_attn(b, q, k, v, d_err=d),
+                     lambda b, d: S.prefix_attn(b, None, q, k, v, 60, d_err=d)):
+            d = _derr()
+            out, lse = call(dict(b, **bad), d)
+            assert int(d.item()) == S.DERR_RANGE_ROW
+            assert (out[1] == 0).all() and (lse[1] == -math.inf).all()
+            assert torch.allclose(out[::2].float(), good[::2].float(), atol=2 ** -6)
+    for cu_bad in ([0, 1, 10 ** 9, 3], [0, 2, 1, 3], [-1, 1, 2, 3], [0, 1, 2, 4],
+                   [0, -5, 2, 3]):
+        d = _derr()
+        S.prompt_attn(dict(b, cu_q=torch.tensor(cu_bad, dtype=torch.int32, device=DEV)), q, k, v,
+                      d_err=d)
+        assert int(d.item()) == S.DERR_BAD_EXTEND, cu_bad
+
+
 def test_two_calls_at_once_with_a_workspace_each():
     """Two shared-prefix calls on two streams, replayed from one graph."""
     args = []
