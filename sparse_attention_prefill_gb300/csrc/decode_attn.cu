@@ -93,6 +93,9 @@ __device__ int run_of(const Seqs &S, int token, int &err) {
 template <typename T, int D, int kN>
 __global__ void __launch_bounds__(kWarps * 32, kN == 2 ? 2 : D == 128 ? 3 : 4)
 decode_attn_kernel(const __grid_constant__ DecodeParams P) {
+  // a kernel launched with launch_behind may start on the SMs that the last items
+  // leave (every item has started by then)
+  asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(16) uint8_t smem[];
   Shared<D, kN> &sh = *reinterpret_cast<Shared<D, kN> *>(smem);
   constexpr int kQ = D / 32, kJ = D / 64;

@@ -320,6 +320,31 @@ inline int check_packed(const csa2_packed *b, int32_t n_heads, int32_t n_kv_head
   return CSA2_OK;
 }
 
+// Launches a kernel; with `early` it may start before the kernel in front of it
+// in the stream has ended, and must wait for that itself (wait_front).
+template <typename... A, typename... B>
+int launch_behind(void (*f)(A...), dim3 grid, int threads, int smem, bool early, cudaStream_t st,
+                  const B &...args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = early ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, f, A(args)...);
+  return launch_status();
+}
+
+// Waits for the kernel in front and all that it wrote; returns at once in a
+// kernel that was not launched early.
+__device__ __forceinline__ void wait_front() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Single tokens over their own rows (decode_attn.cu): groups of at most
 // kDecodeGroup heads; results or partial results as in dense_attn.cu.
 constexpr int kDecodeGroup = 16;
