@@ -8,6 +8,13 @@ short names (``tail_layout``, ``index_score``, ``topk``, ``topk_candidates``,
 ``csa2_*`` function.  Every step of the layer runs in the library's CUDA
 kernels; there is no CPU or PyTorch fallback: if the library cannot be loaded
 or no GPU is present, the calls raise.
+
+Dense caches (plain K and V rows of bf16 or f16, shared by groups of heads) have
+``prompt_attn``, ``prefix_attn``, ``attn_mass``, ``evict_select`` and
+``evict_rows``.  They take a packed batch as a dict: ``num_q``, ``num_req`` and
+the device tensors ``cu_q`` [R+1] int32, ``kv_start`` and ``kv_len`` [R] int64;
+and groups that share prefixes as a dict of ``num_groups``, ``max_prefix`` and
+``cu_group`` [G+1] int32, ``prefix_start`` and ``prefix_len`` [G] int64.
 """
 from __future__ import annotations
 

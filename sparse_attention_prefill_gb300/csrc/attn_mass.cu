@@ -12,17 +12,19 @@
 // lanes).
 //
 // Per item the kernel reads its K tiles once and every query tile once (from
-// L2, where a request's queries stay).  A decode step is bound by the K rows,
-// a window of queries by the exponentials (512 cycles of the special-function
-// units to a 128 x 128 tile, as long as its product takes).  Products and
-// weights rotate over four S^T buffers and four warpgroups: product number x
+// L2, where a request's queries stay).  A decode step is bound by the K rows
+// (61 requests of 3,500 rows on average: 72.8 us, 6.2 TB/s).  A window of
+// queries is bound by shared memory: of some 1,100 cycles to a 128 x 128 tile
+// the product's operands take 512, the reads of -lse' 375, the copies the rest;
+// the exponentials take 512 of their own unit (eight requests of 128 queries
+// over 2,700 rows on average, 64 heads: 54.8 us).  Products and weights rotate over four S^T buffers and four warpgroups: product number x
 // of an item (query tile by query tile, the item's key tiles within) goes to
 // buffer and warpgroup x % 4.  With four key tiles to an item a warpgroup has
 // a key tile to itself; with two or one (few items) 2 or 4 warpgroups share
 // one and add up at its end.  Different warpgroups are at different places of
 // their tiles, which keeps the exponential units busy: with all four on
-// quarters of one tile they idled during its barrier and TMEM load (1400
-// cycles a tile).
+// quarters of one tile they idled during its barrier and TMEM load (63 us for
+// the same window; two warpgroups of twice the registers took 75).
 //
 // Roles (24 warps, one CTA per SM, persistent over items):
 //   0-15       weights: warp w reads TMEM sub-partition w % 4 (keys 32(w % 4)
