@@ -300,6 +300,44 @@ def test_two_calls_at_once_with_a_workspace_each():
             assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1])
 
 
+@pytest.mark.parametrize("grouped", [True, False])
+def test_calls_in_a_row_keep_the_stream_order(grouped):
+    """The call's kernels overlap one another, but nothing in front of the call
+    or behind it: inputs written just before and just after, one workspace."""
+    reqs, heads, kv, dim, prefix = 40, 32, 4, 128, 2500
+    rows = [(37 * i) % 400 + 1 for i in range(reqs)]
+    b, _, start, q, k, v = _inputs([1] * reqs, rows, heads, kv, dim, BF, extra=[prefix])
+    groups = dict(num_groups=1, max_prefix=prefix,
+                  cu_group=torch.tensor([0, reqs - 3], dtype=torch.int32, device=DEV),
+                  prefix_start=torch.tensor([start[-1]], dtype=torch.int64, device=DEV),
+                  prefix_len=torch.tensor([prefix], dtype=torch.int64, device=DEV))
+    g = groups if grouped else None
+    g0 = torch.Generator(device=DEV).manual_seed(5)
+    qs = [torch.randn(q.shape, generator=g0, device=DEV).to(BF) for _ in range(12)]
+    ks = [k + i for i in range(3)]
+    want = []
+    for i, x in enumerate(qs):
+        want.append(S.prefix_attn(b, g, x, ks[i % 3], v, max(rows)))
+        torch.cuda.synchronize()
+    n = S.csa2_prefix_attn_workspace(reqs, reqs, 1 if grouped else 0, heads, kv, dim,
+                                     prefix if grouped else 0, max(rows))
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV)
+    qb, kb = torch.empty_like(q), torch.empty_like(k)
+    got = []
+    for i, x in enumerate(qs):
+        qb.copy_(x)
+        kb.copy_(ks[i % 3])
+        S.prefix_attn(b, g, qb, kb, v, max(rows), out=out, lse=lse, workspace=ws)
+        qb.fill_(math.nan)
+        kb.fill_(math.nan)
+        got.append((out.clone(), lse.clone()))
+        out.fill_(9.0)
+        ws.fill_(255)
+    for (o, l), (wo, wl) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
 def test_prefix_bad_groups_are_flagged():
     new, rows = [1, 1, 1], [30, 40, 50]
     b, cu, start, q, k, v = _inputs(new, rows, 4, 2, 64, BF, extra=[200])
