@@ -20,8 +20,8 @@
 // With the rows as the wide operand (16 of them, half unused by groups of 8)
 // the output took 64 registers a thread instead of 32, and what that spilled
 // were the loads: 143 us for 256 requests x 8 key heads x 512 rows.  Now rows of
-// 731 MB take 130 us (5.6 TB/s; an SM asks for at most 96 KB at a time).  The
-// next block's K is asked for as soon as S is done, its V once O is.
+// 731 MB take 131 us (5.6 TB/s).  The next block's K is asked for as soon as S
+// is done, its V once O is.
 //
 // (On the tcgen05 path of dense_attn.cu a decode item is a chain of copies,
 // products of 128 rows with G of them in use, barriers and a TMEM epilogue:
@@ -159,6 +159,17 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
       for (int j = 0; j < kJ; ++j) vr[u][j] = ld_stream(p + j * 64);
     }
   };
+  // The block after the next, for which there are no registers yet: into L2, a
+  // 128-byte line to a lane (731 MB of rows 135 -> 131 us; two blocks: 133).
+  auto prefetch = [&](int b) {
+    constexpr int kLines = D / 64;
+    if (lane < kKeys * kLines) {
+      const int64_t row = start + min(b * kKeys + lane / kLines, top_row);
+      const int64_t at = (int64_t)h * D + lane % kLines * 64;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T *>(P.k) + row * P.ldk + at));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T *>(P.v) + row * P.ldv + at));
+    }
+  };
   constexpr float kLift = Elem<T>::kBf16 ? 0.f : 8.f;    // as in dense_attn.cu
   constexpr float kMargin = Elem<T>::kBf16 ? 8.f : 7.f;
   // this thread's rows: 8 y + 2 c + r
@@ -171,6 +182,7 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
   if (b < b1) {
     load_k(b);
     load_v(b);
+    if (b + kWarps < b1) prefetch(b + kWarps);
   }
   for (; b < b1; b += kWarps) {
     // accumulator e: key g + 8 (e / 2), row 2 c + e % 2; even and odd channel
@@ -190,6 +202,7 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
     }
     const int nb = b + kWarps;
     if (nb < b1) load_k(nb);
+    if (nb + kWarps < b1) prefetch(nb + kWarps);
     if (b * kKeys + kKeys > keys) {
 #pragma unroll
       for (int y = 0; y < kN; ++y)
