@@ -524,7 +524,10 @@ typedef struct csa2_packed {
  *   lse [num_q, n_heads] fp32 or NULL
  * The weights e^{l_j} are rounded to the inputs' type for the product with v
  * (their sum is not); products accumulate in fp32.  For single tokens over
- * long caches csa2_prefix_attn without groups splits the cache among CTAs. */
+ * long caches csa2_prefix_attn without groups splits the cache among CTAs.
+ * Query rows are tiled by their mean number per request (the lengths are on
+ * the device): with many requests that have no new row, the rows of the others
+ * may be taken one by one. */
 CSA2_API int csa2_prompt_attn(const csa2_packed *b, int32_t n_heads, int32_t n_kv_heads,
                               int32_t dim, int32_t dtype, const void *q, int64_t ldq,
                               const void *k, int64_t ldk, const void *v, int64_t ldv,

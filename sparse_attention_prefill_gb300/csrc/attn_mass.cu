@@ -14,12 +14,14 @@
 // Per item the kernel reads its K tiles once and every query tile once (from
 // L2, where a request's queries stay).  A decode step is bound by the K rows
 // (61 requests of 3,500 rows on average: 72.8 us, 6.2 TB/s).  A window of
-// queries is bound by shared memory: of some 1,100 cycles to a 128 x 128 tile
-// the product's operands take 512, the reads of -lse' 375, the copies the rest;
-// the exponentials take 512 of their own unit (eight requests of 128 queries
-// over 2,700 rows on average, 64 heads: 54.8 us).  Products and weights rotate over four S^T buffers and four warpgroups: product number x
-// of an item (query tile by query tile, the item's key tiles within) goes to
-// buffer and warpgroup x % 4.  With four key tiles to an item a warpgroup has
+// queries takes some 1,200 cycles to a 128 x 128 tile (eight requests of 128
+// queries over 2,700 rows on average, 64 heads: 54.8 us), of which the product
+// and the exponentials need 512 each on units of their own: what the warps wait
+// for is their TMEM loads, beside products that use TMEM too.  (-lse' as three
+// bf16 channels of the product, instead of 128 reads of shared memory to a row,
+// took 56 us.)  Products and weights rotate over four S^T buffers and four
+// warpgroups: product number x of an item (query tile by query tile, the item's
+// key tiles within) goes to buffer and warpgroup x % 4.  With four key tiles to an item a warpgroup has
 // a key tile to itself; with two or one (few items) 2 or 4 warpgroups share
 // one and add up at its end.  Different warpgroups are at different places of
 // their tiles, which keeps the exponential units busy: with all four on
