@@ -16,10 +16,10 @@
 // (61 requests of 3,500 rows on average: 72.8 us, 6.2 TB/s).  A window of
 // queries takes some 1,200 cycles to a 128 x 128 tile (eight requests of 128
 // queries over 2,700 rows on average, 64 heads: 54.8 us), of which the product
-// and the exponentials need 512 each on units of their own: what the warps wait
-// for is their TMEM loads, beside products that use TMEM too.  (-lse' as three
-// bf16 channels of the product, instead of 128 reads of shared memory to a row,
-// took 56 us.)  Products and weights rotate over four S^T buffers and four
+// and the exponentials need 512 each on units of their own; no unit is more than
+// half busy.  (-lse' as three bf16 channels of the product, instead of reads of
+// shared memory, took 56 us; TMEM loads 16 columns ahead of their use 57.6.)
+// Products and weights rotate over four S^T buffers and four
 // warpgroups: product number x of an item (query tile by query tile, the item's
 // key tiles within) goes to buffer and warpgroup x % 4.  With four key tiles to an item a warpgroup has
 // a key tile to itself; with two or one (few items) 2 or 4 warpgroups share
