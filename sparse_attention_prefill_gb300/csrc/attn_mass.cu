@@ -19,14 +19,15 @@
 // and the exponentials need 512 each on units of their own; no unit is more than
 // half busy.  (-lse' as three bf16 channels of the product, instead of reads of
 // shared memory, took 56 us; TMEM loads 16 columns ahead of their use 57.6.)
-// Products and weights rotate over four S^T buffers and four
-// warpgroups: product number x of an item (query tile by query tile, the item's
-// key tiles within) goes to buffer and warpgroup x % 4.  With four key tiles to an item a warpgroup has
-// a key tile to itself; with two or one (few items) 2 or 4 warpgroups share
-// one and add up at its end.  Different warpgroups are at different places of
-// their tiles, which keeps the exponential units busy: with all four on
-// quarters of one tile they idled during its barrier and TMEM load (63 us for
-// the same window; two warpgroups of twice the registers took 75).
+// Products and weights rotate over four S^T buffers and four warpgroups:
+// product number x of an item (query tile by query tile, the item's key tiles
+// within) goes to buffer and warpgroup x % 4.  With four key tiles to an item
+// a warpgroup has a key tile to itself; with two or one (few items) 2 or 4
+// warpgroups share one and add up at its end.  Different warpgroups are at
+// different places of their tiles, which keeps the exponential units busy:
+// with all four on quarters of one tile they idled during its barrier and TMEM
+// load (63 us for the same window; two warpgroups of twice the registers took
+// 75).
 //
 // Roles (24 warps, one CTA per SM, persistent over items):
 //   0-15       weights: warp w reads TMEM sub-partition w % 4 (keys 32(w % 4)
