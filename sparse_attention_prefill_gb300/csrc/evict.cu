@@ -335,16 +335,17 @@ __device__ void move_rows(const MoveParams &P, const csa2_evict_buf &b, int shif
       const int64_t w = w0 + u * kMoveThreads + threadIdx.x;
       const int64_t i = shift >= 0 ? w >> shift : w / pieces;
       p[u] = (w - i * pieces) * (int64_t)sizeof(V);
-      to[u] = d0 + i;
+      to[u] = i;
       j[u] = w < total ? __ldg(idx + i) : -1;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (j[u] >= 0 && (s0 + j[u] >= b.src_rows || to[u] >= b.dst_rows)) {
+      // against what is left of the buffers: a start near 2^63 would wrap the sum
+      if (j[u] >= 0 && (j[u] >= b.src_rows - s0 || to[u] >= b.dst_rows - d0)) {
         err |= CSA2_DERR_RANGE_ROW;
         j[u] = -1;
       }
-      to[u] = to[u] * b.dst_row_stride + p[u];
+      if (j[u] >= 0) to[u] = (d0 + to[u]) * b.dst_row_stride + p[u];
       if (j[u] >= 0)
         v[u] = *reinterpret_cast<const V *>(src + (s0 + j[u]) * b.src_row_stride + p[u]);
     }
