@@ -601,7 +601,9 @@ CSA2_API int csa2_attn_mass(const csa2_packed *b, int32_t n_heads, int32_t n_kv_
  *   mass    [n_heads, kv_rows] fp32
  *   idx     [num_req, n_heads, keep] rows kept, as offsets from kv_start[r],
  *           ascending; -1 behind the last
- *   new_len [num_req] = min(m, keep)
+ *   new_len [num_req] = min(m, keep); may be kv_len itself (the lengths then
+ *           change behind the selection, in one launch more)
+ * Otherwise idx and new_len share no bytes with each other or with an input;
  * sink, recent >= 0, keep >= 1, sink + recent <= keep (CSA2_ERR_INVALID_ARG).
  * A request whose rows leave the pool keeps nothing (CSA2_DERR_RANGE_ROW). */
 CSA2_API int csa2_evict_select(int32_t num_req, int32_t n_heads, const int64_t *kv_start,

@@ -752,7 +752,8 @@ def evict_select(kv_start, kv_len, mass, keep, sink=0, recent=0, idx=None, new_l
                  d_err=None, stream=None):
     """The rows of each request and head that stay: the first ``sink``, the
     last ``recent`` and those of largest mass, ``keep`` in all, ascending.
-    mass is [heads, rows]; returns (idx [R, heads, keep], new_len [R])."""
+    mass is [heads, rows]; returns (idx [R, heads, keep], new_len [R]).
+    ``new_len`` may be ``kv_len`` itself."""
     r, h = int(kv_len.shape[0]), int(mass.shape[0])
     if idx is None:
         idx = _used_on(torch.empty((r, h, int(keep)), dtype=torch.int32, device=mass.device),

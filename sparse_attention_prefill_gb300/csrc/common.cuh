@@ -54,6 +54,12 @@ static inline void allow_smem(int bytes) {
     done.fetch_or(bit, std::memory_order_relaxed);
 }
 
+// Whether two runs of bytes share one.
+static inline bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
+  const uint64_t x = (uint64_t)(uintptr_t)a, y = (uint64_t)(uintptr_t)b;
+  return na && nb && (x < y ? y - x < na : x - y < nb);
+}
+
 // Bound on the pipeline waits of the tensor-core kernels (ns of %globaltimer),
 // read when a launch is issued; set by csa2_set_wait_limit_ns.
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;

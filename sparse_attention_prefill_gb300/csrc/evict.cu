@@ -44,7 +44,7 @@ struct SelParams {
   int64_t kv_rows;
   int keep, sink, recent;
   int32_t *idx;
-  int64_t *new_len;
+  int64_t *new_len;               // null: written behind the selection
   int32_t *d_err;
 };
 
@@ -271,7 +271,7 @@ evict_select_kernel(SelParams P) {
   }
   int32_t *idx = P.idx + pair * P.keep;
   const int64_t kept = n < P.keep ? n : P.keep;
-  if (h == 0 && rank == 0 && threadIdx.x == 0) P.new_len[r] = kept;
+  if (P.new_len && h == 0 && rank == 0 && threadIdx.x == 0) P.new_len[r] = kept;
   const int gtid = rank * kSelThreads + threadIdx.x, gn = nc * kSelThreads;
   if (n <= P.keep) {              // every row stays (the whole cluster leaves)
     for (int i = gtid; i < P.keep; i += gn) idx[i] = i < n ? i : -1;
@@ -291,6 +291,17 @@ evict_select_kernel(SelParams P) {
     select_slice<true>(P, sh, held, src, idx, lo, len, room, nc, rank);
   else
     select_slice<false>(P, sh, held, src, idx, lo, len, room, nc, rank);
+}
+
+// The lengths where new_len is kv_len itself: every CTA of the selection reads
+// kv_len[r], and threads that disagreed on it would leave others at a barrier,
+// so it changes behind the selection only.
+__global__ void evict_lengths_kernel(SelParams P, int64_t *new_len) {
+  const int r = blockIdx.x * blockDim.x + threadIdx.x;
+  if (r >= P.num_req) return;
+  const int64_t start = P.kv_start[r], n = P.kv_len[r];
+  const bool bad = n < 0 || start < 0 || start > P.kv_rows || n > P.kv_rows - start;
+  new_len[r] = bad ? 0 : n < P.keep ? n : P.keep;
 }
 
 // ---------------------------------------------------------------------------
@@ -398,6 +409,16 @@ extern "C" CSA2_API int csa2_evict_select(int32_t num_req, int32_t n_heads,
   if ((uintptr_t)mass & 3u) return CSA2_ERR_UNSUPPORTED;
   const int64_t pairs = (int64_t)num_req * n_heads;
   if (pairs > 0x7fffffffll / 8) return CSA2_ERR_UNSUPPORTED;
+  const uint64_t lens = (uint64_t)num_req * 8, ids = (uint64_t)pairs * keep * 4;
+  // (cut off at 2^60 cells, which no memory has, so that 64 bits hold the bytes)
+  const uint64_t cells = (uint64_t)n_heads * kv_rows;
+  const uint64_t weights = (cells < 1ull << 60 ? cells : 1ull << 60) * 4;
+  const bool shorten = new_len == kv_len;
+  if (overlap(idx, ids, kv_start, lens) || overlap(idx, ids, kv_len, lens) ||
+      overlap(idx, ids, mass, weights) || overlap(idx, ids, new_len, lens) ||
+      overlap(new_len, lens, kv_start, lens) || overlap(new_len, lens, mass, weights) ||
+      (!shorten && overlap(new_len, lens, kv_len, lens)))
+    return CSA2_ERR_INVALID_ARG;
   // CTAs to a (request, head): as many as the GPU holds at a time, but no fewer
   // than kMinSlice rows to each on average (8 x 8 rows of 5200: 10.9 us at
   // 4096 a slice, 11.9 at 2048, 16.8 at 1024; 24 x 8 rows of 26,000: 37.6 us
@@ -407,12 +428,17 @@ extern "C" CSA2_API int csa2_evict_select(int32_t num_req, int32_t n_heads,
   nc = nc < by_rows ? nc : by_rows;
   nc = nc < 1 ? 1 : nc > 8 ? 8 : nc;
   SelParams P{num_req, n_heads, kv_start, kv_len, mass, kv_rows, keep,
-              sink,    recent,  idx,      new_len, d_err};
+              sink,    recent,  idx,      shorten ? nullptr : new_len, d_err};
   constexpr int kSmem = kHeld * 4;
   allow_smem<evict_select_kernel>(kSmem);
+  const auto done = [&]() {
+    const unsigned blocks = (unsigned)(((int64_t)num_req + 255) / 256);
+    if (shorten) evict_lengths_kernel<<<blocks, 256, 0, as_stream(stream)>>>(P, new_len);
+    return launch_status();
+  };
   if (nc == 1) {                  // a plain launch costs the host less
     evict_select_kernel<<<(unsigned)pairs, kSelThreads, kSmem, as_stream(stream)>>>(P);
-    return launch_status();
+    return done();
   }
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
@@ -428,7 +454,7 @@ extern "C" CSA2_API int csa2_evict_select(int32_t num_req, int32_t n_heads,
     (void)cudaGetLastError();
     return CSA2_ERR_CUDA;
   }
-  return launch_status();
+  return done();
 }
 
 extern "C" CSA2_API int csa2_evict_rows(int32_t num_req, int32_t n_heads, const int32_t *idx,
