@@ -548,7 +548,9 @@ __device__ bool softmax_item(const AttnParams &P, M *ms, const Item &it, int t, 
   const int steps = it.steps[t], stride = kNarrow ? 2 : 1;
   int kt = it.kt0 + (kNarrow ? t : 0);
   for (int j = 0; j < steps; ++j, kt += stride) {
-    if (!(ok = wait_bar(&ms->s_full[t], ps, &ms->bd))) break;
+    // the warp goes on or gives up as one: with a lane gone, the votes and TMEM
+    // loads below would wait for it
+    if (!(ok = wait_all(&ms->s_full[t], ps, &ms->bd))) break;
     ps ^= 1;
     if (!rows_here) {
       __syncwarp();
@@ -624,8 +626,7 @@ __device__ bool softmax_item(const AttnParams &P, M *ms, const Item &it, int t, 
     sum = part2.x + part2.y;
   }
   const bool any = steps > 0;
-  if (ok && any) ok = wait_bar(&ms->o_full[t], po, &ms->bd);
-  ok = __all_sync(0xffffffffu, ok);
+  if (ok && any) ok = wait_all(&ms->o_full[t], po, &ms->bd);
   if (!ok) return false;
   if (any) po ^= 1;
   fence_after_sync();

@@ -5,7 +5,7 @@ import torch
 
 import sparse_attention_prefill_gb300 as S
 from tests import dense_ref as R
-from tests.test_gpu_dense_attn import DEV, _derr
+from tests.test_gpu_dense_attn import BF, DEV, HF, _derr, _inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,42 @@ def test_select_in_place_lengths_of_bad_requests():
     idx, _ = S.evict_select(_i64([0, 90, -1, 0]), n, mass, 20, 1, 1, new_len=n, d_err=d)
     assert int(d.item()) == S.DERR_RANGE_ROW and n.tolist() == [20, 0, 0, 0]
     assert (idx[1:] == -1).all() and (idx[0] >= 0).all()
+
+
+# ---------------------------------------------------------------------------
+# waits that run out
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("heads,kv,dim,dtype", [(16, 2, 128, BF), (8, 4, 64, HF)])
+def test_waits_of_every_length_run_out_and_recover(heads, kv, dim, dtype):
+    """Limits around the time that the kernels' steps take, so that a wait runs
+    out in any role and at any step, for some lanes of a warp just before it
+    would have been met: the calls end and the next ones are right."""
+    new, rows = [400, 3, 130, 1], [900, 700, 130, 2000]
+    b, _, start, q, k, v = _inputs(new, rows, heads, kv, dim, dtype, seed=dim, extra=[1500])
+    few, _, fstart, fq, fk, fv = _inputs([5, 2], [800, 3000], heads, kv, dim, dtype, seed=1)
+    gr = dict(num_groups=1, cu_group=_i32([0, 4]), prefix_start=_i64(start[-1:]),
+              prefix_len=_i64([1500]), max_prefix=1500)
+
+    def calls(d):
+        out = S.prompt_attn(b, q, k, v, d_err=d)
+        return (*out, *S.prompt_attn(few, fq, fk, fv, d_err=d),
+                *S.prefix_attn(b, gr, q, k, v, 2000, d_err=d),
+                S.attn_mass(b, q, k, out[1], 2000, d_err=d))
+
+    want = calls(None)
+    d = _derr()
+    try:
+        for limit in (1, 300, 700, 1500, 3000, 6000, 12000, 25000, 50000, 99999, 100001, 200000):
+            S.set_wait_limit_ns(limit)
+            for _ in range(4):
+                calls(d)
+            torch.cuda.synchronize()
+    finally:
+        S.set_wait_limit_ns(0)
+    assert int(d.item()) & S.DERR_TIMEOUT
+    d = _derr()
+    got = calls(d)
+    assert int(d.item()) == 0
+    for x, y in zip(want, got):
+        assert torch.equal(x.nan_to_num(9.0), y.nan_to_num(9.0))
