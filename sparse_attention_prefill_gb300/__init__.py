@@ -568,10 +568,16 @@ def _packed_args(packed, q, k):
     return st, dev, dt, rows, (h, kv, d, _DTYPES[dt], qp, ldq, kp, ldk)
 
 
-def _used_on(t, stream):
-    """t, allocated for the current stream, also held for `stream`."""
-    if stream is not None:
-        t.record_stream(stream)
+def _new(make, shape, dtype, device, stream, returned=True):
+    """make(shape) allocated on the stream that the call runs on: memory of the
+    current stream's pool may still be read by work queued there.  What is
+    returned is held for the current stream too, where the caller goes on."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -584,12 +590,12 @@ def _attn_args(packed, q, k, v, out, lse, want_lse, d_err, stream):
                         % (tuple(k.shape), tuple(v.shape)))
     n = st.num_q * shape[0]
     if out is None:
-        out = _used_on(torch.empty(q.shape, dtype=dt, device=q.device), stream)
+        out = _new(torch.empty, q.shape, dt, q.device, stream)
         op = out.data_ptr()
     else:
         op = _arg(out, dt, "out", n * shape[2], dev)
     if lse is None and want_lse:
-        lse = _used_on(torch.empty(q.shape[:2], dtype=_F32, device=q.device), stream)
+        lse = _new(torch.empty, q.shape[:2], _F32, q.device, stream)
         lp = lse.data_ptr()
     else:
         lp = _arg(lse, _F32, "lse", n, dev)
@@ -635,7 +641,7 @@ def _prefix(packed, groups, q, k, v, max_kv, sm_scale, out, lse, want_lse, works
                                             gr.num_groups, *shape[:3], 0 if gr is None else
                                             gr.max_prefix, max_kv)
         if workspace is None:
-            workspace = _used_on(torch.empty(nbytes, dtype=torch.uint8, device=q.device), stream)
+            workspace = _new(torch.empty, nbytes, torch.uint8, q.device, stream, False)
         else:
             nbytes = max(nbytes, workspace.numel())
     return _call(dev, load().csa2_prefix_attn,
@@ -739,8 +745,7 @@ def attn_mass(packed, q, k, lse, max_kv, sm_scale=None, mass_in=None, mass=None,
     rows], added to ``mass_in`` if given.  ``mass`` may be ``mass_in``; rows of
     no request keep their values (zeros, where it is allocated here)."""
     if mass is None:
-        with torch.cuda.stream(stream):       # zeroed in front of the call
-            mass = torch.zeros((k.shape[1], k.shape[0]), dtype=torch.float32, device=q.device)
+        mass = _new(torch.zeros, (k.shape[1], k.shape[0]), _F32, q.device, stream)
     if sm_scale is None:
         sm_scale = q.shape[2] ** -0.5
     _check(csa2_attn_mass(packed, q, k, lse, max_kv, sm_scale, mass_in, mass, d_err, stream),
@@ -756,10 +761,9 @@ def evict_select(kv_start, kv_len, mass, keep, sink=0, recent=0, idx=None, new_l
     ``new_len`` may be ``kv_len`` itself."""
     r, h = int(kv_len.shape[0]), int(mass.shape[0])
     if idx is None:
-        idx = _used_on(torch.empty((r, h, int(keep)), dtype=torch.int32, device=mass.device),
-                       stream)
+        idx = _new(torch.empty, (r, h, int(keep)), _I32, mass.device, stream)
     if new_len is None:
-        new_len = _used_on(torch.empty(r, dtype=torch.int64, device=mass.device), stream)
+        new_len = _new(torch.empty, r, _I64, mass.device, stream)
     _check(csa2_evict_select(r, kv_start, kv_len, mass, keep, sink, recent, idx, new_len, d_err,
                              stream), "csa2_evict_select")
     return idx, new_len

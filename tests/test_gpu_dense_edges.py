@@ -107,3 +107,57 @@ def test_waits_of_every_length_run_out_and_recover(heads, kv, dim, dtype):
     assert int(d.item()) == 0
     for x, y in zip(want, got):
         assert torch.equal(x.nan_to_num(9.0), y.nan_to_num(9.0))
+
+
+# ---------------------------------------------------------------------------
+# streams
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("call", ["prompt", "prefix", "mass", "select"])
+def test_side_stream_leaves_freed_memory_of_the_current_one(call):
+    """Tensors freed while work on them is still queued on the current stream:
+    what a call on another stream allocates must not be their memory."""
+    rows = [700] * 20
+    b, _, start, q, k, v = _inputs([1] * 20, rows, 16, 2, 128, BF)
+    _, lse = S.prompt_attn(b, q, k, v)
+    weight = torch.rand((2, k.shape[0]), device=DEV)
+    run = {"prompt": lambda s: S.prompt_attn(b, q, k, v, stream=s),
+           "prefix": lambda s: S.prefix_attn(b, None, q, k, v, 700, stream=s),
+           "mass": lambda s: (S.attn_mass(b, q, k, lse, 700, stream=s),),
+           "select": lambda s: S.evict_select(b["kv_start"], b["kv_len"], weight, 100, stream=s)}[call]
+    want = run(None)
+    sizes = [x.numel() * x.element_size() for x in want]
+    sizes.append(S.csa2_prefix_attn_workspace(20, 20, 0, 16, 2, 128, 0, 700))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        used = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for n in sizes]
+        torch.cuda._sleep(200_000_000)       # some 0.1 s
+        read = [x.clone() for x in used]
+        used.clear()
+        got = run(side)
+        side.synchronize()
+        for x, y in zip(want, got):
+            assert torch.equal(x, y)
+        for x in read:
+            assert (x == 7).all()
+
+
+def test_side_stream_results_stay_while_the_current_stream_reads_them():
+    """A result freed while the current stream has yet to read it: calls on the
+    side stream must not be given its memory."""
+    b, _, start, q, k, v = _inputs([300], [300], 8, 2, 128, BF)
+    q2 = -q
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = S.prompt_attn(b, q, k, v)[0]
+    torch.cuda.synchronize()
+    out, lse = S.prompt_attn(b, q, k, v, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(200_000_000)
+    read = out.clone()
+    del out, lse
+    for _ in range(3):
+        S.prompt_attn(b, q2, k, v, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(read, want)
