@@ -484,7 +484,7 @@ CSA2_API int csa2_quantize_rows(int32_t format, int64_t n, const float *src, int
  *   num_q       rows of q and of the outputs
  *   num_req     requests
  *   cu_q[R+1]   request r holds query rows cu_q[r] .. cu_q[r+1]-1, ascending;
- *               rows in front of cu_q[0] and behind cu_q[R] are not touched
+ *               rows that no request holds are not touched
  *   kv_start[R] first row of the request in the K and V pools
  *   kv_len[R]   rows of the request in the pools, m_r, the new ones included:
  *               query i of n_r is at position m_r - n_r + i and sees the rows
@@ -561,8 +561,9 @@ typedef struct csa2_prefix_groups {
  *              the same time need one each).
  * Other arguments, outputs and errors as csa2_prompt_attn; a prefix that
  * leaves the pool counts as empty (CSA2_DERR_RANGE_ROW), and a group that is
- * not a range of requests is skipped, its requests keeping their own rows
- * (CSA2_DERR_BAD_EXTEND). */
+ * not a range of requests, or whose requests' query rows cu_q[first] ..
+ * cu_q[last + 1] - 1 are not a range within num_q, is skipped, its requests
+ * keeping their own rows (CSA2_DERR_BAD_EXTEND). */
 CSA2_API int csa2_prefix_attn_workspace(int32_t num_q, int32_t num_req, int32_t num_groups,
                                         int32_t n_heads, int32_t n_kv_heads, int32_t dim,
                                         int64_t max_prefix, int64_t max_kv, int64_t *bytes);

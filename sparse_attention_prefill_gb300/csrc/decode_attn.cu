@@ -77,6 +77,7 @@ struct Shared {
   uint2 q[kN][D / 16][32];           // Q in fragment order, by lane
   float o[kWarps][8 * kN][D + 4];
   float ref[kWarps][8 * kN], sum[kWarps][8 * kN];
+  bool uncovered;                    // the request is in no group (split 0)
 };
 
 // The run that holds query row `token`, by a warp.
@@ -184,6 +185,11 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
     load_v(b);
     if (b + kWarps < b1) prefetch(b + kWarps);
   }
+  // while the first rows are on their way, by the warp that has the fewest blocks
+  if (P.cover && split == 0 && warp == kWarps - 1) {
+    const bool in = in_groups(P.cover, P.n_cover, run, S);
+    if (lane == 0) sh.uncovered = !in;
+  }
   for (; b < b1; b += kWarps) {
     // accumulator e: key g + 8 (e / 2), row 2 c + e % 2; even and odd channel
     // steps apart, for shorter chains of products
@@ -279,8 +285,6 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
     }
   }
   __syncthreads();
-  const bool uncovered =
-      P.cover && split == 0 && !in_groups(P.cover, P.n_cover, run, S.num_req);
   // a result's rows are channel-innermost, a partial result's blocks row-innermost
   const bool part = P.splits > 0;
   constexpr int kRows = 8 * kN, kTeam = kWarps * 32 / kRows;       // threads of a row
@@ -303,7 +307,7 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
     const int64_t rows = part_rows(S.num_q, P.group), at = (int64_t)token * P.group + row;
     if (col == 0) {
       P.part_lse[part_stat(rows, P.n_kv, split, h, at)] = lse;
-      if (uncovered)
+      if (P.cover && split == 0 && sh.uncovered)
         for (int i = 0; i < P.cover_splits; ++i)
           P.cover_lse[part_stat(rows, P.n_kv, i, h, at)] = -INFINITY;
     }

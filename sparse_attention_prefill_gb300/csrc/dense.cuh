@@ -267,13 +267,17 @@ __device__ __forceinline__ int64_t part_elem(int64_t rows, int n_kv, int dim, in
   return (((int64_t)split * n_kv + h) * rows + (at & ~(int64_t)31)) * dim + (at & 31);
 }
 
-// Whether request r lies in one of the groups, by one warp.
+// Whether request r lies in one of the groups that are not skipped, by one warp:
+// seq_rows' conditions, or a request of a skipped group would wait in the join for
+// a prefix part that nobody wrote.
 __device__ __forceinline__ bool in_groups(const int32_t *cu_group, int groups, int r,
-                                          int num_req) {
+                                          const Seqs &S) {
   bool mine = false;
   for (int g = threadIdx.x & 31; g < groups; g += 32) {
-    const int lo = cu_group[g], hi = cu_group[g + 1];
-    mine |= lo >= 0 && lo <= r && r < hi && hi <= num_req;
+    const int a = cu_group[g], b = cu_group[g + 1];
+    if (a < 0 || a > r || r >= b || b > S.num_req) continue;
+    const int lo = S.cu_q[a], hi = S.cu_q[b];
+    mine |= lo >= 0 && lo <= hi && hi <= S.num_q;
   }
   return __any_sync(0xffffffffu, mine);
 }

@@ -179,7 +179,7 @@ __device__ void find_item(const AttnParams &P, uint32_t cta, const Shares &s, It
     base += __shfl_sync(0xffffffffu, inc, 31);
   }
   if (it.run < 0) return;
-  it.uncovered = P.cover && !in_groups(P.cover, P.n_cover, it.run, P.seqs.num_req);
+  it.uncovered = P.cover && !in_groups(P.cover, P.n_cover, it.run, P.seqs);
   it.ntile = min(tok, it.n - it.tok0) > P.tpt ? 2 : 1;
   int nkt[2];                      // key tiles that each query tile needs
 #pragma unroll
@@ -794,26 +794,43 @@ dense_attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ 
 // Joins the parts of a row: lse = ln sum_s e^{lse_s}, out = sum_s
 // e^{lse_s - lse} out_s.  A block has 32 packed rows of a key head, a lane to a
 // row, a warp to a sixteenth of the channels; parts without keys (-inf) are not
-// read.  Rows in front of or behind the sequences are left.
+// read.  Rows that no request holds are left: nobody wrote their parts.  Which
+// those are takes a look at every request, since cu_q may be malformed (one load
+// a thread for 512 requests, beside those of the statistics).
 template <typename T, int D>
 __global__ void __launch_bounds__(512)
 merge_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse, int parts,
              int num_q, int n_kv, int group, const int32_t *__restrict__ cu_q, int num_req,
              T *__restrict__ out, float *__restrict__ lse) {
-  wait_front();
   constexpr int kCh = D / 16, kBatch = 4;
   __shared__ __align__(16) T tile[32][D + 8];
   __shared__ float weight[2 * kMaxSplits][32];
+  __shared__ uint32_t held[16];          // by warp: bit i: row0 + i is a request's row
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
   const int64_t rows = part_rows(num_q, group), row0 = (int64_t)blockIdx.x * 32;
-  const int64_t lo = (int64_t)cu_q[0] * group;
-  const int64_t hi = (int64_t)min(num_q, cu_q[num_req]) * group;
   const int64_t row = row0 + lane;
-  const bool mine = row >= lo && row < hi;
   const float *po = part_o + part_elem(rows, n_kv, D, 0, h, row) + warp * kCh * 32;
+  uint32_t theirs = 0;
+  for (int r = threadIdx.x; r < num_req; r += 512) {
+    const int lo = cu_q[r], hi = cu_q[r + 1];
+    if (lo < 0 || lo > hi || hi > num_q) continue;
+    const int64_t a = max((int64_t)lo * group - row0, (int64_t)0);
+    const int64_t b = min((int64_t)hi * group - row0, (int64_t)32);
+    if (a < b) theirs |= (0xffffffffu >> (32 - (int)b)) & (0xffffffffu << (int)a);
+  }
+  wait_front();                          // the batch was there before the kernels in front
   for (int s = warp; s < parts; s += 16)
-    weight[s][lane] = mine ? part_lse[part_stat(rows, n_kv, s, h, row)] : -INFINITY;
+    weight[s][lane] = part_lse[part_stat(rows, n_kv, s, h, row)];
+  theirs = __reduce_or_sync(0xffffffffu, theirs);
+  if (lane == 0) held[warp] = theirs;
   __syncthreads();
+  theirs = __reduce_or_sync(0xffffffffu, held[lane & 15]);
+  const bool mine = (theirs >> lane) & 1;
+  if (!__all_sync(0xffffffffu, mine)) {         // in one warp as in the others
+    for (int s = warp; s < parts; s += 16)
+      if (!mine) weight[s][lane] = -INFINITY;
+    __syncthreads();
+  }
   float top = -INFINITY, tot = 0.f;
   bool nan = false;
   for (int s = 0; s < parts; ++s) {
@@ -852,7 +869,7 @@ merge_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ls
   constexpr int kVec = D / 8;            // 16-byte pieces of a row
   for (int i = threadIdx.x; i < 32 * kVec; i += 512) {
     const int64_t r = row0 + i / kVec;
-    if (r < lo || r >= hi) continue;
+    if (!((theirs >> (i / kVec)) & 1)) continue;
     const int64_t at = r / group * heads + (int64_t)h * group + r % group;
     *reinterpret_cast<uint4 *>(out + at * D + (i % kVec) * 8) =
         *reinterpret_cast<const uint4 *>(&tile[i / kVec][(i % kVec) * 8]);

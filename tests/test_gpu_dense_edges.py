@@ -161,3 +161,98 @@ def test_side_stream_results_stay_while_the_current_stream_reads_them():
         S.prompt_attn(b, q2, k, v, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(read, want)
+
+
+# ---------------------------------------------------------------------------
+# malformed batches
+# ---------------------------------------------------------------------------
+
+def _is_range(cu, a, b, num_q):
+    return 0 <= cu[a] <= cu[b] <= num_q
+
+
+def _check_batch(call, cu, rows, num_q, groups, heads, kv, dim, seed=0):
+    """Outputs of a batch whose cu_q or groups may be malformed: right for the
+    requests that are ranges of rows, untouched for all other rows.  groups:
+    (cu_group, prefix lengths) or None."""
+    pre = list(groups[1]) if groups else []
+    _, _, start, _, k, v = _inputs([1] * len(rows), rows, heads, kv, dim, BF, seed=seed, extra=pre)
+    q = torch.randn((num_q, heads, dim), device=DEV).to(BF)
+    b = dict(num_q=num_q, num_req=len(rows), cu_q=_i32(cu), kv_start=_i64(start[:len(rows)]),
+             kv_len=_i64(rows))
+    out = torch.full((num_q, heads, dim), 7.0, dtype=BF, device=DEV)
+    lse = torch.full((num_q, heads), 7.0, device=DEV)
+    d = _derr()
+    if call == "prompt":
+        S.prompt_attn(b, q, k, v, out=out, lse=lse, d_err=d)
+    else:
+        gr = None
+        if groups:
+            gr = dict(num_groups=len(pre), cu_group=_i32(groups[0]), max_prefix=max(pre),
+                      prefix_start=_i64(start[len(rows):]), prefix_len=_i64(pre))
+        need = S.csa2_prefix_attn_workspace(num_q, len(rows), len(pre), heads, kv, dim,
+                                            max(pre, default=0), max(rows))
+        ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)       # NaNs
+        S.prefix_attn(b, gr, q, k, v, max(rows), out=out, lse=lse, workspace=ws, d_err=d)
+    bad = not all(_is_range(cu, r, r + 1, num_q) for r in range(len(rows)))
+    if groups:
+        bad |= not all(0 <= x <= y <= len(rows) and _is_range(cu, x, y, num_q)
+                       for x, y in zip(groups[0], groups[0][1:]))
+    assert int(d.item()) == (S.DERR_BAD_EXTEND if bad else 0)
+    mine = [0] * num_q
+    for r in range(len(rows)):
+        if _is_range(cu, r, r + 1, num_q):
+            for i in range(cu[r], cu[r + 1]):
+                mine[i] += 1
+    for r in range(len(rows)):
+        if not _is_range(cu, r, r + 1, num_q) or cu[r] == cu[r + 1]:
+            continue
+        at = slice(cu[r], cu[r + 1])
+        n = cu[r + 1] - cu[r]
+        kk, vv, off = k[start[r]:start[r] + rows[r]], v[start[r]:start[r] + rows[r]], 0
+        for g in range(len(pre)):
+            x, y = groups[0][g:g + 2]
+            if 0 <= x <= r < y <= len(rows) and _is_range(cu, x, y, num_q):
+                p = start[len(rows) + g]
+                kk, vv, off = torch.cat([k[p:p + pre[g]], kk]), torch.cat([v[p:p + pre[g]], vv]), pre[g]
+        last = torch.clamp(off + rows[r] - n + torch.arange(n, device=DEV), min=off - 1)
+        ref = R.attend(q[at], kk, vv, dim ** -0.5, last)
+        assert max(mine[at]) == 1            # the cases have no row in two requests
+        R.check_attention(out[at], lse[at], ref, BF, max(1, kk.shape[0]))
+    free = torch.tensor([m == 0 for m in mine], device=DEV)
+    assert (out[free] == 7).all() and (lse[free] == 7).all()
+
+
+# heads, key heads: single tokens by the decode kernel and by tensor-core items
+@pytest.mark.parametrize("heads,kv,dim", [(8, 2, 128), (16, 1, 64), (20, 1, 64), (64, 2, 128)])
+@pytest.mark.parametrize("cu,num_q,cug", [
+    ([0, 1, 2, 4], 3, [0, 3]), ([0, 1, 10 ** 9, 3], 3, [0, 2, 3]), ([0, 1, 2, 3], 5, [0, 1, 3]),
+    ([0, 1, 2, 4], 3, [0, 2, 3]), ([0, 1, 1, 2], 2, [0, 2]), ([0, 1, 10 ** 9, 3], 3, None),
+    ([0, 1, 2, 4], 3, None), ([0, 1, 2, 3], 3, [1, 4]), ([0, 1, 2, 3], 3, [2, 1, 3])])
+def test_malformed_batches_of_single_tokens_behind_prefixes(heads, kv, dim, cu, num_q, cug):
+    groups = None if cug is None else (cug, [300, 77][:len(cug) - 1])
+    _check_batch("prefix", cu, [30, 200, 5], num_q, groups, heads, kv, dim)
+
+
+@pytest.mark.parametrize("heads,kv,dim", [(8, 2, 128), (5, 1, 64)])
+@pytest.mark.parametrize("call,cu,num_q,cug", [
+    ("prompt", [0, 20, 50, 76], 75, None), ("prompt", [-4, 20, 50, 75], 80, None),
+    ("prompt", [40, 75, 20, 40], 80, None), ("prefix", [0, 20, 50, 76], 75, None),
+    ("prefix", [-4, 20, 50, 75], 80, None), ("prefix", [40, 75, 20, 40], 80, [0, 2]),
+    ("prefix", [0, 20, 50, 76], 75, [0, 3]), ("prefix", [0, 20, 50, 76], 75, [0, 2, 3]),
+    ("prefix", [0, 20, 10 ** 9, 75], 75, [0, 1, 2]), ("prefix", [-4, 20, 50, 75], 80, [0, 1, 3]),
+    ("prefix", [3, 20, 50, 75], 80, [0, 2, 5])])
+def test_malformed_batches_of_extends(call, heads, kv, dim, cu, num_q, cug):
+    groups = None if cug is None else (cug, [300, 77][:len(cug) - 1])
+    _check_batch(call, cu, [30, 200, 35], num_q, groups, heads, kv, dim)
+
+
+@pytest.mark.parametrize("reqs,free", [(511, 1), (513, 3), (1600, 40)])
+def test_rows_of_many_requests_are_told_from_free_ones(reqs, free):
+    """More requests than a look at each takes one step; a group of 3 heads, so
+    that tokens cross the blocks of the join."""
+    cu = [free + i for i in range(reqs + 1)]
+    cu[reqs // 2] = cu[reqs // 2 - 1]            # one of no token, the next of two
+    cu[-1] += 2                                  # three
+    _check_batch("prefix", cu, [2 + i % 7 for i in range(reqs)], cu[-1] + free,
+                 ([0, reqs // 3], [40]), 6, 2, 64)
