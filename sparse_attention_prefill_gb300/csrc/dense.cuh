@@ -257,6 +257,10 @@ __device__ __forceinline__ void seq_keys(const Seqs &S, int i, int64_t &start, i
 __host__ __device__ __forceinline__ int64_t part_rows(int64_t num_q, int group) {
   return (num_q * group + 31) / 32 * 32;
 }
+// Statistic of a row that no request holds: a NaN that no computation gives.
+// decode_attn.cu looks at every query row and writes it for the first split; where
+// the own part runs by dense_attn.cu the join looks for the rows' requests.
+constexpr uint32_t kNobody = 0x7fffdeadu;
 // statistics of packed row `at`; and the element of its channel 0 (channel d: 32 d on)
 __device__ __forceinline__ int64_t part_stat(int64_t rows, int n_kv, int split, int h,
                                              int64_t at) {

@@ -794,13 +794,14 @@ dense_attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ 
 // Joins the parts of a row: lse = ln sum_s e^{lse_s}, out = sum_s
 // e^{lse_s - lse} out_s.  A block has 32 packed rows of a key head, a lane to a
 // row, a warp to a sixteenth of the channels; parts without keys (-inf) are not
-// read.  Rows that no request holds are left: nobody wrote their parts.  Which
-// those are takes a look at every request, since cu_q may be malformed (one load
-// a thread for 512 requests, beside those of the statistics).
-template <typename T, int D>
+// read.  Rows that no request holds are left: nobody wrote their parts.  The
+// requests' own parts, those from `own` on, say so where they ran by
+// decode_attn.cu; otherwise (kLook) it takes a look at every request, since cu_q
+// may be malformed.
+template <typename T, int D, bool kLook>
 __global__ void __launch_bounds__(512)
 merge_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse, int parts,
-             int num_q, int n_kv, int group, const int32_t *__restrict__ cu_q, int num_req,
+             int own, int num_q, int n_kv, int group, const int32_t *__restrict__ cu_q, int num_req,
              T *__restrict__ out, float *__restrict__ lse) {
   constexpr int kCh = D / 16, kBatch = 4;
   __shared__ __align__(16) T tile[32][D + 8];
@@ -811,7 +812,7 @@ merge_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ls
   const int64_t row = row0 + lane;
   const float *po = part_o + part_elem(rows, n_kv, D, 0, h, row) + warp * kCh * 32;
   uint32_t theirs = 0;
-  for (int r = threadIdx.x; r < num_req; r += 512) {
+  for (int r = threadIdx.x; kLook && r < num_req; r += 512) {
     const int lo = cu_q[r], hi = cu_q[r + 1];
     if (lo < 0 || lo > hi || hi > num_q) continue;
     const int64_t a = max((int64_t)lo * group - row0, (int64_t)0);
@@ -821,12 +822,18 @@ merge_kernel(const float *__restrict__ part_o, const float *__restrict__ part_ls
   wait_front();                          // the batch was there before the kernels in front
   for (int s = warp; s < parts; s += 16)
     weight[s][lane] = part_lse[part_stat(rows, n_kv, s, h, row)];
-  theirs = __reduce_or_sync(0xffffffffu, theirs);
-  if (lane == 0) held[warp] = theirs;
+  if (kLook) {
+    theirs = __reduce_or_sync(0xffffffffu, theirs);
+    if (lane == 0) held[warp] = theirs;
+  }
   __syncthreads();
-  theirs = __reduce_or_sync(0xffffffffu, held[lane & 15]);
+  theirs = kLook
+               ? __reduce_or_sync(0xffffffffu, held[lane & 15])
+               : __ballot_sync(0xffffffffu, row < (int64_t)num_q * group &&
+                                                __float_as_uint(weight[own][lane]) != kNobody);
   const bool mine = (theirs >> lane) & 1;
-  if (!__all_sync(0xffffffffu, mine)) {         // in one warp as in the others
+  if (theirs != 0xffffffffu) {           // the same in every warp
+    __syncthreads();
     for (int s = warp; s < parts; s += 16)
       if (!mine) weight[s][lane] = -INFINITY;
     __syncthreads();
@@ -1121,10 +1128,12 @@ extern "C" CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix
   const int64_t blocks = part_rows(b->num_q, s.group) / 32;
   if (blocks > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
   auto merge = [&](auto *o, auto dim_c) {
+    using T = std::remove_pointer_t<decltype(o)>;
+    constexpr int D = decltype(dim_c)::value;
     return launch_behind(
-        merge_kernel<std::remove_pointer_t<decltype(o)>, decltype(dim_c)::value>,
+        p.own.kind == kSingleTokens ? merge_kernel<T, D, false> : merge_kernel<T, D, true>,
         dim3((unsigned)blocks, (unsigned)s.n_kv), 512, 0, true, cs, part_o, part_lse, parts,
-        b->num_q, s.n_kv, s.group, b->cu_q, b->num_req, o, lse);
+        p.pre.splits, b->num_q, s.n_kv, s.group, b->cu_q, b->num_req, o, lse);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;

@@ -247,6 +247,21 @@ def test_malformed_batches_of_extends(call, heads, kv, dim, cu, num_q, cug):
     _check_batch(call, cu, [30, 200, 35], num_q, groups, heads, kv, dim)
 
 
+@pytest.mark.parametrize("heads,kv,dim", [(8, 2, 128), (16, 1, 64)])
+@pytest.mark.parametrize("cu,num_q,cug", [
+    ([-1, 1, 2, 3], 3, None), ([0, 1, 2, -5], 3, None), ([0, 1, 2, -7, 2], 2, None),
+    ([0, 3, 1, 1, 1, 1, 1, 1, 1], 8, None), ([5, 1, 2, 6, 6, 6, 6, 6, 6], 8, None),
+    ([2, 3, 4, 4, 4, 5], 5, None), ([2 ** 31 - 1, 0, 1, 2], 3, None),
+    ([-2 ** 31, 0, 1, 2], 3, None), ([-1, 1, 2, 3], 3, [0, 2, 3]), ([-1, 1, 2, 3], 3, [1, 3]),
+    ([5, 1, 2, 6, 6, 6, 6, 6, 6], 8, [1, 2, 4])])
+@pytest.mark.parametrize("call", ["prompt", "prefix"])
+def test_single_tokens_of_malformed_batches_are_all_found(call, heads, kv, dim, cu, num_q, cug):
+    """Single tokens whose request has not their number, nor one as far from it
+    as the first query row."""
+    groups = None if cug is None or call == "prompt" else (cug, [300, 77][:len(cug) - 1])
+    _check_batch(call, cu, [30, 200, 5, 64, 1, 17, 2, 3][:len(cu) - 1], num_q, groups, heads, kv, dim)
+
+
 @pytest.mark.parametrize("reqs,free", [(511, 1), (513, 3), (1600, 40)])
 def test_rows_of_many_requests_are_told_from_free_ones(reqs, free):
     """More requests than a look at each takes one step; a group of 3 heads, so
