@@ -554,11 +554,17 @@ typedef struct csa2_prefix_groups {
  * csa2_prompt_attn) apart, and both join in one softmax.  `groups` NULL or
  * without groups: own rows alone, split over the cache (the form for single
  * tokens).  max_kv is the longest kv_len, for the choice of splits only.
- *   workspace  device scratch of at least csa2_prefix_attn_workspace bytes,
- *              256-byte aligned, owned by the caller; its contents do not
- *              matter and are undefined after the call.  Calls sharing one
- *              workspace must not overlap (two captured graphs that may run at
- *              the same time need one each).
+ *   workspace  device scratch, 256-byte aligned, owned by the caller; its
+ *              contents do not matter and are undefined after the call.  Calls
+ *              sharing one workspace must not overlap (two captured graphs that
+ *              may run at the same time need one each).
+ * csa2_prefix_attn_workspace gives the bytes of the splits that the call would
+ * choose.  That number goes up and down with the sizes, so a workspace for the
+ * largest batch may hold less than a smaller one's choice: a call given less
+ * splits less (its last bits may differ then), down to one part each for the
+ * prefixes, where there are groups, and the own rows.  A part has 4 * (dim + 1) *
+ * n_kv_heads * (num_q * n_heads / n_kv_heads, rounded up to 32) bytes; less
+ * than that is CSA2_ERR_INVALID_ARG.
  * Other arguments, outputs and errors as csa2_prompt_attn; a prefix that
  * leaves the pool counts as empty (CSA2_DERR_RANGE_ROW), and a group that is
  * not a range of requests, or whose requests' query rows cu_q[first] ..

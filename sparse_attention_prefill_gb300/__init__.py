@@ -620,7 +620,8 @@ def csa2_prompt_attn(packed, q, k, v, sm_scale, out, lse, d_err, stream=None) ->
 
 def csa2_prefix_attn_workspace(num_q, num_req, num_groups, n_heads, n_kv_heads, dim, max_prefix,
                                max_kv) -> int:
-    """Workspace bytes csa2_prefix_attn needs for these sizes."""
+    """Workspace bytes of the splits csa2_prefix_attn would choose for these sizes;
+    with less it splits less."""
     out = C.c_int64(0)
     _check(load().csa2_prefix_attn_workspace(int(num_q), int(num_req), int(num_groups),
                                              int(n_heads), int(n_kv_heads), int(dim),
@@ -636,14 +637,13 @@ def _prefix(packed, groups, q, k, v, max_kv, sm_scale, out, lse, want_lse, works
     if sm_scale is None:
         sm_scale = shape[2] ** -0.5
     gr = None if groups is None else make_groups(groups, dev)
-    if nbytes is None:
+    if nbytes is None and workspace is None:
         nbytes = csa2_prefix_attn_workspace(st.num_q, st.num_req, 0 if gr is None else
                                             gr.num_groups, *shape[:3], 0 if gr is None else
                                             gr.max_prefix, max_kv)
-        if workspace is None:
-            workspace = _new(torch.empty, nbytes, torch.uint8, q.device, stream, False)
-        else:
-            nbytes = max(nbytes, workspace.numel())
+        workspace = _new(torch.empty, nbytes, torch.uint8, q.device, stream, False)
+    elif nbytes is None:
+        nbytes = workspace.numel()
     return _call(dev, load().csa2_prefix_attn,
                  (C.byref(st), None if gr is None else C.byref(gr), *shape, int(max_kv),
                   float(sm_scale), *outs, _arg(workspace, torch.uint8, "workspace", nbytes, dev),
@@ -732,7 +732,8 @@ def prefix_attn(packed, groups, q, k, v, max_kv, sm_scale=None, out=None, lse=No
                 want_lse=True, workspace=None, d_err=None, stream=None):
     """Attention of requests that share prefixes, each prefix read once for its
     group; without groups, split-cache attention for single tokens.  Allocates
-    the workspace (uint8, csa2_prefix_attn_workspace bytes) if none is given."""
+    the workspace (uint8, csa2_prefix_attn_workspace bytes) if none is given; one
+    for the largest batch serves the smaller ones too."""
     st, out, lse = _prefix(packed, groups, q, k, v, max_kv, sm_scale, out, lse, want_lse,
                            workspace, None, d_err, stream)
     _check(st, "csa2_prefix_attn")

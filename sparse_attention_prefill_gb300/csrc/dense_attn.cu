@@ -1008,8 +1008,22 @@ int run_part(const Shape &s, const Cache &c, AttnParams &P, const PartPlan &p, b
   return decode_attn(s, D, st);
 }
 
-int64_t plan_bytes(const PrefixPlan &p, int64_t num_q, const Shape &s) {
-  return (p.pre.splits + p.own.splits) * part_rows(num_q, s.group) * s.n_kv * (s.dim + 1) * 4;
+int64_t part_bytes(int64_t num_q, const Shape &s) {
+  return part_rows(num_q, s.group) * s.n_kv * (s.dim + 1) * 4;
+}
+
+// Cuts the splits down to `parts` parts in all, the more split side first; false
+// if there is not one to each side.  (The best number of splits goes up and down
+// with the batch, so that a workspace for the largest batch may be short of what
+// a smaller one would like.)
+bool fit_splits(PrefixPlan *p, int64_t parts) {
+  int &pre = p->pre.splits, &own = p->own.splits;
+  while (pre + own > parts) {
+    int &most = pre > own ? pre : own;
+    if (most == 1) return false;
+    --most;
+  }
+  return true;
 }
 
 }  // namespace
@@ -1059,7 +1073,8 @@ extern "C" CSA2_API int csa2_prefix_attn_workspace(int32_t num_q, int32_t num_re
   const csa2_packed b{};
   const int st = check_packed(&b, n_heads, n_kv_heads, dim, CSA2_DT_BF16, 0, 1.f, &s);
   if (st != CSA2_OK) return st;
-  *bytes = plan_bytes(plan_prefix(s, num_q, num_req, num_groups, max_prefix, max_kv), num_q, s);
+  const PrefixPlan p = plan_prefix(s, num_q, num_req, num_groups, max_prefix, max_kv);
+  *bytes = (p.pre.splits + p.own.splits) * part_bytes(num_q, s);
   return CSA2_OK;
 }
 
@@ -1082,9 +1097,9 @@ extern "C" CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix
   if (!out) return CSA2_ERR_INVALID_ARG;
   if ((st = check_cache(b, s, c)) != CSA2_OK) return st;
   if ((uintptr_t)out & 15u) return CSA2_ERR_UNSUPPORTED;
-  const PrefixPlan p =
-      plan_prefix(s, b->num_q, b->num_req, ng, ng ? g->max_prefix : 0, max_kv);
-  if (!workspace || workspace_bytes < plan_bytes(p, b->num_q, s)) return CSA2_ERR_INVALID_ARG;
+  PrefixPlan p = plan_prefix(s, b->num_q, b->num_req, ng, ng ? g->max_prefix : 0, max_kv);
+  if (!workspace || !fit_splits(&p, workspace_bytes / part_bytes(b->num_q, s)))
+    return CSA2_ERR_INVALID_ARG;
   if ((uintptr_t)workspace & 255u) return CSA2_ERR_UNSUPPORTED;
   const cudaStream_t cs = csa2::as_stream(stream);
   const int parts = p.pre.splits + p.own.splits;

@@ -1,5 +1,7 @@
 """Refusals of the dense-cache calls that concern several arguments at once
 (no GPU needed: every call here is refused before a launch)."""
+import ctypes as C
+
 import pytest
 
 import sparse_attention_prefill_gb300 as S
@@ -25,3 +27,39 @@ def test_select_outputs_that_overlap_are_refused(lib, kw):
     d.update(kw)
     assert lib.csa2_evict_select(3, 2, AT, 2 * AT, 3 * AT, 100, 10, 1, 2, d["idx"], d["new"], None,
                                  None) == INV
+
+
+def _prefix_status(lib, n, ws_bytes, heads, kv, dim, groups, max_prefix, max_kv):
+    """INV if the workspace is too small.  (Its address is not aligned, which is
+    refused next: nothing is ever launched.)"""
+    b = S.CPacked(n, n, AT, AT, AT)
+    g = S.CPrefixGroups(groups, 0, AT, AT, AT, max_prefix)
+    return lib.csa2_prefix_attn(C.byref(b), C.byref(g) if groups else None, heads, kv, dim,
+                                S.DT_BF16, AT, heads * dim, AT, kv * dim, AT, kv * dim, 100, max_kv,
+                                0.1, AT, None, AT + 16, ws_bytes, None, None)
+
+
+@pytest.mark.parametrize("heads,kv,dim,groups,max_prefix,max_kv", [
+    (64, 8, 128, 0, 0, 8192), (64, 8, 128, 1, 8192, 700), (16, 4, 64, 3, 900, 30000),
+    (20, 1, 64, 2, 64, 64), (6, 2, 128, 0, 0, 0)])
+@pytest.mark.parametrize("most", [300, 171, 115, 58])
+def test_workspace_of_the_largest_batch_serves_every_smaller_one(lib, heads, kv, dim, groups,
+                                                                 max_prefix, max_kv, most):
+    sizes = (groups, heads, kv, dim, max_prefix, max_kv)
+    need = S.csa2_prefix_attn_workspace(most, most, *sizes)
+    for n in range(most, 0, -1):
+        assert _prefix_status(lib, n, need, heads, kv, dim, groups, max_prefix,
+                              max_kv) == S.ERR_UNSUPPORTED, n
+        # and what it is told to take is enough
+        own = S.csa2_prefix_attn_workspace(n, n, *sizes)
+        assert _prefix_status(lib, n, own, heads, kv, dim, groups, max_prefix,
+                              max_kv) == S.ERR_UNSUPPORTED, n
+
+
+@pytest.mark.parametrize("heads,kv,dim,groups", [(64, 8, 128, 0), (6, 2, 64, 2), (3, 1, 128, 1)])
+@pytest.mark.parametrize("n", [1, 7, 33, 200])
+def test_least_workspace_is_one_part_a_side(lib, heads, kv, dim, groups, n):
+    rows = (n * (heads // kv) + 31) // 32 * 32
+    least = 4 * (dim + 1) * kv * rows * (2 if groups else 1)
+    for size, status in ((least, S.ERR_UNSUPPORTED), (least - 4, INV), (0, INV), (-4, INV)):
+        assert _prefix_status(lib, n, size, heads, kv, dim, groups, 5000, 5000) == status

@@ -271,3 +271,41 @@ def test_rows_of_many_requests_are_told_from_free_ones(reqs, free):
     cu[-1] += 2                                  # three
     _check_batch("prefix", cu, [2 + i % 7 for i in range(reqs)], cu[-1] + free,
                  ([0, reqs // 3], [40]), 6, 2, 64)
+
+
+# ---------------------------------------------------------------------------
+# workspaces
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("heads,kv,dim,dtype,new", [
+    (16, 2, 128, BF, 1), (8, 2, 64, HF, 1), (20, 1, 64, BF, 1), (8, 2, 128, BF, 9)])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_less_workspace_means_fewer_splits(heads, kv, dim, dtype, new, grouped):
+    """From what the call would choose down to one part a side."""
+    reqs, pre = 6, 3000
+    rows = [2500 - 300 * i for i in range(reqs)]
+    b, cu, start, q, k, v = _inputs([new] * reqs, rows, heads, kv, dim, dtype, seed=dim,
+                                    extra=[pre])
+    gr = dict(num_groups=1, cu_group=_i32([0, 4]), max_prefix=pre, prefix_start=_i64(start[-1:]),
+              prefix_len=_i64([pre])) if grouped else None
+    sides = 2 if grouped else 1
+    part = 4 * (dim + 1) * kv * ((reqs * new * heads // kv + 31) // 32 * 32)
+    need = S.csa2_prefix_attn_workspace(b["num_q"], reqs, sides - 1, heads, kv, dim, pre, 2500)
+    assert need > sides * part and need % part == 0
+    refs = []
+    for r in range(reqs):
+        at = slice(cu[r], cu[r + 1])
+        kk, vv, off = k[start[r]:start[r] + rows[r]], v[start[r]:start[r] + rows[r]], 0
+        if grouped and r < 4:
+            p = start[-1]
+            kk, vv, off = torch.cat([k[p:p + pre], kk]), torch.cat([v[p:p + pre], vv]), pre
+        last = off + rows[r] - new + torch.arange(new, device=DEV)
+        refs.append((at, R.attend(q[at], kk, vv, dim ** -0.5, last), kk.shape[0]))
+    for parts in range(sides, need // part + 1):
+        ws = torch.full((parts * part,), 255, dtype=torch.uint8, device=DEV)
+        out, lse = S.prefix_attn(b, gr, q, k, v, 2500, workspace=ws)
+        for at, ref, n in refs:
+            R.check_attention(out[at], lse[at], ref, dtype, n)
+    with pytest.raises(S.Csa2Error):
+        S.prefix_attn(b, gr, q, k, v, 2500,
+                      workspace=torch.empty(sides * part - 1, dtype=torch.uint8, device=DEV))
