@@ -632,9 +632,12 @@ typedef struct csa2_evict_buf {
 /* Moves the rows kept, in up to 8 buffers at once (K, V, their scales, the
  * mass): for i < new_len[r]
  *   dst row dst_start[r] + i, head h  =  src row src_start[r] + idx[r, h, i], head h
- * dst may be src when dst_start is src_start: the rows close up in place
- * (ascending idx, as csa2_evict_select writes them).  Otherwise source and
- * destination rows must not overlap.  Rows of dst that are not named keep
+ * dst may be src, or a view that shares its memory, where row dst_start[r] + i of
+ * dst is row src_start[r] + i of src: the rows close up in place (ascending idx,
+ * as csa2_evict_select writes them).  Otherwise no destination row may be a
+ * source row of the call, of this request or another, in this buffer or another:
+ * blocks move requests, heads and buffers in no order.  Two buffers have two
+ * destinations (CSA2_ERR_INVALID_ARG).  Rows of dst that are not named keep
  * their bytes.  A negative idx is skipped; a row outside src_rows or dst_rows
  * is skipped (CSA2_DERR_RANGE_ROW).  Host structs, read during the call only.
  * Pointers and strides multiples of 4 bytes; copies are widest where they are

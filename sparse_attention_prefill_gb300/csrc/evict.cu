@@ -394,6 +394,29 @@ evict_rows_kernel(const __grid_constant__ MoveParams P) {
   if (err) raise_err(P.d_err, err);
 }
 
+// Bytes from a buffer's first to behind its last (cut off at 2^62).
+uint64_t span(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t elem) {
+  if (rows == 0 || elem == 0) return 0;
+  const double most = (double)(rows - 1) * row_stride + (double)(heads - 1) * head_stride + elem;
+  return most < 4e18 ? (rows - 1) * row_stride + (heads - 1) * head_stride + elem : 1ull << 62;
+}
+
+// Whether a buffer's source and destination may share a byte: their runs of memory
+// meet, and they are not columns side by side of the same longer rows.
+bool shares_memory(const csa2_evict_buf &b, int64_t heads) {
+  const uint64_t one_s = span(1, 0, heads, b.src_head_stride, b.elem_bytes);
+  const uint64_t one_d = span(1, 0, heads, b.dst_head_stride, b.elem_bytes);
+  const uint64_t step = (uint64_t)b.src_row_stride;
+  if (b.src_row_stride == b.dst_row_stride && one_s <= step && one_d <= step && step > 0) {
+    const uint64_t s = (uint64_t)(uintptr_t)b.src, d = (uint64_t)(uintptr_t)b.dst;
+    const uint64_t off = d >= s ? (d - s) % step : (step - (s - d) % step) % step;
+    if (off >= one_s && step - off >= one_d) return false;
+  }
+  return overlap(
+      b.src, span(b.src_rows, b.src_row_stride, heads, b.src_head_stride, b.elem_bytes), b.dst,
+      span(b.dst_rows, b.dst_row_stride, heads, b.dst_head_stride, b.elem_bytes));
+}
+
 }  // namespace
 }  // namespace csa2
 
@@ -492,7 +515,11 @@ extern "C" CSA2_API int csa2_evict_rows(int32_t num_req, int32_t n_heads, const 
     P.buf[i].src_rows = b.src_rows < kMostRows ? b.src_rows : kMostRows;
     P.buf[i].dst_rows = b.dst_rows < kMostRows ? b.dst_rows : kMostRows;
     P.vec[i] = (bits & 15u) ? 4 : 16;
-    in_place |= b.src == b.dst;
+    // sharing memory, the rows are moved in order, whichever views name them
+    in_place |= shares_memory(b, n_heads);
+    for (int j = 0; j < i; ++j)
+      if (b.elem_bytes > 0 && bufs[j].elem_bytes > 0 && bufs[j].dst == b.dst && b.dst)
+        return CSA2_ERR_INVALID_ARG;
     const int64_t pieces = b.elem_bytes / P.vec[i];
     if (pieces > most) most = pieces;
     P.shift[i] = -1;

@@ -63,3 +63,11 @@ def test_least_workspace_is_one_part_a_side(lib, heads, kv, dim, groups, n):
     least = 4 * (dim + 1) * kv * rows * (2 if groups else 1)
     for size, status in ((least, S.ERR_UNSUPPORTED), (least - 4, INV), (0, INV), (-4, INV)):
         assert _prefix_status(lib, n, size, heads, kv, dim, groups, 5000, 5000) == status
+
+
+@pytest.mark.parametrize("first,second", [(0, 1), (0, 7), (3, 6)])
+def test_rows_one_destination_twice_is_refused(lib, first, second):
+    arr = (S.CEvictBuf * 8)(*[S.CEvictBuf(AT, (2 + i) * AT, 10, 10, 64, 32, 64, 32, 32)
+                              for i in range(8)])
+    arr[second].dst = arr[first].dst
+    assert lib.csa2_evict_rows(2, 2, AT, 4, AT, AT, AT, 8, arr, None, None) == INV

@@ -309,3 +309,45 @@ def test_less_workspace_means_fewer_splits(heads, kv, dim, dtype, new, grouped):
     with pytest.raises(S.Csa2Error):
         S.prefix_attn(b, gr, q, k, v, 2500,
                       workspace=torch.empty(sides * part - 1, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("shift", [1, 7, 300])
+def test_rows_close_up_in_place_through_another_view(shift):
+    """The destination is a view further down the same memory, with starts that
+    name the same rows: moved in order, as with one tensor for both."""
+    rows, keep, heads = [6000, 900, 40], 4000, 2
+    start, pool = R.starts(rows, gap=320)
+    mass = torch.rand((heads, pool), device=DEV)
+    c = torch.randn((pool, heads, 64), device=DEV).to(BF)
+    idx, new_len = S.evict_select(_i64(start), _i64(rows), mass, keep, 2, 20)
+    want = c.clone()
+    for r, n in enumerate(rows):
+        m = min(n, keep)
+        for h in range(heads):
+            want[start[r]:start[r] + m, h] = c[start[r] + idx[r, h, :m].long(), h]
+    for down in (True, False):
+        x, w = c.clone(), mass.clone()
+        src, dst = (x, x[shift:]) if down else (x[shift:], x)
+        s0 = _i64(start) - (0 if down else shift)
+        d0 = _i64(start) - (shift if down else 0)
+        d = _derr()
+        S.evict_rows(idx, new_len, s0, d0, [(src, dst)], d_err=d)
+        assert int(d.item()) == 0 and torch.equal(x, want)
+
+
+def test_rows_between_columns_of_longer_rows():
+    """Source and destination side by side in the same rows."""
+    rows, heads = [700, 60], 3
+    start, pool = R.starts(rows)
+    x = torch.randn((pool, 2, heads, 32), device=DEV).to(BF)
+    mass = torch.rand((heads, pool), device=DEV)
+    idx, new_len = S.evict_select(_i64(start), _i64(rows), mass, 100, 2, 20)
+    for a, b in ((0, 1), (1, 0)):
+        y = x.clone()
+        S.evict_rows(idx, new_len, _i64(start), _i64([0, 300]), [(y[:, a], y[:, b])])
+        want = x.clone()
+        for r, to in enumerate((0, 300)):
+            m = int(new_len[r])
+            for h in range(heads):
+                want[to:to + m, b, h] = x[start[r] + idx[r, h, :m].long(), a, h]
+        assert torch.equal(y, want)
