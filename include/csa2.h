@@ -505,7 +505,9 @@ CSA2_API int csa2_quantize_rows(int32_t format, int64_t n, const float *src, int
  * Supported: dim in {64, 128}, n_heads / n_kv_heads <= 128, n_kv_heads <=
  * 1024, kv_rows < 2^31 - 256, 0 < sm_scale < inf (CSA2_ERR_INVALID_ARG);
  * bases and outputs 16-byte aligned, row distances multiples of 8 elements
- * (CSA2_ERR_UNSUPPORTED otherwise).
+ * (CSA2_ERR_UNSUPPORTED otherwise).  Outputs and workspaces share no bytes with
+ * the inputs or each other (CSA2_ERR_INVALID_ARG), except where a call allows
+ * it.
  * ------------------------------------------------------------------------- */
 typedef struct csa2_packed {
   int32_t num_q;
@@ -520,7 +522,8 @@ typedef struct csa2_packed {
  *   out[i,h,:] = sum_j e^{l_j} v[kv_start+j, h/G, :] / sum_j e^{l_j}
  *   lse[i,h]   = ln sum_j e^{l_j}
  * A query that sees nothing gets out = 0, lse = -inf.
- *   out [num_q, n_heads, dim] of the inputs' type, contiguous
+ *   out [num_q, n_heads, dim] of the inputs' type, contiguous; may be q itself,
+ *       where its rows are ldq = n_heads * dim apart
  *   lse [num_q, n_heads] fp32 or NULL
  * The weights e^{l_j} are rounded to the inputs' type for the product with v
  * (their sum is not); products accumulate in fp32.  For single tokens over

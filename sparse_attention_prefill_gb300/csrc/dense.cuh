@@ -379,5 +379,30 @@ inline int check_rows(const void *p, int64_t ld, int heads, int dim) {
   return CSA2_OK;
 }
 
+// Whether n bytes from p on meet rows of `width` bytes, `step` bytes apart (they
+// may lie between two of them).
+inline bool meets_rows(const void *p, uint64_t n, const void *rows, int64_t count, int64_t step,
+                       int64_t width) {
+  if (!p || !rows || count == 0) return false;
+  if (!overlap(p, n, rows, (uint64_t)(count - 1) * step + width)) return false;
+  const uint64_t x = (uint64_t)(uintptr_t)p, y = (uint64_t)(uintptr_t)rows;
+  if (x < y) return true;
+  const uint64_t off = (x - y) % (uint64_t)step;
+  return off < (uint64_t)width || off + n > (uint64_t)step;
+}
+
+// An output (or workspace) of n bytes against what a call reads of a batch.
+inline bool meets_batch(const void *p, uint64_t n, const csa2_packed *b) {
+  const uint64_t r = (uint64_t)b->num_req;
+  return p && (overlap(p, n, b->cu_q, 4 * (r + 1)) || overlap(p, n, b->kv_start, 8 * r) ||
+               overlap(p, n, b->kv_len, 8 * r));
+}
+inline bool meets_groups(const void *p, uint64_t n, const csa2_prefix_groups *g) {
+  if (!p || !g || g->num_groups < 1) return false;
+  const uint64_t c = (uint64_t)g->num_groups;
+  return overlap(p, n, g->cu_group, 4 * (c + 1)) || overlap(p, n, g->prefix_start, 8 * c) ||
+         overlap(p, n, g->prefix_len, 8 * c);
+}
+
 }  // namespace dense
 }  // namespace csa2

@@ -942,6 +942,26 @@ int check_cache(const csa2_packed *b, const Shape &s, const Cache &c) {
   return st;
 }
 
+// Whether an output or the workspace meets an input or another of them.  The
+// outputs may take q's place: every item reads its own query rows before it writes
+// them, and what it reads of others' goes nowhere.
+bool outputs_meet(const csa2_packed *b, const csa2_prefix_groups *g, const Shape &s, const Cache &c,
+                  const void *out, const void *lse, const void *ws, int64_t ws_bytes) {
+  const int64_t wq = (int64_t)s.n_heads * s.dim * 2, wk = (int64_t)s.n_kv * s.dim * 2;
+  const uint64_t no = (uint64_t)b->num_q * wq, nl = (uint64_t)b->num_q * s.n_heads * 4;
+  const auto meets = [&](const void *p, uint64_t n, bool q_too) {
+    return meets_batch(p, n, b) || meets_groups(p, n, g) ||
+           meets_rows(p, n, c.k, c.kv_rows, c.ldk * 2, wk) ||
+           meets_rows(p, n, c.v, c.kv_rows, c.ldv * 2, wk) ||
+           (q_too && meets_rows(p, n, c.q, b->num_q, c.ldq * 2, wq));
+  };
+  const bool in_place = out == c.q && (c.ldq * 2 == wq || b->num_q == 1);
+  return meets(out, no, !in_place) || meets(lse, nl, true) ||
+         (ws && meets(ws, (uint64_t)ws_bytes, true)) || (lse && overlap(out, no, lse, nl)) ||
+         (ws && (overlap(ws, (uint64_t)ws_bytes, out, no) ||
+                 (lse && overlap(ws, (uint64_t)ws_bytes, lse, nl))));
+}
+
 // Single tokens of few heads go by decode_attn.cu; other runs whose rows fill no
 // more than one query tile are narrow items.
 enum Kind { kWideItems, kNarrowItems, kSingleTokens };
@@ -1046,6 +1066,7 @@ extern "C" CSA2_API int csa2_prompt_attn(const csa2_packed *b, int32_t n_heads,
   if (!out) return CSA2_ERR_INVALID_ARG;
   if ((st = check_cache(b, s, c)) != CSA2_OK) return st;
   if ((uintptr_t)out & 15u) return CSA2_ERR_UNSUPPORTED;
+  if (outputs_meet(b, nullptr, s, c, out, lse, nullptr, 0)) return CSA2_ERR_INVALID_ARG;
   AttnParams P{};
   P.seqs = Seqs{b->num_req, b->num_q, b->num_req, b->cu_q, nullptr, b->kv_start, b->kv_len,
                 kv_rows};
@@ -1101,6 +1122,10 @@ extern "C" CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix
   if (!workspace || !fit_splits(&p, workspace_bytes / part_bytes(b->num_q, s)))
     return CSA2_ERR_INVALID_ARG;
   if ((uintptr_t)workspace & 255u) return CSA2_ERR_UNSUPPORTED;
+  // (of the workspace, what the parts take)
+  if (outputs_meet(b, g, s, c, out, lse, workspace,
+                   (p.pre.splits + p.own.splits) * part_bytes(b->num_q, s)))
+    return CSA2_ERR_INVALID_ARG;
   const cudaStream_t cs = csa2::as_stream(stream);
   const int parts = p.pre.splits + p.own.splits;
   const int64_t rows = part_rows(b->num_q, s.group) * s.n_kv;

@@ -71,3 +71,45 @@ def test_rows_one_destination_twice_is_refused(lib, first, second):
                               for i in range(8)])
     arr[second].dst = arr[first].dst
     assert lib.csa2_evict_rows(2, 2, AT, 4, AT, AT, AT, 8, arr, None, None) == INV
+
+
+# 10 query rows of 8 x 128 (20480 bytes), 100 cache rows of 2 x 128 (51200
+# bytes, or 1024 bytes apart), lse 320 bytes, mass 800, 2 requests, 1 group
+def _attn(lib, prefix, **kw):
+    d = dict(cu=AT, ks=2 * AT, kl=3 * AT, q=4 * AT, ldq=1024, k=5 * AT, v=6 * AT, ld=256, out=7 * AT,
+             lse=8 * AT, ws=9 * AT, cug=10 * AT, ps=11 * AT, pl=12 * AT)
+    d.update(kw)
+    b = S.CPacked(10, 2, d["cu"], d["ks"], d["kl"])
+    args = [8, 2, 128, S.DT_BF16, d["q"], d["ldq"], d["k"], d["ld"], d["v"], d["ld"], 100]
+    if not prefix:
+        return lib.csa2_prompt_attn(C.byref(b), *args, 0.1, d["out"], d["lse"], None, None)
+    g = S.CPrefixGroups(1, 0, d["cug"], d["ps"], d["pl"], 50)
+    return lib.csa2_prefix_attn(C.byref(b), C.byref(g), *args, 90, 0.1, d["out"], d["lse"], d["ws"],
+                                1 << 24, None, None)
+
+
+BOTH = [
+    dict(out=5 * AT), dict(out=6 * AT + 51200 - 16), dict(out=5 * AT - 20480 + 16), dict(lse=7 * AT),
+    dict(lse=7 * AT + 20476), dict(lse=4 * AT + 20000), dict(lse=6 * AT), dict(out=4 * AT + 16),
+    dict(out=4 * AT, ldq=2048), dict(out=4 * AT + 2048, ldq=2048), dict(out=AT), dict(out=2 * AT),
+    dict(lse=3 * AT + 12), dict(out=5 * AT + 512, ld=512)]
+
+
+@pytest.mark.parametrize("prefix,kw", [(p, kw) for p in (False, True) for kw in BOTH] + [
+    (True, dict(ws=5 * AT)), (True, dict(ws=4 * AT)), (True, dict(ws=7 * AT)), (True, dict(ws=8 * AT)),
+    (True, dict(ws=6 * AT + 51200 - 256)), (True, dict(ws=10 * AT)), (True, dict(out=11 * AT)),
+    (True, dict(out=12 * AT - 16))])
+def test_attention_outputs_that_overlap_are_refused(lib, prefix, kw):
+    assert _attn(lib, prefix, **kw) == INV
+
+
+@pytest.mark.parametrize("kw", [
+    dict(mass=4 * AT), dict(mass=5 * AT), dict(mass=5 * AT + 51200 - 4), dict(mass=8 * AT),
+    dict(mass=8 * AT - 796), dict(old=13 * AT + 400, mass=13 * AT), dict(old=13 * AT - 4, mass=13 * AT),
+    dict(mass=AT), dict(mass=3 * AT + 8)])
+def test_mass_outputs_that_overlap_are_refused(lib, kw):
+    d = dict(old=None)
+    d.update(kw)
+    b = S.CPacked(10, 2, AT, 2 * AT, 3 * AT)
+    assert lib.csa2_attn_mass(C.byref(b), 8, 2, 128, S.DT_BF16, 4 * AT, 1024, 5 * AT, 256, 100, 8 * AT,
+                              90, 0.1, d["old"], d["mass"], None, None) == INV

@@ -351,3 +351,43 @@ def test_rows_between_columns_of_longer_rows():
             for h in range(heads):
                 want[to:to + m, b, h] = x[start[r] + idx[r, h, :m].long(), a, h]
         assert torch.equal(y, want)
+
+
+# ---------------------------------------------------------------------------
+# outputs in the queries' place, or between the rows of an input
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("heads,kv,dim,dtype", [(16, 2, 128, BF), (6, 2, 64, HF), (20, 1, 64, BF)])
+@pytest.mark.parametrize("new", [[1, 1, 1], [3, 0, 40], [300, 17, 129], [0, 1, 2]])
+@pytest.mark.parametrize("call", ["prompt", "prefix", "groups"])
+def test_output_in_the_queries_place(heads, kv, dim, dtype, new, call):
+    rows = [max(n, 400) for n in new]
+    b, _, start, q, k, v = _inputs(new, rows, heads, kv, dim, dtype, seed=dim, lead=1, tail=2,
+                                   extra=[500])
+    gr = dict(num_groups=1, cu_group=_i32([0, 2]), max_prefix=500, prefix_start=_i64(start[-1:]),
+              prefix_len=_i64([500])) if call == "groups" else None
+
+    def run(q, out):
+        if call == "prompt":
+            return S.prompt_attn(b, q, k, v, out=out)
+        return S.prefix_attn(b, gr, q, k, v, 400, out=out)
+
+    out = q.clone()                      # rows of no request keep their values
+    want, lse = run(q, out)
+    x = q.clone()
+    got, l2 = run(x, x)
+    n = slice(1, 1 + sum(new))
+    assert torch.equal(got.nan_to_num(9.0), want.nan_to_num(9.0)) and torch.equal(lse[n], l2[n])
+
+
+def test_output_between_the_rows_of_an_input():
+    """One row of output beside the one cache row that is read in longer rows."""
+    x = torch.randn((40, 4, 64), device=DEV).to(BF)          # k, v and two heads of room
+    q = torch.randn((1, 2, 64), device=DEV).to(BF)
+    b, _ = R.batch([1], [40], [0], DEV)
+    want, _ = S.prompt_attn(b, q, x[:, :1], x[:, 1:2])
+    y = x.clone()
+    S.prompt_attn(b, q, y[:, :1], y[:, 1:2], out=y[7:8, 2:])
+    assert torch.equal(y[7, 2:], want[0])
+    y[7, 2:] = x[7, 2:]
+    assert torch.equal(x, y)
