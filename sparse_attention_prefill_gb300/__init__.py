@@ -492,11 +492,15 @@ _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 _EVICT_BUF = struct.Struct("=QQ7q")
 
 
-def _arg(t, dtype, name, numel, dev):
+def _arg(t, dtype, name, numel, dev, tail=None):
     """Address of a contiguous tensor of a type, with at least numel values, on
-    CUDA device dev (None: NULL)."""
+    CUDA device dev (None: NULL).  ``tail``: the sizes behind the first that it
+    must have if it has as many dimensions (a flat one is taken as it is)."""
     if t is None:
         return None
+    if tail is not None and t.dim() == len(tail) + 1 and t.shape[1:] != tail:
+        raise Csa2Error("%s: expected a shape of [.., %s], got %s"
+                        % (name, ", ".join(map(str, tail)), tuple(t.shape)))
     if t.dtype is not dtype or t.get_device() != dev or t.numel() < numel \
             or not t.is_contiguous():
         if t.get_device() < 0:
@@ -593,12 +597,12 @@ def _attn_args(packed, q, k, v, out, lse, want_lse, d_err, stream):
         out = _new(torch.empty, q.shape, dt, q.device, stream)
         op = out.data_ptr()
     else:
-        op = _arg(out, dt, "out", n * shape[2], dev)
+        op = _arg(out, dt, "out", n * shape[2], dev, (shape[0], shape[2]))
     if lse is None and want_lse:
         lse = _new(torch.empty, q.shape[:2], _F32, q.device, stream)
         lp = lse.data_ptr()
     else:
-        lp = _arg(lse, _F32, "lse", n, dev)
+        lp = _arg(lse, _F32, "lse", n, dev, (shape[0],))
     return (st, dev, shape + (vp, ldv, rows), (op, lp), _arg(d_err, _I32, "d_err", 1, dev),
             out, lse)
 
@@ -663,9 +667,10 @@ def csa2_attn_mass(packed, q, k, lse, max_kv, sm_scale, mass_in, mass_out, d_err
     st, dev, _, rows, shape = _packed_args(packed, q, k)
     n = rows * shape[1]
     return _call(dev, load().csa2_attn_mass,
-                 (C.byref(st), *shape, rows, _arg(lse, _F32, "lse", st.num_q * shape[0], dev),
-                  int(max_kv), float(sm_scale), _arg(mass_in, _F32, "mass_in", n, dev),
-                  _arg(mass_out, _F32, "mass_out", n, dev),
+                 (C.byref(st), *shape, rows,
+                  _arg(lse, _F32, "lse", st.num_q * shape[0], dev, (shape[0],)), int(max_kv),
+                  float(sm_scale), _arg(mass_in, _F32, "mass_in", n, dev, (rows,)),
+                  _arg(mass_out, _F32, "mass_out", n, dev, (rows,)),
                   _arg(d_err, _I32, "d_err", 1, dev)), stream)
 
 
@@ -677,7 +682,7 @@ def csa2_evict_select(num_req, kv_start, kv_len, mass, keep, sink, recent, idx, 
                  (num_req, h, _arg(kv_start, _I64, "kv_start", num_req, dev),
                   _arg(kv_len, _I64, "kv_len", num_req, dev), _arg(mass, _F32, "mass", 0, dev),
                   rows, keep, int(sink), int(recent),
-                  _arg(idx, _I32, "idx", num_req * h * keep, dev),
+                  _arg(idx, _I32, "idx", num_req * h * keep, dev, (h, keep)),
                   _arg(new_len, _I64, "new_len", num_req, dev),
                   _arg(d_err, _I32, "d_err", 1, dev)), stream)
 
@@ -708,11 +713,12 @@ def csa2_evict_rows(num_req, n_heads, idx, keep, new_len, src_start, dst_start, 
     """``bufs``: (source, destination) pairs of [rows, heads, ...] tensors (a
     transposed view for head-major ones)."""
     num_req, keep, dev = int(num_req), int(keep), idx.get_device()
-    ip = _arg(idx, _I32, "idx", num_req * n_heads * keep, dev)
+    n_heads = int(n_heads)
+    ip = _arg(idx, _I32, "idx", num_req * n_heads * keep, dev, (n_heads, keep))
     # csa2_evict_buf is nine 64-bit fields
     arr = b"".join([_EVICT_BUF.pack(*_evict_buf(s, d, n_heads, dev)) for s, d in bufs])
     return _call(dev, load().csa2_evict_rows,
-                 (num_req, int(n_heads), ip, keep, _arg(new_len, _I64, "new_len", num_req, dev),
+                 (num_req, n_heads, ip, keep, _arg(new_len, _I64, "new_len", num_req, dev),
                   _arg(src_start, _I64, "src_start", num_req, dev),
                   _arg(dst_start, _I64, "dst_start", num_req, dev), len(bufs), arr,
                   _arg(d_err, _I32, "d_err", 1, dev)), stream)

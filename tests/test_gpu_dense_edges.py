@@ -391,3 +391,67 @@ def test_output_between_the_rows_of_an_input():
     assert torch.equal(y[7, 2:], want[0])
     y[7, 2:] = x[7, 2:]
     assert torch.equal(x, y)
+
+
+# ---------------------------------------------------------------------------
+# shapes
+# ---------------------------------------------------------------------------
+
+def test_tensors_of_another_layout_are_refused():
+    """As many values as the call wants, or more, in rows of another length."""
+    b, _, start, q, k, v = _inputs([2, 1], [40, 30], 4, 2, 64, BF)
+    pool = k.shape[0]
+    out, lse = S.prompt_attn(b, q, k, v)
+    mass = S.attn_mass(b, q, k, lse, 40)
+    idx, n = S.evict_select(b["kv_start"], b["kv_len"], mass, 8)
+    e = lambda *s: torch.empty(s, device=DEV)              # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)   # noqa: E731
+    for call in (lambda: S.prompt_attn(b, q, k, v, out=torch.empty((3, 4, 128), dtype=BF, device=DEV)),
+                 lambda: S.prompt_attn(b, q, k, v, out=torch.empty((3, 8, 64), dtype=BF, device=DEV)),
+                 lambda: S.prefix_attn(b, None, q, k, v, 40, lse=e(3, 5)),
+                 lambda: S.attn_mass(b, q, k, e(3, 8), 40),
+                 lambda: S.attn_mass(b, q, k, lse, 40, mass=e(2, pool + 1)),
+                 lambda: S.attn_mass(b, q, k, lse, 40, mass_in=e(2, pool + 1)),
+                 lambda: S.attn_mass(b, q, k, lse, 40, mass=e(pool, 2)),
+                 lambda: S.evict_select(b["kv_start"], b["kv_len"], mass, 8, idx=i(2, 2, 9)),
+                 lambda: S.evict_select(b["kv_start"], b["kv_len"], mass, 8, idx=i(4, 1, 8)),
+                 lambda: S.csa2_evict_rows(2, 2, i(2, 4, 8), 8, n, b["kv_start"], b["kv_start"],
+                                           [(k, k)], None)):
+        with pytest.raises(S.Csa2Error):
+            call()
+    # more rows, or flat
+    big = torch.empty((5, 4, 64), dtype=BF, device=DEV)
+    S.prompt_attn(b, q, k, v, out=big, lse=e(99))
+    assert torch.equal(big[:3], out)
+    flat = torch.zeros(2 * pool, device=DEV)
+    S.attn_mass(b, q, k, lse.view(-1), 40, mass=flat)
+    assert torch.equal(flat.view(2, pool), mass)
+
+
+def test_calls_on_a_side_stream_are_captured():
+    """Outputs and workspaces allocated in a capture, on a stream forked in it."""
+    b, _, start, q, k, v = _inputs([1] * 9, [300] * 9, 8, 2, 128, BF)
+    weight = torch.rand((2, k.shape[0]), device=DEV)
+
+    def calls(stream):
+        out, lse = S.prefix_attn(b, None, q, k, v, 300, stream=stream)
+        o2, _ = S.prompt_attn(b, q, k, v, stream=stream)
+        mass = S.attn_mass(b, q, k, lse, 300, stream=stream)
+        idx, n = S.evict_select(b["kv_start"], b["kv_len"], weight, 100, 3, 5, stream=stream)
+        return out, lse, o2, mass, idx, n
+
+    want = calls(None)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        got = calls(side)
+        main.wait_stream(side)
+    for _ in range(2):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(want, got):
+            assert torch.equal(x, y)
