@@ -1,5 +1,7 @@
 """Dense-cache calls at the edges of what their arguments allow: malformed
 device data, overlapping arguments, streams, sizes that choose rare variants."""
+import math
+
 import pytest
 import torch
 
@@ -455,3 +457,129 @@ def test_calls_on_a_side_stream_are_captured():
         torch.cuda.synchronize()
         for x, y in zip(want, got):
             assert torch.equal(x, y)
+
+
+# ---------------------------------------------------------------------------
+# sizes that choose rare variants
+# ---------------------------------------------------------------------------
+
+def _check_masses(q, k, lse, mass, cu, start, new, rows, scale, which):
+    for r in which:
+        at = slice(start[r], start[r] + rows[r])
+        last = rows[r] - new[r] + torch.arange(new[r], device=DEV)
+        w, tol = R.mass(q[cu[r]:cu[r + 1]], k[at], lse[cu[r]:cu[r + 1]], scale, last)
+        d = (mass[:, at].double() - w).abs()
+        assert (d <= tol + w * 2.0 ** -23 + 1e-30).all(), r
+
+
+@pytest.mark.parametrize("heads,dim,dtype,new", [
+    (8, 64, HF, 70), (24, 128, BF, 131), (64, 128, BF, 1), (128, 64, BF, 3)])
+def test_mass_four_key_tiles_an_item(heads, dim, dtype, new):
+    """Enough rows that an item has four key tiles, the last of it in part."""
+    kv, rows = 8, [9001, 7300, 8000, 7937, 1, 130, 12345, 15100]
+    n = [min(new, m) for m in rows]
+    assert (sum(rows) // 128 + 8) * kv >= 4 * 6 * 152
+    b, cu, start, q, k, v = _inputs(n, rows, heads, kv, dim, dtype, seed=new)
+    _, lse = S.prompt_attn(b, q, k, v)
+    mass = S.attn_mass(b, q, k, lse, max(rows))
+    _check_masses(q, k, lse, mass, cu, start, n, rows, dim ** -0.5, range(8))
+    assert torch.equal(mass, S.attn_mass(b, q, k, lse, 10 ** 9))
+
+
+def test_mass_of_many_requests_shortens_the_ring():
+    """Thousands of requests leave shared memory for three key tiles: items that
+    were meant to have four have two."""
+    reqs = 8000
+    rows = [1 + (53 * i) % 90 if i % 40 else 300 + i % 500 for i in range(reqs)]
+    b, cu, start, q, k, v = _inputs([1] * reqs, rows, 128, 1, 128, BF, seed=3)
+    _, lse = S.prompt_attn(b, q, k, v)
+    mass = S.attn_mass(b, q, k, lse, max(rows))
+    _check_masses(q, k, lse, mass, cu, start, [1] * reqs, rows, 128 ** -0.5,
+                  list(range(0, reqs, 200)) + [1, 7, 3999, 7999])
+    # every query's weights sum to one
+    assert abs(float(mass.double().sum()) - reqs * 128) <= 1e-4 * reqs * 128
+
+
+@pytest.mark.parametrize("rows,pool", [(12400, 0), (16500, 0), (20600, 0), (24700, 0), (28800, 0),
+                                       (40000, 0), (700, 40000)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_select_by_clusters_of_every_size(rows, pool, ties):
+    """Three to eight CTAs to a request and head; a short request in a long pool."""
+    keep, sink, recent, heads = min(rows // 3, 4000), 7, 100, 8
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    mass = torch.rand((heads, max(rows + 9, pool)), generator=g, device=DEV)
+    if ties:
+        mass = (mass * 50).floor()
+    for start in (0, 9):
+        idx, n = S.evict_select(_i64([start]), _i64([rows]), mass, keep, sink, recent)
+        assert n.tolist() == [keep]
+        for h in range(heads):
+            order = mass[h, start:start + rows].clone()
+            order[:sink] = order[rows - recent:] = math.inf
+            want = torch.sort(order, descending=True, stable=True).indices[:keep].sort().values
+            assert torch.equal(idx[0, h].long(), want)
+
+
+def test_mass_of_whole_prompts():
+    """Every query of two prompts, many query tiles to a key tile."""
+    rows = [2500, 701]
+    b, cu, start, q, k, v = _inputs(rows, rows, 8, 1, 128, BF, seed=12)
+    _, lse = S.prompt_attn(b, q, k, v)
+    mass = S.attn_mass(b, q, k, lse, 2500)
+    _check_masses(q, k, lse, mass, cu, start, rows, rows, 128 ** -0.5, range(2))
+    assert abs(float(mass.double().sum()) - 3201 * 8) <= 1e-4 * 3201 * 8
+
+
+def test_mass_without_queries_is_carried_over():
+    b, _, start, _, k, _ = _inputs([0, 0], [300, 40], 4, 2, 64, BF)
+    old = torch.rand((2, k.shape[0]), device=DEV)
+    new = torch.full_like(old, 5.0)
+    q = torch.empty((0, 4, 64), dtype=BF, device=DEV)
+    S.attn_mass(b, q, k, torch.empty((0, 4), device=DEV), 300, mass_in=old, mass=new)
+    held = torch.zeros(k.shape[0], dtype=torch.bool, device=DEV)
+    for s, n in zip(start, (300, 40)):
+        held[s:s + n] = True
+    assert torch.equal(new[:, held], old[:, held]) and (new[:, ~held] == 5).all()
+
+
+@pytest.mark.parametrize("new", [1, 5])
+def test_many_groups_and_many_key_heads(new):
+    """More groups than a warp has lanes, every third request in none; 200 key
+    heads of their own."""
+    reqs, kv, dim = 120, 200, 64
+    rows = [new + 3 * i % 50 for i in range(reqs)]
+    pre = [30 + i for i in range(reqs // 3)]
+    b, cu, start, q, k, v = _inputs([new] * reqs, rows, kv, kv, dim, BF, seed=new, extra=pre)
+    # group g: requests 3 g and 3 g + 1, behind it a group of request 3 g + 2
+    # without a prefix
+    cug, ps, pl = [0], [], []
+    for g in range(reqs // 3):
+        cug += [3 * g + 2, 3 * g + 3]
+        ps += [start[reqs + g], 0]
+        pl += [pre[g], 0]
+    gr = dict(num_groups=len(pl), cu_group=_i32(cug), prefix_start=_i64(ps), prefix_len=_i64(pl),
+              max_prefix=max(pre))
+    out, lse = S.prefix_attn(b, gr, q, k, v, max(rows))
+    for r in list(range(0, reqs, 11)) + [2, 119]:
+        at = slice(cu[r], cu[r + 1])
+        kk, vv, off = k[start[r]:start[r] + rows[r]], v[start[r]:start[r] + rows[r]], 0
+        if r % 3 != 2:
+            p, off = start[reqs + r // 3], pre[r // 3]
+            kk, vv = torch.cat([k[p:p + off], kk]), torch.cat([v[p:p + off], vv])
+        last = off + rows[r] - new + torch.arange(new, device=DEV)
+        ref = R.attend(q[at], kk, vv, dim ** -0.5, last)
+        R.check_attention(out[at], lse[at], ref, BF, kk.shape[0])
+
+
+@pytest.mark.parametrize("new", [[1, 1], [70, 3]])
+def test_without_lse_and_without_groups_in_a_dict(new):
+    b, _, _, q, k, v = _inputs(new, [200, 90], 8, 2, 64, HF, seed=2)
+    none = dict(num_groups=0, cu_group=_i32([0]), prefix_start=_i64([]), prefix_len=_i64([]),
+                max_prefix=0)
+    out, lse = S.prompt_attn(b, q, k, v, want_lse=False)
+    assert lse is None and torch.equal(out, S.prompt_attn(b, q, k, v)[0])
+    want = S.prefix_attn(b, None, q, k, v, 200)
+    out, lse = S.prefix_attn(b, none, q, k, v, 200, want_lse=False)
+    assert lse is None and torch.equal(out, want[0])
+    got = S.prefix_attn(b, none, q, k, v, 200)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
