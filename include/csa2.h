@@ -484,7 +484,8 @@ CSA2_API int csa2_quantize_rows(int32_t format, int64_t n, const float *src, int
  *   num_q       rows of q and of the outputs
  *   num_req     requests
  *   cu_q[R+1]   request r holds query rows cu_q[r] .. cu_q[r+1]-1, ascending;
- *               rows that no request holds are not touched
+ *               rows that no request holds are not touched, and what a row of
+ *               two requests (which takes a descent in cu_q) gets is not defined
  *   kv_start[R] first row of the request in the K and V pools
  *   kv_len[R]   rows of the request in the pools, m_r, the new ones included:
  *               query i of n_r is at position m_r - n_r + i and sees the rows

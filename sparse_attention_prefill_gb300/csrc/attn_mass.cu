@@ -124,12 +124,13 @@ __device__ void schedule_role(const MassParams &P, uint8_t *smem, MassMisc *ms) 
         const int mid = (lo + hi) >> 1;
         if (cum[mid] > tile) hi = mid; else lo = mid + 1;
       }
-      const int kt = (int)(tile - (lo ? cum[lo - 1] : 0u));
+      // (below 0 only where requests that share rows made the sum wrap)
+      const int64_t kt = (int64_t)tile - (lo ? cum[lo - 1] : 0u);
       int64_t start, m;
       seq_rows(P.seqs, lo, it.q0, it.n, err);
       seq_keys(P.seqs, lo, start, m, err);
-      const int64_t k0 = (int64_t)kt * P.span * kTile, left = m - k0;
-      it.keys = left < 0 ? 0 : left < P.span * kTile ? (int)left : P.span * kTile;
+      const int64_t k0 = kt * P.span * kTile, left = m - k0;
+      it.keys = kt < 0 || left < 0 ? 0 : left < P.span * kTile ? (int)left : P.span * kTile;
       it.row = start + k0;
       it.shift = m - it.n - k0;
       const int64_t first = it.shift >= 0 ? 0 : -it.shift;      // first query that sees key 0

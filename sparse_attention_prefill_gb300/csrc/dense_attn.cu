@@ -112,16 +112,17 @@ struct Misc {
   float2 stat[kTile];                // narrow items: reference and sum of stream 1's rows
 };
 // Items of a part's runs, as a warp holds them: lane l has those of an equal
-// share of the runs, and the sum up to and with its share.
+// share of the runs, and the sum up to and with its share.  Unsigned: the runs of
+// a malformed batch may lie over one another and sum up to anything.
 struct Shares {
-  int own, upto;
+  uint32_t own, upto;
 };
 
-__device__ __forceinline__ int lane_scan(int v) {
+__device__ __forceinline__ uint32_t lane_scan(uint32_t v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   return v;
@@ -134,7 +135,7 @@ __device__ Shares count_items(const AttnParams &P, int tok, int &err) {
   for (int i = lane * per; i < min(P.seqs.count, (lane + 1) * per); ++i) {
     int a, c;
     seq_rows(P.seqs, i, a, c, err);
-    s.own += (c + tok - 1) / tok;
+    s.own += ((uint32_t)c + tok - 1) / tok;
   }
   s.upto = lane_scan(s.own);
   return s;
@@ -149,12 +150,12 @@ __device__ void find_item(const AttnParams &P, uint32_t cta, const Shares &s, It
   const int per = (P.seqs.count + 31) / 32;
   it.split = (int)(cta % ns);
   it.h = (int)(cta / ns % P.n_kv);
-  const int slot = (int)(cta / ns / P.n_kv);
+  const uint32_t slot = cta / ns / P.n_kv;
   it.run = -1;
   const uint32_t share = __ballot_sync(0xffffffffu, slot < s.upto);
   if (!share) return;
   const int l = __ffs(share) - 1;
-  int base = __shfl_sync(0xffffffffu, s.upto - s.own, l);
+  uint32_t base = __shfl_sync(0xffffffffu, s.upto - s.own, l);
   const int end = min(P.seqs.count, (l + 1) * per);
   for (int i0 = l * per; i0 < end && it.run < 0; i0 += 32) {
     // everything of a lane's run at once
@@ -164,13 +165,15 @@ __device__ void find_item(const AttnParams &P, uint32_t cta, const Shares &s, It
       seq_rows(P.seqs, i0 + lane, a, c, err);
       seq_keys(P.seqs, i0 + lane, start, m, err);
     }
-    const int inc = lane_scan((c + tok - 1) / tok);
+    const uint32_t here = ((uint32_t)c + tok - 1) / tok, inc = lane_scan(here);
     const uint32_t hit = __ballot_sync(0xffffffffu, slot < base + inc);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      it.run = i0 + src;
       // the longest key ranges first
-      it.tok0 = (__shfl_sync(0xffffffffu, base + inc, src) - 1 - slot) * tok;
+      const uint32_t item = __shfl_sync(0xffffffffu, base + inc, src) - 1 - slot;
+      if (item >= __shfl_sync(0xffffffffu, here, src)) return;      // sums that wrapped
+      it.run = i0 + src;
+      it.tok0 = (int)item * tok;
       it.q0 = __shfl_sync(0xffffffffu, a, src);
       it.n = __shfl_sync(0xffffffffu, c, src);
       it.start = __shfl_sync(0xffffffffu, start, src);

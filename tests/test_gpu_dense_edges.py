@@ -583,3 +583,18 @@ def test_without_lse_and_without_groups_in_a_dict(new):
     assert lse is None and torch.equal(out, want[0])
     got = S.prefix_attn(b, none, q, k, v, 200)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_runs_over_one_another_past_two_to_the_32_items():
+    """Runs of a malformed batch that all hold every row: more items than the grid
+    has, or 32 bits; flagged, and every row written is one of the batch's."""
+    reqs, num_q = 140001, 1 << 16
+    q = torch.randn((num_q, 20, 64), device=DEV).to(BF)
+    k = torch.randn((100, 1, 64), device=DEV).to(BF)
+    b = dict(num_q=num_q, num_req=reqs, kv_start=_i64([0] * reqs), kv_len=_i64([100] * reqs),
+             cu_q=_i32([0, num_q] * (reqs // 2 + 1)))
+    room = torch.full((num_q + 4096, 20, 64), 7.0, dtype=BF, device=DEV)
+    d = _derr()
+    S.prompt_attn(b, q, k, k, out=room[2048:2048 + num_q], d_err=d)
+    assert int(d.item()) == S.DERR_BAD_EXTEND
+    assert (room[:2048] == 7).all() and (room[2048 + num_q:] == 7).all()
