@@ -505,8 +505,8 @@ CSA2_API int csa2_quantize_rows(int32_t format, int64_t n, const float *src, int
  * some query of a tile sees reaches the queries in front of it too.
  * Supported: dim in {64, 128}, n_heads / n_kv_heads <= 128, n_kv_heads <=
  * 1024, kv_rows < 2^31 - 256, 0 < sm_scale < inf (CSA2_ERR_INVALID_ARG);
- * bases and outputs 16-byte aligned, row distances multiples of 8 elements
- * (CSA2_ERR_UNSUPPORTED otherwise).  Outputs and workspaces share no bytes with
+ * bases and `out` 16-byte aligned, other arrays to their elements, row distances
+ * multiples of 8 elements (CSA2_ERR_UNSUPPORTED otherwise).  Outputs and workspaces share no bytes with
  * the inputs or each other (CSA2_ERR_INVALID_ARG), except where a call allows
  * it.
  * ------------------------------------------------------------------------- */
@@ -644,8 +644,9 @@ typedef struct csa2_evict_buf {
  * destinations (CSA2_ERR_INVALID_ARG).  Rows of dst that are not named keep
  * their bytes.  A negative idx is skipped; a row outside src_rows or dst_rows
  * is skipped (CSA2_DERR_RANGE_ROW).  Host structs, read during the call only.
- * Pointers and strides multiples of 4 bytes; copies are widest where they are
- * all multiples of 16. */
+ * Buffers' pointers and strides multiples of 4 bytes, other arrays aligned to
+ * their elements (CSA2_ERR_UNSUPPORTED otherwise); copies are widest where
+ * pointers and strides are all multiples of 16. */
 CSA2_API int csa2_evict_rows(int32_t num_req, int32_t n_heads, const int32_t *idx, int32_t keep,
                              const int64_t *new_len, const int64_t *src_start,
                              const int64_t *dst_start, int32_t n_bufs,

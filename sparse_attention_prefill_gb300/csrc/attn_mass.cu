@@ -510,7 +510,7 @@ extern "C" CSA2_API int csa2_attn_mass(const csa2_packed *b, int32_t n_heads, in
   if (b->num_req > kMaxReq) return CSA2_ERR_UNSUPPORTED;
   if ((st = check_rows(k, ldk, s.n_kv, s.dim)) != CSA2_OK) return st;
   if (b->num_q > 0 && (st = check_rows(q, ldq, s.n_heads, s.dim)) != CSA2_OK) return st;
-  if (((uintptr_t)mass_in | (uintptr_t)mass_out | (uintptr_t)lse) & 3u) return CSA2_ERR_UNSUPPORTED;
+  if (!csa2::aligned(4, mass_in, mass_out, lse, d_err)) return CSA2_ERR_UNSUPPORTED;
   const uint64_t cells = (uint64_t)s.n_kv * kv_rows * 4;
   if (meets_batch(mass_out, cells, b) ||
       meets_rows(mass_out, cells, k, kv_rows, ldk * 2, (int64_t)s.n_kv * s.dim * 2) ||

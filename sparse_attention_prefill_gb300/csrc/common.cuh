@@ -54,6 +54,13 @@ static inline void allow_smem(int bytes) {
     done.fetch_or(bit, std::memory_order_relaxed);
 }
 
+// Whether every array (or null) begins at a multiple of `bytes`, its element's size:
+// a load at any other address would fault.
+template <typename... P>
+static inline bool aligned(uintptr_t bytes, const P *...p) {
+  return (((uintptr_t)p | ... | 0) & (bytes - 1)) == 0;
+}
+
 // Whether two runs of bytes share one.
 static inline bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
   const uint64_t x = (uint64_t)(uintptr_t)a, y = (uint64_t)(uintptr_t)b;

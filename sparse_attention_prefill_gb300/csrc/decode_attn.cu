@@ -350,7 +350,9 @@ decode_attn_kernel(const __grid_constant__ DecodeParams P) {
   int64_t start = S.kv_start[run], m = S.kv_len[run];
   const uint32_t at = (uint32_t)slot + (first > 0 && first < S.num_q ? (uint32_t)first : 0u);
   const int token = (int)(at < (uint32_t)S.num_q ? at : at - S.num_q);
-  const auto holds = [&]() { return q0 >= 0 && q0 <= token && token < behind && behind <= S.num_q; };
+  const auto holds = [&]() {
+    return q0 >= 0 && q0 <= token && token < behind && behind <= S.num_q;
+  };
   bool sweep = false;
   if (!holds()) {
     // Rows in front of the first request and behind the last are nobody's, unless

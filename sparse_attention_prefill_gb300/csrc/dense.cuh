@@ -324,6 +324,7 @@ inline int check_packed(const csa2_packed *b, int32_t n_heads, int32_t n_kv_head
   if (kv_rows > 0x7fffffffll - 2 * kTile) return CSA2_ERR_UNSUPPORTED;
   if (b->num_q > 0 && b->num_req > 0 && (!b->cu_q || !b->kv_start || !b->kv_len))
     return CSA2_ERR_INVALID_ARG;
+  if (!aligned(4, b->cu_q) || !aligned(8, b->kv_start, b->kv_len)) return CSA2_ERR_UNSUPPORTED;
   *s = Shape{n_heads, n_kv_heads, dim, n_heads / n_kv_heads, dtype == CSA2_DT_BF16};
   return CSA2_OK;
 }

@@ -1068,7 +1068,7 @@ extern "C" CSA2_API int csa2_prompt_attn(const csa2_packed *b, int32_t n_heads,
   const Cache c{q, k, v, ldq, ldk, ldv, kv_rows};
   if (!out) return CSA2_ERR_INVALID_ARG;
   if ((st = check_cache(b, s, c)) != CSA2_OK) return st;
-  if ((uintptr_t)out & 15u) return CSA2_ERR_UNSUPPORTED;
+  if (!csa2::aligned(16, out) || !csa2::aligned(4, lse, d_err)) return CSA2_ERR_UNSUPPORTED;
   if (outputs_meet(b, nullptr, s, c, out, lse, nullptr, 0)) return CSA2_ERR_INVALID_ARG;
   AttnParams P{};
   P.seqs = Seqs{b->num_req, b->num_q, b->num_req, b->cu_q, nullptr, b->kv_start, b->kv_len,
@@ -1120,7 +1120,10 @@ extern "C" CSA2_API int csa2_prefix_attn(const csa2_packed *b, const csa2_prefix
   const Cache c{q, k, v, ldq, ldk, ldv, kv_rows};
   if (!out) return CSA2_ERR_INVALID_ARG;
   if ((st = check_cache(b, s, c)) != CSA2_OK) return st;
-  if ((uintptr_t)out & 15u) return CSA2_ERR_UNSUPPORTED;
+  if (!csa2::aligned(16, out) || !csa2::aligned(4, lse, d_err)) return CSA2_ERR_UNSUPPORTED;
+  if (ng > 0 &&
+      !(csa2::aligned(4, g->cu_group) && csa2::aligned(8, g->prefix_start, g->prefix_len)))
+    return CSA2_ERR_UNSUPPORTED;
   PrefixPlan p = plan_prefix(s, b->num_q, b->num_req, ng, ng ? g->max_prefix : 0, max_kv);
   if (!workspace || !fit_splits(&p, workspace_bytes / part_bytes(b->num_q, s)))
     return CSA2_ERR_INVALID_ARG;

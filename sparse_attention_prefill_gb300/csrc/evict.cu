@@ -434,7 +434,8 @@ extern "C" CSA2_API int csa2_evict_select(int32_t num_req, int32_t n_heads,
   if (!kv_start || !kv_len || !idx || !new_len || (kv_rows > 0 && !mass))
     return CSA2_ERR_INVALID_ARG;
   if (kv_rows > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
-  if ((uintptr_t)mass & 3u) return CSA2_ERR_UNSUPPORTED;
+  if (!aligned(4, mass, idx, d_err) || !aligned(8, kv_start, kv_len, new_len))
+    return CSA2_ERR_UNSUPPORTED;
   const int64_t pairs = (int64_t)num_req * n_heads;
   if (pairs > 0x7fffffffll / 8) return CSA2_ERR_UNSUPPORTED;
   const uint64_t lens = (uint64_t)num_req * 8, ids = (uint64_t)pairs * keep * 4;
@@ -495,6 +496,8 @@ extern "C" CSA2_API int csa2_evict_rows(int32_t num_req, int32_t n_heads, const 
   if (num_req == 0 || n_bufs == 0) return CSA2_OK;
   if (!idx || !new_len || !src_start || !dst_start || !bufs) return CSA2_ERR_INVALID_ARG;
   if (n_bufs > kMaxBufs) return CSA2_ERR_UNSUPPORTED;
+  if (!aligned(4, idx, d_err) || !aligned(8, new_len, src_start, dst_start))
+    return CSA2_ERR_UNSUPPORTED;
   MoveParams P{};
   bool in_place = false;
   int64_t most = 0;

@@ -21,7 +21,8 @@ def lib():
 @pytest.mark.parametrize("kw", [
     dict(new=2 * AT + 8), dict(new=2 * AT - 8), dict(new=AT), dict(new=AT + 16), dict(new=3 * AT),
     dict(new=3 * AT + 792), dict(idx=AT), dict(idx=AT - 236), dict(idx=2 * AT + 20),
-    dict(idx=3 * AT + 796), dict(idx=5 * AT + 20), dict(idx=5 * AT - 236), dict(idx=2 * AT, new=2 * AT)])
+    dict(idx=3 * AT + 796), dict(idx=5 * AT + 20), dict(idx=5 * AT - 236),
+    dict(idx=2 * AT, new=2 * AT)])
 def test_select_outputs_that_overlap_are_refused(lib, kw):
     d = dict(idx=4 * AT, new=5 * AT)
     d.update(kw)
@@ -76,8 +77,8 @@ def test_rows_one_destination_twice_is_refused(lib, first, second):
 # 10 query rows of 8 x 128 (20480 bytes), 100 cache rows of 2 x 128 (51200
 # bytes, or 1024 bytes apart), lse 320 bytes, mass 800, 2 requests, 1 group
 def _attn(lib, prefix, **kw):
-    d = dict(cu=AT, ks=2 * AT, kl=3 * AT, q=4 * AT, ldq=1024, k=5 * AT, v=6 * AT, ld=256, out=7 * AT,
-             lse=8 * AT, ws=9 * AT, cug=10 * AT, ps=11 * AT, pl=12 * AT)
+    d = dict(cu=AT, ks=2 * AT, kl=3 * AT, q=4 * AT, ldq=1024, k=5 * AT, v=6 * AT, ld=256,
+             out=7 * AT, lse=8 * AT, ws=9 * AT, cug=10 * AT, ps=11 * AT, pl=12 * AT)
     d.update(kw)
     b = S.CPacked(10, 2, d["cu"], d["ks"], d["kl"])
     args = [8, 2, 128, S.DT_BF16, d["q"], d["ldq"], d["k"], d["ld"], d["v"], d["ld"], 100]
@@ -89,14 +90,15 @@ def _attn(lib, prefix, **kw):
 
 
 BOTH = [
-    dict(out=5 * AT), dict(out=6 * AT + 51200 - 16), dict(out=5 * AT - 20480 + 16), dict(lse=7 * AT),
-    dict(lse=7 * AT + 20476), dict(lse=4 * AT + 20000), dict(lse=6 * AT), dict(out=4 * AT + 16),
+    dict(out=5 * AT), dict(out=6 * AT + 51200 - 16), dict(out=5 * AT - 20480 + 16),
+    dict(lse=7 * AT), dict(lse=7 * AT + 20476), dict(lse=4 * AT + 20000), dict(lse=6 * AT), dict(out=4 * AT + 16),
     dict(out=4 * AT, ldq=2048), dict(out=4 * AT + 2048, ldq=2048), dict(out=AT), dict(out=2 * AT),
     dict(lse=3 * AT + 12), dict(out=5 * AT + 512, ld=512)]
 
 
 @pytest.mark.parametrize("prefix,kw", [(p, kw) for p in (False, True) for kw in BOTH] + [
-    (True, dict(ws=5 * AT)), (True, dict(ws=4 * AT)), (True, dict(ws=7 * AT)), (True, dict(ws=8 * AT)),
+    (True, dict(ws=5 * AT)), (True, dict(ws=4 * AT)), (True, dict(ws=7 * AT)),
+    (True, dict(ws=8 * AT)),
     (True, dict(ws=6 * AT + 51200 - 256)), (True, dict(ws=10 * AT)), (True, dict(out=11 * AT)),
     (True, dict(out=12 * AT - 16))])
 def test_attention_outputs_that_overlap_are_refused(lib, prefix, kw):
@@ -105,11 +107,52 @@ def test_attention_outputs_that_overlap_are_refused(lib, prefix, kw):
 
 @pytest.mark.parametrize("kw", [
     dict(mass=4 * AT), dict(mass=5 * AT), dict(mass=5 * AT + 51200 - 4), dict(mass=8 * AT),
-    dict(mass=8 * AT - 796), dict(old=13 * AT + 400, mass=13 * AT), dict(old=13 * AT - 4, mass=13 * AT),
+    dict(mass=8 * AT - 796), dict(old=13 * AT + 400, mass=13 * AT),
+    dict(old=13 * AT - 4, mass=13 * AT),
     dict(mass=AT), dict(mass=3 * AT + 8)])
 def test_mass_outputs_that_overlap_are_refused(lib, kw):
     d = dict(old=None)
     d.update(kw)
     b = S.CPacked(10, 2, AT, 2 * AT, 3 * AT)
-    assert lib.csa2_attn_mass(C.byref(b), 8, 2, 128, S.DT_BF16, 4 * AT, 1024, 5 * AT, 256, 100, 8 * AT,
-                              90, 0.1, d["old"], d["mass"], None, None) == INV
+    assert lib.csa2_attn_mass(C.byref(b), 8, 2, 128, S.DT_BF16, 4 * AT, 1024, 5 * AT, 256, 100,
+                              8 * AT, 90, 0.1, d["old"], d["mass"], None, None) == INV
+
+
+# ---------------------------------------------------------------------------
+# arrays that are not aligned to their elements
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("prefix,kw", [(p, kw) for p in (False, True) for kw in (
+    dict(cu=AT + 2), dict(ks=2 * AT + 4), dict(kl=3 * AT + 4), dict(lse=8 * AT + 2),
+    dict(out=7 * AT + 8))] + [
+    (True, dict(cug=10 * AT + 1)), (True, dict(ps=11 * AT + 4)), (True, dict(pl=12 * AT + 4))])
+def test_attention_misaligned_arrays_are_refused(lib, prefix, kw):
+    assert _attn(lib, prefix, **kw) == S.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("at", range(6))
+def test_mass_misaligned_arrays_are_refused(lib, at):
+    off = [0] * 6
+    off[at] = 4 if at in (1, 2) else 2
+    b = S.CPacked(10, 2, AT + off[0], 2 * AT + off[1], 3 * AT + off[2])
+    assert lib.csa2_attn_mass(C.byref(b), 8, 2, 128, S.DT_BF16, 4 * AT, 1024, 5 * AT, 256, 100,
+                              8 * AT + off[3], 90, 0.1, 9 * AT + off[4], 13 * AT, 14 * AT + off[5],
+                              None) == S.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("at", range(5))
+def test_select_misaligned_arrays_are_refused(lib, at):
+    off = [0] * 5
+    off[at] = 2 if at in (2, 4) else 4
+    assert lib.csa2_evict_select(3, 2, AT + off[0], 2 * AT + off[1], 3 * AT, 100, 10, 1, 2,
+                                 4 * AT + off[2], 5 * AT + off[3], 6 * AT + off[4],
+                                 None) == S.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("at", range(5))
+def test_rows_misaligned_arrays_are_refused(lib, at):
+    off = [0] * 5
+    off[at] = 4 if 0 < at < 4 else 2
+    arr = (S.CEvictBuf * 1)(S.CEvictBuf(8 * AT, 9 * AT, 10, 10, 64, 32, 64, 32, 32))
+    assert lib.csa2_evict_rows(2, 2, AT + off[0], 4, 2 * AT + off[1], 3 * AT + off[2],
+                               4 * AT + off[3], 1, arr, 5 * AT + off[4], None) == S.ERR_UNSUPPORTED

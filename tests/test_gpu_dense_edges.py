@@ -126,7 +126,8 @@ def test_side_stream_leaves_freed_memory_of_the_current_one(call):
     run = {"prompt": lambda s: S.prompt_attn(b, q, k, v, stream=s),
            "prefix": lambda s: S.prefix_attn(b, None, q, k, v, 700, stream=s),
            "mass": lambda s: (S.attn_mass(b, q, k, lse, 700, stream=s),),
-           "select": lambda s: S.evict_select(b["kv_start"], b["kv_len"], weight, 100, stream=s)}[call]
+           "select": lambda s: S.evict_select(b["kv_start"], b["kv_len"], weight, 100,
+                                               stream=s)}[call]
     want = run(None)
     sizes = [x.numel() * x.element_size() for x in want]
     sizes.append(S.csa2_prefix_attn_workspace(20, 20, 0, 16, 2, 128, 0, 700))
@@ -216,7 +217,8 @@ def _check_batch(call, cu, rows, num_q, groups, heads, kv, dim, seed=0):
             x, y = groups[0][g:g + 2]
             if 0 <= x <= r < y <= len(rows) and _is_range(cu, x, y, num_q):
                 p = start[len(rows) + g]
-                kk, vv, off = torch.cat([k[p:p + pre[g]], kk]), torch.cat([v[p:p + pre[g]], vv]), pre[g]
+                off = pre[g]
+                kk, vv = torch.cat([k[p:p + off], kk]), torch.cat([v[p:p + off], vv])
         last = torch.clamp(off + rows[r] - n + torch.arange(n, device=DEV), min=off - 1)
         ref = R.attend(q[at], kk, vv, dim ** -0.5, last)
         assert max(mine[at]) == 1            # the cases have no row in two requests
@@ -261,7 +263,8 @@ def test_single_tokens_of_malformed_batches_are_all_found(call, heads, kv, dim, 
     """Single tokens whose request has not their number, nor one as far from it
     as the first query row."""
     groups = None if cug is None or call == "prompt" else (cug, [300, 77][:len(cug) - 1])
-    _check_batch(call, cu, [30, 200, 5, 64, 1, 17, 2, 3][:len(cu) - 1], num_q, groups, heads, kv, dim)
+    rows = [30, 200, 5, 64, 1, 17, 2, 3][:len(cu) - 1]
+    _check_batch(call, cu, rows, num_q, groups, heads, kv, dim)
 
 
 @pytest.mark.parametrize("reqs,free", [(511, 1), (513, 3), (1600, 40)])
@@ -408,8 +411,9 @@ def test_tensors_of_another_layout_are_refused():
     idx, n = S.evict_select(b["kv_start"], b["kv_len"], mass, 8)
     e = lambda *s: torch.empty(s, device=DEV)              # noqa: E731
     i = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)   # noqa: E731
-    for call in (lambda: S.prompt_attn(b, q, k, v, out=torch.empty((3, 4, 128), dtype=BF, device=DEV)),
-                 lambda: S.prompt_attn(b, q, k, v, out=torch.empty((3, 8, 64), dtype=BF, device=DEV)),
+    o = lambda *s: torch.empty(s, dtype=BF, device=DEV)    # noqa: E731
+    for call in (lambda: S.prompt_attn(b, q, k, v, out=o(3, 4, 128)),
+                 lambda: S.prompt_attn(b, q, k, v, out=o(3, 8, 64)),
                  lambda: S.prefix_attn(b, None, q, k, v, 40, lse=e(3, 5)),
                  lambda: S.attn_mass(b, q, k, e(3, 8), 40),
                  lambda: S.attn_mass(b, q, k, lse, 40, mass=e(2, pool + 1)),
