@@ -475,9 +475,10 @@ CSA2_API int csa2_quantize_rows(int32_t format, int64_t n, const float *src, int
  * Dense caches: attention over every cached row, and eviction
  *
  * Beside the sparse attention over the latent pool, a stack needs attention
- * that reads every row of a plain K/V cache: for layers without compression,
- * for a drafter, and as the dense form a sparse layer is measured against.
- * These calls take bf16 or f16 rows (`dtype`), n_heads query heads that share
+ * that reads every row of a plain K/V cache: for layers without compression
+ * and for a drafter.  (The layer's own latent rows, 512 channels of FP8 or FP4,
+ * are not read by these calls; csa2_evict_rows moves any.)
+ * They take bf16 or f16 rows (`dtype`), n_heads query heads that share
  * n_kv_heads key heads (head h reads key head h / G, G = n_heads /
  * n_kv_heads), and requests that are runs of rows in one pool, as above.
  *

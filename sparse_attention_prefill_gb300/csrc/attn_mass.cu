@@ -18,7 +18,10 @@
 // queries over 2,700 rows on average, 64 heads: 54.8 us), of which the product
 // and the exponentials need 512 each on units of their own; no unit is more than
 // half busy.  (-lse' as three bf16 channels of the product, instead of reads of
-// shared memory, took 56 us; TMEM loads 16 columns ahead of their use 57.6.)
+// shared memory, took 56 us; TMEM loads 16 columns ahead of their use 57.6.)  The
+// rest is waiting: a warpgroup gives its buffer back once a tile's arithmetic is
+// done, and only then can the next product into it be issued, behind those of the
+// other three.
 // Products and weights rotate over four S^T buffers and four warpgroups:
 // product number x of an item (query tile by query tile, the item's key tiles
 // within) goes to buffer and warpgroup x % 4.  With four key tiles to an item
@@ -156,8 +159,8 @@ __device__ void schedule_role(const MassParams &P, uint8_t *smem, MassMisc *ms) 
   if (lane == 0) raise_err(P.d_err, err);
 }
 
-// The items of this CTA, one after another, as every role sees them.  `lanes`:
-// a single thread (0) or a whole warp (1) calls.
+// The items of this CTA, one after another, as every role sees them; called by a
+// whole warp (kWarp) or by a single thread.
 template <bool kWarp, typename F>
 __device__ __forceinline__ bool for_items(MassMisc *ms, F f) {
   for (uint32_t u = 0;; ++u) {

@@ -19,13 +19,14 @@
 //   key are 16 bytes of it.
 // With the rows as the wide operand (16 of them, half unused by groups of 8)
 // the output took 64 registers a thread instead of 32, and what that spilled
-// were the loads: 143 us for 256 requests x 8 key heads x 512 rows.  Now rows of
-// 731 MB take 131 us (5.6 TB/s).  The next block's K is asked for as soon as S
-// is done, its V once O is.
+// were the loads: 143 us for 256 requests x 8 key heads x 512 rows (537 MB).
+// Those take 92 us now, the join included; 256 requests of 693 rows on average
+// (731 MB) 131 us without it, 5.6 TB/s, and 125 us where nothing is split.  The
+// next block's K is asked for as soon as S is done, its V once O is.
 //
 // (On the tcgen05 path of dense_attn.cu a decode item is a chain of copies,
-// products of 128 rows with G of them in use, barriers and a TMEM epilogue:
-// 107 us for the same rows.)
+// products of 128 rows with G of them in use, barriers and a TMEM epilogue: 108
+// us for the 537 MB with the join, 171 for the 731 MB where nothing is split.)
 #include "dense.cuh"
 
 namespace csa2 {
@@ -144,7 +145,7 @@ __device__ __forceinline__ void decode_item(const DecodeParams &P, Shared<D, kN>
     }
   };
   // The block after the next, for which there are no registers yet: into L2, a
-  // 128-byte line to a lane (731 MB of rows 135 -> 131 us; two blocks: 133).
+  // 128-byte line to a lane (731 MB of rows 135 -> 131 us; two blocks ahead: 133).
   auto prefetch = [&](int b) {
     constexpr int kLines = D / 64;
     if (lane < kKeys * kLines) {

@@ -310,8 +310,8 @@ __global__ void evict_lengths_kernel(SelParams P, int64_t *new_len) {
 // ascending batches, loads a whole batch before it stores it, and has a
 // barrier between, so that closing up in place is safe: idx ascends, hence
 // row i's source is never in front of i, and a later batch's sources lie
-// behind every row stored so far.  Where nothing moves in place, several
-// blocks share the rows.
+// behind every row stored so far.  Where no buffer shares memory with itself,
+// several blocks share the rows.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
 constexpr int kMaxBufs = 8;
@@ -451,7 +451,9 @@ extern "C" CSA2_API int csa2_evict_select(int32_t num_req, int32_t n_heads,
   // CTAs to a (request, head): as many as the GPU holds at a time, but no fewer
   // than kMinSlice rows to each on average (8 x 8 rows of 5200: 10.9 us at
   // 4096 a slice, 11.9 at 2048, 16.8 at 1024; 24 x 8 rows of 26,000: 37.6 us
-  // with two CTAs, 43 with three, 56 with one)
+  // with two CTAs, 43 with three, 56 with one).  The lengths are on the device, so
+  // this goes by the pool's rows to a request: in a pool far longer than its
+  // requests the slices come out shorter than that.
   const int64_t by_rows = kv_rows / num_req / kMinSlice;
   int64_t nc = kSelPlaces / pairs;
   nc = nc < by_rows ? nc : by_rows;
