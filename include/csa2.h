@@ -641,7 +641,9 @@ typedef struct csa2_evict_buf {
  * dst is row src_start[r] + i of src: the rows close up in place (ascending idx,
  * as csa2_evict_select writes them).  Otherwise no destination row may be a
  * source row of the call, of this request or another, in this buffer or another:
- * blocks move requests, heads and buffers in no order.  Two buffers have two
+ * blocks move requests, heads and buffers in no order.  Where dst is src, a request
+ * that moves further up over its own rows, or to rows between another's src_start
+ * and last source row, is skipped (CSA2_DERR_RANGE_ROW).  Two buffers have two
  * destinations (CSA2_ERR_INVALID_ARG).  Rows of dst that are not named keep
  * their bytes.  A negative idx is skipped; a row outside src_rows or dst_rows
  * is skipped (CSA2_DERR_RANGE_ROW).  Host structs, read during the call only.

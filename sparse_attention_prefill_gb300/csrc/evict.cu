@@ -322,7 +322,7 @@ struct MoveParams {
   csa2_evict_buf buf[kMaxBufs];
   int vec[kMaxBufs];              // bytes of a lane's piece: 16 or 4
   int shift[kMaxBufs];            // log2 of the pieces of an element, or -1
-  int n_heads, keep;
+  int num_req, n_heads, keep;
   const int32_t *idx;
   const int64_t *new_len, *src_start, *dst_start;
   int32_t *d_err;
@@ -367,6 +367,23 @@ __device__ void move_rows(const MoveParams &P, const csa2_evict_buf &b, int shif
   }
 }
 
+// Whether the destination [d0, d0 + n) of request r in a tensor that is its own
+// source meets rows between another request's start and last source row, which
+// another block may not have read yet, or lies further up over its own (further
+// down is safe: the block goes upwards).
+__device__ __noinline__ bool meets_sources(const MoveParams &P, const csa2_evict_buf &b, int r, int h, int64_t s0,
+                              int64_t d0, int n) {
+  bool hit = false;
+  for (int q = threadIdx.x; q < P.num_req; q += kMoveThreads) {
+    const int64_t len = P.new_len[q], a = min(P.src_start[q], b.src_rows);
+    const int m = (int)(len < 0 ? 0 : len < P.keep ? len : P.keep);
+    if (m == 0 || a < 0) continue;
+    const int64_t behind = a + P.idx[((int64_t)q * P.n_heads + h) * P.keep + m - 1] + 1;
+    hit |= d0 < behind && a < d0 + n && (q != r || d0 > s0);
+  }
+  return __syncthreads_or(hit);
+}
+
 template <bool kInPlace>
 __global__ void __launch_bounds__(kMoveThreads)
 evict_rows_kernel(const __grid_constant__ MoveParams P) {
@@ -384,6 +401,9 @@ evict_rows_kernel(const __grid_constant__ MoveParams P) {
   int err = 0;
   if (s0 < 0 || d0 < 0) {
     err = n > 0 ? CSA2_DERR_RANGE_ROW : 0;
+  } else if (kInPlace && s0 != d0 && n > 0 && b.src == b.dst &&
+             meets_sources(P, b, r, (int)(pair % P.n_heads), s0, d0, n)) {
+    err = CSA2_DERR_RANGE_ROW;
   } else if (P.vec[blockIdx.y] == 16) {
     move_rows<uint4, kInPlace>(P, b, shift, pair, s0, d0, n, pair % P.n_heads, blockIdx.z,
                                gridDim.z, err);
@@ -531,6 +551,7 @@ extern "C" CSA2_API int csa2_evict_rows(int32_t num_req, int32_t n_heads, const 
     for (int s = 0; s < 24; ++s)
       if (pieces == (1ll << s)) P.shift[i] = s;
   }
+  P.num_req = num_req;
   P.n_heads = n_heads;
   P.keep = keep;
   P.idx = idx;

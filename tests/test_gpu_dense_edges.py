@@ -602,3 +602,31 @@ def test_runs_over_one_another_past_two_to_the_32_items():
     S.prompt_attn(b, q, k, k, out=room[2048:2048 + num_q], d_err=d)
     assert int(d.item()) == S.DERR_BAD_EXTEND
     assert (room[:2048] == 7).all() and (room[2048 + num_q:] == 7).all()
+
+
+@pytest.mark.parametrize("to,ok", [
+    ([100, 600, 900], [1, 1, 1]),              # closed up in place
+    ([1500, 2500, 3500], [1, 1, 1]),           # elsewhere in the same tensor
+    ([70, 600, 900], [1, 1, 1]),               # the first moves down over itself
+    ([130, 600, 900], [0, 1, 1]),              # up over itself
+    ([100, 200, 300], [1, 0, 0]),              # closed up over the others' sources
+    ([850, 1500, 1900], [0, 1, 1]), ([0, 1500, 899], [1, 1, 1])])
+def test_rows_moved_within_one_tensor(to, ok):
+    """Requests at 100, 600 and 900 of 400, 250 and 90 rows, of which the first
+    and the last among others stay."""
+    start, rows, keep, heads = [100, 600, 900], [400, 250, 90], 60, 2
+    c = torch.randn((4000, heads, 32), device=DEV).to(BF)
+    idx = torch.empty((3, heads, keep), dtype=torch.int32, device=DEV)
+    for r, n in enumerate(rows):
+        for h in range(heads):
+            pick = torch.randperm(n - 2, device=DEV)[:keep - 2] + 1
+            idx[r, h] = torch.cat([pick, torch.tensor([0, n - 1], device=DEV)]).sort().values
+    want = c.clone()
+    for r in range(3):
+        for h in range(heads):
+            if ok[r]:
+                want[to[r]:to[r] + keep, h] = c[start[r] + idx[r, h].long(), h]
+    d = _derr()
+    S.evict_rows(idx, _i64([keep] * 3), _i64(start), _i64(to), [(c, c)], d_err=d)
+    assert int(d.item()) == (0 if all(ok) else S.DERR_RANGE_ROW)
+    assert torch.equal(c, want)
