@@ -655,6 +655,131 @@ CSA2_API int csa2_evict_rows(int32_t num_req, int32_t n_heads, const int32_t *id
                              const int64_t *dst_start, int32_t n_bufs,
                              const csa2_evict_buf *bufs, int32_t *d_err, csa2_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions, and caches of 8-bit pages
+ *
+ * Next to the caches in 16 bits, whose requests are runs of one pool, there are
+ * caches in pages: a request's rows lie in pages that a table names, in any order,
+ * and are held in 8 bits with a scale for each page and head.  A serving step
+ * rotates its queries, appends its keys (rotated on the way) and values, and
+ * attends over what the pages hold, the new rows included.
+ *
+ * The batch is a csa2_packed whose kv_start is not read (NULL will do): cu_q gives
+ * each request's query rows, kv_len its cached rows with the new ones included.
+ * ------------------------------------------------------------------------- */
+
+/* Rotary positions.  Host struct; the arrays are device memory.  The first `rot`
+ * channels of a head are rot / 2 pairs; pair i of a row at position p becomes
+ *   (x, y) -> amplitude * (x cos a - y sin a, y cos a + x sin a),  a = p * freq[i]
+ * and the other channels stay as they are.
+ *   freq        [rot / 2] radians per position, float64, 8-byte aligned: scaled
+ *               for a longer context by whoever made it.  A position times a
+ *               frequency is reduced to a turn exactly (in 2^-64 turns), so that
+ *               far positions lose nothing; frequencies are finite
+ *   pos         [num_q] position of each query row, or NULL: its row in the
+ *               request's cache, kv_len - n + i for query i of n
+ *   interleaved 0: pair i is channels i and i + rot / 2; else 2 i and 2 i + 1
+ * rot is a multiple of 16 from 16 to the head's size (CSA2_ERR_UNSUPPORTED). */
+typedef struct csa2_rope {
+  const double *freq;
+  const int64_t *pos;
+  int32_t rot;
+  int32_t interleaved;
+  float amplitude;
+  int32_t reserved;
+} csa2_rope;
+
+/* Rotates rows [num_q, n_heads, dim] of bf16 or f16, in fp32, rounded once.
+ *   inverse  not 0: by -a, which takes the gradient of the rotated rows to that of
+ *            the rows (the amplitude still multiplies)
+ *   out      rows `ldo` elements apart; may be x itself where ldo = ldx, and else
+ *            shares no bytes with the rows of x
+ * With rope->pos every row is rotated, and of the batch only num_q is looked at;
+ * without it rows that no request holds are left as they are, and a row at a
+ * negative position is rotated the other way.  dim is 64 or 128, n_heads <= 65535;
+ * bases 16-byte aligned, row distances multiples of 8 elements
+ * (CSA2_ERR_UNSUPPORTED). */
+CSA2_API int csa2_rotate(const csa2_packed *b, int32_t n_heads, int32_t dim, int32_t dtype,
+                         const void *x, int64_t ldx, const csa2_rope *rope, int32_t inverse,
+                         void *out, int64_t ldo, int32_t *d_err, csa2_stream_t stream);
+
+/* A cache of 8-bit pages.  Host struct; the arrays are device memory.
+ *   page      rows of a page: 16, 32, 64 or 128
+ *   k, v      E4M3 (OCP "FN") codes: page i is [n_kv_heads, page, dim] at byte
+ *             i * k_stride (v_stride), so that K and V may lie page by page in one
+ *             array; strides are multiples of 16 bytes, bases 16-byte aligned
+ *   k_scale,  [num_pages, n_kv_heads] fp32: value = code * scale.  Scales lie in
+ *   v_scale   [2^-32, 2^32]; another one sets CSA2_DERR_SCALE and is taken as the
+ *             nearest end (NaN: the lower)
+ *   table     [num_req, table_ld]: row j of request r is row j % page of page
+ *             table[r, j / page].  Entries behind a request's last page are not read;
+ *             one that names no page (negative, or num_pages and above) sets
+ *             CSA2_DERR_RANGE_ROW, and its rows are neither written nor seen
+ * A request of more than table_ld * page rows has none (CSA2_DERR_RANGE_ROW).
+ * table_ld * page < 2^31 - 256 (CSA2_ERR_UNSUPPORTED). */
+typedef struct csa2_pages {
+  int32_t num_pages;
+  int32_t page;
+  void *k, *v;
+  int64_t k_stride, v_stride;
+  float *k_scale, *v_scale;
+  const int32_t *table;
+  int64_t table_ld;
+} csa2_pages;
+
+/* Writes a batch's new keys and values, rows [num_q, n_kv_heads, dim] of bf16 or
+ * f16, into their requests' pages: query i of n of a request of m rows is its row
+ * m - n + i.  Keys are rotated on the way where `rope` is not NULL.  For each
+ * block (a page and head) that new rows fall into, keys and values apart:
+ *   need  = smallest power of two with |x| <= 448 need over its new rows
+ *   scale = need, where the block has no older row; else max(old scale, need)
+ *   codes = E4M3(x / scale), to nearest, ties to even; where the scale grew, the
+ *           older rows' codes become E4M3(code * old scale / scale)
+ * Rotated keys are not rounded in between.  A power of two changes no code but
+ * those that fall below 2^-6, so a block that is filled row by row holds what it
+ * would if it were filled at once, but for these.  (A scale that is no power of two
+ * is kept as long as it is the largest.)  `need` stays within [2^-32, 2^32]: larger
+ * rows saturate (CSA2_DERR_SCALE).  A head's row with a NaN or infinity is written
+ * as zeros (CSA2_DERR_NONFINITE).
+ * Rows in front of position 0 (n > m) are left out (CSA2_DERR_BAD_EXTEND), as are
+ * requests whose query rows are not a range within num_q.  Rows of the pages behind
+ * row m - 1, and pages without new rows, keep their bytes.  A page that new rows
+ * fall into belongs to one request of the batch alone: what two make of it is not
+ * defined.  Supported: dim in {64, 128}, n_kv_heads <= 1024.  The cache shares no
+ * bytes with the inputs, nor its four arrays with each other (CSA2_ERR_INVALID_ARG);
+ * K and V may take turns in one array, page by page. */
+CSA2_API int csa2_page_append(const csa2_packed *b, int32_t n_kv_heads, int32_t dim,
+                              int32_t dtype, const void *k, int64_t ldk, const void *v,
+                              int64_t ldv, const csa2_rope *rope, const csa2_pages *cache,
+                              int32_t *d_err, csa2_stream_t stream);
+
+/* Causal attention over the pages, for prompts, extends and single tokens:
+ *   l_j = sm_scale * <q[i,h], K_j>,  j = 0 .. m - n + i,  K_j the row's value
+ *   out = sum_j e^{l_j} V_j / sum_j e^{l_j},  lse = ln sum_j e^{l_j}
+ * with q, out and lse as in csa2_prompt_attn (out may be q), and what that says of
+ * queries that see nothing and of rows of no request.  Rows of a page behind the
+ * request's last may hold anything, NaN codes included; rows that a request has
+ * hold none.
+ *   max_kv     the longest kv_len, for the choice of splits only
+ *   workspace  device scratch, 256-byte aligned, as csa2_prefix_attn's; NULL with
+ *              workspace_bytes = 0: the cache is not split
+ * csa2_page_attn_workspace gives the bytes of the splits that the call would choose
+ * (0: it would not split); with less it splits less, with less than two parts' bytes
+ * (a part as csa2_prefix_attn's) not at all.
+ * Queries in bf16 are scaled by a power of two for each row and head and taken as
+ * f16, which keeps their bits unless they lie 2^28 below the row's largest; codes
+ * are exact in f16; the weights, times their block's scale, are rounded to f16 for
+ * the product with V (2^-11 each; their sum is not rounded).
+ * Supported as csa2_prompt_attn. */
+CSA2_API int csa2_page_attn_workspace(int32_t num_q, int32_t num_req, int32_t n_heads,
+                                      int32_t n_kv_heads, int32_t dim, int64_t max_kv,
+                                      int64_t *bytes);
+CSA2_API int csa2_page_attn(const csa2_packed *b, int32_t n_heads, int32_t n_kv_heads,
+                            int32_t dim, int32_t dtype, const void *q, int64_t ldq,
+                            const csa2_pages *cache, int64_t max_kv, float sm_scale, void *out,
+                            float *lse, void *workspace, int64_t workspace_bytes, int32_t *d_err,
+                            csa2_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

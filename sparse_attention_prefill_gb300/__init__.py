@@ -15,10 +15,18 @@ Dense caches (plain K and V rows of bf16 or f16, shared by groups of heads) have
 the device tensors ``cu_q`` [R+1] int32, ``kv_start`` and ``kv_len`` [R] int64;
 and groups that share prefixes as a dict of ``num_groups``, ``max_prefix`` and
 ``cu_group`` [G+1] int32, ``prefix_start`` and ``prefix_len`` [G] int64.
+
+Caches of 8-bit pages have ``rotate`` (rotary positions, with ``rope_freqs`` for their
+frequencies), ``page_append`` and ``page_attn``.  They take the same batch without
+``kv_start``; the cache as a dict of ``k`` and ``v`` [pages, kv heads, page, dim]
+(uint8 or float8_e4m3fn codes), ``k_scale`` and ``v_scale`` [pages, kv heads] fp32 and
+``table`` [R, width] int32; and the rotation as a dict of ``freq`` [rot / 2] float64,
+``interleaved`` and ``amplitude``.
 """
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 import struct
 from typing import Optional
@@ -41,7 +49,8 @@ EXPORTED = ("csa2_status_string", "csa2_tail_layout", "csa2_index_score", "csa2_
             "csa2_quantize_rows", "csa2_set_wait_limit_ns", "csa2_index_topk_workspace",
             "csa2_index_topk", "csa2_index_k_project", "csa2_index_topk_static_capacity",
             "csa2_index_topk_static", "csa2_prompt_attn", "csa2_prefix_attn_workspace",
-            "csa2_prefix_attn", "csa2_attn_mass", "csa2_evict_select", "csa2_evict_rows")
+            "csa2_prefix_attn", "csa2_attn_mass", "csa2_evict_select", "csa2_evict_rows",
+            "csa2_rotate", "csa2_page_append", "csa2_page_attn_workspace", "csa2_page_attn")
 EVICT_MAX_BUFS = 8
 
 
@@ -66,6 +75,18 @@ class CPrefixGroups(C.Structure):
     _fields_ = [("num_groups", C.c_int32), ("reserved", C.c_int32), ("cu_group", C.c_void_p),
                 ("prefix_start", C.c_void_p), ("prefix_len", C.c_void_p),
                 ("max_prefix", C.c_int64)]
+
+
+class CRope(C.Structure):
+    _fields_ = [("freq", C.c_void_p), ("pos", C.c_void_p), ("rot", C.c_int32),
+                ("interleaved", C.c_int32), ("amplitude", C.c_float), ("reserved", C.c_int32)]
+
+
+class CPages(C.Structure):
+    _fields_ = [("num_pages", C.c_int32), ("page", C.c_int32), ("k", C.c_void_p),
+                ("v", C.c_void_p), ("k_stride", C.c_int64), ("v_stride", C.c_int64),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("table", C.c_void_p),
+                ("table_ld", C.c_int64)]
 
 
 class CEvictBuf(C.Structure):
@@ -121,6 +142,11 @@ def load(path: Optional[str] = None):
                                    vp, vp, vp, vp]
     lib.csa2_evict_select.argtypes = [i32, i32, vp, vp, vp, i64, i32, i32, i32, vp, vp, vp, vp]
     lib.csa2_evict_rows.argtypes = [i32, i32, vp, i32, vp, vp, vp, i32, vp, vp, vp]
+    lib.csa2_rotate.argtypes = [vp, i32, i32, i32, vp, i64, vp, i32, vp, i64, vp, vp]
+    lib.csa2_page_append.argtypes = [vp, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp]
+    lib.csa2_page_attn_workspace.argtypes = [i32, i32, i32, i32, i32, i64, vp]
+    lib.csa2_page_attn.argtypes = [vp, i32, i32, i32, i32, vp, i64, vp, i64, f32, vp, vp, vp, i64,
+                                   vp, vp]
     for name in EXPORTED[1:]:
         getattr(lib, name).restype = C.c_int
     _lib = lib
@@ -783,3 +809,204 @@ def evict_rows(idx, new_len, src_start, dst_start, bufs, d_err=None, stream=None
     r, h, keep = idx.shape
     _check(csa2_evict_rows(r, h, idx, keep, new_len, src_start, dst_start, bufs, d_err, stream),
            "csa2_evict_rows")
+
+
+# ---------------------------------------------------------------------------
+# rotary positions and caches of 8-bit pages.  ``packed`` as above, without
+# kv_start; ``rope`` a dict of freq (float64 [rot / 2], radians per position) and,
+# optionally, interleaved (False) and amplitude (1.0); ``cache`` a dict of k, v
+# ([pages, kv heads, page, dim] uint8 or float8_e4m3fn, pages any distance apart that
+# is a multiple of 16 bytes), k_scale, v_scale ([pages, kv heads] fp32) and table
+# ([R, width] int32).
+# ---------------------------------------------------------------------------
+
+_F64 = torch.float64
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _paged(b, dev, lens=True):
+    """Host struct for a packed dict without kv_start (lens: with its lengths)."""
+    r = int(b["num_req"]) if lens else 0
+    return CPacked(int(b["num_q"]), r, _arg(b["cu_q"], _I32, "cu_q", r + 1, dev) if lens else None,
+                   None, _arg(b["kv_len"], _I64, "kv_len", r, dev) if lens else None)
+
+
+def _rope_arg(rope, pos, num_q, dev):
+    """Host struct for a rope dict."""
+    f = rope["freq"]
+    return CRope(_arg(f, _F64, "freq", 0, dev), _arg(pos, _I64, "pos", num_q, dev), 2 * f.numel(),
+                 bool(rope.get("interleaved", False)), float(rope.get("amplitude", 1.0)), 0)
+
+
+def _cache_arg(cache, num_req, kv, dim, dev):
+    """Host struct for a cache dict."""
+    k, v, table = cache["k"], cache["v"], cache["table"]
+    shape, side = k.shape, []
+    for t, name in ((k, "k"), (v, "v")):
+        if t.get_device() != dev or t.dtype not in _CODES:
+            raise Csa2Error("the cache's %s: expected uint8 or float8_e4m3fn codes on cuda:%d, got "
+                            "%s on %s" % (name, dev, t.dtype, t.device))
+        if t.dim() != 4 or t.shape != shape or shape[1] != kv or shape[3] != dim:
+            raise Csa2Error("the cache's %s: expected [pages, %d, page, %d], got %s"
+                            % (name, kv, dim, tuple(t.shape)))
+        s = t.stride()
+        if s[3] != 1 or s[2] != dim or (s[1] != shape[2] * dim and kv > 1):
+            raise Csa2Error("the cache's %s: the rows of a page must be contiguous" % name)
+        side.append(s[0] if shape[0] > 1 else kv * shape[2] * dim)
+    if table.dim() != 2 or table.get_device() != dev or table.dtype is not _I32 \
+            or table.shape[0] < num_req or (table.stride(1) != 1 and table.shape[1] > 1):
+        raise Csa2Error("table: expected [%d, width] of int32 on cuda:%d with contiguous rows, got "
+                        "%s of %s on %s" % (num_req, dev, tuple(table.shape), table.dtype,
+                                            table.device))
+    width, ld = table.shape[1], table.stride(0)
+    if ld != width and table.shape[0] > 1 and num_req > 1:
+        raise Csa2Error("libcsa2 takes contiguous tensors; table is not")
+    n = shape[0] * kv
+    return CPages(shape[0], shape[2], k.data_ptr(), v.data_ptr(), side[0], side[1],
+                  _arg(cache["k_scale"], _F32, "k_scale", n, dev, (kv,)),
+                  _arg(cache["v_scale"], _F32, "v_scale", n, dev, (kv,)), table.data_ptr(), width)
+
+
+def csa2_rotate(packed, x, rope, pos, inverse, out, d_err, stream=None) -> int:
+    dt, dev = x.dtype, x.get_device()
+    xp, ldx, rows, heads = _rows3(x, "x", dt, dev, x.shape[-1])
+    op, ldo, orows, oheads = _rows3(out, "out", dt, dev, x.shape[-1])
+    st = _paged(packed, dev, pos is None)
+    if st.num_q > rows or st.num_q > orows or oheads != heads:
+        raise Csa2Error("x has %d rows and out %d of %d heads, the batch names %d of %d"
+                        % (rows, orows, oheads, st.num_q, heads))
+    ro = _rope_arg(rope, pos, st.num_q, dev)
+    return _call(dev, load().csa2_rotate,
+                 (C.byref(st), heads, x.shape[2], _DTYPES[dt], xp, ldx, C.byref(ro), bool(inverse),
+                  op, ldo, _arg(d_err, _I32, "d_err", 1, dev)), stream)
+
+
+def csa2_page_append(packed, k, v, rope, pos, cache, d_err, stream=None) -> int:
+    dt, dev = k.dtype, k.get_device()
+    kp, ldk, rows, kv = _rows3(k, "k", dt, dev, k.shape[-1])
+    vp, ldv, vrows, vkv = _rows3(v, "v", dt, dev, k.shape[-1])
+    dim = k.shape[2]
+    st = _paged(packed, dev)
+    if vkv != kv or st.num_q > rows or st.num_q > vrows:
+        raise Csa2Error("k is %s and v %s, the batch names %d rows"
+                        % (tuple(k.shape), tuple(v.shape), st.num_q))
+    ro = None if rope is None else _rope_arg(rope, pos, st.num_q, dev)
+    ca = _cache_arg(cache, st.num_req, kv, dim, dev)
+    return _call(dev, load().csa2_page_append,
+                 (C.byref(st), kv, dim, _DTYPES[dt], kp, ldk, vp, ldv,
+                  None if ro is None else C.byref(ro), C.byref(ca),
+                  _arg(d_err, _I32, "d_err", 1, dev)), stream)
+
+
+def csa2_page_attn_workspace(num_q, num_req, n_heads, n_kv_heads, dim, max_kv) -> int:
+    """Workspace bytes of the splits csa2_page_attn would choose for these sizes (0:
+    none); with less it splits less."""
+    out = C.c_int64(0)
+    _check(load().csa2_page_attn_workspace(int(num_q), int(num_req), int(n_heads),
+                                           int(n_kv_heads), int(dim), int(max_kv), C.byref(out)),
+           "csa2_page_attn_workspace")
+    return out.value
+
+
+def _page_attn(packed, q, cache, max_kv, sm_scale, out, lse, want_lse, workspace, nbytes, d_err,
+               stream):
+    dt, dev = q.dtype, q.get_device()
+    qp, ldq, rows, h = _rows3(q, "q", dt, dev, q.shape[-1])
+    dim, kv = q.shape[2], cache["k"].shape[1]
+    st = _paged(packed, dev)
+    if st.num_q > rows:
+        raise Csa2Error("q has %d rows, the batch names %d" % (rows, st.num_q))
+    ca = _cache_arg(cache, st.num_req, kv, dim, dev)
+    n = st.num_q * h
+    if out is None:
+        out = _new(torch.empty, q.shape, dt, q.device, stream)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, dt, "out", n * dim, dev, (h, dim))
+    if lse is None and want_lse:
+        lse = _new(torch.empty, q.shape[:2], _F32, q.device, stream)
+        lp = lse.data_ptr()
+    else:
+        lp = _arg(lse, _F32, "lse", n, dev, (h,))
+    if nbytes is None and workspace is None:
+        nbytes = csa2_page_attn_workspace(st.num_q, st.num_req, h, kv, dim, max_kv)
+        if nbytes:
+            workspace = _new(torch.empty, nbytes, torch.uint8, q.device, stream, False)
+    elif nbytes is None:
+        nbytes = workspace.numel()
+    if sm_scale is None:
+        sm_scale = dim ** -0.5
+    return _call(dev, load().csa2_page_attn,
+                 (C.byref(st), h, kv, dim, _DTYPES[dt], qp, ldq, C.byref(ca), int(max_kv),
+                  float(sm_scale), op, lp, _arg(workspace, torch.uint8, "workspace", nbytes, dev),
+                  nbytes, _arg(d_err, _I32, "d_err", 1, dev)), stream), out, lse
+
+
+def csa2_page_attn(packed, q, cache, max_kv, sm_scale, out, lse, workspace, workspace_bytes, d_err,
+                   stream=None) -> int:
+    if out is None:
+        raise Csa2Error("csa2_page_attn: out is missing")
+    return _page_attn(packed, q, cache, max_kv, sm_scale, out, lse, False, workspace,
+                      int(workspace_bytes), d_err, stream)[0]
+
+
+def rope_freqs(rot, base=10000.0, scaling=None, factor=1.0, original=None, low=1.0, high=32.0,
+               device="cuda"):
+    """Frequencies and amplitude of ``rot`` rotated channels, as the start of a rope
+    dict: freq[i] = base ** (-2 i / rot) radians per position, scaled for contexts
+    ``factor`` times longer:
+      None      as they are
+      "linear"  divided by factor: every position counts as a fraction of one
+      "base"    of the base times factor ** (rot / (rot - 2)), which leaves the first
+                pair as it is and divides the last one by factor
+      "ramp"    by the turns that a pair makes over the ``original`` context: divided
+                by factor up to ``low`` of them, as they are from ``high`` on, mixed
+                linearly between; amplitude 0.1 ln(factor) + 1, which makes up for the
+                flatter softmax over a longer context"""
+    if rot < 16 or rot % 16:
+        raise Csa2Error("rope_freqs: rot is a multiple of 16, got %r" % (rot,))
+    if not (base > 0 and factor >= 1):
+        raise Csa2Error("rope_freqs: base > 0 and factor >= 1, got %r and %r" % (base, factor))
+    if scaling == "base":
+        base = base * factor ** (rot / (rot - 2))
+    f = float(base) ** (-2.0 * torch.arange(rot // 2, dtype=_F64) / rot)
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "ramp":
+        if not original or not high > low:
+            raise Csa2Error("rope_freqs: a ramp needs the original context, and high > low")
+        keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+        amplitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise Csa2Error("rope_freqs: unknown scaling %r" % (scaling,))
+    return dict(freq=f.to(device), amplitude=amplitude)
+
+
+def rotate(packed, x, rope, pos=None, inverse=False, out=None, d_err=None, stream=None):
+    """Rotary positions of rows [num_q, heads, dim]: at ``pos`` (int64 [num_q]) if given,
+    else each at its row of its request's cache.  ``inverse`` takes the gradient of the
+    rotated rows to that of the rows.  ``out`` may be ``x``; rows of no request are
+    left as they were (unset, where it is allocated here)."""
+    if out is None:
+        out = _new(torch.empty, x.shape, x.dtype, x.device, stream)
+    _check(csa2_rotate(packed, x, rope, pos, inverse, out, d_err, stream), "csa2_rotate")
+    return out
+
+
+def page_append(packed, k, v, cache, rope=None, pos=None, d_err=None, stream=None):
+    """Writes new keys (rotated on the way, with ``rope``) and values into the 8-bit
+    pages of their requests, and the blocks' scales."""
+    _check(csa2_page_append(packed, k, v, rope, pos, cache, d_err, stream), "csa2_page_append")
+
+
+def page_attn(packed, q, cache, max_kv, sm_scale=None, out=None, lse=None, want_lse=True,
+              workspace=None, d_err=None, stream=None):
+    """Causal attention over a cache of 8-bit pages, for prompts, extends and single
+    tokens.  Allocates the workspace (uint8, csa2_page_attn_workspace bytes) if none is
+    given; one for the largest batch serves the smaller ones too."""
+    st, out, lse = _page_attn(packed, q, cache, max_kv, sm_scale, out, lse, want_lse, workspace,
+                              None, d_err, stream)
+    _check(st, "csa2_page_attn")
+    return out, lse

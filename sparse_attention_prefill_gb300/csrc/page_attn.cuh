@@ -1,0 +1,45 @@
+// Attention over 8-bit pages: what its kernels and its entry point share.
+//
+// A block's codes K8, V8 have the scales a and b (rows are a K8 and b V8).  With
+//   x_j = c a_j <q, K8_j> + log2 b_j        (c: sm_scale log2 e)
+// the weight of V8_j is 2^x_j, and that of the softmax's sum 2^x_j / b_j: the scales
+// of V ride in the exponent, and the running maximum is that of x, so that weights fit
+// f16 whatever the scales are.
+#pragma once
+#include "pages.cuh"
+
+namespace csa2 {
+namespace pages {
+
+struct PageAttnParams {
+  Seqs seqs;                     // kv_start is null, kv_rows what the table has room for
+  Pages cache;
+  const void *q;
+  int64_t ldq;
+  int n_heads, n_kv, group;
+  int splits;                    // of the key range; 0: the output itself is written
+  float *part_o, *part_lse;      // partial results (dense.cuh)
+  float scale_log2;
+  void *out;                     // [num_q, n_heads, D]
+  float *lse;                    // [num_q, n_heads] or null
+  int32_t *d_err;
+  uint64_t wait_ns;
+};
+
+// f16 weights: scaled up by 2^kLift, so that those down to 2^-22 of the largest keep
+// full precision; the reference moves when a logit passes it by kMargin, and the
+// largest weight stays below 2^16.
+constexpr float kLift = 8.f, kMargin = 7.f;
+
+// Single tokens (page_decode.cu).
+int page_decode(const Shape &s, const PageAttnParams &P, const csa2_pages *c, cudaStream_t st);
+
+// Power of two that takes a query row's largest magnitude to [2^14, 2^15), so that
+// its bf16 channels are f16 ones.
+__device__ __forceinline__ float lift_of(float amax) {
+  const int e = (int)(__float_as_uint(amax) >> 23) - 127;
+  return __uint_as_float((uint32_t)(min(14 - e, 100) + 127) << 23);
+}
+
+}  // namespace pages
+}  // namespace csa2
