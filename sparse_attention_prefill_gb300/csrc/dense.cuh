@@ -354,6 +354,23 @@ __device__ __forceinline__ void wait_front() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+struct AttnParams {
+  Seqs seqs;
+  int n_heads, n_kv, group, tpt, causal;
+  int splits;        // of the key range; 0: the output itself is written
+  float *part_o, *part_lse;      // partial results (dense.cuh)
+  float scale_log2;
+  void *out;         // [num_q, n_heads, D]
+  float *lse;        // [num_q, n_heads] or null
+  // shared-prefix call: rows of requests in no group get -inf in the prefix
+  // part's statistics
+  const int32_t *cover;
+  int n_cover, cover_splits;
+  float *cover_lse;
+  int32_t *d_err;
+  uint64_t wait_ns;
+};
+
 // Single tokens over their own rows (decode_attn.cu): groups of at most
 // kDecodeGroup heads; results or partial results as in dense_attn.cu.
 constexpr int kDecodeGroup = 16;

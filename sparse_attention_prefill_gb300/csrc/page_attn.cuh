@@ -12,18 +12,10 @@ namespace csa2 {
 namespace pages {
 
 struct PageAttnParams {
-  Seqs seqs;                     // kv_start is null, kv_rows what the table has room for
+  dense::AttnParams at;          // seqs.kv_start is null, kv_rows what the table has room for
   Pages cache;
   const void *q;
   int64_t ldq;
-  int n_heads, n_kv, group;
-  int splits;                    // of the key range; 0: the output itself is written
-  float *part_o, *part_lse;      // partial results (dense.cuh)
-  float scale_log2;
-  void *out;                     // [num_q, n_heads, D]
-  float *lse;                    // [num_q, n_heads] or null
-  int32_t *d_err;
-  uint64_t wait_ns;
 };
 
 // f16 weights: scaled up by 2^kLift, so that those down to 2^-22 of the largest keep

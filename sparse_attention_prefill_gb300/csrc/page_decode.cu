@@ -86,7 +86,7 @@ __device__ __forceinline__ void decode_item(const PageAttnParams &P, const CUten
                                             uint32_t &used, int &err) {
   constexpr int kSide = Shared<D, kN>::kSide;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const int ns = P.splits > 0 ? P.splits : 1;
+  const int ns = P.at.splits > 0 ? P.at.splits : 1;
   const Pages &C = P.cache;
   const int64_t last = m - n + (token - q0);           // keys seen: 0 .. last
   const int keys = last < 0 ? 0 : (int)last + 1;
@@ -114,8 +114,8 @@ __device__ __forceinline__ void decode_item(const PageAttnParams &P, const CUten
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       checked[x] = id[x] >= 0;
-      na[x] = checked[x] ? C.k_scale[(int64_t)id[x] * P.n_kv + h] : 0.f;
-      nb[x] = checked[x] ? C.v_scale[(int64_t)id[x] * P.n_kv + h] : 0.f;
+      na[x] = checked[x] ? C.k_scale[(int64_t)id[x] * P.at.n_kv + h] : 0.f;
+      nb[x] = checked[x] ? C.v_scale[(int64_t)id[x] * P.at.n_kv + h] : 0.f;
     }
   };
   const auto fetch = [&](int i) {
@@ -147,11 +147,11 @@ __device__ __forceinline__ void decode_item(const PageAttnParams &P, const CUten
   for (int i = 0; i < kStages && i < mine; ++i) fetch(i);
 
   // Q's fragments; rows past the group's heads are zeros
-  const T *q = static_cast<const T *>(P.q) + (int64_t)token * P.ldq + (int64_t)h * P.group * D;
+  const T *q = static_cast<const T *>(P.q) + (int64_t)token * P.ldq + (int64_t)h * P.at.group * D;
   if (Elem<T>::kBf16) {
     for (int r = warp; r < 8 * kN; r += kWarps) {
       float amax = 0.f;
-      if (r < P.group)
+      if (r < P.at.group)
         for (int d = lane; d < D; d += 32) amax = fmaxf(amax, fabsf((float)q[r * D + d]));
 #pragma unroll
       for (int k = 1; k < 32; k <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, k));
@@ -167,7 +167,7 @@ __device__ __forceinline__ void decode_item(const PageAttnParams &P, const CUten
     const int l = i & 31, x = (i >> 5) % (D / 16), r = (i >> 5) / (D / 16) * 8 + (l >> 2);
     const int ch = 16 * ((l & 3) + 4 * (x >> 2)) + 4 * (x & 3);
     uint2 w = make_uint2(0, 0);
-    if (r < P.group) {
+    if (r < P.at.group) {
       w = *reinterpret_cast<const uint2 *>(q + r * D + ch);
       if (Elem<T>::kBf16) {
         const float f = sh.lift[r];
@@ -188,7 +188,7 @@ __device__ __forceinline__ void decode_item(const PageAttnParams &P, const CUten
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       ref[y][r] = -INFINITY, sum[y][r] = 0.f;
-      unit[y][r] = P.scale_log2 * (Elem<T>::kBf16 ? sh.unlift[8 * y + 2 * c + r] : 1.f);
+      unit[y][r] = P.at.scale_log2 * (Elem<T>::kBf16 ? sh.unlift[8 * y + 2 * c + r] : 1.f);
     }
   bool ok = true;
   int i = 0;
@@ -359,11 +359,11 @@ __device__ __forceinline__ void decode_item(const PageAttnParams &P, const CUten
   }
   __syncthreads();
   // a result's rows are channel-innermost, a partial result's blocks row-innermost
-  const bool part = P.splits > 0;
+  const bool part = P.at.splits > 0;
   constexpr int kRows = 8 * kN, kTeam = kWarps * 32 / kRows;       // threads of a row
   const int row = part ? threadIdx.x % kRows : threadIdx.x / kTeam;
   const int col = part ? threadIdx.x / kRows : threadIdx.x % kTeam;
-  if (row >= P.group) return;
+  if (row >= P.at.group) return;
   float top = -INFINITY, tot = 0.f, w[kWarps];
 #pragma unroll
   for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sh.ref[k][row]);
@@ -377,10 +377,10 @@ __device__ __forceinline__ void decode_item(const PageAttnParams &P, const CUten
   const float inv = seen ? 1.f / tot : 0.f;
   const float lse = seen ? (base + log2f(tot)) * 0.6931471805599453f : -INFINITY;
   if (part) {
-    const int64_t rows = part_rows(P.seqs.num_q, P.group), at = (int64_t)token * P.group + row;
-    if (col == 0) P.part_lse[part_stat(rows, P.n_kv, split, h, at)] = lse;
+    const int64_t rows = part_rows(P.at.seqs.num_q, P.at.group), at = (int64_t)token * P.at.group + row;
+    if (col == 0) P.at.part_lse[part_stat(rows, P.at.n_kv, split, h, at)] = lse;
     if (!seen) return;
-    float *dst = P.part_o + part_elem(rows, P.n_kv, D, split, h, at);
+    float *dst = P.at.part_o + part_elem(rows, P.at.n_kv, D, split, h, at);
 #pragma unroll 4
     for (int d = col; d < D; d += kTeam) {
       float f = 0.f;
@@ -389,8 +389,8 @@ __device__ __forceinline__ void decode_item(const PageAttnParams &P, const CUten
       dst[d * 32] = f * inv;
     }
   } else {
-    const int64_t at = (int64_t)token * P.n_heads + h * P.group + row;
-    if (col == 0 && P.lse) P.lse[at] = lse;
+    const int64_t at = (int64_t)token * P.at.n_heads + h * P.at.group + row;
+    if (col == 0 && P.at.lse) P.at.lse[at] = lse;
 #pragma unroll
     for (int d = 4 * col; d < D; d += 4 * kTeam) {
       float f[4] = {0.f, 0.f, 0.f, 0.f};
@@ -402,7 +402,7 @@ __device__ __forceinline__ void decode_item(const PageAttnParams &P, const CUten
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) f[e] = seen ? f[e] * inv : 0.f;
-      *reinterpret_cast<uint2 *>(static_cast<T *>(P.out) + at * D + d) =
+      *reinterpret_cast<uint2 *>(static_cast<T *>(P.at.out) + at * D + d) =
           make_uint2(Elem<T>::pack(f[0], f[1]), Elem<T>::pack(f[2], f[3]));
     }
   }
@@ -420,14 +420,14 @@ page_decode_kernel(const __grid_constant__ PageAttnParams P, const __grid_consta
     for (int w = 0; w < kWarps; ++w)
       for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[w][s], 1);
     sh.bd.abort = 0;
-    sh.bd.wait_ns = P.wait_ns;
+    sh.bd.wait_ns = P.at.wait_ns;
     mbar_fence_init();
   }
   __syncthreads();
   uint32_t used = 0;
   int err = 0;
   bool again = false;
-  each_item<kWarps, true>(P.seqs, P.n_kv, P.group, P.splits, P.part_lse, P.d_err, sh.runs,
+  each_item<kWarps, true>(P.at.seqs, P.at.n_kv, P.at.group, P.at.splits, P.at.part_lse, P.at.d_err, sh.runs,
                           [&](int token, int run, int q0, int n, int64_t, int64_t m, int h,
                               int split) {
                             if (again) {  // the ring held a join's sums
@@ -439,7 +439,7 @@ page_decode_kernel(const __grid_constant__ PageAttnParams P, const __grid_consta
                                                   split, used, err);
                           });
   if (*(volatile int *)&sh.bd.abort) err |= CSA2_DERR_TIMEOUT;
-  if (err) raise_err(P.d_err, err);
+  if (err) raise_err(P.at.d_err, err);
 }
 
 template <typename T, int D, int kN>
@@ -465,7 +465,7 @@ int launch_any(const Shape &s, const PageAttnParams &P, int grid, const CUtensor
 
 int page_decode(const Shape &s, const PageAttnParams &P, const csa2_pages *c, cudaStream_t st) {
   // an item to a block, and one that looks the batch over
-  const int64_t grid = (int64_t)P.seqs.num_q * P.n_kv * (P.splits > 0 ? P.splits : 1) + 1;
+  const int64_t grid = (int64_t)P.at.seqs.num_q * P.at.n_kv * (P.at.splits > 0 ? P.at.splits : 1) + 1;
   if (grid > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
   CUtensorMap mk, mv;
   if (!make_cache_maps(&mk, &mv, c, P.q, s, kKeys)) return CSA2_ERR_UNSUPPORTED;

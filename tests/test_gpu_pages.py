@@ -349,6 +349,7 @@ def _check_attn(out, lse, b, cu, new, rows, c, q, scale, dtype, which=None):
 ATTN = [  # heads, key heads, dim, page, type
     (8, 1, 128, 64, BF), (16, 2, 64, 16, HF), (6, 2, 64, 32, BF), (4, 4, 128, 16, HF),
     (5, 1, 64, 128, BF), (32, 2, 128, 32, BF), (24, 2, 128, 128, HF), (9, 1, 64, 64, HF),
+    (40, 1, 128, 16, BF), (128, 1, 64, 32, HF), (34, 2, 64, 128, BF), (128, 1, 128, 64, BF),
 ]
 
 
@@ -391,6 +392,20 @@ def test_attn_ragged(heads, kv, dim, page, dtype):
     _check_attn(out, lse, b, cu, new, rows, c, q, scale, dtype)
     for t in (out, lse):
         assert (t[:cu[0]] == 7).all() and (t[cu[-1]:] == 7).all()
+
+
+@pytest.mark.parametrize("n,m", [(2, 1000), (127, 127), (129, 129), (31, 4000), (700, 2100),
+                                 (2049, 2049), (16, 9001), (4, 20000)])
+@pytest.mark.parametrize("heads,kv,dim,page,dtype", [(8, 2, 128, 16, BF), (3, 1, 64, 64, HF),
+                                                     (8, 1, 64, 32, BF), (8, 2, 128, 128, HF)])
+def test_attn_one_request(n, m, heads, kv, dim, page, dtype):
+    b, cu = R.batch([n], [m], DEV)
+    c = R.make_cache([m], kv, dim, page, seed=n + m)
+    q = _normal((n, heads, dim), dtype, 3)
+    d = _derr()
+    out, lse = S.page_attn(b, q, c, max_kv=m, sm_scale=0.02, d_err=d)
+    assert int(d.item()) == 0
+    _check_attn(out, lse, b, cu, [n], [m], c, q, 0.02, dtype)
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
