@@ -552,7 +552,10 @@ PartPlan plan(const Shape &s, int64_t num_q, int64_t num_req, int64_t max_kv) {
   const int64_t tok = p.kind == kWideItems ? 2 * p.tpt : p.tpt;
   const int64_t runs = num_req > 0 ? num_req : 1;
   const int64_t items = (num_q / tok > runs ? num_q / tok : runs) * s.n_kv;
-  if (p.kind != kSingleTokens && items >= kSms) p.splits = 1;
+  if (p.kind == kSingleTokens)         // three CTAs to an SM, 128 keys a step
+    p.splits = plan_splits(items, 3 * kSms, (max_kv + kTile - 1) / kTile, 4.0);
+  else if (items >= kSms)
+    p.splits = 1;
   return p;
 }
 
