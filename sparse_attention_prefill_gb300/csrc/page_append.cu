@@ -10,7 +10,13 @@
 // floor((n - 1) / page) + 2 pages, which is what lies between there and the next
 // request's first place, so no prefix sum is needed.)
 //
-// A page to a CTA; its blocks are shared out among the CTA's warps.
+// Two kernels do the pages.  Few rows to a request (decode steps): a block to a warp,
+// and a CTA to two places (one request's, most of the time); four rows at a time, gone over twice where there are more.
+// Otherwise a CTA has one side of a page and some of its heads, and a thread 16
+// channels of a row (two rows in pages of 128 rows of 128 channels), so that an
+// angle's sine and cosine are spent once for all of the heads; a head's rows stay in
+// registers between the maximum, which the CTA finds together, and the codes, while
+// the next head's are on their way.
 #include "pages.cuh"
 #include "rope.cuh"
 
@@ -28,8 +34,12 @@ struct AppendParams {
   int64_t ldk, ldv;
   Pages cache;
   rope::Rope rope;                       // freq null: keys are not rotated
+  int each;                              // heads of a CTA (many rows)
   int32_t *d_err;
 };
+
+// New rows to a request on average up to which a block goes to a warp.
+constexpr int kFewRows = 4;
 
 // Rows of a request and what they touch.
 struct Touched {
@@ -40,14 +50,14 @@ struct Touched {
 };
 
 __device__ __forceinline__ Touched touched_by(const AppendParams &P, int r, int lo, int hi,
-                                              int &err) {
+                                              int64_t m, int &err) {
   Touched t{lo, 0, 0, (int64_t)(lo >> P.cache.shift) + 2ll * r, 0};
   if (lo < 0 || hi < lo || hi > P.num_q) {
     err |= CSA2_DERR_BAD_EXTEND;
     return t;
   }
   if (hi == lo) return t;
-  const int64_t m = P.kv_len[r], n = hi - lo;
+  const int64_t n = hi - lo;
   if (m < 0 || m > P.cache.most) {
     err |= CSA2_DERR_RANGE_ROW;
     return t;
@@ -75,22 +85,49 @@ __device__ __forceinline__ float need_of(float amax, int &err) {
   return __uint_as_float(e << 23);
 }
 
-// x / scale: by the reciprocal where that is exact
+// x / scale, by the reciprocal where that is exact.  (Divisions take a path of their
+// own: chosen for each value, they cost 14 of 20 instructions a value.)
 struct Divider {
   float scale, inv;
   bool exact;
-  __device__ __forceinline__ float operator()(float x) const {
-    return exact ? x * inv : __fdiv_rn(x, scale);
-  }
 };
-
 __device__ __forceinline__ Divider by_scale(float s) {
-  return Divider{s, 1.f / s, (__float_as_uint(s) & 0x7fffffu) == 0};
+  const uint32_t u = __float_as_uint(s);                 // 2^e: 2^-e has 254 - its exponent
+  return Divider{s, __uint_as_float((254u << 23) - u), (u & 0x7fffffu) == 0};
 }
 
-__device__ __forceinline__ uint2 codes8(const float *x, const Divider &by) {
-  return make_uint2(e4m3x2_of(by(x[0]), by(x[1])) | (e4m3x2_of(by(x[2]), by(x[3])) << 16),
-                    e4m3x2_of(by(x[4]), by(x[5])) | (e4m3x2_of(by(x[6]), by(x[7])) << 16));
+// codes of four values
+__device__ __forceinline__ uint32_t codes4(float x0, float x1, float x2, float x3) {
+  uint32_t r;
+  asm("{ .reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h}; }"
+      : "=r"(r)
+      : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+  return r;
+}
+
+// a thread's 16 channels, divided
+__device__ __forceinline__ void divide16(float (&x)[2 * kUnit], const Divider &by) {
+  if (by.exact) {
+    const uint64_t inv = pack2(by.inv, by.inv);
+#pragma unroll
+    for (int i = 0; i < 2 * kUnit; i += 2) {
+      const float2 y = unpack2(rope::mul2(pack2(x[i], x[i + 1]), inv));
+      x[i] = y.x, x[i + 1] = y.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2 * kUnit; ++i) x[i] = __fdiv_rn(x[i], by.scale);
+  }
+}
+__device__ __forceinline__ void store16(uint8_t *row, const rope::Place &at,
+                                        const float (&x)[2 * kUnit]) {
+  *reinterpret_cast<uint2 *>(row + at.a) =
+      make_uint2(codes4(x[0], x[1], x[2], x[3]), codes4(x[4], x[5], x[6], x[7]));
+  *reinterpret_cast<uint2 *>(row + at.b) =
+      make_uint2(codes4(x[8], x[9], x[10], x[11]), codes4(x[12], x[13], x[14], x[15]));
 }
 
 // 16 codes times `ratio`, rounded again
@@ -101,87 +138,157 @@ __device__ __forceinline__ uint4 rescaled(uint4 w, float ratio) {
     const uint32_t a = f16x2_of(v[i]), b = f16x2_of_high(v[i]);
     const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
     const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
-    v[i] = e4m3x2_of(x.x * ratio, x.y * ratio) | (e4m3x2_of(y.x * ratio, y.y * ratio) << 16);
+    v[i] = codes4(x.x * ratio, x.y * ratio, y.x * ratio, y.y * ratio);
   }
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// 16 channels of a row: loaded, rotated, and zeros where the row's head (the lanes
-// of a team) has anything that is not finite; its largest magnitude.
-template <typename T, int D>
-__device__ __forceinline__ float load_row(const T *src, const rope::Place &at, bool turns,
-                                          bool interleaved, const float (&c)[kUnit],
-                                          const float (&s)[kUnit], float (&x)[2 * kUnit],
-                                          bool there, int &err) {
+// 16 channels as they lie in memory
+struct Raw {
+  uint4 a, b;
+};
+template <typename T>
+__device__ __forceinline__ Raw load_raw(const T *src, const rope::Place &at) {
+  return Raw{*reinterpret_cast<const uint4 *>(src + at.a), *reinterpret_cast<const uint4 *>(src + at.b)};
+}
+
+// The channels, rotated, and as zeros where the row's head (the lanes of a team) has
+// anything that is not finite; their largest magnitude.
+template <typename T, int D, bool kInterleaved>
+__device__ __forceinline__ float open_row(const Raw &raw, const rope::Place &at,
+                                          const float (&c)[kUnit], const float (&s)[kUnit],
+                                          float (&x)[2 * kUnit], int &err) {
   constexpr int kTeam = D / 16;
-  if (there) {
-    rope::unpack8<T>(*reinterpret_cast<const uint4 *>(src + at.a), x);
-    rope::unpack8<T>(*reinterpret_cast<const uint4 *>(src + at.b), x + kUnit);
-    if (turns) rope::turn16(x, interleaved, c, s);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2 * kUnit; ++i) x[i] = 0.f;
-  }
-  bool fine = true;
+  rope::unpack8<T>(raw.a, x);
+  rope::unpack8<T>(raw.b, x + kUnit);
+  rope::turn16<kInterleaved>(x, at, c, s);
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 2 * kUnit; ++i) {
-    fine &= fabsf(x[i]) <= 3.402823466e38f;
-    amax = fmaxf(amax, fabsf(x[i]));
-  }
-  const uint32_t bad = __ballot_sync(0xffffffffu, !fine);
-  const int lane = threadIdx.x & 31, team = lane / kTeam * kTeam;
-  if ((bad >> team) & ((1u << kTeam) - 1)) {
-    err |= CSA2_DERR_NONFINITE;
-    amax = 0.f;
+  for (int i = 0; i < 2 * kUnit; i += 2)                 // (a NaN stays)
+    asm("max.NaN.f32 %0, %1, %2, %3;"
+        : "=f"(amax)
+        : "f"(amax), "f"(fabsf(x[i])), "f"(fabsf(x[i + 1])));
+  const uint32_t bad = __ballot_sync(0xffffffffu, !(amax <= 3.402823466e38f));
+  if (bad) {
+    const int lane = threadIdx.x & 31, team = lane / kTeam * kTeam;
+    if ((bad >> team) & ((1u << kTeam) - 1)) {
+      err |= CSA2_DERR_NONFINITE;
+      amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * kUnit; ++i) x[i] = 0.f;
+      for (int i = 0; i < 2 * kUnit; ++i) x[i] = 0.f;
+    }
   }
   return amax;
 }
 
+// The page that a CTA has: request, its rows, page number in the request, id (-1: none).
+struct Found {
+  Touched t;
+  int run, id;
+  int64_t p;
+};
+
+// Calls f(found) for each page of a request that has one of `places` places from `place`
+// on (in a malformed batch places may be several requests').
+template <typename F>
+__device__ __forceinline__ void each_page(const AppendParams &P, int64_t place, int places,
+                                          int &err, const F &f) {
+  __shared__ Touched held;
+  __shared__ int found, matches;
+  for (int from = 0;;) {
+    if (threadIdx.x == 0) found = 0x7fffffff, matches = 0;
+    __syncthreads();
+    int mine = 0x7fffffff;
+    Touched t;
+#pragma unroll 2
+    for (int r = from + threadIdx.x; r < P.num_req; r += blockDim.x) {
+      int ignored = 0;
+      const Touched u = touched_by(P, r, P.cu_q[r], P.cu_q[r + 1], P.kv_len[r], ignored);
+      if (place + places > u.place && place - u.place < u.pages) {
+        if (mine == 0x7fffffff) mine = r, t = u;
+        atomicMin(&found, r);
+        atomicAdd(&matches, 1);
+      }
+    }
+    __syncthreads();
+    const int r = found, n = matches;
+    if (n == 0) return;
+    if (r == mine) held = t;
+    __syncthreads();
+    const Touched u = held;
+    const int i1 = (int)min((int64_t)u.pages, place + places - u.place);
+    for (int i = (int)max(place - u.place, (int64_t)0); i < i1; ++i) {
+      const int64_t p = (u.row0 >> P.cache.shift) + i;
+      f(Found{u, r, P.cache.table[r * P.cache.table_ld + p], p});
+    }
+    if (n == 1) return;
+    from = r + 1;
+    __syncthreads();
+  }
+}
+
+__device__ __forceinline__ bool is_page(const AppendParams &P, int id, int &err) {
+  if (id >= 0 && id < P.cache.num_pages) return true;
+  err |= CSA2_DERR_RANGE_ROW;
+  return false;
+}
+
+// the last block of a grid has no page: it looks at every request
+__device__ __forceinline__ void check_batch(const AppendParams &P) {
+  int err = 0;
+  for (int r = threadIdx.x; r < P.num_req; r += blockDim.x)
+    touched_by(P, r, P.cu_q[r], P.cu_q[r + 1], P.kv_len[r], err);
+  if (err) raise_err(P.d_err, err);
+}
+
+// ---------------------------------------------------------------------------
+// few rows to a request: a block to a warp
+// ---------------------------------------------------------------------------
 constexpr int kWarps = 16;
 
-// One block by a warp: its rows are gone over twice, for the scale and for the
-// codes (the last of them stay in registers).
-template <typename T, int D>
-__device__ void append_block(const AppendParams &P, const uint64_t *turn, const Touched &t,
-                             int64_t p, int id, int h, int side, int &err) {
+template <typename T, int D, bool kInterleaved>
+__device__ __forceinline__ void append_block(const AppendParams &P, const uint64_t *turn,
+                                             const Found &F, int h, int side, int &err) {
   constexpr int kTeam = D / 16, kStep = 32 / kTeam;      // lanes of a row, rows at a time
   const Pages &C = P.cache;
+  const Touched &t = F.t;
   const int lane = threadIdx.x & 31, i = lane % kTeam;
-  const int64_t base = p << C.shift;
+  const int64_t base = F.p << C.shift;
   const int first = (int)max(t.row0 - base, (int64_t)0), end = (int)min(t.m - base, (int64_t)C.page);
-  const bool rot = side == 0 && P.rope.freq;
-  const rope::Place at =
-      rot ? rope::place_of(i, P.rope.rot, P.rope.interleaved) : rope::place_of(i, 0, true);
+  const rope::Place at = rope::place_of<D, kInterleaved>(i, side == 0 && P.rope.freq ? P.rope.rot : 0);
   const int64_t ld = side ? P.ldv : P.ldk;
   const T *src = static_cast<const T *>(side ? P.v : P.k) + (int64_t)h * D;
-  uint8_t *codes = (side ? C.v + id * C.v_stride : C.k + id * C.k_stride) +
-                   (int64_t)h * C.page * D;
-  float x[2 * kUnit];
-  const auto load = [&](int row) {
-    const bool there = row < end;
-    const int64_t q = t.q0 + (base + row - t.row0);
-    float c[kUnit], s[kUnit];
-    const bool turns = rot && at.turns && there;
-    if (turns)
-      rope::angles(turn, i, P.rope.pos ? P.rope.pos[q] : base + row, P.rope.amplitude, 1.f, c, s);
-    return load_row<T, D>(src + (there ? q * ld : 0), at, turns, P.rope.interleaved, c, s, x,
-                          there, err);
+  const auto query = [&](int row) { return t.q0 + (base + row - t.row0); };
+  const auto raw_of = [&](int row) {
+    return row < end ? load_raw(src + query(row) * ld, at) : Raw{};
   };
-  float amax = 0.f;
+  float x[2 * kUnit];
+  const auto open = [&](const Raw &raw, int row) {
+    float c[kUnit], s[kUnit];
+    if ((at.ta || at.tb) && row < end)
+      rope::angles<D, kInterleaved>(turn, i, at, P.rope.pos ? P.rope.pos[query(row)] : base + row,
+                                    P.rope.amplitude, 1.f, c, s);
+    else
+      for (int k = 0; k < kUnit; ++k) c[k] = s[k] = 0.f;       // of zeros
+    return open_row<T, D, kInterleaved>(raw, at, c, s, x, err);
+  };
+  // the first rows are asked for before the page is known to be one
+  const Raw first_rows = raw_of(first + lane / kTeam);
+  if (!is_page(P, F.id, err)) return;
+  float *scale = (side ? C.v_scale : C.k_scale) + (int64_t)F.id * P.n_kv + h;
+  const float stored = first > 0 ? *scale : 0.f;
+  uint8_t *codes = (side ? C.v + F.id * C.v_stride : C.k + F.id * C.k_stride) +
+                   (int64_t)h * C.page * D;
+  float amax = open(first_rows, first + lane / kTeam);
   int row0 = first;
-  for (int r = first; r < end; r += kStep) {
+  for (int r = first + kStep; r < end; r += kStep) {
     row0 = r;
-    amax = fmaxf(amax, load(r + lane / kTeam));
+    amax = fmaxf(amax, open(raw_of(r + lane / kTeam), r + lane / kTeam));
   }
-#pragma unroll
-  for (int k = 1; k < 32; k <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, k));
-  float *scale = (side ? C.v_scale : C.k_scale) + (int64_t)id * P.n_kv + h;
+  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
   float now = need_of(amax, err);
   if (first > 0) {
-    const float old = scale_of(*scale, err);
+    const float old = scale_of(stored, err);
     if (now > old) {
       uint4 *w = reinterpret_cast<uint4 *>(codes);
       for (int j = lane; j < first * (D / 16); j += 32) w[j] = rescaled(w[j], old / now);
@@ -194,67 +301,179 @@ __device__ void append_block(const AppendParams &P, const uint64_t *turn, const 
   const Divider by = by_scale(now);
   for (int r = row0;; r -= kStep) {
     const int row = r + lane / kTeam;
-    if (row < end) {
-      *reinterpret_cast<uint2 *>(codes + row * D + at.a) = codes8(x, by);
-      *reinterpret_cast<uint2 *>(codes + row * D + at.b) = codes8(x + kUnit, by);
-    }
+    divide16(x, by);
+    if (row < end) store16(codes + row * D, at, x);
     if (r == first) break;
-    load(r - kStep + lane / kTeam);
+    open(raw_of(row - kStep), row - kStep);
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kInterleaved>
 __global__ void __launch_bounds__(kWarps * 32)
-append_kernel(const __grid_constant__ AppendParams P) {
+append_few_kernel(const __grid_constant__ AppendParams P) {
   __shared__ uint64_t turn[D / 2];
-  __shared__ int found, matches;
-  const int64_t place = blockIdx.x;
+  if (blockIdx.x == gridDim.x - 1) return check_batch(P);
   int err = 0;
-  if (blockIdx.x == gridDim.x - 1) {         // no page: looks at every request
-    for (int r = threadIdx.x; r < P.num_req; r += kWarps * 32)
-      touched_by(P, r, P.cu_q[r], P.cu_q[r + 1], err);
-    err = __reduce_or_sync(0xffffffffu, err);
-    if ((threadIdx.x & 31) == 0) raise_err(P.d_err, err);
+  if (P.rope.freq) rope::load_turns(P.rope, turn);       // (a barrier follows)
+  each_page(P, 2 * (int64_t)blockIdx.x, 2, err, [&](const Found &F) {
+    for (int i = threadIdx.x >> 5; i < 2 * P.n_kv; i += kWarps)
+      append_block<T, D, kInterleaved>(P, turn, F, i >> 1, i & 1, err);
+  });
+  if (err) raise_err(P.d_err, err);
+}
+
+// ---------------------------------------------------------------------------
+// many rows: a side of a page to a CTA, kRows rows of 16 channels to a thread
+// ---------------------------------------------------------------------------
+constexpr int kAhead = 4;                // heads whose rows are on their way or there
+
+// 16 bytes into shared memory, or zeros
+__device__ __forceinline__ void copy16(void *to, const void *from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+
+template <typename T, int D, bool kInterleaved, int kRows>
+__global__ void __launch_bounds__(512, kRows == 1 ? 2 : 1)
+append_many_kernel(const __grid_constant__ AppendParams P) {
+  constexpr int kTeam = D / 16;
+  __shared__ uint64_t turn[D / 2];
+  __shared__ uint32_t top[3];                            // a head's maximum, by head modulo 3
+  extern __shared__ __align__(16) uint4 staged[];        // [kAhead][kRows][2][threads]
+  if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y == 0) check_batch(P);
     return;
   }
-  if (P.rope.freq) rope::load_turns(P.rope, turn);
-  // The request that has this place; in a malformed batch more than one may.
-  for (int from = 0;;) {
-    if (threadIdx.x == 0) found = 0x7fffffff, matches = 0;
-    __syncthreads();
-#pragma unroll 4
-    for (int r = from + threadIdx.x; r < P.num_req; r += kWarps * 32) {
-      const int lo = P.cu_q[r], hi = P.cu_q[r + 1];
-      const int64_t off = place - ((lo >> P.cache.shift) + 2ll * r);
-      if (off < 0 || lo < 0 || hi < lo || off > ((int64_t)hi - lo) / P.cache.page + 1) continue;
-      int ignored = 0;
-      if (off < touched_by(P, r, lo, hi, ignored).pages) {
-        atomicMin(&found, r);
-        atomicAdd(&matches, 1);
+  const Pages &C = P.cache;
+  const int side = blockIdx.y & 1;
+  const int h0 = (int)(blockIdx.y >> 1) * P.each, h1 = min(P.n_kv, h0 + P.each);
+  int err = 0;
+  const bool rot = side == 0 && P.rope.freq;
+  if (rot) rope::load_turns(P.rope, turn);               // (a barrier follows)
+  if (threadIdx.x < 3) top[threadIdx.x] = 0;
+  each_page(P, blockIdx.x, 1, err, [&](const Found &F) {
+    if (!is_page(P, F.id, err)) return;
+    const Touched &t = F.t;
+    const int64_t base = F.p << C.shift;
+    const int first = (int)max(t.row0 - base, (int64_t)0);
+    const int end = (int)min(t.m - base, (int64_t)C.page);
+    const int i = threadIdx.x % kTeam, mine = threadIdx.x / kTeam, step = blockDim.x / kTeam;
+    const rope::Place at = rope::place_of<D, kInterleaved>(i, rot ? P.rope.rot : 0);
+    const int64_t ld = side ? P.ldv : P.ldk;
+    const T *src[kRows];
+    bool there[kRows];
+    float c[kRows][kUnit], s[kRows][kUnit];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int row = mine + k * step;
+      const int64_t q = t.q0 + (base + row - t.row0);
+      there[k] = row >= first && row < end;
+      src[k] = static_cast<const T *>(side ? P.v : P.k) + (there[k] ? q * ld : 0) +
+               (int64_t)h0 * D;
+#pragma unroll
+      for (int e = 0; e < kUnit; ++e) c[k][e] = s[k][e] = 0.f;
+      if ((at.ta || at.tb) && there[k])
+        rope::angles<D, kInterleaved>(turn, i, at, P.rope.pos ? P.rope.pos[q] : base + row,
+                                      P.rope.amplitude, 1.f, c[k], s[k]);
+    }
+    float *scale = (side ? C.v_scale : C.k_scale) + (int64_t)F.id * P.n_kv;
+    uint8_t *page = side ? C.v + F.id * C.v_stride : C.k + F.id * C.k_stride;
+    // a thread copies what it reads itself, so that no barrier is needed for it
+    uint4 *const own = staged + threadIdx.x;
+    const int unit = blockDim.x, stage = 2 * kRows * unit;
+    int to = 0, from = 0, next = h0;                     // stages, and the next head to copy
+    const auto fetch = [&]() {
+      if (next < h1) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          copy16(own + to + 2 * k * unit, src[k] + at.a, there[k]);
+          copy16(own + to + (2 * k + 1) * unit, src[k] + at.b, there[k]);
+          src[k] += D;
+        }
+        to = to == (kAhead - 1) * stage ? 0 : to + stage;
+        ++next;
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int h = 0; h < kAhead - 1; ++h) fetch();
+    for (int h = h0, slot = 0; h < h1; ++h, slot = slot == 2 ? 0 : slot + 1) {
+      const float kept = first > 0 ? scale[h] : 0.f;
+      fetch();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      float x[kRows][2 * kUnit], amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        amax = fmaxf(amax, open_row<T, D, kInterleaved>(Raw{own[from + 2 * k * unit], own[from + (2 * k + 1) * unit]}, at, c[k], s[k], x[k], err));
+      from = from == (kAhead - 1) * stage ? 0 : from + stage;
+      const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+      if ((threadIdx.x & 31) == 0) atomicMax(&top[slot], most);
+      __syncthreads();
+      float now = need_of(__uint_as_float(top[slot]), err);
+      // the slot before this was read before the barrier, and is next used after another
+      if (threadIdx.x == 0) top[slot == 0 ? 2 : slot - 1] = 0;
+      uint8_t *codes = page + (int64_t)h * C.page * D;
+      if (first > 0) {
+        const float old = scale_of(kept, err);
+        if (now > old) {
+          uint4 *w = reinterpret_cast<uint4 *>(codes);
+          for (int j = threadIdx.x; j < first * (D / 16); j += blockDim.x)
+            w[j] = rescaled(w[j], old / now);
+        } else {
+          now = old;
+        }
+      }
+      if (threadIdx.x == 0) scale[h] = now;
+      const Divider by = by_scale(now);
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        if (there[k]) {
+          divide16(x[k], by);
+          store16(codes + (mine + k * step) * D, at, x[k]);
+        }
     }
     __syncthreads();
-    const int r = found, n = matches;
-    if (n == 0) break;
-    int ignored = 0;
-    const Touched t = touched_by(P, r, P.cu_q[r], P.cu_q[r + 1], ignored);
-    const int64_t p = (t.row0 >> P.cache.shift) + (place - t.place);
-    const int id = page_id(P.cache, r, p, err);
-    if (id >= 0)
-      for (int i = threadIdx.x >> 5; i < 2 * P.n_kv; i += kWarps)
-        append_block<T, D>(P, turn, t, p, id, i >> 1, i & 1, err);
-    if (n == 1) break;
-    from = r + 1;
+    if (threadIdx.x < 3) top[threadIdx.x] = 0;           // for another page
     __syncthreads();
+  });
+  if (err) raise_err(P.d_err, err);
+}
+
+template <typename T, int D, bool kInterleaved>
+int launch_many(const AppendParams &P, dim3 grid, cudaStream_t st) {
+  const int threads = P.cache.page * (D / 16);
+  const int smem = kAhead * 2 * 16 * threads;
+  if (threads <= 512) {
+    allow_smem<append_many_kernel<T, D, kInterleaved, 1>>(kAhead * 2 * 16 * 512);
+    append_many_kernel<T, D, kInterleaved, 1><<<grid, threads, smem, st>>>(P);
+  } else if (D == 128) {                 // (pages of 128 rows)
+    allow_smem<append_many_kernel<T, 128, kInterleaved, 2>>(kAhead * 2 * 16 * 1024);
+    append_many_kernel<T, 128, kInterleaved, 2><<<grid, 512, smem, st>>>(P);
   }
-  err = __reduce_or_sync(0xffffffffu, err);
-  if ((threadIdx.x & 31) == 0) raise_err(P.d_err, err);
+  return launch_status();
 }
 
 template <typename T, int D>
-int launch(const AppendParams &P, int places, cudaStream_t st) {
-  append_kernel<T, D><<<places + 1, kWarps * 32, 0, st>>>(P);
-  return launch_status();
+int launch(AppendParams &P, int places, cudaStream_t st) {
+  if (P.num_q <= (int64_t)kFewRows * P.num_req) {
+    const int grid = (places + 1) / 2 + 1;
+    if (P.rope.freq && P.rope.interleaved)
+      append_few_kernel<T, D, true><<<grid, kWarps * 32, 0, st>>>(P);
+    else
+      append_few_kernel<T, D, false><<<grid, kWarps * 32, 0, st>>>(P);
+    return launch_status();
+  }
+  // all heads of a side in one CTA, unless the pages are too few to fill the GPU with
+  // 1024 threads to an SM
+  int chunks = 1;
+  const int64_t pages = (P.num_q >> P.cache.shift) + P.num_req;
+  while (chunks < P.n_kv && pages * 4 * chunks * P.cache.page * (D / 16) <= 1024ll * kSms)
+    chunks *= 2;
+  P.each = (P.n_kv + chunks - 1) / chunks;
+  const dim3 grid((unsigned)places + 1, 2u * (unsigned)((P.n_kv + P.each - 1) / P.each));
+  return P.rope.freq && P.rope.interleaved ? launch_many<T, D, true>(P, grid, st)
+                                           : launch_many<T, D, false>(P, grid, st);
 }
 
 // n bytes from p on against rows of one side's codes, page by page

@@ -47,9 +47,9 @@ struct Cfg {
   static_assert(kStages + kRaw <= 12, "scales");
   static constexpr int kThreads = 4 * 128;
   // 128 registers to a thread at launch, and the sum stays
-  static constexpr int kRegsSoftmax = 184;
+  static constexpr int kRegsSoftmax = 200;
   static constexpr int kRegsRest = 56;
-  static constexpr int kRegsConvert = 88;
+  static constexpr int kRegsConvert = 56;
   static_assert(2 * kRegsSoftmax + kRegsRest + kRegsConvert <= 4 * 128, "registers");
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColO = 2 * 128;
@@ -301,9 +301,9 @@ __device__ void convert_role(uint8_t *smem, Misc<D> *ms) {
   }
 }
 
-// Softmax of one item's stream t and its output; one row to a thread.  `tiles`: key
-// tiles of the items before.  False if a wait ran out.
-template <typename T, int D, bool kNarrow>
+// Softmax of one item's stream t and its output; one row to a thread.  A page has kG
+// columns of a tile or a multiple.  `tiles`: key tiles of the items before.  False if a wait ran out.
+template <typename T, int D, bool kNarrow, int kG>
 __device__ bool softmax_item(const AttnParams &P, Misc<D> *ms, const Item &it, uint32_t slot,
                              int t, uint32_t tiles, uint32_t &ps, uint32_t &po, uint32_t &pst) {
   using C = Cfg<D>;
@@ -352,20 +352,23 @@ __device__ bool softmax_item(const AttnParams &P, Misc<D> *ms, const Item &it, u
         for (int e = 0; e < 32; ++e)
           if (32 * c + e > vis) s[c][e] = 0xff800000u;
     }
-    float mx = -INFINITY;
+    // by blocks of kG columns: what S is multiplied by (a factor of 0 would make -inf a
+    // NaN), and the largest x
+    constexpr int kBlocks = kTile / kG, kEntry = kG / 16;
+    float f[kBlocks], mx = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int k = 0; k < kBlocks; ++k) {
+      f[k] = fmaxf(sc.a[k * kEntry] * unit, 1e-37f);
+      float m4[kG / 16];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t *y = s[c] + 16 * h;
-        float mg = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
-#pragma unroll
-        for (int e = 2; e < 16; e += 2)
-          mg = max3(mg, __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
-        // (a factor of 0 would make -inf a NaN)
-        const float f = fmaxf(sc.a[2 * c + h] * unit, 1e-37f);
-        mx = fmaxf(mx, fmaf(mg, f, sc.lb[2 * c + h]));
+      for (int e = 0; e < kG; e += 2) {
+        const uint32_t *y = &s[(k * kG + e) / 32][(k * kG + e) % 32];
+        float &m = m4[e / 16];
+        m = e % 16 ? max3(m, __uint_as_float(y[0]), __uint_as_float(y[1]))
+                   : fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
       }
+      const float mg = kG == 16 ? m4[0] : fmaxf(max3(m4[0], m4[1 % kEntry], m4[2 % kEntry]), m4[3 % kEntry]);
+      mx = fmaxf(mx, fmaf(mg, f[k], sc.lb[k * kEntry]));
     }
     const bool move = mx > ref + (kLift + kMargin);
     if (__any_sync(0xffffffffu, move)) {
@@ -386,25 +389,24 @@ __device__ bool softmax_item(const AttnParams &P, Misc<D> *ms, const Item &it, u
       }
     }
     const float sub = ref == -INFINITY ? 0.f : ref;
+    uint64_t part[2];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t p[32];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float f = fmaxf(sc.a[2 * c + h] * unit, 1e-37f), l = sc.lb[2 * c + h] - sub;
-        const uint64_t f2 = pack2(f, f), l2 = pack2(l, l);
-        uint64_t part[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float2 v = unpack2(fma2(pack2(__uint_as_float(s[c][16 * h + e]),
-                                              __uint_as_float(s[c][16 * h + e + 1])),
-                                        f2, l2));
-          const float a = ex2(v.x), b = ex2(v.y);
-          part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], pack2(a, b));
-          p[8 * h + e / 2] = Elem<__half>::pack(a, b);
+      for (int e = 0; e < 32; e += 2) {
+        const int at = 32 * c + e, k = at / kG;
+        const float l = sc.lb[k * kEntry] - sub;
+        const float2 v = unpack2(fma2(pack2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                      pack2(f[k], f[k]), pack2(l, l)));
+        const float a = ex2(v.x), b = ex2(v.y);
+        uint64_t &sums = part[(e >> 1) & 1];
+        sums = at % kG < 4 ? pack2(a, b) : add2(sums, pack2(a, b));
+        p[e / 2] = Elem<__half>::pack(a, b);
+        if (at % kG == kG - 2) {
+          const float2 both = unpack2(add2(part[0], part[1]));
+          sum = fmaf(both.x + both.y, sc.ib[k * kEntry], sum);
         }
-        const float2 both = unpack2(add2(part[0], part[1]));
-        sum = fmaf(both.x + both.y, sc.ib[2 * c + h], sum);
       }
       tmem_st32x32b_x16(ts + 16 * c, p);
       if (c & 1) {                 // 64 keys written: their product may start
@@ -418,7 +420,7 @@ __device__ bool softmax_item(const AttnParams &P, Misc<D> *ms, const Item &it, u
   return ok && finish_item<T, C, kNarrow>(P, ms, it, t, i, valid, rows_here, ref, sum, to, po, pst);
 }
 
-template <typename T, int D, bool kNarrow>
+template <typename T, int D, bool kNarrow, int kG>
 __device__ void softmax_role(const AttnParams &P, Misc<D> *ms) {
   const int t = threadIdx.x >> 7;
   uint32_t ps = 0, po = 0, pst = 0, tiles = 0;
@@ -429,7 +431,7 @@ __device__ void softmax_role(const AttnParams &P, Misc<D> *ms) {
     const Item &it = ms->item[slot];
     if (it.run < 0) return;
     if ((kNarrow || t < it.ntile) &&
-        !softmax_item<T, D, kNarrow>(P, ms, it, slot, t, tiles, ps, po, pst))
+        !softmax_item<T, D, kNarrow, kG>(P, ms, it, slot, t, tiles, ps, po, pst))
       return;
     tiles += max(it.nk, 0);
     __syncwarp();
@@ -437,7 +439,7 @@ __device__ void softmax_role(const AttnParams &P, Misc<D> *ms) {
   }
 }
 
-template <typename T, int D, bool kNarrow>
+template <typename T, int D, bool kNarrow, int kG>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 page_attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ Pages C8,
                  const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -498,7 +500,7 @@ page_attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ P
       item_role<kNarrow, true>(P, ms);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
-    softmax_role<T, D, kNarrow>(P, ms);
+    softmax_role<T, D, kNarrow, kG>(P, ms);
   }
   fence_before_sync();
   __syncthreads();
@@ -513,22 +515,22 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
-template <typename T, int D, bool kNarrow>
+template <typename T, int D, bool kNarrow, int kG>
 int launch(const AttnParams &P, const Pages &C8, int items, const Maps &m, cudaStream_t st) {
-  allow_smem<page_attn_kernel<T, D, kNarrow>>((int)smem_bytes<D>());
-  page_attn_kernel<T, D, kNarrow>
+  allow_smem<page_attn_kernel<T, D, kNarrow, kG>>((int)smem_bytes<D>());
+  page_attn_kernel<T, D, kNarrow, kG>
       <<<items, Cfg<D>::kThreads, smem_bytes<D>(), st>>>(P, C8, m.q, m.k, m.v);
   return launch_status();
 }
 
-template <typename T>
-int launch_any(const Shape &s, const AttnParams &P, const Pages &C8, bool narrow, int items,
-               const Maps &m, cudaStream_t st) {
-  if (s.dim == 128)
-    return narrow ? launch<T, 128, true>(P, C8, items, m, st)
-                  : launch<T, 128, false>(P, C8, items, m, st);
-  return narrow ? launch<T, 64, true>(P, C8, items, m, st)
-                : launch<T, 64, false>(P, C8, items, m, st);
+template <typename T, int D>
+int launch_any(const AttnParams &P, const Pages &C8, bool narrow, int items, const Maps &m,
+               cudaStream_t st) {
+  if (C8.page >= 64)
+    return narrow ? launch<T, D, true, 64>(P, C8, items, m, st)
+                  : launch<T, D, false, 64>(P, C8, items, m, st);
+  return narrow ? launch<T, D, true, 16>(P, C8, items, m, st)
+                : launch<T, D, false, 16>(P, C8, items, m, st);
 }
 
 int run_tiles(const Shape &s, const csa2_pages *c, const Pages &C8, const void *q, int64_t ldq,
@@ -542,8 +544,12 @@ int run_tiles(const Shape &s, const csa2_pages *c, const Pages &C8, const void *
   if (!make_rows_map(&m.q, s.bf16, q, P.seqs.num_q, s.n_heads, s.dim, ldq, s.group, P.tpt) ||
       !make_cache_maps(&m.k, &m.v, c, q, s, kTile))
     return CSA2_ERR_UNSUPPORTED;
-  return s.bf16 ? launch_any<__nv_bfloat16>(s, P, C8, narrow, (int)items, m, st)
-                : launch_any<__half>(s, P, C8, narrow, (int)items, m, st);
+  const int n = (int)items;
+  if (s.bf16)
+    return s.dim == 128 ? launch_any<__nv_bfloat16, 128>(P, C8, narrow, n, m, st)
+                        : launch_any<__nv_bfloat16, 64>(P, C8, narrow, n, m, st);
+  return s.dim == 128 ? launch_any<__half, 128>(P, C8, narrow, n, m, st)
+                      : launch_any<__half, 64>(P, C8, narrow, n, m, st);
 }
 
 // Splits where the items alone leave SMs idle; more would only add their join.

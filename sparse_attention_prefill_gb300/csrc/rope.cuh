@@ -39,25 +39,34 @@ __device__ __forceinline__ void load_turns(const Rope &R, uint64_t *turn) {
   }
 }
 
-// Thread t of a row and head (dim / 16 of them) has two units of 8 channels: with
-// halves and t < rot / 16, channels 8 t.. and rot / 2 + 8 t.., whose pairs 8 t.. it
-// rotates; otherwise 16 neighbouring ones.
+// Thread t of a row and head (dim / 16 of them) has two units of 8 channels, each
+// unit's neighbours with the neighbouring threads.  Halves: with t < rot / 16, channels
+// 8 t.. and rot / 2 + 8 t.., whose pairs it rotates; the others share out the channels
+// behind.  Interleaved: channels 8 t.. and dim / 2 + 8 t.., four pairs each.
 struct Place {
   int a, b;                              // first channels of the units
-  bool turns;                            // whether they are rotated, by pairs 8 t..
+  bool ta, tb;                           // whether they are rotated
 };
-__device__ __forceinline__ Place place_of(int t, int rot, bool interleaved) {
-  const bool turns = t < rot / 16;
-  if (interleaved || !turns) return Place{16 * t, 16 * t + kUnit, turns};
-  return Place{kUnit * t, rot / 2 + kUnit * t, true};
+template <int D, bool kInterleaved>
+__device__ __forceinline__ Place place_of(int t, int rot) {
+  if (kInterleaved) return Place{kUnit * t, D / 2 + kUnit * t, kUnit * t < rot, D / 2 + kUnit * t < rot};
+  const bool in = t < rot / 16;
+  const int first = in ? kUnit * t : rot / 2 + kUnit * t;      // rot + 8 (t - rot / 16)
+  return Place{first, first + (in ? rot : D - rot) / 2, in, in};
 }
 
-// cosines and sines of pairs 8 t .. 8 t + 7 at position p, times the amplitude
-__device__ __forceinline__ void angles(const uint64_t *turn, int t, int64_t p, float amplitude,
-                                       float sign, float (&c)[kUnit], float (&s)[kUnit]) {
+// cosines and sines of a thread's pairs at position p, times the amplitude
+template <int D, bool kInterleaved>
+__device__ __forceinline__ void angles(const uint64_t *turn, int t, const Place &at, int64_t p,
+                                       float amplitude, float sign, float (&c)[kUnit],
+                                       float (&s)[kUnit]) {
 #pragma unroll
   for (int i = 0; i < kUnit; ++i) {
-    const uint64_t turns = (uint64_t)p * turn[kUnit * t + i];
+    if (i < kUnit / 2 ? !at.ta : !at.tb) continue;
+    const int pair = !kInterleaved     ? kUnit * t + i
+                     : i < kUnit / 2 ? kUnit / 2 * t + i
+                                     : D / 4 + kUnit / 2 * (t - 1) + i;
+    const uint64_t turns = (uint64_t)p * turn[pair];
     // half turns from -1 to 1, to 2^-24
     const float x = (float)(int32_t)(turns >> 32) * 0x1p-31f;
     float si, co;
@@ -83,17 +92,39 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float *x) {
   }
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // the 16 channels of a thread's two units; every product is rounded, so that a
 // rotation has the same bits wherever it is computed
-__device__ __forceinline__ void turn16(float (&x)[2 * kUnit], bool interleaved,
+template <bool kInterleaved>
+__device__ __forceinline__ void turn16(float (&x)[2 * kUnit], const Place &at,
                                        const float (&c)[kUnit], const float (&s)[kUnit]) {
+  using dense::add2;
+  using dense::pack2;
+  using dense::unpack2;
+  if constexpr (!kInterleaved) {         // two pairs at a time
+    if (!at.ta) return;
 #pragma unroll
-  for (int i = 0; i < kUnit; ++i) {
-    float &a = interleaved ? x[2 * i] : x[i];
-    float &b = interleaved ? x[2 * i + 1] : x[kUnit + i];
-    const float u = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-    const float w = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
-    a = u, b = w;
+    for (int i = 0; i < kUnit; i += 2) {
+      const uint64_t a = pack2(x[i], x[i + 1]), b = pack2(x[kUnit + i], x[kUnit + i + 1]);
+      const uint64_t co = pack2(c[i], c[i + 1]);
+      const float2 u = unpack2(add2(mul2(a, co), mul2(b, pack2(-s[i], -s[i + 1]))));
+      const float2 w = unpack2(add2(mul2(b, co), mul2(a, pack2(s[i], s[i + 1]))));
+      x[i] = u.x, x[i + 1] = u.y, x[kUnit + i] = w.x, x[kUnit + i + 1] = w.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      if (i < kUnit / 2 ? !at.ta : !at.tb) continue;
+      float &a = x[2 * i], &b = x[2 * i + 1];
+      const float u = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
+      const float w = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+      a = u, b = w;
+    }
   }
 }
 

@@ -68,9 +68,9 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
   }
   const int t = threadIdx.x % kTeam, row = threadIdx.x / kTeam % kRows;
   if (!held[row]) return;
-  const Place at = place_of(t, P.rope.rot, kInterleaved);
+  const Place at = place_of<D, kInterleaved>(t, P.rope.rot);
   float c[kUnit], s[kUnit];
-  if (at.turns) angles(turn, t, pos[row], P.rope.amplitude, P.sign, c, s);
+  angles<D, kInterleaved>(turn, t, at, pos[row], P.rope.amplitude, P.sign, c, s);
   const T *x = static_cast<const T *>(P.x) + (row0 + row) * P.ldx;
   T *out = static_cast<T *>(P.out) + (row0 + row) * P.ldo;
   const int h1 = min(P.n_heads, ((int)blockIdx.y + 1) * P.each);
@@ -89,11 +89,11 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
     for (int i = 0; i < kAhead; ++i) {
       const int h = h0 + i * kSlots;
       if (h >= h1) break;
-      if (at.turns) {
+      if (at.ta || at.tb) {
         float v[2 * kUnit];
         unpack8<T>(a[i], v);
         unpack8<T>(b[i], v + kUnit);
-        turn16(v, kInterleaved, c, s);
+        turn16<kInterleaved>(v, at, c, s);
         a[i] = make_uint4(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3]),
                           Elem<T>::pack(v[4], v[5]), Elem<T>::pack(v[6], v[7]));
         b[i] = make_uint4(Elem<T>::pack(v[8], v[9]), Elem<T>::pack(v[10], v[11]),

@@ -207,6 +207,27 @@ def test_append_ragged(kv, dim, page, dtype, rotated):
     _check_append(new, rows, cu, before, c, (kk, v.double()), (ke, torch.zeros_like(ke)), page)
 
 
+@pytest.mark.parametrize("kv,dim,page,dtype", SHAPES)
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_few_rows_and_one_long(kv, dim, page, dtype, inter):
+    """Few rows to a request on average, and one with many: blocks go to warps."""
+    new = [1] * 50 + [150] + [2] * 9
+    rows = [1 + 7 * i for i in range(50)] + [190] + [2 + 30 * i for i in range(9)]
+    b, cu = R.batch(new, rows, DEV, lead=1)
+    c = R.make_cache(rows, kv, dim, page, seed=page + dim, spread=0.0)
+    before = _copy(c)
+    gain = torch.exp(1.5 * _normal((b["num_q"], kv, 1), torch.float32, 5))
+    k, v = ((_normal((b["num_q"], kv, dim), torch.float32, s) * gain).to(dtype) for s in (1, 2))
+    rope = dict(S.rope_freqs(dim if page > 32 else 16, base=500.0), interleaved=inter)
+    d = _derr()
+    S.page_append(b, k, v, c, rope=rope, d_err=d)
+    assert int(d.item()) == 0
+    at, pos = slice(cu[0], cu[-1]), _positions(new, rows)
+    kk, ke = k.double(), torch.zeros_like(k, dtype=torch.float64)
+    kk[at], ke[at] = R.rotate(k[at], pos, rope), R.rotate_error(k[at], rope)
+    _check_append(new, rows, cu, before, c, (kk, v.double()), (ke, torch.zeros_like(ke)), page)
+
+
 @pytest.mark.parametrize("page", [16, 64])
 def test_append_row_by_row_is_appending_at_once(page):
     """Blocks filled one row at a time, their rows of growing strength, hold what they
