@@ -558,10 +558,7 @@ PartPlan plan(const Shape &s, int64_t num_q, int64_t num_req, int64_t max_kv) {
   const int64_t tok = p.kind == kWideItems ? 2 * p.tpt : p.tpt;
   const int64_t runs = num_req > 0 ? num_req : 1;
   const int64_t items = (num_q / tok > runs ? num_q / tok : runs) * s.n_kv;
-  if (p.kind == kSingleTokens)         // three CTAs to an SM, 128 keys a step
-    p.splits = plan_splits(items, 3 * kSms, (max_kv + kTile - 1) / kTile, 4.0);
-  else if (items >= kSms)
-    p.splits = 1;
+  if (p.kind == kSingleTokens || items >= kSms) p.splits = 1;
   return p;
 }
 
@@ -588,8 +585,11 @@ extern "C" CSA2_API int csa2_page_attn_workspace(int32_t num_q, int32_t num_req,
   dense::Shape s;
   const int st = pages::check_call(&b, n_heads, n_kv_heads, dim, CSA2_DT_BF16, 1.f, &s);
   if (st != CSA2_OK) return st;
-  const int splits = pages::plan(s, num_q, num_req, max_kv).splits;
-  *bytes = splits > 1 ? splits * dense::part_bytes(num_q, s) : 0;
+  const dense::PartPlan p = pages::plan(s, num_q, num_req, max_kv);
+  *bytes = num_q == 0 || num_req == 0            ? 0
+           : p.kind == dense::kSingleTokens ? pages::page_decode_bytes(s)
+           : p.splits > 1                       ? p.splits * dense::part_bytes(num_q, s)
+                                                : 0;
   return CSA2_OK;
 }
 
@@ -614,7 +614,9 @@ extern "C" CSA2_API int csa2_page_attn(const csa2_packed *b, int32_t n_heads, in
   const dense::PartPlan plan = pages::plan(s, b->num_q, b->num_req, max_kv);
   int splits = plan.splits;
   if (splits > workspace_bytes / part) splits = (int)(workspace_bytes / part);
-  const uint64_t ws = splits > 1 ? (uint64_t)(splits * part) : 0;
+  const bool single = plan.kind == dense::kSingleTokens;
+  uint64_t ws = splits > 1 ? (uint64_t)(splits * part) : 0;
+  if (single && workspace_bytes >= pages::page_decode_bytes(s)) ws = pages::page_decode_bytes(s);
   // outputs and workspace against the inputs and each other; out may be q
   const int64_t wide = (int64_t)n_heads * dim * 2;
   const uint64_t no = (uint64_t)b->num_q * wide, nl = (uint64_t)b->num_q * n_heads * 4;
@@ -651,10 +653,11 @@ extern "C" CSA2_API int csa2_page_attn(const csa2_packed *b, int32_t n_heads, in
     P.part_lse = P.part_o + splits * rows * s.dim;
   }
   const cudaStream_t cs = as_stream(stream);
-  const bool single = plan.kind == dense::kSingleTokens;
-  st = single ? pages::page_decode(s, pages::PageAttnParams{P, C8, q, ldq}, c, cs)
-              : pages::run_tiles(s, c, C8, q, ldq, P, plan.kind == dense::kNarrowItems, cs);
+  if (single)
+    return pages::page_decode(s, pages::PageAttnParams{P, C8, q, ldq}, c, ws ? workspace : nullptr,
+                              cs);
+  st = pages::run_tiles(s, c, C8, q, ldq, P, plan.kind == dense::kNarrowItems, cs);
   if (st != CSA2_OK || splits <= 1) return st;
   const dense::Join j{P.part_o, P.part_lse, splits, 0, b->num_q, b->num_req, b->cu_q, out, lse};
-  return dense::join_parts(s, j, !single, cs);
+  return dense::join_parts(s, j, true, cs);
 }

@@ -2,11 +2,19 @@
 // heads to a key head.
 //
 // Bound by the pages' bytes, each read once: at 128 channels a key's row is 128
-// bytes, and a few query rows meet it.  A CTA has one (token, key head, split); its
-// four warps take blocks of 32 keys in turn, each with its own running maximum, sum
-// and output, which are joined once at the end.  Each warp has a ring of kStages
-// blocks of its own in shared memory, filled by TMA: 24 copies of 8 KB in flight to
-// an SM, with no registers under them.
+// bytes, and a few query rows meet it.  All blocks of 32 keys of all (token, key
+// head) items lie in one row, and each of two CTAs to an SM takes an equal run of them,
+// whatever items it crosses, so that lengths of any mixture fill the GPU evenly and a
+// CTA starts once.  (With a CTA to an item or an equal split of one, each start and end
+// cost 5 us of memory time: 83 us for 61 requests of 2831 rows on average where this
+// takes RESULT_STEP, 331 for 96 of 10.9 thousand where this takes RESULT_LONG.)  An
+// item that two or more CTAs share is left as parts, at most two to a CTA, which
+// a second kernel joins.
+//
+// In a CTA one warp looks up pages and keeps a ring of blocks filled by TMA, across
+// items; four warps take the blocks in turn, each with its own running maximum, sum and
+// output of the item at hand, and join them at its end, while the ring holds some
+// microseconds of the next.
 //
 // Codes become f16 in registers, exactly, on their way into m16n8k16 products whose
 // wide operand the cache is:
@@ -19,16 +27,17 @@
 // Lines of 128 bytes are swizzled by TMA (16-byte chunk i of line l lies at i ^ l %
 // 8), and the keys' order within 16 is chosen so that no load of either operand meets
 // a bank twice: fragment row a holds key key_of(a).
-#include "decode_rows.cuh"
 #include "page_attn.cuh"
 
 namespace csa2 {
 namespace pages {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;                // that compute
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kKeys = 32;                // keys of a block
-constexpr int kStages = 2;
+constexpr int kLeast = 2;                // blocks of a CTA, at least: fewer CTAs run then
+constexpr int kSegs = 3;                 // segments published at a time
 
 // 8 x 8 16-bit values, transposed over the warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -46,20 +55,49 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// A run of blocks of one (token, key head).
+struct Segment {
+  int token, h;                          // token -1: no more
+  int keys;                              // that the token sees
+  int blk0, blocks;
+  int part;                              // 0: the item began in an earlier CTA, 1: it goes on
+                                         // in a later one; -1: the whole item
+  bool through;                          // it does both
+};
+
+// What of an item a CTA's first segment is, for the join; token -1: its own start.
+struct Mark {
+  int token, h, through, pad;
+};
+
+// CTAs of the grid, by groups of 8 query rows: as many to an SM as registers allow
+template <int kN>
+constexpr int kToSm = kN == 1 ? 3 : 2;
+template <int kN>
+constexpr int kCtas = kToSm<kN> * kSms;
+
 // kN: groups of 8 query rows
 template <int D, int kN>
 struct Shared {
   static constexpr int kSide = kKeys * D;            // bytes of a block's K or V
+  static constexpr int kRing = D == 128 ? 8 : 16;    // blocks, 64 KB
+  // A stage is one warp's for good: the warp waits for each of its phases in turn.  (A
+  // wait by parity that skips a phase does not wait.)
+  static_assert(kRing % kWarps == 0, "ring");
+  uint8_t ring[kRing][2][kSide];
   union {
-    uint8_t ring[kWarps][kStages][2][kSide];
-    float o[kWarps][8 * kN][D + 4];                  // once the ring is done with
+    uint2 q[kN][D / 16][32];                         // Q in fragment order, by lane
+    float o[kWarps][8 * kN][D / 2 + 4];              // half of the warps' channels
   };
-  uint2 q[kN][D / 16][32];                           // Q in fragment order, by lane
-  float lift[8 * kN], unlift[8 * kN];
+  float4 scales[kRing];                              // K's and V's of a block's halves
+  float lift[8 * kN];
   float ref[kWarps][8 * kN], sum[kWarps][8 * kN];
-  uint64_t full[kWarps][kStages];
+  uint64_t full[kRing], empty[kRing], seg_full[kSegs], seg_empty[kSegs];
+  Segment seg[kSegs];
   Bound bd;
-  uint32_t runs[kWarps];
+  int64_t scan[kThreads / 32];
+  int64_t total;
+  int run, i, h, blk;                                // where the CTA's blocks begin
 };
 
 // key of fragment row a (0..15) within 16
@@ -77,400 +115,656 @@ __device__ __forceinline__ int byte_of(int row, int chunk) {
   return line * 128 + ((at ^ (line & 7)) << 4);
 }
 
-// One item: the token's rows of key head h over a split of its request's m rows,
-// whose n query rows begin at q0.  `used`: blocks that this warp's ring has had.
-template <typename T, int D, int kN>
-__device__ __forceinline__ void decode_item(const PageAttnParams &P, const CUtensorMap *mk,
-                                            const CUtensorMap *mv, Shared<D, kN> &sh, int token,
-                                            int run, int q0, int n, int64_t m, int h, int split,
-                                            uint32_t &used, int &err) {
-  constexpr int kSide = Shared<D, kN>::kSide;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const int ns = P.at.splits > 0 ? P.at.splits : 1;
-  const Pages &C = P.cache;
-  const int64_t last = m - n + (token - q0);           // keys seen: 0 .. last
-  const int keys = last < 0 ? 0 : (int)last + 1;
-  const int blocks = (keys + kKeys - 1) / kKeys, each = (blocks + ns - 1) / ns;
-  const int b0 = min(blocks, split * each), b1 = min(blocks, b0 + each);
-  const int mine = b1 - b0 > warp ? (b1 - b0 - warp + kWarps - 1) / kWarps : 0;
-
-  // Pages of this warp's next 32 blocks, a block to a lane: ids of the pages of its
-  // halves (the same one where a page has 32 rows or more), and their scales, which
-  // are asked for with the copies and used two blocks later.
-  int id[2] = {-1, -1};
-  float na[2], nb[2], a[2], b[2];
-  bool checked[2];
-  const auto look_up = [&](int i0) {
-    const int64_t blk = b0 + warp + (int64_t)kWarps * (i0 + lane);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int64_t key = blk * kKeys + 16 * x;
-      if (x == 1 && C.shift > 4) {
-        id[1] = id[0];
-        continue;
-      }
-      id[x] = i0 + lane < mine && key < keys ? page_id(C, run, key >> C.shift, err) : -1;
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      checked[x] = id[x] >= 0;
-      na[x] = checked[x] ? C.k_scale[(int64_t)id[x] * P.at.n_kv + h] : 0.f;
-      nb[x] = checked[x] ? C.v_scale[(int64_t)id[x] * P.at.n_kv + h] : 0.f;
-    }
-  };
-  const auto fetch = [&](int i) {
-    if (i % 32 == 0) look_up(i);
-    const int p0 = __shfl_sync(0xffffffffu, id[0], i % 32);
-    const int p1 = __shfl_sync(0xffffffffu, id[1], i % 32);
-    if (lane == 0) {
-      const uint32_t s = used % kStages;
-      uint8_t *to = &sh.ring[warp][s][0][0];
-      uint64_t *bar = &sh.full[warp][s];
-      const int blk = b0 + warp + kWarps * i;
-      if (C.shift == 4) {
-        mbar_arrive_expect_tx(bar, (uint32_t)kSide * ((p0 >= 0) + (p1 >= 0)));
-        const int line = h * (16 * D / 128);
-        if (p0 >= 0) tma_load_3d(to, mk, 0, line, p0, bar);
-        if (p1 >= 0) tma_load_3d(to + kSide / 2, mk, 0, line, p1, bar);
-        if (p0 >= 0) tma_load_3d(to + kSide, mv, 0, line, p0, bar);
-        if (p1 >= 0) tma_load_3d(to + kSide + kSide / 2, mv, 0, line, p1, bar);
-      } else {
-        mbar_arrive_expect_tx(bar, p0 >= 0 ? 2u * kSide : 0u);
-        const int line = (h * C.page + ((blk * kKeys) & (C.page - 1))) * D / 128;
-        if (p0 >= 0) tma_load_3d(to, mk, 0, line, p0, bar);
-        if (p0 >= 0) tma_load_3d(to + kSide, mv, 0, line, p0, bar);
-      }
-    }
-    ++used;
-  };
-  const uint32_t used0 = used;
-  for (int i = 0; i < kStages && i < mine; ++i) fetch(i);
-
-  // Q's fragments; rows past the group's heads are zeros
-  const T *q = static_cast<const T *>(P.q) + (int64_t)token * P.ldq + (int64_t)h * P.at.group * D;
-  if (Elem<T>::kBf16) {
-    for (int r = warp; r < 8 * kN; r += kWarps) {
-      float amax = 0.f;
-      if (r < P.at.group)
-        for (int d = lane; d < D; d += 32) amax = fmaxf(amax, fabsf((float)q[r * D + d]));
-#pragma unroll
-      for (int k = 1; k < 32; k <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, k));
-      if (lane == 0) {
-        const float lift = lift_of(amax);
-        sh.lift[r] = lift;
-        sh.unlift[r] = 1.f / lift;
-      }
-    }
-    __syncthreads();
+// Runs of query rows as the blocks go over them.
+struct Run {
+  int lo, n;                             // query rows (n = 0: none, or skipped)
+  int64_t m;                             // cache rows
+};
+__device__ __forceinline__ Run run_at(const PageAttnParams &P, int r, int &err) {
+  const Seqs &S = P.at.seqs;
+  Run u;
+  seq_rows(S, r, u.lo, u.n, err);
+  u.m = S.kv_len[r];
+  if (u.m < 0 || u.m > S.kv_rows) {
+    if (u.n) err |= CSA2_DERR_RANGE_ROW;
+    u.m = 0;
   }
-  for (int i = threadIdx.x; i < kN * D / 16 * 32; i += kWarps * 32) {
-    const int l = i & 31, x = (i >> 5) % (D / 16), r = (i >> 5) / (D / 16) * 8 + (l >> 2);
-    const int ch = 16 * ((l & 3) + 4 * (x >> 2)) + 4 * (x & 3);
-    uint2 w = make_uint2(0, 0);
-    if (r < P.at.group) {
-      w = *reinterpret_cast<const uint2 *>(q + r * D + ch);
-      if (Elem<T>::kBf16) {
-        const float f = sh.lift[r];
-        w = make_uint2(Elem<__half>::pack(__uint_as_float(w.x << 16) * f,
-                                          __uint_as_float(w.x & 0xffff0000u) * f),
-                       Elem<__half>::pack(__uint_as_float(w.y << 16) * f,
-                                          __uint_as_float(w.y & 0xffff0000u) * f));
+  return u;
+}
+__device__ __forceinline__ int keys_of(const Run &u, int i) {
+  const int64_t last = u.m - u.n + i;                // keys seen: 0 .. last
+  return last < 0 ? 0 : (int)last + 1;
+}
+// a token that sees nothing has a block, too: its output is written
+__device__ __forceinline__ int blocks_of(int keys) { return max(1, (keys + kKeys - 1) / kKeys); }
+
+// Finds the CTA's share of the blocks: [begin, end) of the total, and the run, token and
+// head at `begin`.  By the whole CTA; false if it has none.
+template <int D, int kN>
+__device__ bool find_share(const PageAttnParams &P, Shared<D, kN> &sh, int64_t &begin,
+                           int64_t &end, int &err) {
+  const Seqs &S = P.at.seqs;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (S.count + kThreads - 1) / kThreads;
+  const int r0 = min(S.count, (int)threadIdx.x * per), r1 = min(S.count, r0 + per);
+  int64_t own = 0;
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) {
+    const Run u = run_at(P, r, err);
+    for (int i = 0; i < u.n; ++i) own += blocks_of(keys_of(u, i));
+  }
+  int64_t upto = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) sh.scan[warp] = upto;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) upto += sh.scan[w];
+    total += sh.scan[w];
+  }
+  total *= P.at.n_kv;
+  // (32 bits divide in a fifth of the time)
+  const int64_t ctas = max(1, (int)min((int64_t)gridDim.x, total / kLeast));
+  const int64_t share = total >> 32 ? total / ctas : (int64_t)((uint32_t)total / (uint32_t)ctas);
+  const int64_t more = total - share * ctas;         // CTAs that have one more
+  if (blockIdx.x >= ctas || total == 0) return false;
+  begin = share * blockIdx.x + min((int64_t)blockIdx.x, more);
+  end = begin + share + (blockIdx.x < more);
+  int64_t at = (upto - own) * P.at.n_kv;             // of this thread's first run
+  if (at <= begin && begin < at + own * P.at.n_kv) {
+    int ignored = 0;
+    for (int r = r0; r < r1; ++r) {
+      const Run u = run_at(P, r, ignored);
+      for (int i = 0; i < u.n; ++i) {
+        const int64_t b = blocks_of(keys_of(u, i));
+        if (begin < at + b * P.at.n_kv) {
+          sh.run = r, sh.i = i;
+          int head = 0;
+          for (; begin - at >= b; ++head) at += b;
+          sh.h = head;
+          sh.blk = (int)(begin - at);
+          r = r1;
+          break;
+        }
+        at += b * P.at.n_kv;
       }
     }
-    (&sh.q[0][0][0])[i] = w;
   }
   __syncthreads();
+  return true;
+}
 
-  // this thread's rows: 8 y + 2 c + r
-  float o[kN][D / 16][4] = {}, ref[kN][2], sum[kN][2], unit[kN][2];
-#pragma unroll
-  for (int y = 0; y < kN; ++y)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      ref[y][r] = -INFINITY, sum[y][r] = 0.f;
-      unit[y][r] = P.at.scale_log2 * (Elem<T>::kBf16 ? sh.unlift[8 * y + 2 * c + r] : 1.f);
-    }
+// The warp that fills the ring.  A lane holds one of 32 neighbouring blocks of the
+// segment: the ids of its halves' pages (the same one where a page has 32 rows or more)
+// and their scales.
+template <int D, int kN>
+__device__ void producer_role(const PageAttnParams &P, Shared<D, kN> &sh, const CUtensorMap *mk,
+                              const CUtensorMap *mv, int64_t begin, int64_t end, int &err) {
+  using Sh = Shared<D, kN>;
+  constexpr int kSide = Sh::kSide;
+  const int lane = threadIdx.x & 31;
+  const Pages &C = P.cache;
+  const Seqs &S = P.at.seqs;
+  const bool whole = P.at.splits == 0;   // items are not shared: those that begin in the share
+  int run = sh.run, i = sh.i, h = sh.h, blk = sh.blk, ignored = 0;
+  Run u = run_at(P, run, ignored);
+  uint32_t g = 0, segs = 0;              // blocks and segments so far
   bool ok = true;
-  int i = 0;
-  for (; i < mine; ++i) {
-    if (i % 32 == 0) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        a[x] = checked[x] ? scale_of(na[x], err) : 0.f;
-        b[x] = checked[x] ? scale_of(nb[x], err) : 0.f;
+  for (int64_t at = begin; ok;) {
+    const int keys = keys_of(u, i), all = blocks_of(keys);
+    int n = 0;
+    if (at >= end) break;
+    if (whole) {
+      n = blk == 0 ? all : 0;
+      at += all - blk;
+    } else {
+      n = (int)min((int64_t)(all - blk), end - at);
+      at += n;
+    }
+    if (n > 0) {
+      const uint32_t slot = segs % kSegs;
+      if (!(ok = wait_all(&sh.seg_empty[slot], ((segs / kSegs) & 1) ^ 1, &sh.bd))) break;
+      if (lane == 0) {
+        const bool cut = blk + n < all;
+        sh.seg[slot] = Segment{u.lo + i, h, keys, blk, n, blk > 0 ? 0 : cut ? 1 : -1, blk > 0 && cut};
+        mbar_arrive(&sh.seg_full[slot]);
       }
+      __syncwarp();
+      ++segs;
     }
-    const uint32_t s = (used0 + i) % kStages;
-    if (!(ok = wait_all(&sh.full[warp][s], ((used0 + i) / kStages) & 1, &sh.bd))) break;
-    uint8_t *kt = &sh.ring[warp][s][0][0], *vt = kt + kSide;
-    const int key0 = (b0 + warp + kWarps * i) * kKeys;
-    float ka[2], vb[2];
+    int id[2] = {-1, -1};
+    float a[2], b[2];
+    for (int k = 0; k < n; ++k, ++g) {
+      const int first = blk + k;
+      if (k % 32 == 0) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      ka[x] = __shfl_sync(0xffffffffu, a[x], i % 32);
-      vb[x] = __shfl_sync(0xffffffffu, b[x], i % 32);
-    }
-    const bool whole = key0 + kKeys <= keys && vb[0] != 0.f && vb[1] != 0.f;
-    if (!whole) {
-      // rows behind the last and rows without a page may hold NaN: 0 * NaN
-      for (int r = 0; r < kKeys; ++r)
-        if (key0 + r >= keys || vb[r >> 4] == 0.f)
-          for (int d = lane; d < D / 16; d += 32)
-            *reinterpret_cast<uint4 *>(vt + byte_of<D>(r, d)) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();          // the next copy into them comes later
+        for (int x = 0; x < 2; ++x) {
+          const int64_t key = (int64_t)(first + lane) * kKeys + 16 * x;
+          if (x == 1 && C.shift > 4)
+            id[1] = id[0];
+          else
+            id[x] = k + lane < n && key < keys ? page_id(C, run, key >> C.shift, err) : -1;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          a[x] = id[x] >= 0 ? C.k_scale[(int64_t)id[x] * P.at.n_kv + h] : 0.f;
+          b[x] = id[x] >= 0 ? C.v_scale[(int64_t)id[x] * P.at.n_kv + h] : 0.f;
+        }
+      }
+      const uint32_t s = g % Sh::kRing;
+      if (!(ok = wait_all(&sh.empty[s], ((g / Sh::kRing) & 1) ^ 1, &sh.bd))) break;
+      const int p0 = __shfl_sync(0xffffffffu, id[0], k % 32);
+      const int p1 = __shfl_sync(0xffffffffu, id[1], k % 32);
+      if (lane == 0) {
+        uint8_t *to = sh.ring[s][0];
+        uint64_t *bar = &sh.full[s];
+        if (C.shift == 4) {
+          mbar_arrive_expect_tx(bar, (uint32_t)kSide * ((p0 >= 0) + (p1 >= 0)));
+          const int line = h * (16 * D / 128);
+          if (p0 >= 0) tma_load_3d(to, mk, 0, line, p0, bar);
+          if (p1 >= 0) tma_load_3d(to + kSide / 2, mk, 0, line, p1, bar);
+          if (p0 >= 0) tma_load_3d(to + kSide, mv, 0, line, p0, bar);
+          if (p1 >= 0) tma_load_3d(to + kSide + kSide / 2, mv, 0, line, p1, bar);
+        } else {
+          mbar_arrive_expect_tx(bar, p0 >= 0 ? 2u * kSide : 0u);
+          const int line = (h * C.page + ((first * kKeys) & (C.page - 1))) * D / 128;
+          if (p0 >= 0) tma_load_3d(to, mk, 0, line, p0, bar);
+          if (p0 >= 0) tma_load_3d(to + kSide, mv, 0, line, p0, bar);
+        }
+      }
+      __syncwarp();
+      // the scales come after the copies: they may still be on their way
+      if (k % 32 == 0) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          a[x] = id[x] >= 0 ? scale_of(a[x], err) : 0.f;
+          b[x] = id[x] >= 0 ? scale_of(b[x], err) : 0.f;
+        }
+      }
+      if (lane == k % 32) {
+        sh.scales[s] = make_float4(a[0], a[1], b[0], b[1]);
+        mbar_arrive(&sh.full[s]);
+      }
       __syncwarp();
     }
-    // S^T: accumulator e: fragment row g + 8 (e / 2), query row 2 c + e % 2
-    float st[2][kN][4] = {};
+    // the next item
+    blk = 0;
+    if (++h < P.at.n_kv) continue;
+    h = 0;
+    if (++i < u.n) continue;
+    i = 0;
+    for (++run; run < S.count; run += 32) {
+      int lo = 0, c = 0;
+      if (run + lane < S.count) seq_rows(S, run + lane, lo, c, ignored);
+      const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
+      if (some) {
+        run += __ffs(some) - 1;
+        break;
+      }
+    }
+    if (run >= S.count) break;
+    u = run_at(P, run, ignored);
+  }
+  if (ok) {
+    const uint32_t slot = segs % kSegs;
+    ok = wait_all(&sh.seg_empty[slot], ((segs / kSegs) & 1) ^ 1, &sh.bd);
+    if (ok && lane == 0) {
+      sh.seg[slot].token = -1;
+      mbar_arrive(&sh.seg_full[slot]);
+    }
+  }
+  // copies land before the CTA leaves
+  if (!ok && lane == 0)
+    for (uint32_t k = g > (uint32_t)Sh::kRing ? g - Sh::kRing : 0; k < g; ++k)
+      drain_bar(&sh.full[k % Sh::kRing], (k / Sh::kRing) & 1);
+  __syncwarp();
+}
+
+// barrier of the warps that compute; whether any thread says so
+__device__ __forceinline__ bool any_of_us(bool say) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((int)say), "n"(32 * kWarps)
+      : "memory");
+  return r != 0;
+}
+
+// The four warps that compute.
+template <typename T, int D, int kN>
+__device__ __forceinline__ void compute_role(const PageAttnParams &P, Shared<D, kN> &sh) {
+  using Sh = Shared<D, kN>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  uint32_t taken = 0;                    // blocks of the segments so far
+  for (uint32_t u = 0;; ++u) {
+    const uint32_t slot = u % kSegs;
+    bool ok = wait_all(&sh.seg_full[slot], (u / kSegs) & 1, &sh.bd);
+    // (also: the last segment's sums in shared memory are read)
+    if (any_of_us(!ok)) return;
+    const Segment seg = sh.seg[slot];
+    if (seg.token < 0) return;
+    // Q's fragments; rows past the group's heads are zeros
+    const T *q = static_cast<const T *>(P.q) + (int64_t)seg.token * P.ldq +
+                 (int64_t)seg.h * P.at.group * D;
+    if (Elem<T>::kBf16) {
+      for (int r = warp; r < 8 * kN; r += kWarps) {
+        float amax = 0.f;
+        if (r < P.at.group) {
+          if (D == 128) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(q + r * D + 4 * lane);
+            amax = fmaxf(max3(fabsf(__uint_as_float(w.x << 16)),
+                              fabsf(__uint_as_float(w.x & 0xffff0000u)),
+                              fabsf(__uint_as_float(w.y << 16))),
+                         fabsf(__uint_as_float(w.y & 0xffff0000u)));
+          } else {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(q + r * D + 2 * lane);
+            amax = fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u)));
+          }
+        }
+        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+        if (lane == 0) sh.lift[r] = lift_of(amax);
+      }
+      any_of_us(false);
+    }
+    for (int i = threadIdx.x; i < kN * D / 16 * 32; i += kWarps * 32) {
+      const int l = i & 31, x = (i >> 5) % (D / 16), r = (i >> 5) / (D / 16) * 8 + (l >> 2);
+      const int ch = 16 * ((l & 3) + 4 * (x >> 2)) + 4 * (x & 3);
+      uint2 w = make_uint2(0, 0);
+      if (r < P.at.group) {
+        w = *reinterpret_cast<const uint2 *>(q + r * D + ch);
+        if (Elem<T>::kBf16) {
+          const float f = sh.lift[r];
+          w = make_uint2(Elem<__half>::pack(__uint_as_float(w.x << 16) * f,
+                                            __uint_as_float(w.x & 0xffff0000u) * f),
+                         Elem<__half>::pack(__uint_as_float(w.y << 16) * f,
+                                            __uint_as_float(w.y & 0xffff0000u) * f));
+        }
+      }
+      (&sh.q[0][0][0])[i] = w;
+    }
+    any_of_us(false);
+
+    // this thread's rows: 8 y + 2 c + r
+    float o[kN][D / 16][4] = {}, ref[kN][2], sum[kN][2], unit[kN][2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int y = 0; y < kN; ++y)
 #pragma unroll
-      for (int ch = 0; ch < D / 64; ++ch) {
-        uint4 w[2];
+      for (int r = 0; r < 2; ++r) {
+        ref[y][r] = -INFINITY, sum[y][r] = 0.f;
+        unit[y][r] = P.at.scale_log2 / (Elem<T>::kBf16 ? sh.lift[8 * y + 2 * c + r] : 1.f);
+      }
+    for (int k = (int)((warp - taken) & (kWarps - 1)); k < seg.blocks; k += kWarps) {
+      const uint32_t s = (taken + k) % Sh::kRing;
+      if (!(ok = wait_all(&sh.full[s], ((taken + k) / Sh::kRing) & 1, &sh.bd))) break;
+      uint8_t *kt = sh.ring[s][0], *vt = sh.ring[s][1];
+      const int key0 = (seg.blk0 + k) * kKeys;
+      const float4 sc = sh.scales[s];
+      const float ka[2] = {sc.x, sc.y}, vb[2] = {sc.z, sc.w};
+      const bool all = key0 + kKeys <= seg.keys && vb[0] != 0.f && vb[1] != 0.f;
+      if (!all) {
+        // rows behind the last and rows without a page may hold NaN: 0 * NaN
+        for (int r = 0; r < kKeys; ++r)
+          if (key0 + r >= seg.keys || vb[r >> 4] == 0.f)
+            for (int d = lane; d < D / 16; d += 32)
+              *reinterpret_cast<uint4 *>(vt + byte_of<D>(r, d)) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();          // the next copy into them comes later
+        __syncwarp();
+      }
+      // S^T: accumulator e: fragment row g + 8 (e / 2), query row 2 c + e % 2
+      float st[2][kN][4] = {};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          w[t] = *reinterpret_cast<const uint4 *>(
-              kt + byte_of<D>(16 * x + key_of<D>(g + 8 * t), c + 4 * ch));
-        const uint32_t *w0 = &w[0].x, *w1 = &w[1].x;
+      for (int x = 0; x < 2; ++x) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a0 = f16x2_of(w0[j]), a1 = f16x2_of(w1[j]);
-          const uint32_t a2 = f16x2_of_high(w0[j]), a3 = f16x2_of_high(w1[j]);
+        for (int ch = 0; ch < D / 64; ++ch) {
+          uint4 w[2];
 #pragma unroll
-          for (int y = 0; y < kN; ++y) {
-            const uint2 qv = sh.q[y][4 * ch + j][lane];
-            mma16816(st[x][y], a0, a1, a2, a3, qv.x, qv.y);
+          for (int t = 0; t < 2; ++t)
+            w[t] = *reinterpret_cast<const uint4 *>(
+                kt + byte_of<D>(16 * x + key_of<D>(g + 8 * t), c + 4 * ch));
+          const uint32_t *w0 = &w[0].x, *w1 = &w[1].x;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a0 = f16x2_of(w0[j]), a1 = f16x2_of(w1[j]);
+            const uint32_t a2 = f16x2_of_high(w0[j]), a3 = f16x2_of_high(w1[j]);
+#pragma unroll
+            for (int y = 0; y < kN; ++y) {
+              const uint2 qv = sh.q[y][4 * ch + j][lane];
+              mma16816(st[x][y], a0, a1, a2, a3, qv.x, qv.y);
+            }
           }
         }
       }
-    }
-    float lb[2], ib[2];
+      float lb[2], ib[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      lb[x] = log2f(vb[x]);              // -inf without a page: masked below
-      ib[x] = vb[x] != 0.f ? 1.f / vb[x] : 0.f;
+      for (int x = 0; x < 2; ++x) {
+        lb[x] = log2f(vb[x]);              // -inf without a page: masked below
+        ib[x] = vb[x] != 0.f ? 1.f / vb[x] : 0.f;
+#pragma unroll
+        for (int y = 0; y < kN; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            st[x][y][e] = fmaf(st[x][y][e], unit[y][e & 1] * ka[x], lb[x]);
+      }
+      if (!all) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key0 + 16 * x + key_of<D>(g + 8 * (e >> 1)) >= seg.keys || vb[x] == 0.f)
+#pragma unroll
+              for (int y = 0; y < kN; ++y) st[x][y][e] = -INFINITY;
+      }
+      uint32_t pt[2][kN][2];
+#pragma unroll
+      for (int y = 0; y < kN; ++y) {
+        float alpha[2];
+        bool moved = false;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) mx = max3(mx, st[x][y][r], st[x][y][2 + r]);
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+          alpha[r] = 1.f;
+          if (mx > ref[y][r] + (kLift + kMargin)) {
+            alpha[r] = ex2(ref[y][r] - (mx - kLift));
+            ref[y][r] = mx - kLift;
+            moved = true;
+          }
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+          sum[y][0] *= alpha[0], sum[y][1] *= alpha[1];
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            o[y][d][0] *= alpha[0], o[y][d][1] *= alpha[1];
+            o[y][d][2] *= alpha[0], o[y][d][3] *= alpha[1];
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float base = ref[y][e & 1] == -INFINITY ? 0.f : ref[y][e & 1];
+            w[e] = ex2(st[x][y][e] - base);
+          }
+          sum[y][0] = fmaf(w[0] + w[2], ib[x], sum[y][0]);
+          sum[y][1] = fmaf(w[1] + w[3], ib[x], sum[y][1]);
+          pt[x][y][0] = transpose8(Elem<__half>::pack(w[0], w[1]));
+          pt[x][y][1] = transpose8(Elem<__half>::pack(w[2], w[3]));
+        }
+      }
+      // O^T: product d has channels (D / 8) g + 2 d (rows g) and + 1 (rows g + 8)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = 16 * x + key_of<D>(2 * c + (u & 1) + 8 * (u >> 1));
+          if (D == 128) {
+            *reinterpret_cast<uint4 *>(v[u]) =
+                *reinterpret_cast<const uint4 *>(vt + byte_of<D>(row, g));
+          } else {
+            *reinterpret_cast<uint2 *>(v[u]) =
+                *reinterpret_cast<const uint2 *>(vt + byte_of<D>(row, g >> 1) + 8 * (g & 1));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t p = __byte_perm(v[0][j], v[1][j], e ? 0x7362 : 0x5140);
+            const uint32_t r = __byte_perm(v[2][j], v[3][j], e ? 0x7362 : 0x5140);
+            const uint32_t a0 = f16x2_of(p), a1 = f16x2_of_high(p);
+            const uint32_t a2 = f16x2_of(r), a3 = f16x2_of_high(r);
+#pragma unroll
+            for (int y = 0; y < kN; ++y)
+              mma16816(o[y][2 * j + e], a0, a1, a2, a3, pt[x][y][0], pt[x][y][1]);
+          }
+        }
+      }
+      __syncwarp();                        // every lane has read the stage
+      if (lane == 0) mbar_arrive(&sh.empty[s]);
+    }
+    taken += seg.blocks;
+
+    // join the warps: each row's statistics and sums, weighted, by halves of the products
+    // (the channels (D / 8) g + 2 d and + 1 of products d)
+    if (any_of_us(!ok)) return;          // (and Q is done with)
+    if (threadIdx.x == 0) mbar_arrive(&sh.seg_empty[slot]);
+#pragma unroll
+    for (int y = 0; y < kN; ++y)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) sum[y][r] += __shfl_xor_sync(0xffffffffu, sum[y][r], k);
+        const int row = 8 * y + 2 * c + r;
+        if (g == 0) sh.ref[warp][row] = ref[y][r], sh.sum[warp][row] = sum[y][r];
+      }
+    constexpr int kRows = 8 * kN, kTeam = kWarps * 32 / kRows;       // threads of a row
+    constexpr int kHalf = D / 16;        // channels of a lane group in a half
+    const int row = threadIdx.x / kTeam, col = threadIdx.x % kTeam;
+    const bool mine = row < P.at.group;
+    const int64_t part = (2 * (int64_t)blockIdx.x + seg.part) * kRows + row;
+    const int64_t at = (int64_t)seg.token * P.at.n_heads + seg.h * P.at.group + row;
+    float w[kWarps];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (half) any_of_us(false);        // the first half is read
 #pragma unroll
       for (int y = 0; y < kN; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          st[x][y][e] = fmaf(st[x][y][e], unit[y][e & 1] * ka[x], lb[x]);
-    }
-    if (!whole) {
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+          for (int d = 0; d < D / 32; ++d)
+            *reinterpret_cast<float2 *>(&sh.o[warp][8 * y + 2 * c + r][kHalf * g + 2 * d]) =
+                make_float2(o[y][half * (D / 32) + d][r], o[y][half * (D / 32) + d][2 + r]);
+      any_of_us(false);
+      if (half == 0) {
+        float top = -INFINITY, tot = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (key0 + 16 * x + key_of<D>(g + 8 * (e >> 1)) >= keys || vb[x] == 0.f)
+        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sh.ref[k][row]);
+        const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-            for (int y = 0; y < kN; ++y) st[x][y][e] = -INFINITY;
-    }
-    uint32_t pt[2][kN][2];
+        for (int k = 0; k < kWarps; ++k) {
+          w[k] = ex2(sh.ref[k][row] - base);
+          tot += sh.sum[k][row] * w[k];
+        }
+        const bool seen = !(tot == 0.f);   // a NaN stays a NaN
+        const float inv = seen ? 1.f / tot : 0.f;
 #pragma unroll
-    for (int y = 0; y < kN; ++y) {
-      float alpha[2];
-      bool moved = false;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) mx = max3(mx, st[x][y][r], st[x][y][2 + r]);
-#pragma unroll
-        for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-        alpha[r] = 1.f;
-        if (mx > ref[y][r] + (kLift + kMargin)) {
-          alpha[r] = ex2(ref[y][r] - (mx - kLift));
-          ref[y][r] = mx - kLift;
-          moved = true;
+        for (int k = 0; k < kWarps; ++k) w[k] = seen ? w[k] * inv : 0.f;
+        const float lse = seen ? (base + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+        if (col == 0 && mine) {
+          if (seg.part >= 0)
+            P.at.part_lse[part] = lse;
+          else if (P.at.lse)
+            P.at.lse[at] = lse;
         }
       }
-      if (__any_sync(0xffffffffu, moved)) {
-        sum[y][0] *= alpha[0], sum[y][1] *= alpha[1];
+      if (mine) {
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-          o[y][d][0] *= alpha[0], o[y][d][1] *= alpha[1];
-          o[y][d][2] *= alpha[0], o[y][d][3] *= alpha[1];
+        for (int x = 4 * col; x < D / 2; x += 4 * kTeam) {
+          const int d = x / kHalf * (D / 8) + half * kHalf + x % kHalf;
+          float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) {
+            const float4 v = *reinterpret_cast<const float4 *>(&sh.o[k][row][x]);
+            f[0] = fmaf(w[k], v.x, f[0]), f[1] = fmaf(w[k], v.y, f[1]);
+            f[2] = fmaf(w[k], v.z, f[2]), f[3] = fmaf(w[k], v.w, f[3]);
+          }
+          if (seg.part >= 0)
+            *reinterpret_cast<float4 *>(P.at.part_o + part * D + d) =
+                make_float4(f[0], f[1], f[2], f[3]);
+          else
+            *reinterpret_cast<uint2 *>(static_cast<T *>(P.at.out) + at * D + d) =
+                make_uint2(Elem<T>::pack(f[0], f[1]), Elem<T>::pack(f[2], f[3]));
         }
       }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float base = ref[y][e & 1] == -INFINITY ? 0.f : ref[y][e & 1];
-          w[e] = ex2(st[x][y][e] - base);
-        }
-        sum[y][0] = fmaf(w[0] + w[2], ib[x], sum[y][0]);
-        sum[y][1] = fmaf(w[1] + w[3], ib[x], sum[y][1]);
-        pt[x][y][0] = transpose8(Elem<__half>::pack(w[0], w[1]));
-        pt[x][y][1] = transpose8(Elem<__half>::pack(w[2], w[3]));
-      }
-    }
-    // O^T: product d has channels (D / 8) g + 2 d (rows g) and + 1 (rows g + 8)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      uint32_t v[4][D / 32];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int row = 16 * x + key_of<D>(2 * c + (u & 1) + 8 * (u >> 1));
-        if (D == 128) {
-          *reinterpret_cast<uint4 *>(v[u]) =
-              *reinterpret_cast<const uint4 *>(vt + byte_of<D>(row, g));
-        } else {
-          *reinterpret_cast<uint2 *>(v[u]) =
-              *reinterpret_cast<const uint2 *>(vt + byte_of<D>(row, g >> 1) + 8 * (g & 1));
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t p = __byte_perm(v[0][j], v[1][j], e ? 0x7362 : 0x5140);
-          const uint32_t r = __byte_perm(v[2][j], v[3][j], e ? 0x7362 : 0x5140);
-          const uint32_t a0 = f16x2_of(p), a1 = f16x2_of_high(p);
-          const uint32_t a2 = f16x2_of(r), a3 = f16x2_of_high(r);
-#pragma unroll
-          for (int y = 0; y < kN; ++y)
-            mma16816(o[y][2 * j + e], a0, a1, a2, a3, pt[x][y][0], pt[x][y][1]);
-        }
-      }
-    }
-    __syncwarp();                        // every lane has read the stage
-    if (i + kStages < mine) fetch(i + kStages);
-  }
-  if (!ok && lane == 0)                  // copies land before the CTA leaves
-    for (uint32_t u = used0 + i; u != used; ++u)
-      drain_bar(&sh.full[warp][u % kStages], (u / kStages) & 1);
-  __syncthreads();                       // the ring is done with
-
-  // join the warps: each row's statistics and sums, weighted
-#pragma unroll
-  for (int y = 0; y < kN; ++y) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-#pragma unroll
-      for (int k = 4; k < 32; k <<= 1) sum[y][r] += __shfl_xor_sync(0xffffffffu, sum[y][r], k);
-      const int row = 8 * y + 2 * c + r;
-      if (g == 0) sh.ref[warp][row] = ref[y][r], sh.sum[warp][row] = sum[y][r];
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d)
-        *reinterpret_cast<float2 *>(&sh.o[warp][row][D / 8 * g + 2 * d]) =
-            make_float2(o[y][d][r], o[y][d][2 + r]);
-    }
-  }
-  __syncthreads();
-  // a result's rows are channel-innermost, a partial result's blocks row-innermost
-  const bool part = P.at.splits > 0;
-  constexpr int kRows = 8 * kN, kTeam = kWarps * 32 / kRows;       // threads of a row
-  const int row = part ? threadIdx.x % kRows : threadIdx.x / kTeam;
-  const int col = part ? threadIdx.x / kRows : threadIdx.x % kTeam;
-  if (row >= P.at.group) return;
-  float top = -INFINITY, tot = 0.f, w[kWarps];
-#pragma unroll
-  for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sh.ref[k][row]);
-  const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-  for (int k = 0; k < kWarps; ++k) {
-    w[k] = ex2(sh.ref[k][row] - base);
-    tot += sh.sum[k][row] * w[k];
-  }
-  const bool seen = !(tot == 0.f);   // a NaN stays a NaN
-  const float inv = seen ? 1.f / tot : 0.f;
-  const float lse = seen ? (base + log2f(tot)) * 0.6931471805599453f : -INFINITY;
-  if (part) {
-    const int64_t rows = part_rows(P.at.seqs.num_q, P.at.group), at = (int64_t)token * P.at.group + row;
-    if (col == 0) P.at.part_lse[part_stat(rows, P.at.n_kv, split, h, at)] = lse;
-    if (!seen) return;
-    float *dst = P.at.part_o + part_elem(rows, P.at.n_kv, D, split, h, at);
-#pragma unroll 4
-    for (int d = col; d < D; d += kTeam) {
-      float f = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) f = fmaf(w[k], sh.o[k][row][d], f);
-      dst[d * 32] = f * inv;
-    }
-  } else {
-    const int64_t at = (int64_t)token * P.at.n_heads + h * P.at.group + row;
-    if (col == 0 && P.at.lse) P.at.lse[at] = lse;
-#pragma unroll
-    for (int d = 4 * col; d < D; d += 4 * kTeam) {
-      float f[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        const float4 v = *reinterpret_cast<const float4 *>(&sh.o[k][row][d]);
-        f[0] = fmaf(w[k], v.x, f[0]), f[1] = fmaf(w[k], v.y, f[1]);
-        f[2] = fmaf(w[k], v.z, f[2]), f[3] = fmaf(w[k], v.w, f[3]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = seen ? f[e] * inv : 0.f;
-      *reinterpret_cast<uint2 *>(static_cast<T *>(P.at.out) + at * D + d) =
-          make_uint2(Elem<T>::pack(f[0], f[1]), Elem<T>::pack(f[2], f[3]));
+      __syncwarp();
     }
   }
 }
 
 template <typename T, int D, int kN>
-__global__ void __launch_bounds__(kWarps * 32, kN == 2 ? 2 : 3)
-page_decode_kernel(const __grid_constant__ PageAttnParams P, const __grid_constant__ CUtensorMap mk,
-                   const __grid_constant__ CUtensorMap mv) {
-  // the join may start on the SMs that the last items leave
+__global__ void __launch_bounds__(kThreads, kToSm<kN>)
+page_decode_kernel(const __grid_constant__ PageAttnParams P, Mark *marks,
+                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  // the join may start on the SMs that the last CTAs leave
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(1024) uint8_t smem[];
   Shared<D, kN> &sh = *reinterpret_cast<Shared<D, kN> *>(smem);
   if (threadIdx.x == 0) {
-    for (int w = 0; w < kWarps; ++w)
-      for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[w][s], 1);
+    for (int s = 0; s < Shared<D, kN>::kRing; ++s) {
+      mbar_init(&sh.full[s], 2);         // copies asked for, scales written
+      mbar_init(&sh.empty[s], 1);
+    }
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(&sh.seg_full[s], 1);
+      mbar_init(&sh.seg_empty[s], 1);
+    }
     sh.bd.abort = 0;
     sh.bd.wait_ns = P.at.wait_ns;
     mbar_fence_init();
   }
-  __syncthreads();
-  uint32_t used = 0;
   int err = 0;
-  bool again = false;
-  each_item<kWarps, true>(P.at.seqs, P.at.n_kv, P.at.group, P.at.splits, P.at.part_lse, P.at.d_err, sh.runs,
-                          [&](int token, int run, int q0, int n, int64_t, int64_t m, int h,
-                              int split) {
-                            if (again) {  // the ring held a join's sums
-                              fence_proxy_async_smem();
-                              __syncthreads();
-                            }
-                            again = true;
-                            decode_item<T, D, kN>(P, &mk, &mv, sh, token, run, q0, n, m, h,
-                                                  split, used, err);
-                          });
-  if (*(volatile int *)&sh.bd.abort) err |= CSA2_DERR_TIMEOUT;
+  int64_t begin = 0, end = 0;
+  const bool some = find_share(P, sh, begin, end, err);
+  if (blockIdx.x > 0) err = 0;           // one CTA speaks of the requests
+  if (marks && threadIdx.x == 0) {
+    Mark mark{-1, 0, 0, 0};
+    if (some && sh.blk > 0) {
+      int ignored = 0;
+      const Run u = run_at(P, sh.run, ignored);
+      const int all = blocks_of(keys_of(u, sh.i));
+      mark = Mark{u.lo + sh.i, sh.h, sh.blk + (end - begin) < all, 0};
+    }
+    marks[blockIdx.x] = mark;
+  }
+  if (some) {
+    if (threadIdx.x >= 32 * kWarps)
+      producer_role(P, sh, &mk, &mv, begin, end, err);
+    else
+      compute_role<T>(P, sh);
+    __syncthreads();
+    if (threadIdx.x == 0 && sh.bd.abort) err |= CSA2_DERR_TIMEOUT;
+  }
   if (err) raise_err(P.at.d_err, err);
 }
 
+// Joins the parts of items that CTAs shared: block j - 1 those of the item that goes on
+// in CTA j, if it began in the CTA before.
+constexpr int kJoin = 256;
+
 template <typename T, int D, int kN>
-int launch(const PageAttnParams &P, int grid, const CUtensorMap &mk, const CUtensorMap &mv,
+__global__ void __launch_bounds__(kJoin)
+page_join_kernel(const __grid_constant__ PageAttnParams P, const Mark *marks) {
+  constexpr int kRows = 8 * kN;
+  __shared__ float weight[kCtas<kN>][kRows];         // by part
+  __shared__ float total[kRows];
+  const int j = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_front();
+  const Mark mark = marks[j], before = marks[j - 1];
+  if (mark.token < 0 || (before.token >= 0 && before.through)) return;
+  int parts = 2;                                     // CTA j - 1's second, then first ones
+  for (int k = j; marks[k].through; ++k) ++parts;
+  const auto part = [&](int k) {
+    return (k == 0 ? 2 * (int64_t)(j - 1) + 1 : 2 * (int64_t)(j - 1 + k)) * kRows;
+  };
+  for (int r = warp; r < P.at.group; r += kJoin / 32) {
+    float top = -INFINITY, tot = 0.f;
+    bool nan = false;
+    for (int k = lane; k < parts; k += 32) {
+      const float l = P.at.part_lse[part(k) + r];
+      weight[k][r] = l;
+      nan |= l != l;
+      top = fmaxf(top, l);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (int k = lane; k < parts; k += 32) {
+      const float w = ex2((weight[k][r] - ref) * 1.4426950408889634f);
+      weight[k][r] = w;
+      tot += w;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    nan = __any_sync(0xffffffffu, nan);
+    if (lane == 0) {
+      total[r] = tot;
+      if (P.at.lse)
+        P.at.lse[(int64_t)mark.token * P.at.n_heads + mark.h * P.at.group + r] =
+            tot > 0.f || nan ? ref + log2f(tot) * 0.6931471805599453f : -INFINITY;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < P.at.group * (D / 4); i += kJoin) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float w = weight[k][r];
+      const float4 v = *reinterpret_cast<const float4 *>(P.at.part_o + (part(k) + r) * D + d);
+      f[0] = fmaf(w, v.x, f[0]), f[1] = fmaf(w, v.y, f[1]);
+      f[2] = fmaf(w, v.z, f[2]), f[3] = fmaf(w, v.w, f[3]);
+    }
+    const float inv = total[r] == 0.f ? 0.f : 1.f / total[r];
+    const int64_t at = (int64_t)mark.token * P.at.n_heads + mark.h * P.at.group + r;
+    *reinterpret_cast<uint2 *>(static_cast<T *>(P.at.out) + at * D + d) =
+        make_uint2(Elem<T>::pack(f[0] * inv, f[1] * inv), Elem<T>::pack(f[2] * inv, f[3] * inv));
+  }
+}
+
+template <typename T, int D, int kN>
+int launch(PageAttnParams P, const CUtensorMap &mk, const CUtensorMap &mv, void *ws,
            cudaStream_t st) {
   constexpr int kSmem = (int)sizeof(Shared<D, kN>);
+  static_assert(kSmem <= 232448 / kToSm<kN> - 1024, "CTAs to an SM");
   allow_smem<page_decode_kernel<T, D, kN>>(kSmem);
-  page_decode_kernel<T, D, kN><<<grid, kWarps * 32, kSmem, st>>>(P, mk, mv);
-  return launch_status();
+  Mark *marks = static_cast<Mark *>(ws);
+  P.at.splits = ws != nullptr;
+  if (ws) {
+    P.at.part_lse = reinterpret_cast<float *>(marks + kCtas<kN>);
+    P.at.part_o = P.at.part_lse + 2 * kCtas<kN> * 8 * kN;
+  }
+  page_decode_kernel<T, D, kN><<<kCtas<kN>, kThreads, kSmem, st>>>(P, marks, mk, mv);
+  const int e = launch_status();
+  if (e != CSA2_OK || !ws) return e;
+  return launch_behind(page_join_kernel<T, D, kN>, dim3(kCtas<kN> - 1), kJoin, 0, true, st, P,
+                       (const Mark *)marks);
 }
 
 template <typename T>
-int launch_any(const Shape &s, const PageAttnParams &P, int grid, const CUtensorMap &mk,
-               const CUtensorMap &mv, cudaStream_t st) {
+int launch_any(const Shape &s, const PageAttnParams &P, const CUtensorMap &mk,
+               const CUtensorMap &mv, void *ws, cudaStream_t st) {
   if (s.dim == 128)
-    return s.group <= 8 ? launch<T, 128, 1>(P, grid, mk, mv, st)
-                        : launch<T, 128, 2>(P, grid, mk, mv, st);
-  return s.group <= 8 ? launch<T, 64, 1>(P, grid, mk, mv, st)
-                      : launch<T, 64, 2>(P, grid, mk, mv, st);
+    return s.group <= 8 ? launch<T, 128, 1>(P, mk, mv, ws, st) : launch<T, 128, 2>(P, mk, mv, ws, st);
+  return s.group <= 8 ? launch<T, 64, 1>(P, mk, mv, ws, st) : launch<T, 64, 2>(P, mk, mv, ws, st);
 }
 
 }  // namespace
 
-int page_decode(const Shape &s, const PageAttnParams &P, const csa2_pages *c, cudaStream_t st) {
-  // an item to a block, and one that looks the batch over
-  const int64_t grid = (int64_t)P.at.seqs.num_q * P.at.n_kv * (P.at.splits > 0 ? P.at.splits : 1) + 1;
-  if (grid > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
+int64_t page_decode_bytes(const Shape &s) {
+  const int rows = s.group <= 8 ? 8 : 16;
+  const int64_t ctas = s.group <= 8 ? kCtas<1> : kCtas<2>;
+  return ctas * (int64_t)sizeof(Mark) + 2 * ctas * rows * (s.dim + 1) * 4;
+}
+
+int page_decode(const Shape &s, const PageAttnParams &P, const csa2_pages *c, void *ws,
+                cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!make_cache_maps(&mk, &mv, c, P.q, s, kKeys)) return CSA2_ERR_UNSUPPORTED;
-  return s.bf16 ? launch_any<__nv_bfloat16>(s, P, (int)grid, mk, mv, st)
-                : launch_any<__half>(s, P, (int)grid, mk, mv, st);
+  return s.bf16 ? launch_any<__nv_bfloat16>(s, P, mk, mv, ws, st)
+                : launch_any<__half>(s, P, mk, mv, ws, st);
 }
 
 }  // namespace pages

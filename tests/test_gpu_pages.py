@@ -395,6 +395,29 @@ def test_attn_single_tokens(heads, kv, dim, page, dtype):
             assert (t[:cu[0]] == 7).all() and (t[cu[-1]:] == 7).all()
 
 
+@pytest.mark.parametrize("shared", [False, True])
+def test_attn_single_tokens_of_any_number(shared):
+    """One long cache, many short ones, several tokens to a request among idle ones: items
+    that one, two and many CTAs share."""
+    heads, kv, dim, page, dtype = 6, 2, 64, 32, BF
+    for new, rows in (([1], [70000]), ([1] * 700, [1 + (37 * i) % 190 for i in range(700)]),
+                      ([3, 0, 0, 0, 2, 0], [900, 5, 0, 40, 1, 7]),
+                      ([1] * 5, [33000, 1, 20000, 64, 3]), ([1, 0, 1], [0, 0, 31])):
+        b, cu = R.batch(new, rows, DEV, lead=1)
+        c = R.make_cache(rows, kv, dim, page, seed=len(rows))
+        q = _normal((b["num_q"], heads, dim), dtype, 3)
+        out = torch.full((b["num_q"], heads, dim), 7.0, dtype=dtype, device=DEV)
+        lse = torch.full((b["num_q"], heads), 7.0, device=DEV)
+        d = _derr()
+        ws = None if shared else torch.empty(0, dtype=torch.uint8, device=DEV)
+        S.page_attn(b, q, c, max_kv=max(rows), sm_scale=0.03, out=out, lse=lse, workspace=ws,
+                    d_err=d)
+        assert int(d.item()) == 0
+        which = range(len(new)) if len(new) < 100 else range(0, 700, 13)
+        _check_attn(out, lse, b, cu, new, rows, c, q, 0.03, dtype, which=which)
+        assert (out[:1] == 7).all() and (out[1:] != 7).any(2).all()
+
+
 @pytest.mark.parametrize("heads,kv,dim,page,dtype", ATTN)
 def test_attn_ragged(heads, kv, dim, page, dtype):
     # whole prompts, extends, one token, nothing new, nothing cached, more queries

@@ -155,12 +155,12 @@ def test_null_structs(lib):
 
 
 def test_workspace(lib):
-    part = 64 * 8 * 8 * 129 * 4
-    assert S.csa2_page_attn_workspace(4, 4, 64, 8, 128, 100000) % (32 * 8 * 129 * 4) == 0
-    assert S.csa2_page_attn_workspace(4, 4, 64, 8, 128, 100000) > 0
-    assert S.csa2_page_attn_workspace(64, 64, 64, 8, 128, 1 << 40) <= 16 * part
-    assert S.csa2_page_attn_workspace(20000, 1, 32, 4, 128, 20000) == 0       # items enough
-    assert S.csa2_page_attn_workspace(4, 4, 64, 8, 128, 100) == 0             # nothing to split
+    # single tokens: two parts to a CTA, whatever the batch
+    one = S.csa2_page_attn_workspace(4, 4, 64, 8, 128, 100000)
+    assert one == S.csa2_page_attn_workspace(700, 700, 64, 8, 128, 1 << 40) > 0
+    # a few longer extends: split; many items: not
+    assert S.csa2_page_attn_workspace(40, 1, 64, 8, 128, 100000) >= 2 * 40 * 64 * 129 * 4
+    assert S.csa2_page_attn_workspace(20000, 1, 32, 4, 128, 20000) == 0
     assert S.csa2_page_attn_workspace(0, 0, 8, 2, 64, 0) == 0
     for bad in ((-1, 1, 8, 2, 64, 1), (1, -1, 8, 2, 64, 1), (1, 1, 8, 3, 64, 1),
                 (1, 1, 8, 2, 80, 1), (1, 1, 8, 2, 64, -1)):
