@@ -616,7 +616,10 @@ extern "C" CSA2_API int csa2_page_attn(const csa2_packed *b, int32_t n_heads, in
   if (splits > workspace_bytes / part) splits = (int)(workspace_bytes / part);
   const bool single = plan.kind == dense::kSingleTokens;
   uint64_t ws = splits > 1 ? (uint64_t)(splits * part) : 0;
-  if (single && workspace_bytes >= pages::page_decode_bytes(s)) ws = pages::page_decode_bytes(s);
+  if (single) {
+    ws = (uint64_t)pages::page_decode_bytes(s);
+    if (workspace_bytes < (int64_t)ws) ws = 0;
+  }
   // outputs and workspace against the inputs and each other; out may be q
   const int64_t wide = (int64_t)n_heads * dim * 2;
   const uint64_t no = (uint64_t)b->num_q * wide, nl = (uint64_t)b->num_q * n_heads * 4;
@@ -654,8 +657,8 @@ extern "C" CSA2_API int csa2_page_attn(const csa2_packed *b, int32_t n_heads, in
   }
   const cudaStream_t cs = as_stream(stream);
   if (single)
-    return pages::page_decode(s, pages::PageAttnParams{P, C8, q, ldq}, c, ws ? workspace : nullptr,
-                              cs);
+    return pages::page_decode(s, pages::PageAttnParams{P, C8, q, ldq}, max_kv, c,
+                              ws ? workspace : nullptr, cs);
   st = pages::run_tiles(s, c, C8, q, ldq, P, plan.kind == dense::kNarrowItems, cs);
   if (st != CSA2_OK || splits <= 1) return st;
   const dense::Join j{P.part_o, P.part_lse, splits, 0, b->num_q, b->num_req, b->cu_q, out, lse};

@@ -26,8 +26,8 @@ constexpr float kLift = 8.f, kMargin = 7.f;
 // Single tokens (page_decode.cu); ws: page_decode_bytes, or null: items are not shared
 // among CTAs.
 int64_t page_decode_bytes(const Shape &s);
-int page_decode(const Shape &s, const PageAttnParams &P, const csa2_pages *c, void *ws,
-                cudaStream_t st);
+int page_decode(const Shape &s, const PageAttnParams &P, int64_t max_kv, const csa2_pages *c,
+                void *ws, cudaStream_t st);
 
 // Power of two that takes a query row's largest magnitude to [2^14, 2^15), so that
 // its bf16 channels are f16 ones.

@@ -2,14 +2,15 @@
 // heads to a key head.
 //
 // Bound by the pages' bytes, each read once: at 128 channels a key's row is 128
-// bytes, and a few query rows meet it.  All blocks of 32 keys of all (token, key
-// head) items lie in one row, and each of two CTAs to an SM takes an equal run of them,
-// whatever items it crosses, so that lengths of any mixture fill the GPU evenly and a
-// CTA starts once.  (With a CTA to an item or an equal split of one, each start and end
-// cost 5 us of memory time: 83 us for 61 requests of 2831 rows on average where this
-// takes RESULT_STEP, 331 for 96 of 10.9 thousand where this takes RESULT_LONG.)  An
-// item that two or more CTAs share is left as parts, at most two to a CTA, which
-// a second kernel joins.
+// bytes, and a few query rows meet it.  96 requests of 10.0 thousand rows on average
+// take 295 us (6.7 TB/s, what a copy does), 61 of 2831 rows 67 us (5.3 TB/s).
+//
+// All (token, key head) items' blocks of 32 keys lie in one row, and each CTA (three to
+// an SM) takes an equal run of them, whatever items it crosses, where an item counts as
+// kFixed blocks more than it has: what its start and end take.  So lengths of any mixture
+// fill the GPU evenly, and a CTA starts once.  (A CTA to an item or an equal split of
+// one: 83 and 331 us; runs equal in blocks alone: 76 and 305.)  An item that two or more
+// CTAs share is left as parts, at most two to a CTA, which a second kernel joins.
 //
 // In a CTA one warp looks up pages and keeps a ring of blocks filled by TMA, across
 // items; four warps take the blocks in turn, each with its own running maximum, sum and
@@ -36,8 +37,10 @@ namespace {
 constexpr int kWarps = 4;                // that compute
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kKeys = 32;                // keys of a block
-constexpr int kLeast = 2;                // blocks of a CTA, at least: fewer CTAs run then
-constexpr int kSegs = 3;                 // segments published at a time
+constexpr int kFixed = 12;               // blocks' time that an item's start and end take
+constexpr int kLeast = 4;                // cost of a share, at least
+constexpr int kSegs = 2;                 // segments published at a time
+constexpr int kBurst = 4;                // blocks asked for at a time, a lane to each
 
 // 8 x 8 16-bit values, transposed over the warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -60,22 +63,33 @@ struct Segment {
   int token, h;                          // token -1: no more
   int keys;                              // that the token sees
   int blk0, blocks;
-  int part;                              // 0: the item began in an earlier CTA, 1: it goes on
-                                         // in a later one; -1: the whole item
-  bool through;                          // it does both
+  int part;                              // of the partial results; -1: the whole item
 };
 
-// What of an item a CTA's first segment is, for the join; token -1: its own start.
+// Runs of query rows as the blocks go over them.
+struct Run {
+  int lo, n;                             // query rows (n = 0: none, or skipped)
+  int64_t m;                             // cache rows
+};
+// A point of all items' costs, kFixed and one for each block to an item: token i of run
+// `run`, its head, and how far into the item.
+struct Place {
+  int run, i, h, off;
+  Run u;
+};
+
+// For the join: the item that began in the share before and goes on in this one, and the
+// parts it has, the first of them the share before's second one, then first ones; token
+// -1: none.
 struct Mark {
-  int token, h, through, pad;
+  int token, h, parts, pad;
 };
 
-// CTAs of the grid, by groups of 8 query rows: as many to an SM as registers allow
+// CTAs, by groups of 8 query rows: as many to an SM as registers allow
 template <int kN>
 constexpr int kToSm = kN == 1 ? 3 : 2;
 template <int kN>
 constexpr int kCtas = kToSm<kN> * kSms;
-
 // kN: groups of 8 query rows
 template <int D, int kN>
 struct Shared {
@@ -85,10 +99,12 @@ struct Shared {
   // wait by parity that skips a phase does not wait.)
   static_assert(kRing % kWarps == 0, "ring");
   uint8_t ring[kRing][2][kSide];
+  // Q of a segment: the copy of its rows, then fragments by lane
   union {
-    uint2 q[kN][D / 16][32];                         // Q in fragment order, by lane
-    float o[kWarps][8 * kN][D / 2 + 4];              // half of the warps' channels
-  };
+    uint4 rows[8 * kN * D / 8];
+    uint2 frag[kN][D / 16][32];
+  } q[kSegs];
+  float o[kWarps][8 * kN][D / 4 + 4];                // a quarter of the warps' channels
   float4 scales[kRing];                              // K's and V's of a block's halves
   float lift[8 * kN];
   float ref[kWarps][8 * kN], sum[kWarps][8 * kN];
@@ -96,8 +112,7 @@ struct Shared {
   Segment seg[kSegs];
   Bound bd;
   int64_t scan[kThreads / 32];
-  int64_t total;
-  int run, i, h, blk;                                // where the CTA's blocks begin
+  Place place;                                       // where the CTA's share begins
 };
 
 // key of fragment row a (0..15) within 16
@@ -115,17 +130,13 @@ __device__ __forceinline__ int byte_of(int row, int chunk) {
   return line * 128 + ((at ^ (line & 7)) << 4);
 }
 
-// Runs of query rows as the blocks go over them.
-struct Run {
-  int lo, n;                             // query rows (n = 0: none, or skipped)
-  int64_t m;                             // cache rows
-};
 __device__ __forceinline__ Run run_at(const PageAttnParams &P, int r, int &err) {
   const Seqs &S = P.at.seqs;
   Run u;
+  const int64_t m = S.kv_len[r];
   seq_rows(S, r, u.lo, u.n, err);
-  u.m = S.kv_len[r];
-  if (u.m < 0 || u.m > S.kv_rows) {
+  u.m = m;
+  if (m < 0 || m > S.kv_rows) {
     if (u.n) err |= CSA2_DERR_RANGE_ROW;
     u.m = 0;
   }
@@ -137,21 +148,62 @@ __device__ __forceinline__ int keys_of(const Run &u, int i) {
 }
 // a token that sees nothing has a block, too: its output is written
 __device__ __forceinline__ int blocks_of(int keys) { return max(1, (keys + kKeys - 1) / kKeys); }
+__device__ __forceinline__ int cost_of(const Run &u, int i) {
+  return kFixed + blocks_of(keys_of(u, i));
+}
+// of one head of a run
+__device__ __forceinline__ int64_t cost_of(const Run &u) {
+  int64_t c = 0;
+  for (int i = 0; i < u.n; ++i) c += cost_of(u, i);
+  return c;
+}
 
-// Finds the CTA's share of the blocks: [begin, end) of the total, and the run, token and
-// head at `begin`.  By the whole CTA; false if it has none.
+// The place of a run's point `at`.
+__device__ __forceinline__ Place place_in(const Run &u, int run, int n_kv, int64_t at) {
+  Place p{run, 0, 0, 0, u};
+  for (int64_t c; at >= (c = cost_of(u, p.i)) * n_kv; ++p.i) at -= c * n_kv;
+  const int c = cost_of(u, p.i);
+  for (; at >= c; ++p.h) at -= c;
+  p.off = (int)at;
+  return p;
+}
+
+// Equal shares of the cost: `more` of them have one more.
+struct Plan {
+  int64_t share;
+  int shares, more;
+};
+__device__ __forceinline__ Plan plan_of(int64_t total) {
+  Plan p;
+  p.shares = max(1, (int)min((int64_t)gridDim.x, total / kLeast));
+  // (32 bits divide in a fifth of the time)
+  p.share = total >> 32 ? total / p.shares : (int64_t)((uint32_t)total / (uint32_t)p.shares);
+  p.more = (int)(total - p.share * p.shares);
+  return p;
+}
+__device__ __forceinline__ int64_t share_begin(const Plan &p, int s) {
+  return s < p.shares ? s * p.share + min(s, p.more) : p.shares * p.share + p.more;
+}
+__device__ __forceinline__ int share_of(const Plan &p, int64_t at) {
+  const int64_t big = p.more * (p.share + 1);
+  const int64_t off = at < big ? at : at - big, by = at < big ? p.share + 1 : p.share;
+  return (at < big ? 0 : p.more) +
+         (int)(off >> 32 || by >> 32 ? off / by : (int64_t)((uint32_t)off / (uint32_t)by));
+}
+
+// The shares, and the place of the CTA's own, by the whole CTA.
 template <int D, int kN>
-__device__ bool find_share(const PageAttnParams &P, Shared<D, kN> &sh, int64_t &begin,
-                           int64_t &end, int &err) {
+__device__ Plan find_share(const PageAttnParams &P, Shared<D, kN> &sh, int &err) {
   const Seqs &S = P.at.seqs;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (S.count + kThreads - 1) / kThreads;
   const int r0 = min(S.count, (int)threadIdx.x * per), r1 = min(S.count, r0 + per);
   int64_t own = 0;
+  Run u{0, 0, 0};
 #pragma unroll 4
   for (int r = r0; r < r1; ++r) {
-    const Run u = run_at(P, r, err);
-    for (int i = 0; i < u.n; ++i) own += blocks_of(keys_of(u, i));
+    u = run_at(P, r, err);
+    own += cost_of(u) * P.at.n_kv;
   }
   int64_t upto = own;
 #pragma unroll
@@ -167,84 +219,85 @@ __device__ bool find_share(const PageAttnParams &P, Shared<D, kN> &sh, int64_t &
     if (w < warp) upto += sh.scan[w];
     total += sh.scan[w];
   }
-  total *= P.at.n_kv;
-  // (32 bits divide in a fifth of the time)
-  const int64_t ctas = max(1, (int)min((int64_t)gridDim.x, total / kLeast));
-  const int64_t share = total >> 32 ? total / ctas : (int64_t)((uint32_t)total / (uint32_t)ctas);
-  const int64_t more = total - share * ctas;         // CTAs that have one more
-  if (blockIdx.x >= ctas || total == 0) return false;
-  begin = share * blockIdx.x + min((int64_t)blockIdx.x, more);
-  end = begin + share + (blockIdx.x < more);
-  int64_t at = (upto - own) * P.at.n_kv;             // of this thread's first run
-  if (at <= begin && begin < at + own * P.at.n_kv) {
+  const Plan plan = plan_of(total);
+  const int64_t begin = share_begin(plan, (int)blockIdx.x);
+  int64_t base = upto - own;                         // of this thread's first run
+  if (base <= begin && begin < upto) {
     int ignored = 0;
     for (int r = r0; r < r1; ++r) {
-      const Run u = run_at(P, r, ignored);
-      for (int i = 0; i < u.n; ++i) {
-        const int64_t b = blocks_of(keys_of(u, i));
-        if (begin < at + b * P.at.n_kv) {
-          sh.run = r, sh.i = i;
-          int head = 0;
-          for (; begin - at >= b; ++head) at += b;
-          sh.h = head;
-          sh.blk = (int)(begin - at);
-          r = r1;
-          break;
-        }
-        at += b * P.at.n_kv;
+      if (per > 1) u = run_at(P, r, ignored);
+      const int64_t c = cost_of(u) * P.at.n_kv;
+      if (begin < base + c) {
+        sh.place = place_in(u, r, P.at.n_kv, begin - base);
+        break;
       }
+      base += c;
     }
   }
   __syncthreads();
-  return true;
+  return plan;
+}
+
+__device__ __forceinline__ void bulk_load(void *to, const void *from, uint32_t bytes,
+                                          uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(to)),
+      "l"(from), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 
 // The warp that fills the ring.  A lane holds one of 32 neighbouring blocks of the
 // segment: the ids of its halves' pages (the same one where a page has 32 rows or more)
-// and their scales.
-template <int D, int kN>
-__device__ void producer_role(const PageAttnParams &P, Shared<D, kN> &sh, const CUtensorMap *mk,
-                              const CUtensorMap *mv, int64_t begin, int64_t end, int &err) {
+// and their scales.  It asks for kBurst blocks at a time: a block by itself takes some
+// 1000 cycles of waits and issue, which is what a CTA has for 8 KB (one at a time, 96
+// requests took 319 us instead of 306).
+template <typename T, int D, int kN>
+__device__ void producer_role(const PageAttnParams &P, bool whole, Shared<D, kN> &sh,
+                              const CUtensorMap *mk, const CUtensorMap *mv, int64_t at, int64_t end,
+                              int &err) {
   using Sh = Shared<D, kN>;
   constexpr int kSide = Sh::kSide;
   const int lane = threadIdx.x & 31;
   const Pages &C = P.cache;
   const Seqs &S = P.at.seqs;
-  const bool whole = P.at.splits == 0;   // items are not shared: those that begin in the share
-  int run = sh.run, i = sh.i, h = sh.h, blk = sh.blk, ignored = 0;
-  Run u = run_at(P, run, ignored);
+  Place p = sh.place;
+  int ignored = 0;
   uint32_t g = 0, segs = 0;              // blocks and segments so far
   bool ok = true;
-  for (int64_t at = begin; ok;) {
-    const int keys = keys_of(u, i), all = blocks_of(keys);
-    int n = 0;
-    if (at >= end) break;
-    if (whole) {
-      n = blk == 0 ? all : 0;
-      at += all - blk;
-    } else {
-      n = (int)min((int64_t)(all - blk), end - at);
-      at += n;
-    }
+  while (at < end) {
+    const int keys = keys_of(p.u, p.i), all = blocks_of(keys), h = p.h;
+    const int run = p.run, token = p.u.lo + p.i;
+    // the item's blocks in the share: a share that ends within its fixed cost has none
+    const int blk = max(0, p.off - kFixed);
+    const int upto = (int)min((int64_t)(kFixed + all), p.off + (end - at));
+    int n = max(0, upto - kFixed) - blk;
+    at += kFixed + all - p.off;          // the next item
+    if (whole) n = blk == 0 && n > 0 ? all : 0;      // items are not shared
     if (n > 0) {
       const uint32_t slot = segs % kSegs;
       if (!(ok = wait_all(&sh.seg_empty[slot], ((segs / kSegs) & 1) ^ 1, &sh.bd))) break;
       if (lane == 0) {
-        const bool cut = blk + n < all;
-        sh.seg[slot] = Segment{u.lo + i, h, keys, blk, n, blk > 0 ? 0 : cut ? 1 : -1, blk > 0 && cut};
-        mbar_arrive(&sh.seg_full[slot]);
+        sh.seg[slot] = Segment{token, h, keys, blk, n,
+                               blk > 0           ? 2 * (int)blockIdx.x
+                               : blk + n < all ? 2 * (int)blockIdx.x + 1
+                                               : -1};
+        const uint32_t bytes = (uint32_t)P.at.group * D * 2;
+        mbar_arrive_expect_tx(&sh.seg_full[slot], bytes);
+        bulk_load(sh.q[slot].rows,
+                  static_cast<const T *>(P.q) + (int64_t)token * P.ldq + (int64_t)h * P.at.group * D,
+                  bytes, &sh.seg_full[slot]);
       }
       __syncwarp();
       ++segs;
     }
     int id[2] = {-1, -1};
     float a[2], b[2];
-    for (int k = 0; k < n; ++k, ++g) {
-      const int first = blk + k;
+    for (int k = 0; k < n; k += kBurst) {
       if (k % 32 == 0) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int64_t key = (int64_t)(first + lane) * kKeys + 16 * x;
+          const int64_t key = (int64_t)(blk + k + lane) * kKeys + 16 * x;
           if (x == 1 && C.shift > 4)
             id[1] = id[0];
           else
@@ -256,11 +309,15 @@ __device__ void producer_role(const PageAttnParams &P, Shared<D, kN> &sh, const 
           b[x] = id[x] >= 0 ? C.v_scale[(int64_t)id[x] * P.at.n_kv + h] : 0.f;
         }
       }
-      const uint32_t s = g % Sh::kRing;
-      if (!(ok = wait_all(&sh.empty[s], ((g / Sh::kRing) & 1) ^ 1, &sh.bd))) break;
-      const int p0 = __shfl_sync(0xffffffffu, id[0], k % 32);
-      const int p1 = __shfl_sync(0xffffffffu, id[1], k % 32);
-      if (lane == 0) {
+      // a block to a lane
+      const int mine = lane % kBurst, some = min(kBurst, n - k);
+      const bool busy = lane < some;
+      const uint32_t s = (g + mine) % Sh::kRing;
+      ok = !busy || wait_bar(&sh.empty[s], (((g + mine) / Sh::kRing) & 1) ^ 1, &sh.bd);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const int p0 = __shfl_sync(0xffffffffu, id[0], (k + mine) % 32);
+      const int p1 = __shfl_sync(0xffffffffu, id[1], (k + mine) % 32);
+      if (busy) {
         uint8_t *to = sh.ring[s][0];
         uint64_t *bar = &sh.full[s];
         if (C.shift == 4) {
@@ -272,7 +329,7 @@ __device__ void producer_role(const PageAttnParams &P, Shared<D, kN> &sh, const 
           if (p1 >= 0) tma_load_3d(to + kSide + kSide / 2, mv, 0, line, p1, bar);
         } else {
           mbar_arrive_expect_tx(bar, p0 >= 0 ? 2u * kSide : 0u);
-          const int line = (h * C.page + ((first * kKeys) & (C.page - 1))) * D / 128;
+          const int line = (h * C.page + (((blk + k + mine) * kKeys) & (C.page - 1))) * D / 128;
           if (p0 >= 0) tma_load_3d(to, mk, 0, line, p0, bar);
           if (p0 >= 0) tma_load_3d(to + kSide, mv, 0, line, p0, bar);
         }
@@ -286,29 +343,36 @@ __device__ void producer_role(const PageAttnParams &P, Shared<D, kN> &sh, const 
           b[x] = id[x] >= 0 ? scale_of(b[x], err) : 0.f;
         }
       }
-      if (lane == k % 32) {
-        sh.scales[s] = make_float4(a[0], a[1], b[0], b[1]);
+      float4 sc;
+      sc.x = __shfl_sync(0xffffffffu, a[0], (k + mine) % 32);
+      sc.y = __shfl_sync(0xffffffffu, a[1], (k + mine) % 32);
+      sc.z = __shfl_sync(0xffffffffu, b[0], (k + mine) % 32);
+      sc.w = __shfl_sync(0xffffffffu, b[1], (k + mine) % 32);
+      if (busy) {
+        sh.scales[s] = sc;
         mbar_arrive(&sh.full[s]);
       }
       __syncwarp();
+      g += some;
     }
-    // the next item
-    blk = 0;
-    if (++h < P.at.n_kv) continue;
-    h = 0;
-    if (++i < u.n) continue;
-    i = 0;
-    for (++run; run < S.count; run += 32) {
+    if (!ok) break;
+    p.off = 0;
+    if (++p.h < P.at.n_kv) continue;
+    p.h = 0;
+    if (++p.i < p.u.n) continue;
+    p.i = 0;
+    if (at >= end) break;
+    for (++p.run; p.run < S.count; p.run += 32) {
       int lo = 0, c = 0;
-      if (run + lane < S.count) seq_rows(S, run + lane, lo, c, ignored);
+      if (p.run + lane < S.count) seq_rows(S, p.run + lane, lo, c, ignored);
       const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
       if (some) {
-        run += __ffs(some) - 1;
+        p.run += __ffs(some) - 1;
         break;
       }
     }
-    if (run >= S.count) break;
-    u = run_at(P, run, ignored);
+    if (p.run >= S.count) break;         // (not reached: the blocks are there)
+    p.u = run_at(P, p.run, ignored);
   }
   if (ok) {
     const uint32_t slot = segs % kSegs;
@@ -319,9 +383,12 @@ __device__ void producer_role(const PageAttnParams &P, Shared<D, kN> &sh, const 
     }
   }
   // copies land before the CTA leaves
-  if (!ok && lane == 0)
+  if (!ok && lane == 0) {
+    for (uint32_t k = segs > (uint32_t)kSegs ? segs - kSegs : 0; k < segs; ++k)
+      drain_bar(&sh.seg_full[k % kSegs], (k / kSegs) & 1);
     for (uint32_t k = g > (uint32_t)Sh::kRing ? g - Sh::kRing : 0; k < g; ++k)
       drain_bar(&sh.full[k % Sh::kRing], (k / Sh::kRing) & 1);
+  }
   __syncwarp();
 }
 
@@ -350,44 +417,42 @@ __device__ __forceinline__ void compute_role(const PageAttnParams &P, Shared<D, 
     if (any_of_us(!ok)) return;
     const Segment seg = sh.seg[slot];
     if (seg.token < 0) return;
-    // Q's fragments; rows past the group's heads are zeros
-    const T *q = static_cast<const T *>(P.q) + (int64_t)seg.token * P.ldq +
-                 (int64_t)seg.h * P.at.group * D;
-    if (Elem<T>::kBf16) {
-      for (int r = warp; r < 8 * kN; r += kWarps) {
+    // Q's rows become fragments where they are; rows past the group's heads are zeros
+    constexpr int kPieces = 8 * kN * D / 8, kEach = (kPieces + 32 * kWarps - 1) / (32 * kWarps);
+    uint4 piece[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x + 32 * kWarps * e, r = i / (D / 8);
+      if (i >= kPieces) break;           // (whole warps)
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < P.at.group) v = sh.q[slot].rows[i];
+      if (Elem<T>::kBf16) {
+        uint32_t x[4] = {v.x, v.y, v.z, v.w};
         float amax = 0.f;
-        if (r < P.at.group) {
-          if (D == 128) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(q + r * D + 4 * lane);
-            amax = fmaxf(max3(fabsf(__uint_as_float(w.x << 16)),
-                              fabsf(__uint_as_float(w.x & 0xffff0000u)),
-                              fabsf(__uint_as_float(w.y << 16))),
-                         fabsf(__uint_as_float(w.y & 0xffff0000u)));
-          } else {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(q + r * D + 2 * lane);
-            amax = fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u)));
-          }
-        }
-        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-        if (lane == 0) sh.lift[r] = lift_of(amax);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          amax = max3(amax, fabsf(__uint_as_float(x[k] << 16)),
+                      fabsf(__uint_as_float(x[k] & 0xffff0000u)));
+#pragma unroll
+        for (int k = 1; k < D / 8; k <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, k));
+        const float lift = lift_of(amax);
+        if (i % (D / 8) == 0) sh.lift[r] = lift;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          x[k] = Elem<__half>::pack(__uint_as_float(x[k] << 16) * lift,
+                                    __uint_as_float(x[k] & 0xffff0000u) * lift);
+        v = make_uint4(x[0], x[1], x[2], x[3]);
       }
-      any_of_us(false);
+      piece[e] = v;
     }
-    for (int i = threadIdx.x; i < kN * D / 16 * 32; i += kWarps * 32) {
-      const int l = i & 31, x = (i >> 5) % (D / 16), r = (i >> 5) / (D / 16) * 8 + (l >> 2);
-      const int ch = 16 * ((l & 3) + 4 * (x >> 2)) + 4 * (x & 3);
-      uint2 w = make_uint2(0, 0);
-      if (r < P.at.group) {
-        w = *reinterpret_cast<const uint2 *>(q + r * D + ch);
-        if (Elem<T>::kBf16) {
-          const float f = sh.lift[r];
-          w = make_uint2(Elem<__half>::pack(__uint_as_float(w.x << 16) * f,
-                                            __uint_as_float(w.x & 0xffff0000u) * f),
-                         Elem<__half>::pack(__uint_as_float(w.y << 16) * f,
-                                            __uint_as_float(w.y & 0xffff0000u) * f));
-        }
-      }
-      (&sh.q[0][0][0])[i] = w;
+    any_of_us(false);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x + 32 * kWarps * e, r = i / (D / 8), ch = i % (D / 8) * 8;
+      if (i >= kPieces) break;
+      const int x = 4 * (ch >> 6) + (ch >> 2 & 3), l = (r & 7) * 4 + (ch >> 4 & 3);
+      sh.q[slot].frag[r >> 3][x][l] = make_uint2(piece[e].x, piece[e].y);
+      sh.q[slot].frag[r >> 3][x + 1][l] = make_uint2(piece[e].z, piece[e].w);
     }
     any_of_us(false);
 
@@ -435,7 +500,7 @@ __device__ __forceinline__ void compute_role(const PageAttnParams &P, Shared<D, 
             const uint32_t a2 = f16x2_of_high(w0[j]), a3 = f16x2_of_high(w1[j]);
 #pragma unroll
             for (int y = 0; y < kN; ++y) {
-              const uint2 qv = sh.q[y][4 * ch + j][lane];
+              const uint2 qv = sh.q[slot].frag[y][4 * ch + j][lane];
               mma16816(st[x][y], a0, a1, a2, a3, qv.x, qv.y);
             }
           }
@@ -536,8 +601,9 @@ __device__ __forceinline__ void compute_role(const PageAttnParams &P, Shared<D, 
     }
     taken += seg.blocks;
 
-    // join the warps: each row's statistics and sums, weighted, by halves of the products
+    // join the warps: each row's statistics and sums, weighted, by quarters of the products
     // (the channels (D / 8) g + 2 d and + 1 of products d)
+    fence_proxy_async_smem();            // the next copy of Q into the slot comes later
     if (any_of_us(!ok)) return;          // (and Q is done with)
     if (threadIdx.x == 0) mbar_arrive(&sh.seg_empty[slot]);
 #pragma unroll
@@ -550,25 +616,25 @@ __device__ __forceinline__ void compute_role(const PageAttnParams &P, Shared<D, 
         if (g == 0) sh.ref[warp][row] = ref[y][r], sh.sum[warp][row] = sum[y][r];
       }
     constexpr int kRows = 8 * kN, kTeam = kWarps * 32 / kRows;       // threads of a row
-    constexpr int kHalf = D / 16;        // channels of a lane group in a half
+    constexpr int kPart = D / 32;        // channels of a lane group in a quarter
     const int row = threadIdx.x / kTeam, col = threadIdx.x % kTeam;
     const bool mine = row < P.at.group;
-    const int64_t part = (2 * (int64_t)blockIdx.x + seg.part) * kRows + row;
+    const int64_t part = (int64_t)seg.part * kRows + row;
     const int64_t at = (int64_t)seg.token * P.at.n_heads + seg.h * P.at.group + row;
     float w[kWarps];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (half) any_of_us(false);        // the first half is read
+    for (int z = 0; z < 4; ++z) {
+      if (z) any_of_us(false);           // the quarter before is read
 #pragma unroll
       for (int y = 0; y < kN; ++y)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int d = 0; d < D / 32; ++d)
-            *reinterpret_cast<float2 *>(&sh.o[warp][8 * y + 2 * c + r][kHalf * g + 2 * d]) =
-                make_float2(o[y][half * (D / 32) + d][r], o[y][half * (D / 32) + d][2 + r]);
+          for (int d = 0; d < D / 64; ++d)
+            *reinterpret_cast<float2 *>(&sh.o[warp][8 * y + 2 * c + r][kPart * g + 2 * d]) =
+                make_float2(o[y][z * (D / 64) + d][r], o[y][z * (D / 64) + d][2 + r]);
       any_of_us(false);
-      if (half == 0) {
+      if (z == 0) {
         float top = -INFINITY, tot = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sh.ref[k][row]);
@@ -592,21 +658,19 @@ __device__ __forceinline__ void compute_role(const PageAttnParams &P, Shared<D, 
       }
       if (mine) {
 #pragma unroll
-        for (int x = 4 * col; x < D / 2; x += 4 * kTeam) {
-          const int d = x / kHalf * (D / 8) + half * kHalf + x % kHalf;
-          float f[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int x = 2 * col; x < D / 4; x += 2 * kTeam) {
+          const int d = x / kPart * (D / 8) + z * kPart + x % kPart;
+          float f[2] = {0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < kWarps; ++k) {
-            const float4 v = *reinterpret_cast<const float4 *>(&sh.o[k][row][x]);
+            const float2 v = *reinterpret_cast<const float2 *>(&sh.o[k][row][x]);
             f[0] = fmaf(w[k], v.x, f[0]), f[1] = fmaf(w[k], v.y, f[1]);
-            f[2] = fmaf(w[k], v.z, f[2]), f[3] = fmaf(w[k], v.w, f[3]);
           }
           if (seg.part >= 0)
-            *reinterpret_cast<float4 *>(P.at.part_o + part * D + d) =
-                make_float4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<float2 *>(P.at.part_o + part * D + d) = make_float2(f[0], f[1]);
           else
-            *reinterpret_cast<uint2 *>(static_cast<T *>(P.at.out) + at * D + d) =
-                make_uint2(Elem<T>::pack(f[0], f[1]), Elem<T>::pack(f[2], f[3]));
+            *reinterpret_cast<uint32_t *>(static_cast<T *>(P.at.out) + at * D + d) =
+                Elem<T>::pack(f[0], f[1]);
         }
       }
       __syncwarp();
@@ -636,22 +700,24 @@ page_decode_kernel(const __grid_constant__ PageAttnParams P, Mark *marks,
     mbar_fence_init();
   }
   int err = 0;
-  int64_t begin = 0, end = 0;
-  const bool some = find_share(P, sh, begin, end, err);
-  if (blockIdx.x > 0) err = 0;           // one CTA speaks of the requests
-  if (marks && threadIdx.x == 0) {
+  const Plan plan = find_share(P, sh, err);
+  const int share = (int)blockIdx.x;
+  const int64_t begin = share_begin(plan, share), end = share_begin(plan, share + 1);
+  if (share > 0) err = 0;                // one CTA speaks of the requests
+  if (marks && threadIdx.x == 32 * kWarps - 1) {
     Mark mark{-1, 0, 0, 0};
-    if (some && sh.blk > 0) {
-      int ignored = 0;
-      const Run u = run_at(P, sh.run, ignored);
-      const int all = blocks_of(keys_of(u, sh.i));
-      mark = Mark{u.lo + sh.i, sh.h, sh.blk + (end - begin) < all, 0};
+    if (begin < end && sh.place.off > kFixed) {
+      const Place &p = sh.place;
+      const int64_t first = begin - p.off + kFixed;  // of the item's blocks
+      const int64_t last = first + blocks_of(keys_of(p.u, p.i)) - 1;
+      if (first >= share_begin(plan, share - 1))
+        mark = Mark{p.u.lo + p.i, p.h, share_of(plan, last) - share + 2, 0};
     }
-    marks[blockIdx.x] = mark;
+    marks[share] = mark;
   }
-  if (some) {
+  if (begin < end) {
     if (threadIdx.x >= 32 * kWarps)
-      producer_role(P, sh, &mk, &mv, begin, end, err);
+      producer_role<T>(P, !marks, sh, &mk, &mv, begin, end, err);
     else
       compute_role<T>(P, sh);
     __syncthreads();
@@ -660,9 +726,9 @@ page_decode_kernel(const __grid_constant__ PageAttnParams P, Mark *marks,
   if (err) raise_err(P.at.d_err, err);
 }
 
-// Joins the parts of items that CTAs shared: block j - 1 those of the item that goes on
-// in CTA j, if it began in the CTA before.
-constexpr int kJoin = 256;
+// Joins the parts of items that shares cut, an item to a block.  A chain of loads in the
+// main: the first parts are asked for together with all statistics.
+constexpr int kJoin = 256, kBatch = 8;
 
 template <typename T, int D, int kN>
 __global__ void __launch_bounds__(kJoin)
@@ -670,27 +736,40 @@ page_join_kernel(const __grid_constant__ PageAttnParams P, const Mark *marks) {
   constexpr int kRows = 8 * kN;
   __shared__ float weight[kCtas<kN>][kRows];         // by part
   __shared__ float total[kRows];
-  const int j = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.x + 1;
   wait_front();
-  const Mark mark = marks[j], before = marks[j - 1];
-  if (mark.token < 0 || (before.token >= 0 && before.through)) return;
-  int parts = 2;                                     // CTA j - 1's second, then first ones
-  for (int k = j; marks[k].through; ++k) ++parts;
+  const Mark mark = marks[j];
+  if (mark.token < 0) return;
+  const int parts = mark.parts;
   const auto part = [&](int k) {
     return (k == 0 ? 2 * (int64_t)(j - 1) + 1 : 2 * (int64_t)(j - 1 + k)) * kRows;
   };
+  constexpr int kQuads = kRows * D / 4, kEach = (kQuads + kJoin - 1) / kJoin;
+  float4 v[kEach][kBatch];
+  const auto fetch = [&](int k0) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x + e * kJoin, r = i / (D / 4), d = i % (D / 4) * 4;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        v[e][k] = r < P.at.group && k0 + k < parts
+                      ? *reinterpret_cast<const float4 *>(P.at.part_o + (part(k0 + k) + r) * D + d)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  fetch(0);
   for (int r = warp; r < P.at.group; r += kJoin / 32) {
-    float top = -INFINITY, tot = 0.f;
+    float most = -INFINITY, tot = 0.f;
     bool nan = false;
     for (int k = lane; k < parts; k += 32) {
       const float l = P.at.part_lse[part(k) + r];
       weight[k][r] = l;
       nan |= l != l;
-      top = fmaxf(top, l);
+      most = fmaxf(most, l);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
+    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float ref = most == -INFINITY ? 0.f : most;
     for (int k = lane; k < parts; k += 32) {
       const float w = ex2((weight[k][r] - ref) * 1.4426950408889634f);
       weight[k][r] = w;
@@ -707,48 +786,63 @@ page_join_kernel(const __grid_constant__ PageAttnParams P, const Mark *marks) {
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < P.at.group * (D / 4); i += kJoin) {
-    const int r = i / (D / 4), d = i % (D / 4) * 4;
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const float w = weight[k][r];
-      const float4 v = *reinterpret_cast<const float4 *>(P.at.part_o + (part(k) + r) * D + d);
-      f[0] = fmaf(w, v.x, f[0]), f[1] = fmaf(w, v.y, f[1]);
-      f[2] = fmaf(w, v.z, f[2]), f[3] = fmaf(w, v.w, f[3]);
+  float f[kEach][4] = {};
+  for (int k0 = 0;;) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int r = min((int)(threadIdx.x + e * kJoin) / (D / 4), P.at.group - 1);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float w = k0 + k < parts ? weight[k0 + k][r] : 0.f;
+        f[e][0] = fmaf(w, v[e][k].x, f[e][0]), f[e][1] = fmaf(w, v[e][k].y, f[e][1]);
+        f[e][2] = fmaf(w, v[e][k].z, f[e][2]), f[e][3] = fmaf(w, v[e][k].w, f[e][3]);
+      }
     }
+    if ((k0 += kBatch) >= parts) break;
+    fetch(k0);
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = threadIdx.x + e * kJoin, r = i / (D / 4), d = i % (D / 4) * 4;
+    if (r >= P.at.group) break;
     const float inv = total[r] == 0.f ? 0.f : 1.f / total[r];
     const int64_t at = (int64_t)mark.token * P.at.n_heads + mark.h * P.at.group + r;
     *reinterpret_cast<uint2 *>(static_cast<T *>(P.at.out) + at * D + d) =
-        make_uint2(Elem<T>::pack(f[0] * inv, f[1] * inv), Elem<T>::pack(f[2] * inv, f[3] * inv));
+        make_uint2(Elem<T>::pack(f[e][0] * inv, f[e][1] * inv),
+                   Elem<T>::pack(f[e][2] * inv, f[e][3] * inv));
   }
 }
 
 template <typename T, int D, int kN>
-int launch(PageAttnParams P, const CUtensorMap &mk, const CUtensorMap &mv, void *ws,
-           cudaStream_t st) {
+int launch(PageAttnParams P, int64_t max_kv, const CUtensorMap &mk, const CUtensorMap &mv,
+           void *ws, cudaStream_t st) {
   constexpr int kSmem = (int)sizeof(Shared<D, kN>);
   static_assert(kSmem <= 232448 / kToSm<kN> - 1024, "CTAs to an SM");
   allow_smem<page_decode_kernel<T, D, kN>>(kSmem);
+  // no more CTAs than the blocks may need
+  const double most = (double)P.at.seqs.num_q * P.at.n_kv * (double)(max_kv / kKeys + 1 + kFixed);
+  const int grid =
+      most >= (double)kLeast * kCtas<kN> ? kCtas<kN> : (int)(most / kLeast) + 1;
   Mark *marks = static_cast<Mark *>(ws);
-  P.at.splits = ws != nullptr;
   if (ws) {
     P.at.part_lse = reinterpret_cast<float *>(marks + kCtas<kN>);
     P.at.part_o = P.at.part_lse + 2 * kCtas<kN> * 8 * kN;
   }
-  page_decode_kernel<T, D, kN><<<kCtas<kN>, kThreads, kSmem, st>>>(P, marks, mk, mv);
+  page_decode_kernel<T, D, kN><<<grid, kThreads, kSmem, st>>>(P, marks, mk, mv);
   const int e = launch_status();
-  if (e != CSA2_OK || !ws) return e;
-  return launch_behind(page_join_kernel<T, D, kN>, dim3(kCtas<kN> - 1), kJoin, 0, true, st, P,
+  if (e != CSA2_OK || !ws || grid == 1) return e;
+  return launch_behind(page_join_kernel<T, D, kN>, dim3(grid - 1), kJoin, 0, true, st, P,
                        (const Mark *)marks);
 }
 
 template <typename T>
-int launch_any(const Shape &s, const PageAttnParams &P, const CUtensorMap &mk,
+int launch_any(const Shape &s, const PageAttnParams &P, int64_t max_kv, const CUtensorMap &mk,
                const CUtensorMap &mv, void *ws, cudaStream_t st) {
   if (s.dim == 128)
-    return s.group <= 8 ? launch<T, 128, 1>(P, mk, mv, ws, st) : launch<T, 128, 2>(P, mk, mv, ws, st);
-  return s.group <= 8 ? launch<T, 64, 1>(P, mk, mv, ws, st) : launch<T, 64, 2>(P, mk, mv, ws, st);
+    return s.group <= 8 ? launch<T, 128, 1>(P, max_kv, mk, mv, ws, st)
+                        : launch<T, 128, 2>(P, max_kv, mk, mv, ws, st);
+  return s.group <= 8 ? launch<T, 64, 1>(P, max_kv, mk, mv, ws, st)
+                      : launch<T, 64, 2>(P, max_kv, mk, mv, ws, st);
 }
 
 }  // namespace
@@ -759,12 +853,12 @@ int64_t page_decode_bytes(const Shape &s) {
   return ctas * (int64_t)sizeof(Mark) + 2 * ctas * rows * (s.dim + 1) * 4;
 }
 
-int page_decode(const Shape &s, const PageAttnParams &P, const csa2_pages *c, void *ws,
-                cudaStream_t st) {
+int page_decode(const Shape &s, const PageAttnParams &P, int64_t max_kv, const csa2_pages *c,
+                void *ws, cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!make_cache_maps(&mk, &mv, c, P.q, s, kKeys)) return CSA2_ERR_UNSUPPORTED;
-  return s.bf16 ? launch_any<__nv_bfloat16>(s, P, mk, mv, ws, st)
-                : launch_any<__half>(s, P, mk, mv, ws, st);
+  return s.bf16 ? launch_any<__nv_bfloat16>(s, P, max_kv, mk, mv, ws, st)
+                : launch_any<__half>(s, P, max_kv, mk, mv, ws, st);
 }
 
 }  // namespace pages
