@@ -760,12 +760,12 @@ CSA2_API int csa2_page_append(const csa2_packed *b, int32_t n_kv_heads, int32_t 
  * queries that see nothing and of rows of no request.  Rows of a page behind the
  * request's last may hold anything, NaN codes included; rows that a request has
  * hold none.
- *   max_kv     the longest kv_len, for the choice of splits only
+ *   max_kv     the longest kv_len, for the choice of kernels and grids only
  *   workspace  device scratch, 256-byte aligned, as csa2_prefix_attn's; NULL with
- *              workspace_bytes = 0: the cache is not split
- * csa2_page_attn_workspace gives the bytes of the splits that the call would choose
- * (0: it would not split); with less it splits less, with less than two parts' bytes
- * (a part as csa2_prefix_attn's) not at all.
+ *              workspace_bytes = 0: no request's cache is shared among CTAs
+ * csa2_page_attn_workspace gives the bytes with which the call shares caches among CTAs (0:
+ * it would not; no more for any batch of single tokens of as many heads than for
+ * another); with less it does not.
  * Queries in bf16 are scaled by a power of two for each row and head and taken as
  * f16, which keeps their bits unless they lie 2^28 below the row's largest; codes
  * are exact in f16; the weights, times their block's scale, are rounded to f16 for

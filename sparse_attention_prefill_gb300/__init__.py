@@ -838,33 +838,47 @@ def _rope_arg(rope, pos, num_q, dev):
                  bool(rope.get("interleaved", False)), float(rope.get("amplitude", 1.0)), 0)
 
 
-def _cache_arg(cache, num_req, kv, dim, dev):
-    """Host struct for a cache dict."""
-    k, v, table = cache["k"], cache["v"], cache["table"]
-    shape, side = k.shape, []
+def _check_cache(k, v, table, num_req, kv, dim, dev):
+    """Raises for what _cache_arg does not take."""
     for t, name in ((k, "k"), (v, "v")):
         if t.get_device() != dev or t.dtype not in _CODES:
             raise Csa2Error("the cache's %s: expected uint8 or float8_e4m3fn codes on cuda:%d, got "
                             "%s on %s" % (name, dev, t.dtype, t.device))
-        if t.dim() != 4 or t.shape != shape or shape[1] != kv or shape[3] != dim:
+        if t.dim() != 4 or t.shape != k.shape or t.shape[1] != kv or t.shape[3] != dim:
             raise Csa2Error("the cache's %s: expected [pages, %d, page, %d], got %s"
                             % (name, kv, dim, tuple(t.shape)))
         s = t.stride()
-        if s[3] != 1 or s[2] != dim or (s[1] != shape[2] * dim and kv > 1):
+        if s[3] != 1 or s[2] != dim or (s[1] != t.shape[2] * dim and kv > 1):
             raise Csa2Error("the cache's %s: the rows of a page must be contiguous" % name)
-        side.append(s[0] if shape[0] > 1 else kv * shape[2] * dim)
     if table.dim() != 2 or table.get_device() != dev or table.dtype is not _I32 \
             or table.shape[0] < num_req or (table.stride(1) != 1 and table.shape[1] > 1):
         raise Csa2Error("table: expected [%d, width] of int32 on cuda:%d with contiguous rows, got "
                         "%s of %s on %s" % (num_req, dev, tuple(table.shape), table.dtype,
                                             table.device))
-    width, ld = table.shape[1], table.stride(0)
-    if ld != width and table.shape[0] > 1 and num_req > 1:
+    if table.stride(0) != table.shape[1] and table.shape[1] and table.shape[0] > 1 and num_req > 1:
         raise Csa2Error("libcsa2 takes contiguous tensors; table is not")
-    n = shape[0] * kv
-    return CPages(shape[0], shape[2], k.data_ptr(), v.data_ptr(), side[0], side[1],
-                  _arg(cache["k_scale"], _F32, "k_scale", n, dev, (kv,)),
-                  _arg(cache["v_scale"], _F32, "v_scale", n, dev, (kv,)), table.data_ptr(), width)
+
+
+def _cache_arg(cache, num_req, kv, dim, dev):
+    """Host struct for a cache dict."""
+    k, v, table = cache["k"], cache["v"], cache["table"]
+    shape, ks, vs, ts, rows = k.shape, k.stride(), v.stride(), table.shape, None
+    if len(shape) == 4:
+        rows = (shape[2] * dim, dim, 1)
+    # (the same in one go, for the layouts that caches have)
+    if not (rows is not None and ks[1:] == rows == vs[1:] and v.shape == shape and shape[1] == kv
+            and shape[3] == dim and k.dtype in _CODES and v.dtype in _CODES
+            and k.get_device() == dev == v.get_device() == table.get_device()
+            and table.dtype is _I32 and len(ts) == 2 and ts[0] >= num_req
+            and table.is_contiguous()):
+        _check_cache(k, v, table, num_req, kv, dim, dev)
+    n, page = shape[0], shape[2]
+    wide = kv * page * dim
+    return CPages(n, page, k.data_ptr(), v.data_ptr(), ks[0] if n > 1 else wide,
+                  vs[0] if n > 1 else wide,
+                  _arg(cache["k_scale"], _F32, "k_scale", n * kv, dev, (kv,)),
+                  _arg(cache["v_scale"], _F32, "v_scale", n * kv, dev, (kv,)), table.data_ptr(),
+                  ts[1])
 
 
 def csa2_rotate(packed, x, rope, pos, inverse, out, d_err, stream=None) -> int:
@@ -899,8 +913,8 @@ def csa2_page_append(packed, k, v, rope, pos, cache, d_err, stream=None) -> int:
 
 
 def csa2_page_attn_workspace(num_q, num_req, n_heads, n_kv_heads, dim, max_kv) -> int:
-    """Workspace bytes of the splits csa2_page_attn would choose for these sizes (0:
-    none); with less it splits less."""
+    """Workspace bytes with which csa2_page_attn shares caches of these sizes among CTAs
+    (0: it would not); with less it does not."""
     out = C.c_int64(0)
     _check(load().csa2_page_attn_workspace(int(num_q), int(num_req), int(n_heads),
                                            int(n_kv_heads), int(dim), int(max_kv), C.byref(out)),
@@ -1005,7 +1019,7 @@ def page_attn(packed, q, cache, max_kv, sm_scale=None, out=None, lse=None, want_
               workspace=None, d_err=None, stream=None):
     """Causal attention over a cache of 8-bit pages, for prompts, extends and single
     tokens.  Allocates the workspace (uint8, csa2_page_attn_workspace bytes) if none is
-    given; one for the largest batch serves the smaller ones too."""
+    given."""
     st, out, lse = _page_attn(packed, q, cache, max_kv, sm_scale, out, lse, want_lse, workspace,
                               None, d_err, stream)
     _check(st, "csa2_page_attn")

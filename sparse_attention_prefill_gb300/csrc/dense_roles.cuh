@@ -368,8 +368,10 @@ __device__ __forceinline__ void store_rows(const AttnParams &P, uint32_t to, int
 }
 
 // The end of one item's stream t: row x of the tile (token i of the run, if `valid`),
-// whose O is at `to` in TMEM, is normalised and stored.  False if a wait ran out.
-template <typename T, typename C, bool kNarrow, typename M>
+// whose O is at `to` in TMEM, is normalised and stored.  kRuns: partial results are those
+// of single items, number it.split (-1: none), with all rows of the item.  False if a
+// wait ran out.
+template <typename T, typename C, bool kNarrow, bool kRuns = false, typename M>
 __device__ __forceinline__ bool finish_item(const AttnParams &P, M *ms, const Item &it, int t,
                                             int i, bool valid, bool rows_here, float ref, float sum,
                                             uint32_t to, uint32_t &po, uint32_t &pst) {
@@ -409,17 +411,29 @@ __device__ __forceinline__ bool finish_item(const AttnParams &P, M *ms, const It
   w0 *= inv, w1 *= inv;
   const float lse =
       seen ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-  if (P.splits > 0) {
-    const int64_t rows = part_rows(P.seqs.num_q, P.group);
-    const int64_t at = (int64_t)(it.q0 + i) * P.group + x % P.group;
+  if (kRuns ? P.part_o && it.split >= 0 : P.splits > 0) {
+    int64_t stat, elem;
+    if (kRuns) {
+      constexpr int kRows = kNarrow ? kTile : 2 * kTile;
+      stat = (int64_t)it.split * kRows + (kNarrow ? 0 : t * kTile) + x;
+      elem = (stat & ~(int64_t)31) * D + (x & 31);
+    } else {
+      const int64_t rows = part_rows(P.seqs.num_q, P.group);
+      const int64_t at = (int64_t)(it.q0 + i) * P.group + x % P.group;
+      stat = part_stat(rows, P.n_kv, it.split, it.h, at);
+      elem = part_elem(rows, P.n_kv, D, it.split, it.h, at);
+    }
     if (valid) {
-      P.part_lse[part_stat(rows, P.n_kv, it.split, it.h, at)] = lse;
-      if (it.uncovered && it.split == 0)
+      P.part_lse[stat] = lse;
+      if (!kRuns && it.uncovered && it.split == 0) {
+        const int64_t rows = part_rows(P.seqs.num_q, P.group);
+        const int64_t at = (int64_t)(it.q0 + i) * P.group + x % P.group;
         for (int s = 0; s < P.cover_splits; ++s)
           P.cover_lse[part_stat(rows, P.n_kv, s, it.h, at)] = -INFINITY;
+      }
     }
     if (rows_here && any) {
-      float *dst = P.part_o + part_elem(rows, P.n_kv, D, it.split, it.h, at);
+      float *dst = P.part_o + elem;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];

@@ -1,27 +1,5 @@
-// Attention over 8-bit pages on the 5th-generation tensor cores (csa2_page_attn):
-// prompts, extends, and single tokens of more than 16 heads to a key head; and the
-// call's entry points.
-//
-// Items, streams and products are those of dense_attn.cu, with codes for K and V and
-// the scales of page_attn.cuh in the softmax.  Both products take f16 operands, in
-// which codes are exact, as are bf16 queries times a power of two for each row.
-// (Products of the codes themselves would need the queries and weights in 8 bits: two
-// products for what two codes of a query hold, and a weight of 4 bits is too coarse.)
-// So the roles are, 16 warps to a CTA:
-//   0-7    softmax, a row of a query tile to a thread;
-//   8      issues the products;
-//   9      producer: TMA copies of Q, and of the pages' codes into a ring of raw tiles;
-//          it also looks up the pages and writes the scales of each tile's 16-key groups;
-//   10     hands out items;
-//   12-15  converters, a key to a thread: a raw tile to an f16 tile in the products'
-//          swizzle, rows behind the last and rows without a page as zeros (0 * NaN);
-//          an item's bf16 queries, where they are.
-// A step of 128 keys (D = 128) has 2 x 16384 codes: some 250 instructions to a
-// converter thread, a tenth of what the SM can issue while the products run.
-//
-// Every wait is bounded; on expiry the kernel raises CSA2_DERR_TIMEOUT, drains its
-// copies and products, frees TMEM and returns.
-#include "dense_join.cuh"
+// Entry points of the attention over 8-bit pages (csa2_page_attn), and the choice among its
+// kernels: page_decode.cu for single tokens, page_tiles.cuh for the rest.
 #include "dense_roles.cuh"
 #include "page_attn.cuh"
 
@@ -29,536 +7,46 @@ namespace csa2 {
 namespace pages {
 namespace {
 
-constexpr int kGroups = 8;           // 16-key groups of a tile, each within a page
-constexpr int kSlots = 8;            // tiles whose scales are kept (see the producer)
-constexpr int kConvertWarp = 12;
-
-template <int D_>
-struct Cfg {
-  static constexpr int D = D_;
-  static constexpr int kStages = D == 128 ? 3 : 6;     // f16 tiles
-  static constexpr int kRaw = D == 128 ? 3 : 6;        // tiles of codes
-  static constexpr uint32_t kQTile = (D / 64) * kBlk;
-  static constexpr uint32_t kStage = (D / 64) * kBlk;
-  static constexpr uint32_t kRawStage = kTile * D;
-  static constexpr uint32_t kOffRing = 2 * kQTile;
-  static constexpr uint32_t kOffRaw = kOffRing + kStages * kStage;
-  static constexpr uint32_t kOffMisc = kOffRaw + kRaw * kRawStage;
-  static_assert(kStages + kRaw <= 12, "scales");
-  static constexpr int kThreads = 4 * 128;
-  // 128 registers to a thread at launch, and the sum stays
-  static constexpr int kRegsSoftmax = 200;
-  static constexpr int kRegsRest = 56;
-  static constexpr int kRegsConvert = 56;
-  static_assert(2 * kRegsSoftmax + kRegsRest + kRegsConvert <= 4 * 128, "registers");
-  static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kColO = 2 * 128;
-};
-
-// Scales of a key tile's groups: a (times c of the softmax), log2 b and 1 / b; log2 b =
-// -inf where there is no page.
-struct TileScales {
-  float a[kGroups], lb[kGroups], ib[kGroups];
-};
-
-template <int D>
-struct Misc {
-  using C = Cfg<D>;
-  uint64_t full[C::kStages], empty[C::kStages];
-  uint64_t raw_full[C::kRaw], raw_empty[C::kRaw], scales_full[kSlots];
-  uint64_t q_full, q_ready, q_empty, s_full[2], p_full[2][2], o_full[2], done, clc;
-  uint64_t item_full[kItems], item_empty[kItems];
-  Bound bd;
-  uint32_t tmem;
-  uint64_t loaded, stat_full, stat_empty;
-  alignas(16) uint64_t next[2];      // answer to the request for another CTA's work
-  Item item[kItems];
-  float2 stat[kTile];                // narrow items: reference and sum of stream 1's rows
-  alignas(16) TileScales scales[kSlots];
-  float unlift[kItems][2 * kTile];   // bf16 queries: what undoes a row's power of two
-};
-
-template <int D>
-constexpr uint32_t smem_bytes() {
-  return Cfg<D>::kOffMisc + (uint32_t)sizeof(Misc<D>);
-}
-static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory");
-
-// Key tile x of an item's k-th pair (narrow) or step, as the order K, K, V, V or K, V
-// of the rings goes.
-struct Order {
-  int both, kt;                      // tiles of this pair; tile of the item
-  bool value;
-};
-template <bool kNarrow>
-__device__ __forceinline__ Order order_of(int nk, int k0, int x) {
-  const int both = min(kNarrow ? 2 : 1, nk - k0);
-  return Order{both, k0 + (x >= both ? x - both : x), x >= both};
-}
-
-// Producer warp: an item's Q, then the codes of its K and V tiles, page by page.  A lane
-// holds one of 32 neighbouring pages of the request and its scales.
-template <int D, bool kNarrow>
-__device__ void producer_role(const AttnParams &P, const Pages &C8, uint8_t *smem, Misc<D> *ms,
-                              const CUtensorMap *mq, const CUtensorMap *mk,
-                              const CUtensorMap *mv) {
-  using C = Cfg<D>;
-  const int lane = threadIdx.x & 31;
-  const int per = kTile >> C8.shift;    // pages of a tile
-  const uint32_t page_bytes = (uint32_t)C8.page * D;
-  uint32_t g = 0, nq = 0, tiles = 0;    // uses so far
-  int err = 0;
-  bool ok = true;
-  for (uint32_t u = 0; ok; ++u) {
-    if (!(ok = wait_all(&ms->item_full[u % kItems], (u / kItems) & 1, &ms->bd))) break;
-    const Item cur = ms->item[u % kItems];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ms->item_empty[u % kItems]);
-    if (cur.run < 0) break;
-    if (cur.nk <= 0) {
-      if (lane == 0) mbar_arrive(&ms->loaded);
-      continue;
-    }
-    int id = -1;
-    float a = 0.f, b = 0.f;
-    const int64_t held = (cur.m + C8.page - 1) >> C8.shift;
-    int64_t from = 0;                   // the first of the lanes' pages
-    const auto look_up = [&](int64_t p) {
-      from = p;
-      const bool there = p + lane < held;
-      id = there ? page_id(C8, cur.run, p + lane, err) : -1;
-      a = id >= 0 ? C8.k_scale[(int64_t)id * P.n_kv + cur.h] : 0.f;
-      b = id >= 0 ? C8.v_scale[(int64_t)id * P.n_kv + cur.h] : 0.f;
-    };
-    look_up((int64_t)cur.kt0 * per);
-    if (!(ok = wait_all(&ms->q_empty, (nq & 1) ^ 1, &ms->bd))) break;
-    if (lane == 0) {
-      const uint32_t box = (uint32_t)P.tpt * P.group * 128u;
-      mbar_arrive_expect_tx(&ms->q_full, box * (D / 64) * cur.ntile);
-      for (int t = 0; t < cur.ntile; ++t)
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(smem + t * C::kQTile + c * kBlk, mq, c * 64, cur.h * P.group,
-                      cur.q0 + cur.tok0 + t * P.tpt, &ms->q_full);
-    }
-    ++nq;
-    for (int k0 = 0; k0 < cur.nk && ok; k0 += kNarrow ? 2 : 1) {
-      const int both = order_of<kNarrow>(cur.nk, k0, 0).both;
-      if ((int64_t)(cur.kt0 + k0 + both) * per > from + 32)
-        look_up((int64_t)(cur.kt0 + k0) * per);
-      for (int x = 0; x < 2 * both; ++x, ++g) {
-        const Order o = order_of<kNarrow>(cur.nk, k0, x);
-        const int64_t p0 = (int64_t)(cur.kt0 + o.kt) * per;
-        const uint32_t s = g % C::kRaw, ph = (g / C::kRaw) & 1;
-        if (!(ok = wait_all(&ms->raw_empty[s], ph ^ 1, &ms->bd))) break;
-        const int off = (int)(p0 - from);
-        uint8_t *to = smem + C::kOffRaw + s * C::kRawStage;
-        uint64_t *bar = &ms->raw_full[s];
-        const uint32_t valid =
-            __ballot_sync(0xffffffffu, id >= 0 && lane >= off && lane < off + per);
-        if (lane == 0) mbar_arrive_expect_tx(bar, page_bytes * __popc(valid));
-        __syncwarp();
-        if ((valid >> lane) & 1)         // a copy to a lane, which has the page's number
-          tma_load_3d(to + (lane - off) * page_bytes, o.value ? mv : mk, 0,
-                      (int)((int64_t)cur.h * C8.page * D / 128), id, bar);
-        __syncwarp();
-        if (!o.value) {
-          // scales: the last tile that used this slot is done with.  (The rings let in
-          // this tile once the product of the 12th entry before it, or an earlier one,
-          // has ended, and the V tiles of eight tiles before lie further back.)
-          const uint32_t tile = tiles + o.kt;
-          const int src = off + ((lane % kGroups) * 16 >> C8.shift);
-          const int gid = __shfl_sync(0xffffffffu, id, src);
-          const float ga = __shfl_sync(0xffffffffu, a, src), gb = __shfl_sync(0xffffffffu, b, src);
-          if (lane < kGroups) {
-            TileScales &ts = ms->scales[tile % kSlots];
-            const float sa = gid >= 0 ? scale_of(ga, err) : 0.f;
-            const float sb = gid >= 0 ? scale_of(gb, err) : 0.f;
-            ts.a[lane] = sa * P.scale_log2;
-            ts.lb[lane] = log2f(sb);
-            ts.ib[lane] = gid >= 0 ? 1.f / sb : 0.f;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ms->scales_full[tile % kSlots]);
-        }
-      }
-    }
-    tiles += cur.nk;
-    if (lane == 0) mbar_arrive(&ms->loaded);
-  }
-  // every copy has to land before the CTA leaves
-  if (lane == 0) {
-    if (nq) drain_bar(&ms->q_full, (nq - 1) & 1);
-    for (uint32_t i = g > (uint32_t)C::kRaw ? g - C::kRaw : 0; i < g; ++i)
-      drain_bar(&ms->raw_full[i % C::kRaw], (i / C::kRaw) & 1);
-  }
-  __syncwarp();
-  err = __reduce_or_sync(0xffffffffu, err);
-  if (lane == 0) raise_err(P.d_err, err);
-}
-
-// bf16 queries of row `row` of a tile to f16, in place; what undoes their scaling.
-template <int D>
-__device__ __forceinline__ float convert_query(uint8_t *tile, int row) {
-  uint8_t *line = tile + row * 128;
-  float amax = 0.f;
-#pragma unroll 4
-  for (int c = 0; c < D / 8; ++c) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(line + (c >> 3) * kBlk +
-                                                     (((c & 7) ^ (row & 7)) << 4));
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      amax = max3(amax, fabsf(__uint_as_float(v[i] << 16)),
-                  fabsf(__uint_as_float(v[i] & 0xffff0000u)));
-  }
-  const float lift = lift_of(amax);
-#pragma unroll 4
-  for (int c = 0; c < D / 8; ++c) {
-    uint4 *at = reinterpret_cast<uint4 *>(line + (c >> 3) * kBlk + (((c & 7) ^ (row & 7)) << 4));
-    const uint4 w = *at;
-    uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = Elem<__half>::pack(__uint_as_float(v[i] << 16) * lift,
-                                __uint_as_float(v[i] & 0xffff0000u) * lift);
-    *at = make_uint4(v[0], v[1], v[2], v[3]);
-  }
-  return 1.f / lift;
-}
-
-// Converter warps, a row of a tile to a thread.  Eight neighbouring lanes have eight
-// rows, whose chunks the swizzles of both tiles lay in different banks.
-template <typename T, int D, bool kNarrow>
-__device__ void convert_role(uint8_t *smem, Misc<D> *ms) {
-  using C = Cfg<D>;
-  const int lane = threadIdx.x & 31, row = threadIdx.x & 127;
-  uint32_t g = 0, nq = 0, tiles = 0;
-  bool ok = true;
-  for (uint32_t u = 0; ok; ++u) {
-    const uint32_t slot = u % kItems;
-    if (!wait_all(&ms->item_full[slot], (u / kItems) & 1, &ms->bd)) return;
-    const Item &it = ms->item[slot];
-    const int run = it.run, nk = it.nk, kt0 = it.kt0, ntile = it.ntile;
-    const int64_t m = it.m;
-    if (run < 0) return;
-    if (nk > 0) {
-      if (Elem<T>::kBf16) {
-        if (!wait_all(&ms->q_full, nq & 1, &ms->bd)) return;
-        for (int t = 0; t < ntile; ++t)
-          ms->unlift[slot][t * kTile + row] = convert_query<D>(smem + t * C::kQTile, row);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->q_ready);
-        ++nq;
-      }
-      for (int k0 = 0; k0 < nk && ok; k0 += kNarrow ? 2 : 1) {
-        const int both = order_of<kNarrow>(nk, k0, 0).both;
-        for (int x = 0; x < 2 * both; ++x, ++g) {
-          const Order o = order_of<kNarrow>(nk, k0, x);
-          const uint32_t tile = tiles + o.kt, s = g % C::kStages, r = g % C::kRaw;
-          if (!(ok = wait_all(&ms->raw_full[r], (g / C::kRaw) & 1, &ms->bd))) break;
-          if (!(ok = wait_all(&ms->scales_full[tile % kSlots], (tile / kSlots) & 1, &ms->bd)))
-            break;
-          const bool dead = (int64_t)(kt0 + o.kt) * kTile + row >= m ||
-                            ms->scales[tile % kSlots].lb[row >> 4] == -INFINITY;
-          const uint8_t *raw = smem + C::kOffRaw + r * C::kRawStage;
-          uint8_t *to = smem + C::kOffRing + s * C::kStage + row * 128;
-          if (!(ok = wait_all(&ms->empty[s], ((g / C::kStages) & 1) ^ 1, &ms->bd))) break;
-#pragma unroll
-          for (int c0 = 0; c0 < D / 16; c0 += 4) {
-            uint4 w[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int line = D == 128 ? row : row >> 1;
-              const int at = D == 128 ? c0 + c : (row & 1) * 4 + c;
-              w[c] = *reinterpret_cast<const uint4 *>(raw + line * 128 + ((at ^ (line & 7)) << 4));
-              if (dead) w[c] = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint8_t *blk = to + ((c0 + c) >> 2) * kBlk;
-              const int at = 2 * ((c0 + c) & 3);
-              *reinterpret_cast<uint4 *>(blk + ((at ^ (row & 7)) << 4)) =
-                  make_uint4(f16x2_of(w[c].x), f16x2_of_high(w[c].x), f16x2_of(w[c].y),
-                             f16x2_of_high(w[c].y));
-              *reinterpret_cast<uint4 *>(blk + (((at + 1) ^ (row & 7)) << 4)) =
-                  make_uint4(f16x2_of(w[c].z), f16x2_of_high(w[c].z), f16x2_of(w[c].w),
-                             f16x2_of_high(w[c].w));
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ms->full[s]);
-            mbar_arrive(&ms->raw_empty[r]);
-          }
-        }
-      }
-      tiles += nk;
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ms->item_empty[slot]);
-  }
-}
-
-// Softmax of one item's stream t and its output; one row to a thread.  A page has kG
-// columns of a tile or a multiple.  `tiles`: key tiles of the items before.  False if a wait ran out.
-template <typename T, int D, bool kNarrow, int kG>
-__device__ bool softmax_item(const AttnParams &P, Misc<D> *ms, const Item &it, uint32_t slot,
-                             int t, uint32_t tiles, uint32_t &ps, uint32_t &po, uint32_t &pst) {
-  using C = Cfg<D>;
-  const int x = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
-  const int tok = x / P.group;
-  const int i = it.tok0 + (kNarrow ? 0 : t * P.tpt) + tok;     // token of the run
-  const bool valid = tok < P.tpt && i < it.n;
-  const bool rows_here = __any_sync(0xffffffffu, valid);
-  const uint32_t lane_addr = (uint32_t)(32 * warp) << 16;
-  const uint32_t ts = ms->tmem + t * 128 + lane_addr, to = ms->tmem + C::kColO + t * D + lane_addr;
-  // keys this row sees: j <= last (rows without a token are never masked: what they
-  // hold goes nowhere)
-  const int last = !valid ? 0x7fffffff : (int)(it.m - it.n + i);
-  const int min_last = __reduce_min_sync(0xffffffffu, last);
-  float ref = -INFINITY, sum = 0.f, unit = 1.f;
-  bool ok = true;
-  const int steps = it.steps[t], stride = kNarrow ? 2 : 1;
-  int kt = kNarrow ? t : 0;              // tile of the item
-  for (int j = 0; j < steps; ++j, kt += stride) {
-    if (!(ok = wait_all(&ms->s_full[t], ps, &ms->bd))) break;
-    ps ^= 1;
-    const uint32_t tile = tiles + kt;
-    if (!(ok = wait_all(&ms->scales_full[tile % kSlots], (tile / kSlots) & 1, &ms->bd))) break;
-    if (!rows_here) {
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) {
-        mbar_arrive(&ms->p_full[t][0]);
-        mbar_arrive(&ms->p_full[t][1]);
-      }
-      continue;
-    }
-    fence_after_sync();
-    // (S is there, so the queries were converted)
-    if (Elem<T>::kBf16 && j == 0) unit = ms->unlift[slot][(kNarrow ? 0 : t * kTile) + x];
-    const TileScales &sc = ms->scales[tile % kSlots];
-    uint32_t s[4][32];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32x32b_x32(ts + 32 * c, s[c]);
-    tmem_wait_ld();
-    const int key0 = (it.kt0 + kt) * kTile;
-    if (key0 + kTile - 1 > min_last) {
-      const int vis = last - key0;       // columns <= vis are seen
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (32 * c + e > vis) s[c][e] = 0xff800000u;
-    }
-    // by blocks of kG columns: what S is multiplied by (a factor of 0 would make -inf a
-    // NaN), and the largest x
-    constexpr int kBlocks = kTile / kG, kEntry = kG / 16;
-    float f[kBlocks], mx = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kBlocks; ++k) {
-      f[k] = fmaxf(sc.a[k * kEntry] * unit, 1e-37f);
-      float m4[kG / 16];
-#pragma unroll
-      for (int e = 0; e < kG; e += 2) {
-        const uint32_t *y = &s[(k * kG + e) / 32][(k * kG + e) % 32];
-        float &m = m4[e / 16];
-        m = e % 16 ? max3(m, __uint_as_float(y[0]), __uint_as_float(y[1]))
-                   : fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
-      }
-      const float mg = kG == 16 ? m4[0] : fmaxf(max3(m4[0], m4[1 % kEntry], m4[2 % kEntry]), m4[3 % kEntry]);
-      mx = fmaxf(mx, fmaf(mg, f[k], sc.lb[k * kEntry]));
-    }
-    const bool move = mx > ref + (kLift + kMargin);
-    if (__any_sync(0xffffffffu, move)) {
-      const float nref = move ? mx - kLift : ref;
-      const float alpha = move ? ex2(ref - nref) : 1.f;     // ref = -inf: 0
-      ref = nref;
-      sum *= alpha;
-      if (j > 0) {
-#pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t o[32];
-          tmem_ld32x32b_x16(to + 16 * c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32x32b_x16(to + 16 * c, o);
-        }
-      }
-    }
-    const float sub = ref == -INFINITY ? 0.f : ref;
-    uint64_t part[2];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t p[32];
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        const int at = 32 * c + e, k = at / kG;
-        const float l = sc.lb[k * kEntry] - sub;
-        const float2 v = unpack2(fma2(pack2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
-                                      pack2(f[k], f[k]), pack2(l, l)));
-        const float a = ex2(v.x), b = ex2(v.y);
-        uint64_t &sums = part[(e >> 1) & 1];
-        sums = at % kG < 4 ? pack2(a, b) : add2(sums, pack2(a, b));
-        p[e / 2] = Elem<__half>::pack(a, b);
-        if (at % kG == kG - 2) {
-          const float2 both = unpack2(add2(part[0], part[1]));
-          sum = fmaf(both.x + both.y, sc.ib[k * kEntry], sum);
-        }
-      }
-      tmem_st32x32b_x16(ts + 16 * c, p);
-      if (c & 1) {                 // 64 keys written: their product may start
-        tmem_wait_st();
-        fence_before_sync();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->p_full[t][c >> 1]);
-      }
-    }
-  }
-  return ok && finish_item<T, C, kNarrow>(P, ms, it, t, i, valid, rows_here, ref, sum, to, po, pst);
-}
-
-template <typename T, int D, bool kNarrow, int kG>
-__device__ void softmax_role(const AttnParams &P, Misc<D> *ms) {
-  const int t = threadIdx.x >> 7;
-  uint32_t ps = 0, po = 0, pst = 0, tiles = 0;
-  for (uint32_t u = 0;; ++u) {
-    const uint32_t slot = u % kItems;
-    if (!wait_all(&ms->item_full[slot], (u / kItems) & 1, &ms->bd)) return;
-    // the item stays in shared memory until its output is written: registers are short
-    const Item &it = ms->item[slot];
-    if (it.run < 0) return;
-    if ((kNarrow || t < it.ntile) &&
-        !softmax_item<T, D, kNarrow, kG>(P, ms, it, slot, t, tiles, ps, po, pst))
-      return;
-    tiles += max(it.nk, 0);
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&ms->item_empty[slot]);
-  }
-}
-
-template <typename T, int D, bool kNarrow, int kG>
-__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
-page_attn_kernel(const __grid_constant__ AttnParams P, const __grid_constant__ Pages C8,
-                 const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                 const __grid_constant__ CUtensorMap mv) {
-  using C = Cfg<D>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  Misc<D> *ms = reinterpret_cast<Misc<D> *>(smem + C::kOffMisc);
-  const int warp = threadIdx.x >> 5;
-  if (warp == kMmaWarp) {
-    tmem_alloc(&ms->tmem, C::kTmemCols);
-    tmem_relinquish();
-  } else if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&ms->full[i], 4);                    // converter warps
-      mbar_init(&ms->empty[i], 1);
-    }
-    for (int i = 0; i < C::kRaw; ++i) {
-      mbar_init(&ms->raw_full[i], 1);
-      mbar_init(&ms->raw_empty[i], 4);
-    }
-    for (int i = 0; i < kSlots; ++i) mbar_init(&ms->scales_full[i], 1);
-    mbar_init(&ms->q_full, 1);
-    mbar_init(&ms->q_ready, 4);
-    mbar_init(&ms->q_empty, 1);
-    mbar_init(&ms->done, 1);
-    mbar_init(&ms->clc, 1);
-    mbar_init(&ms->loaded, 1);
-    mbar_init(&ms->stat_full, 4);
-    mbar_init(&ms->stat_empty, 4);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&ms->s_full[t], 1);
-      mbar_init(&ms->p_full[t][0], 4);
-      mbar_init(&ms->p_full[t][1], 4);
-      mbar_init(&ms->o_full[t], 1);
-    }
-    for (int i = 0; i < kItems; ++i) {
-      mbar_init(&ms->item_full[i], 1);
-      mbar_init(&ms->item_empty[i], 8 + 4 + 2);      // softmax, converters, MMA, producer
-    }
-    ms->bd.abort = 0;
-    ms->bd.wait_ns = P.wait_ns;
-    mbar_fence_init();
-  }
-  fence_before_sync();
-  __syncthreads();
-  fence_after_sync();
-  if (warp >= kConvertWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsConvert));
-    convert_role<T, D, kNarrow>(smem, ms);
-  } else if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
-    if (warp == kProducerWarp)
-      producer_role<D, kNarrow>(P, C8, smem, ms, &mq, &mk, &mv);
-    else if (warp == kMmaWarp)
-      mma_role<C, idesc_of<__half>(kTile, kTile, false), idesc_of<__half>(kTile, D, true), kNarrow>(
-          smem, ms, Elem<T>::kBf16 ? &ms->q_ready : &ms->q_full);
-    else if (warp == kItemWarp)
-      item_role<kNarrow, true>(P, ms);
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
-    softmax_role<T, D, kNarrow, kG>(P, ms);
-  }
-  fence_before_sync();
-  __syncthreads();
-  if (threadIdx.x == 0 && ms->bd.abort) raise_err(P.d_err, CSA2_DERR_TIMEOUT);
-  if (warp == kMmaWarp) {
-    fence_after_sync();
-    tmem_dealloc(ms->tmem, C::kTmemCols);
-  }
-}
-
-struct Maps {
-  CUtensorMap q, k, v;
-};
-
-template <typename T, int D, bool kNarrow, int kG>
-int launch(const AttnParams &P, const Pages &C8, int items, const Maps &m, cudaStream_t st) {
-  allow_smem<page_attn_kernel<T, D, kNarrow, kG>>((int)smem_bytes<D>());
-  page_attn_kernel<T, D, kNarrow, kG>
-      <<<items, Cfg<D>::kThreads, smem_bytes<D>(), st>>>(P, C8, m.q, m.k, m.v);
-  return launch_status();
-}
-
-template <typename T, int D>
-int launch_any(const AttnParams &P, const Pages &C8, bool narrow, int items, const Maps &m,
-               cudaStream_t st) {
-  if (C8.page >= 64)
-    return narrow ? launch<T, D, true, 64>(P, C8, items, m, st)
-                  : launch<T, D, false, 64>(P, C8, items, m, st);
-  return narrow ? launch<T, D, true, 16>(P, C8, items, m, st)
-                : launch<T, D, false, 16>(P, C8, items, m, st);
-}
+constexpr int kMostRuns = 2;         // items to an SM, up to which they are cut
 
 int run_tiles(const Shape &s, const csa2_pages *c, const Pages &C8, const void *q, int64_t ldq,
-              const AttnParams &P, bool narrow, cudaStream_t st) {
+              const AttnParams &P, const TilesWs &ws, bool narrow, cudaStream_t st) {
   // an upper bound of the items, since the lengths are on the device
   const int64_t tok = narrow ? P.tpt : 2 * P.tpt;
-  const int64_t items =
-      (P.seqs.num_q / tok + P.seqs.count) * s.n_kv * (P.splits > 0 ? P.splits : 1);
+  const int64_t items = (P.seqs.num_q / tok + P.seqs.count) * s.n_kv;
   if (items > 0x7fffffffll) return CSA2_ERR_UNSUPPORTED;
-  Maps m;
+  TileMaps m;
   if (!make_rows_map(&m.q, s.bf16, q, P.seqs.num_q, s.n_heads, s.dim, ldq, s.group, P.tpt) ||
       !make_cache_maps(&m.k, &m.v, c, q, s, kTile))
     return CSA2_ERR_UNSUPPORTED;
-  const int n = (int)items;
-  if (s.bf16)
-    return s.dim == 128 ? launch_any<__nv_bfloat16, 128>(P, C8, narrow, n, m, st)
-                        : launch_any<__nv_bfloat16, 64>(P, C8, narrow, n, m, st);
-  return s.dim == 128 ? launch_any<__half, 128>(P, C8, narrow, n, m, st)
-                      : launch_any<__half, 64>(P, C8, narrow, n, m, st);
+  return s.dim == 128 ? page_tiles_128(s.bf16, P, C8, ws, narrow, (int)items, m, st)
+                      : page_tiles_64(s.bf16, P, C8, ws, narrow, (int)items, m, st);
 }
 
-// Splits where the items alone leave SMs idle; more would only add their join.
-PartPlan plan(const Shape &s, int64_t num_q, int64_t num_req, int64_t max_kv) {
-  PartPlan p = plan_part(s, num_q, num_req > 0 ? num_req : 1, max_kv, true);
-  const int64_t tok = p.kind == kWideItems ? 2 * p.tpt : p.tpt;
+// How a call runs, and the workspace that it would like.
+struct CallPlan {
+  int tpt;
+  Kind kind;
+  int64_t bytes;                         // 0: items whole
+};
+
+CallPlan plan(const Shape &s, int64_t num_q, int64_t num_req, int64_t max_kv) {
+  CallPlan p{};
   const int64_t runs = num_req > 0 ? num_req : 1;
+  p.tpt = tile_tokens(num_q, runs, s.group);
+  p.kind = kind_of(num_q, runs, p.tpt, s.group, true);
+  if (num_q == 0 || num_req == 0) return p;
+  if (p.kind == kSingleTokens) {
+    p.bytes = page_decode_bytes(s);
+    return p;
+  }
+  // Runs of tiles where the items are few and there is something to cut; handed out whole,
+  // more items even out by themselves, and none is joined.
+  const int64_t tok = p.kind == kWideItems ? 2 * p.tpt : p.tpt;
   const int64_t items = (num_q / tok > runs ? num_q / tok : runs) * s.n_kv;
-  if (p.kind == kSingleTokens || items >= kSms) p.splits = 1;
+  const int64_t rows = p.kind == kWideItems ? 2 * kTile : kTile;
+  if (items <= kMostRuns * kSms && max_kv > 2 * kTile)
+    p.bytes = kSms * ((int64_t)sizeof(TileMark) + 2 * rows * (s.dim + 1) * 4);
   return p;
 }
 
@@ -585,11 +73,7 @@ extern "C" CSA2_API int csa2_page_attn_workspace(int32_t num_q, int32_t num_req,
   dense::Shape s;
   const int st = pages::check_call(&b, n_heads, n_kv_heads, dim, CSA2_DT_BF16, 1.f, &s);
   if (st != CSA2_OK) return st;
-  const dense::PartPlan p = pages::plan(s, num_q, num_req, max_kv);
-  *bytes = num_q == 0 || num_req == 0            ? 0
-           : p.kind == dense::kSingleTokens ? pages::page_decode_bytes(s)
-           : p.splits > 1                       ? p.splits * dense::part_bytes(num_q, s)
-                                                : 0;
+  *bytes = pages::plan(s, num_q, num_req, max_kv).bytes;
   return CSA2_OK;
 }
 
@@ -610,16 +94,8 @@ extern "C" CSA2_API int csa2_page_attn(const csa2_packed *b, int32_t n_heads, in
   if (!out) return CSA2_ERR_INVALID_ARG;
   if (!aligned(16, out) || !aligned(4, lse, d_err) || ((uintptr_t)workspace & 255u))
     return CSA2_ERR_UNSUPPORTED;
-  const int64_t part = dense::part_bytes(b->num_q, s);
-  const dense::PartPlan plan = pages::plan(s, b->num_q, b->num_req, max_kv);
-  int splits = plan.splits;
-  if (splits > workspace_bytes / part) splits = (int)(workspace_bytes / part);
-  const bool single = plan.kind == dense::kSingleTokens;
-  uint64_t ws = splits > 1 ? (uint64_t)(splits * part) : 0;
-  if (single) {
-    ws = (uint64_t)pages::page_decode_bytes(s);
-    if (workspace_bytes < (int64_t)ws) ws = 0;
-  }
+  const pages::CallPlan plan = pages::plan(s, b->num_q, b->num_req, max_kv);
+  const uint64_t ws = workspace_bytes >= plan.bytes ? (uint64_t)plan.bytes : 0;
   // outputs and workspace against the inputs and each other; out may be q
   const int64_t wide = (int64_t)n_heads * dim * 2;
   const uint64_t no = (uint64_t)b->num_q * wide, nl = (uint64_t)b->num_q * n_heads * 4;
@@ -649,18 +125,16 @@ extern "C" CSA2_API int csa2_page_attn(const csa2_packed *b, int32_t n_heads, in
   P.lse = lse;
   P.d_err = d_err;
   P.wait_ns = wait_limit_ns();
-  if (splits > 1) {
-    const int64_t rows = dense::part_rows(b->num_q, s.group) * s.n_kv;
-    P.splits = splits;
-    P.part_o = static_cast<float *>(workspace);
-    P.part_lse = P.part_o + splits * rows * s.dim;
-  }
   const cudaStream_t cs = as_stream(stream);
-  if (single)
+  if (plan.kind == dense::kSingleTokens)
     return pages::page_decode(s, pages::PageAttnParams{P, C8, q, ldq}, max_kv, c,
                               ws ? workspace : nullptr, cs);
-  st = pages::run_tiles(s, c, C8, q, ldq, P, plan.kind == dense::kNarrowItems, cs);
-  if (st != CSA2_OK || splits <= 1) return st;
-  const dense::Join j{P.part_o, P.part_lse, splits, 0, b->num_q, b->num_req, b->cu_q, out, lse};
-  return dense::join_parts(s, j, true, cs);
+  const bool narrow = plan.kind == dense::kNarrowItems;
+  pages::TilesWs parts{nullptr, narrow ? dense::kTile : 2 * dense::kTile};
+  if (ws) {
+    parts.marks = static_cast<pages::TileMark *>(workspace);
+    P.part_lse = reinterpret_cast<float *>(parts.marks + dense::kSms);
+    P.part_o = P.part_lse + 2 * dense::kSms * parts.rows;
+  }
+  return pages::run_tiles(s, c, C8, q, ldq, P, parts, narrow, cs);
 }

@@ -29,6 +29,23 @@ int64_t page_decode_bytes(const Shape &s);
 int page_decode(const Shape &s, const PageAttnParams &P, int64_t max_kv, const csa2_pages *c,
                 void *ws, cudaStream_t st);
 
+// Tiles (page_tiles.cuh).  For the join: the item that began in the share before and goes on
+// in this one: its first query row, tokens, key head and parts.
+struct TileMark {
+  int q0, tokens, h, parts;
+};
+struct TilesWs {
+  TileMark *marks;                       // null: items are handed out whole
+  int rows;                              // of a part
+};
+struct TileMaps {
+  CUtensorMap q, k, v;
+};
+int page_tiles_64(bool bf16, const AttnParams &P, const Pages &C8, const TilesWs &ws, bool narrow,
+                  int items, const TileMaps &m, cudaStream_t st);
+int page_tiles_128(bool bf16, const AttnParams &P, const Pages &C8, const TilesWs &ws, bool narrow,
+                   int items, const TileMaps &m, cudaStream_t st);
+
 // Power of two that takes a query row's largest magnitude to [2^14, 2^15), so that
 // its bf16 channels are f16 ones.
 __device__ __forceinline__ float lift_of(float amax) {

@@ -3,12 +3,10 @@
 //
 // Bound by the pages' bytes, each read once: at 128 channels a key's row is 128
 // bytes, and a few query rows meet it.  96 requests of 10.0 thousand rows on average
-// take 295 us (6.7 TB/s, what a copy does), 61 of 2831 rows 67 us (5.3 TB/s).
+// take 295 us (6.7 TB/s, what a copy does), 61 of 2815 rows 67 us (5.3 TB/s).
 //
 // All (token, key head) items' blocks of 32 keys lie in one row, and each CTA (three to
-// an SM) takes an equal run of them, whatever items it crosses, where an item counts as
-// kFixed blocks more than it has: what its start and end take.  So lengths of any mixture
-// fill the GPU evenly, and a CTA starts once.  (A CTA to an item or an equal split of
+// an SM) takes an equal run of them (page_runs.cuh), so that it starts once.  (A CTA to an item or an equal split of
 // one: 83 and 331 us; runs equal in blocks alone: 76 and 305.)  An item that two or more
 // CTAs share is left as parts, at most two to a CTA, which a second kernel joins.
 //
@@ -28,7 +26,7 @@
 // Lines of 128 bytes are swizzled by TMA (16-byte chunk i of line l lies at i ^ l %
 // 8), and the keys' order within 16 is chosen so that no load of either operand meets
 // a bank twice: fragment row a holds key key_of(a).
-#include "page_attn.cuh"
+#include "page_runs.cuh"
 
 namespace csa2 {
 namespace pages {
@@ -37,8 +35,6 @@ namespace {
 constexpr int kWarps = 4;                // that compute
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kKeys = 32;                // keys of a block
-constexpr int kFixed = 12;               // blocks' time that an item's start and end take
-constexpr int kLeast = 4;                // cost of a share, at least
 constexpr int kSegs = 2;                 // segments published at a time
 constexpr int kBurst = 4;                // blocks asked for at a time, a lane to each
 
@@ -66,21 +62,23 @@ struct Segment {
   int part;                              // of the partial results; -1: the whole item
 };
 
-// Runs of query rows as the blocks go over them.
-struct Run {
-  int lo, n;                             // query rows (n = 0: none, or skipped)
-  int64_t m;                             // cache rows
-};
-// A point of all items' costs, kFixed and one for each block to an item: token i of run
-// `run`, its head, and how far into the item.
-struct Place {
-  int run, i, h, off;
-  Run u;
+// Single tokens: a unit is a token, a step a block of keys.
+struct Tokens {
+  static constexpr int kFixed = 12;      // blocks' time that an item's start and end take
+  static constexpr int kLeast = 4;       // cost of a share, at least
+  static __device__ __forceinline__ int units(const Run &u) { return u.n; }
+  static __device__ __forceinline__ int keys(const Run &u, int i) {
+    const int64_t last = u.m - u.n + i;  // keys seen: 0 .. last
+    return last < 0 ? 0 : (int)last + 1;
+  }
+  // a token that sees nothing has a block, too: its output is written
+  static __device__ __forceinline__ int steps(const Run &u, int i) {
+    return max(1, (keys(u, i) + kKeys - 1) / kKeys);
+  }
 };
 
-// For the join: the item that began in the share before and goes on in this one, and the
-// parts it has, the first of them the share before's second one, then first ones; token
-// -1: none.
+// For the join: the item that began in the share before and goes on in this one, and its
+// parts (parts_of).
 struct Mark {
   int token, h, parts, pad;
 };
@@ -90,6 +88,7 @@ template <int kN>
 constexpr int kToSm = kN == 1 ? 3 : 2;
 template <int kN>
 constexpr int kCtas = kToSm<kN> * kSms;
+
 // kN: groups of 8 query rows
 template <int D, int kN>
 struct Shared {
@@ -130,114 +129,6 @@ __device__ __forceinline__ int byte_of(int row, int chunk) {
   return line * 128 + ((at ^ (line & 7)) << 4);
 }
 
-__device__ __forceinline__ Run run_at(const PageAttnParams &P, int r, int &err) {
-  const Seqs &S = P.at.seqs;
-  Run u;
-  const int64_t m = S.kv_len[r];
-  seq_rows(S, r, u.lo, u.n, err);
-  u.m = m;
-  if (m < 0 || m > S.kv_rows) {
-    if (u.n) err |= CSA2_DERR_RANGE_ROW;
-    u.m = 0;
-  }
-  return u;
-}
-__device__ __forceinline__ int keys_of(const Run &u, int i) {
-  const int64_t last = u.m - u.n + i;                // keys seen: 0 .. last
-  return last < 0 ? 0 : (int)last + 1;
-}
-// a token that sees nothing has a block, too: its output is written
-__device__ __forceinline__ int blocks_of(int keys) { return max(1, (keys + kKeys - 1) / kKeys); }
-__device__ __forceinline__ int cost_of(const Run &u, int i) {
-  return kFixed + blocks_of(keys_of(u, i));
-}
-// of one head of a run
-__device__ __forceinline__ int64_t cost_of(const Run &u) {
-  int64_t c = 0;
-  for (int i = 0; i < u.n; ++i) c += cost_of(u, i);
-  return c;
-}
-
-// The place of a run's point `at`.
-__device__ __forceinline__ Place place_in(const Run &u, int run, int n_kv, int64_t at) {
-  Place p{run, 0, 0, 0, u};
-  for (int64_t c; at >= (c = cost_of(u, p.i)) * n_kv; ++p.i) at -= c * n_kv;
-  const int c = cost_of(u, p.i);
-  for (; at >= c; ++p.h) at -= c;
-  p.off = (int)at;
-  return p;
-}
-
-// Equal shares of the cost: `more` of them have one more.
-struct Plan {
-  int64_t share;
-  int shares, more;
-};
-__device__ __forceinline__ Plan plan_of(int64_t total) {
-  Plan p;
-  p.shares = max(1, (int)min((int64_t)gridDim.x, total / kLeast));
-  // (32 bits divide in a fifth of the time)
-  p.share = total >> 32 ? total / p.shares : (int64_t)((uint32_t)total / (uint32_t)p.shares);
-  p.more = (int)(total - p.share * p.shares);
-  return p;
-}
-__device__ __forceinline__ int64_t share_begin(const Plan &p, int s) {
-  return s < p.shares ? s * p.share + min(s, p.more) : p.shares * p.share + p.more;
-}
-__device__ __forceinline__ int share_of(const Plan &p, int64_t at) {
-  const int64_t big = p.more * (p.share + 1);
-  const int64_t off = at < big ? at : at - big, by = at < big ? p.share + 1 : p.share;
-  return (at < big ? 0 : p.more) +
-         (int)(off >> 32 || by >> 32 ? off / by : (int64_t)((uint32_t)off / (uint32_t)by));
-}
-
-// The shares, and the place of the CTA's own, by the whole CTA.
-template <int D, int kN>
-__device__ Plan find_share(const PageAttnParams &P, Shared<D, kN> &sh, int &err) {
-  const Seqs &S = P.at.seqs;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (S.count + kThreads - 1) / kThreads;
-  const int r0 = min(S.count, (int)threadIdx.x * per), r1 = min(S.count, r0 + per);
-  int64_t own = 0;
-  Run u{0, 0, 0};
-#pragma unroll 4
-  for (int r = r0; r < r1; ++r) {
-    u = run_at(P, r, err);
-    own += cost_of(u) * P.at.n_kv;
-  }
-  int64_t upto = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) sh.scan[warp] = upto;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) upto += sh.scan[w];
-    total += sh.scan[w];
-  }
-  const Plan plan = plan_of(total);
-  const int64_t begin = share_begin(plan, (int)blockIdx.x);
-  int64_t base = upto - own;                         // of this thread's first run
-  if (base <= begin && begin < upto) {
-    int ignored = 0;
-    for (int r = r0; r < r1; ++r) {
-      if (per > 1) u = run_at(P, r, ignored);
-      const int64_t c = cost_of(u) * P.at.n_kv;
-      if (begin < base + c) {
-        sh.place = place_in(u, r, P.at.n_kv, begin - base);
-        break;
-      }
-      base += c;
-    }
-  }
-  __syncthreads();
-  return plan;
-}
-
 __device__ __forceinline__ void bulk_load(void *to, const void *from, uint32_t bytes,
                                           uint64_t *bar) {
   asm volatile(
@@ -262,18 +153,14 @@ __device__ void producer_role(const PageAttnParams &P, bool whole, Shared<D, kN>
   const Pages &C = P.cache;
   const Seqs &S = P.at.seqs;
   Place p = sh.place;
-  int ignored = 0;
   uint32_t g = 0, segs = 0;              // blocks and segments so far
   bool ok = true;
   while (at < end) {
-    const int keys = keys_of(p.u, p.i), all = blocks_of(keys), h = p.h;
+    const int keys = Tokens::keys(p.u, p.i), all = Tokens::steps(p.u, p.i), h = p.h;
     const int run = p.run, token = p.u.lo + p.i;
-    // the item's blocks in the share: a share that ends within its fixed cost has none
-    const int blk = max(0, p.off - kFixed);
-    const int upto = (int)min((int64_t)(kFixed + all), p.off + (end - at));
-    int n = max(0, upto - kFixed) - blk;
-    at += kFixed + all - p.off;          // the next item
-    if (whole) n = blk == 0 && n > 0 ? all : 0;      // items are not shared
+    const Steps part = steps_in<Tokens>(p, all, end - at);
+    const int blk = part.from, n = whole ? (blk == 0 && part.n > 0 ? all : 0) : part.n;
+    at += Tokens::kFixed + all - p.off;  // the next item
     if (n > 0) {
       const uint32_t slot = segs % kSegs;
       if (!(ok = wait_all(&sh.seg_empty[slot], ((segs / kSegs) & 1) ^ 1, &sh.bd))) break;
@@ -355,24 +242,7 @@ __device__ void producer_role(const PageAttnParams &P, bool whole, Shared<D, kN>
       __syncwarp();
       g += some;
     }
-    if (!ok) break;
-    p.off = 0;
-    if (++p.h < P.at.n_kv) continue;
-    p.h = 0;
-    if (++p.i < p.u.n) continue;
-    p.i = 0;
-    if (at >= end) break;
-    for (++p.run; p.run < S.count; p.run += 32) {
-      int lo = 0, c = 0;
-      if (p.run + lane < S.count) seq_rows(S, p.run + lane, lo, c, ignored);
-      const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
-      if (some) {
-        p.run += __ffs(some) - 1;
-        break;
-      }
-    }
-    if (p.run >= S.count) break;         // (not reached: the blocks are there)
-    p.u = run_at(P, p.run, ignored);
+    if (!ok || at >= end || !next_item(Tokens{}, S, P.at.n_kv, p)) break;
   }
   if (ok) {
     const uint32_t slot = segs % kSegs;
@@ -382,9 +252,13 @@ __device__ void producer_role(const PageAttnParams &P, bool whole, Shared<D, kN>
       mbar_arrive(&sh.seg_full[slot]);
     }
   }
-  // copies land before the CTA leaves
-  if (!ok && lane == 0) {
-    for (uint32_t k = segs > (uint32_t)kSegs ? segs - kSegs : 0; k < segs; ++k)
+  // copies land before the CTA leaves: the warps that compute wait for all of them, but not
+  // once a wait has run out
+  if (lane == 0) {
+    // (the last phase of each barrier alone can be waited for: once the end is published, it
+    // is that of the slot of the segment before the last, whose copy was read by then)
+    const uint32_t open = ok ? 1 : kSegs;
+    for (uint32_t k = segs > open ? segs - open : 0; k < segs; ++k)
       drain_bar(&sh.seg_full[k % kSegs], (k / kSegs) & 1);
     for (uint32_t k = g > (uint32_t)Sh::kRing ? g - Sh::kRing : 0; k < g; ++k)
       drain_bar(&sh.full[k % Sh::kRing], (k / Sh::kRing) & 1);
@@ -700,19 +574,16 @@ page_decode_kernel(const __grid_constant__ PageAttnParams P, Mark *marks,
     mbar_fence_init();
   }
   int err = 0;
-  const Plan plan = find_share(P, sh, err);
+  const Plan plan =
+      find_share<kThreads>(Tokens{}, P.at.seqs, P.at.n_kv, sh.scan, sh.place, err);
   const int share = (int)blockIdx.x;
   const int64_t begin = share_begin(plan, share), end = share_begin(plan, share + 1);
   if (share > 0) err = 0;                // one CTA speaks of the requests
   if (marks && threadIdx.x == 32 * kWarps - 1) {
     Mark mark{-1, 0, 0, 0};
-    if (begin < end && sh.place.off > kFixed) {
-      const Place &p = sh.place;
-      const int64_t first = begin - p.off + kFixed;  // of the item's blocks
-      const int64_t last = first + blocks_of(keys_of(p.u, p.i)) - 1;
-      if (first >= share_begin(plan, share - 1))
-        mark = Mark{p.u.lo + p.i, p.h, share_of(plan, last) - share + 2, 0};
-    }
+    const Place &p = sh.place;
+    if (const int parts = parts_of(Tokens{}, plan, share, p))
+      mark = Mark{p.u.lo + p.i, p.h, parts, 0};
     marks[share] = mark;
   }
   if (begin < end) {
@@ -820,9 +691,10 @@ int launch(PageAttnParams P, int64_t max_kv, const CUtensorMap &mk, const CUtens
   static_assert(kSmem <= 232448 / kToSm<kN> - 1024, "CTAs to an SM");
   allow_smem<page_decode_kernel<T, D, kN>>(kSmem);
   // no more CTAs than the blocks may need
-  const double most = (double)P.at.seqs.num_q * P.at.n_kv * (double)(max_kv / kKeys + 1 + kFixed);
-  const int grid =
-      most >= (double)kLeast * kCtas<kN> ? kCtas<kN> : (int)(most / kLeast) + 1;
+  const double most =
+      (double)P.at.seqs.num_q * P.at.n_kv * (double)(max_kv / kKeys + 1 + Tokens::kFixed);
+  const int grid = most >= (double)Tokens::kLeast * kCtas<kN> ? kCtas<kN>
+                                                                : (int)(most / Tokens::kLeast) + 1;
   Mark *marks = static_cast<Mark *>(ws);
   if (ws) {
     P.at.part_lse = reinterpret_cast<float *>(marks + kCtas<kN>);
