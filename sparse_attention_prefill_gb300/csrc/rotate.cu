@@ -1,7 +1,8 @@
 // Rotary positions of rows [num_q, n_heads, dim] (csa2_rotate), and with the sign
 // turned round the gradient.
 //
-// Bound by memory: two bytes read and written for each channel.  A thread has eight
+// Bound by memory: two bytes read and written for each channel; 16001 rows of 64 heads x
+// 128 channels take 82 us (6.4 TB/s).  A thread has eight
 // pairs of one row's channels (rope.cuh) and goes over the row's heads with them, so
 // that an angle's reduction, sine and cosine are spent once for all of the heads that
 // it does.
@@ -12,8 +13,13 @@ namespace rope {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 8;                 // rows of a block
+constexpr int kSlots = 4;                // heads of a row that a block does at a time
 constexpr int kAhead = 4;                // heads that a thread has in flight
+// rows of a block (with 8 heads at a time and half the rows, 12345 rows of 24 heads x 64
+// took 17.7 us instead of 15.8; with 2 and twice the rows, 16001 of 64 x 128 85 instead of
+// 82)
+template <int D>
+constexpr int kRows = kThreads / (D / 16) / kSlots;
 
 struct RotateParams {
   int num_q, num_req, n_heads;
@@ -31,12 +37,11 @@ struct RotateParams {
 template <typename T, int D, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateParams P) {
   constexpr int kTeam = D / 16;                          // threads of a row and head
-  constexpr int kSlots = kThreads / kTeam / kRows;       // heads that a block does at a time
   __shared__ uint64_t turn[D / 2];
-  __shared__ int64_t pos[kRows];
-  __shared__ int held[kRows];
-  const int64_t row0 = (int64_t)blockIdx.x * kRows;
-  if (threadIdx.x < kRows) {
+  __shared__ int64_t pos[kRows<D>];
+  __shared__ int held[kRows<D>];
+  const int64_t row0 = (int64_t)blockIdx.x * kRows<D>;
+  if (threadIdx.x < kRows<D>) {
     const int64_t row = row0 + threadIdx.x;
     held[threadIdx.x] = P.rope.pos && row < P.num_q;
     if (P.rope.pos && row < P.num_q) pos[threadIdx.x] = P.rope.pos[row];
@@ -52,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
         err |= CSA2_DERR_BAD_EXTEND;
         continue;
       }
-      const int64_t a = max((int64_t)lo, row0), b = min((int64_t)hi, row0 + kRows);
+      const int64_t a = max((int64_t)lo, row0), b = min((int64_t)hi, row0 + kRows<D>);
       if (a >= b) continue;
       const int64_t first = P.kv_len[r] - (hi - lo) - lo;
       for (int64_t i = a; i < b; ++i) {
@@ -66,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
     }
     __syncthreads();
   }
-  const int t = threadIdx.x % kTeam, row = threadIdx.x / kTeam % kRows;
+  const int t = threadIdx.x % kTeam, row = threadIdx.x / kTeam % kRows<D>;
   if (!held[row]) return;
   const Place at = place_of<D, kInterleaved>(t, P.rope.rot);
   float c[kUnit], s[kUnit];
@@ -74,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
   const T *x = static_cast<const T *>(P.x) + (row0 + row) * P.ldx;
   T *out = static_cast<T *>(P.out) + (row0 + row) * P.ldo;
   const int h1 = min(P.n_heads, ((int)blockIdx.y + 1) * P.each);
-  for (int h0 = (int)blockIdx.y * P.each + threadIdx.x / kTeam / kRows; h0 < h1;
+  for (int h0 = (int)blockIdx.y * P.each + threadIdx.x / kTeam / kRows<D>; h0 < h1;
        h0 += kAhead * kSlots) {
     uint4 a[kAhead], b[kAhead];
 #pragma unroll
@@ -165,10 +170,10 @@ extern "C" CSA2_API int csa2_rotate(const csa2_packed *b, int32_t n_heads, int32
   P.sign = inverse ? -1.f : 1.f;
   P.d_err = d_err;
   // all heads of a row in one block, unless there are too few rows to fill the GPU
-  const int blocks = (b->num_q + rope::kRows - 1) / rope::kRows;
-  const int slots = rope::kThreads / (dim / 16) / rope::kRows;
+  const int rows = dim == 128 ? rope::kRows<128> : rope::kRows<64>;
+  const int blocks = (b->num_q + rows - 1) / rows;
   int chunks = 1;
-  while (chunks * slots < n_heads && (int64_t)blocks * chunks < 4 * dense::kSms) chunks *= 2;
+  while (chunks * rope::kSlots < n_heads && (int64_t)blocks * chunks < 4 * dense::kSms) chunks *= 2;
   P.each = (n_heads + chunks - 1) / chunks;
   const dim3 grid((unsigned)blocks, (unsigned)((n_heads + P.each - 1) / P.each));
   const cudaStream_t cs = as_stream(stream);

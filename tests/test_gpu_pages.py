@@ -210,9 +210,9 @@ def test_append_ragged(kv, dim, page, dtype, rotated):
 @pytest.mark.parametrize("kv,dim,page,dtype", SHAPES)
 @pytest.mark.parametrize("inter", [False, True])
 def test_append_few_rows_and_one_long(kv, dim, page, dtype, inter):
-    """Few rows to a request on average, and one with many: blocks go to warps."""
-    new = [1] * 50 + [150] + [2] * 9
-    rows = [1 + 7 * i for i in range(50)] + [190] + [2 + 30 * i for i in range(9)]
+    """No more rows than requests, and one with many: blocks go to warps."""
+    new = [1] * 50 + [150] + [2] * 9 + [0] * 170
+    rows = [1 + 7 * i for i in range(50)] + [190] + [2 + 30 * i for i in range(9)] + [3] * 170
     b, cu = R.batch(new, rows, DEV, lead=1)
     c = R.make_cache(rows, kv, dim, page, seed=page + dim, spread=0.0)
     before = _copy(c)
