@@ -352,10 +352,8 @@ __device__ void convert_role(uint8_t *smem, Misc<D> *ms) {
                             ms->scales[tile % kSlots].lb[row >> 4] == -INFINITY;
           const uint8_t *raw = smem + C::kOffRaw + r * C::kRawStage;
           uint8_t *to = smem + C::kOffRing + s * C::kStage + row * 128;
-          if (!(ok = wait_all(&ms->empty[s], ((g / C::kStages) & 1) ^ 1, &ms->bd))) break;
-#pragma unroll
-          for (int c0 = 0; c0 < D / 16; c0 += 4) {
-            uint4 w[4];
+          uint4 w[4];
+          const auto load = [&](int c0) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int line = D == 128 ? row : row >> 1;
@@ -363,6 +361,12 @@ __device__ void convert_role(uint8_t *smem, Misc<D> *ms) {
               w[c] = *reinterpret_cast<const uint4 *>(raw + line * 128 + ((at ^ (line & 7)) << 4));
               if (dead) w[c] = make_uint4(0, 0, 0, 0);
             }
+          };
+          load(0);                       // while the stage may still be read
+          if (!(ok = wait_all(&ms->empty[s], ((g / C::kStages) & 1) ^ 1, &ms->bd))) break;
+#pragma unroll
+          for (int c0 = 0; c0 < D / 16; c0 += 4) {
+            if (c0) load(c0);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint8_t *blk = to + ((c0 + c) >> 2) * kBlk;
