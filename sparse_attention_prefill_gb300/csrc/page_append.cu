@@ -3,7 +3,9 @@
 // A block (page, head, side) has one scale s, the smallest power of two with |x| <=
 // 448 s, so that rescaling older rows by old / new is exact but below 2^-6.
 //
-// Bound by memory: two bytes read and one written for each channel.
+// Bound by memory in the end, two bytes read and one written for each channel, but near it
+// by instructions (the issue slots are 71 % busy): eight prompts of 8192 rows, 8 heads x
+// 128, take 87 us (4.6 TB/s; 72 without the rotation), 256 single rows 8.4.
 //
 // Which page a block of the grid has: the pages that request r's new rows touch
 // take the places from floor(cu_q[r] / page) + 2 r on.  (n rows touch at most
@@ -11,8 +13,8 @@
 // request's first place, so no prefix sum is needed.)
 //
 // Two kernels do the pages.  No more rows than requests (decode steps): a block to a warp,
-// and a CTA to two places (one request's, most of the time); four rows at a time, gone over twice where there are more.
-// Otherwise a CTA has one side of a page and some of its heads, and a thread 16
+// and a CTA to two places (one request's, most of the time); four rows at a time, gone over
+// twice where there are more.  Otherwise a CTA has one side of a page and some of its heads, and a thread 16
 // channels of a row (two rows in pages of 128 rows of 128 channels), so that an
 // angle's sine and cosine are spent once for all of the heads; a head's rows stay in
 // registers between the maximum, which the CTA finds together, and the codes, while

@@ -636,6 +636,17 @@ page_tiles_join_kernel(const __grid_constant__ AttnParams P, const TileMark *mar
   const auto part = [&](int k) {
     return (k == 0 ? 2 * (int64_t)(j - 1) + 1 : 2 * (int64_t)(j - 1 + k)) * rows;
   };
+  const float *po = P.part_o + lane + warp * kCh * 32;
+  float v[kBatch][kCh];
+  const auto fetch = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const float *src = po + (part(k0 + u) + row0) * D;
+#pragma unroll
+      for (int d = 0; d < kCh; ++d) v[u][d] = k0 + u < mark.parts ? src[d * 32] : 0.f;
+    }
+  };
+  fetch(0);                              // together with the statistics
   for (int k = warp; k < mark.parts; k += 16)
     weight[k][lane] = mine ? P.part_lse[part(k) + row] : -INFINITY;
   __syncthreads();
@@ -648,22 +659,18 @@ page_tiles_join_kernel(const __grid_constant__ AttnParams P, const TileMark *mar
   }
   const float ref = top == -INFINITY ? 0.f : top;
   float acc[kCh] = {};
-  const float *po = P.part_o + lane + warp * kCh * 32;
-  for (int k0 = 0; k0 < mark.parts; k0 += kBatch) {
-    float v[kBatch][kCh], w[kBatch];
+  for (int k0 = 0;;) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      w[u] = k0 + u < mark.parts ? ex2((weight[k0 + u][lane] - ref) * 1.4426950408889634f) : 0.f;
-      const float *src = po + (part(k0 + u) + row0) * D;
+      const float w =
+          k0 + u < mark.parts ? ex2((weight[k0 + u][lane] - ref) * 1.4426950408889634f) : 0.f;
+      tot += w;
+      // (what nobody saw was not written)
 #pragma unroll
-      for (int d = 0; d < kCh; ++d) v[u][d] = w[u] != 0.f ? src[d * 32] : 0.f;
+      for (int d = 0; d < kCh; ++d) acc[d] = w != 0.f ? fmaf(w, v[u][d], acc[d]) : acc[d];
     }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      tot += w[u];
-#pragma unroll
-      for (int d = 0; d < kCh; ++d) acc[d] = fmaf(w[u], v[u][d], acc[d]);
-    }
+    if ((k0 += kBatch) >= mark.parts) break;
+    fetch(k0);
   }
   const float inv = tot > 0.f || nan ? 1.f / tot : 0.f;
 #pragma unroll
