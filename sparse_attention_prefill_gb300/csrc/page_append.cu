@@ -4,8 +4,8 @@
 // 448 s, so that rescaling older rows by old / new is exact but below 2^-6.
 //
 // Bound by memory in the end, two bytes read and one written for each channel, but near it
-// by instructions (the issue slots are 71 % busy): eight prompts of 8192 rows, 8 heads x
-// 128, take 87 us (4.6 TB/s; 72 without the rotation), 256 single rows 8.4.
+// by instructions: eight prompts of 8192 rows, 8 heads x 128, take 81.5 us (4.9 TB/s; one
+// row to a thread 87.6, of which the rotation was 15), 256 single rows 8.2.
 //
 // Which page a block of the grid has: the pages that request r's new rows touch
 // take the places from floor(cu_q[r] / page) + 2 r on.  (n rows touch at most
@@ -14,11 +14,11 @@
 //
 // Two kernels do the pages.  No more rows than requests (decode steps): a block to a warp,
 // and a CTA to two places (one request's, most of the time); four rows at a time, gone over
-// twice where there are more.  Otherwise a CTA has one side of a page and some of its heads, and a thread 16
-// channels of a row (two rows in pages of 128 rows of 128 channels), so that an
-// angle's sine and cosine are spent once for all of the heads; a head's rows stay in
-// registers between the maximum, which the CTA finds together, and the codes, while
-// the next head's are on their way.
+// twice where there are more.  Otherwise a CTA has one side of a page and some of its heads,
+// and a thread 16 channels of two rows (of one in the smallest pages), so that an angle's
+// sine and cosine are spent once for all of the heads; a head's rows stay in registers
+// between the maximum, which the CTA finds together, and the codes, while the next heads'
+// are on their way.
 #include "pages.cuh"
 #include "rope.cuh"
 
@@ -334,7 +334,7 @@ __device__ __forceinline__ void copy16(void *to, const void *from, bool there) {
 }
 
 template <typename T, int D, bool kInterleaved, int kRows>
-__global__ void __launch_bounds__(512, kRows == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kRows == 1 ? 128 : 512, kRows == 1 ? 8 : 1)
 append_many_kernel(const __grid_constant__ AppendParams P) {
   constexpr int kTeam = D / 16;
   __shared__ uint64_t turn[D / 2];
@@ -443,12 +443,12 @@ template <typename T, int D, bool kInterleaved>
 int launch_many(const AppendParams &P, dim3 grid, cudaStream_t st) {
   const int threads = P.cache.page * (D / 16);
   const int smem = kAhead * 2 * 16 * threads;
-  if (threads <= 512) {
-    allow_smem<append_many_kernel<T, D, kInterleaved, 1>>(kAhead * 2 * 16 * 512);
+  if (threads < 256) {
+    allow_smem<append_many_kernel<T, D, kInterleaved, 1>>(kAhead * 2 * 16 * 128);
     append_many_kernel<T, D, kInterleaved, 1><<<grid, threads, smem, st>>>(P);
-  } else if (D == 128) {                 // (pages of 128 rows)
-    allow_smem<append_many_kernel<T, 128, kInterleaved, 2>>(kAhead * 2 * 16 * 1024);
-    append_many_kernel<T, 128, kInterleaved, 2><<<grid, 512, smem, st>>>(P);
+  } else {
+    allow_smem<append_many_kernel<T, D, kInterleaved, 2>>(kAhead * 2 * 16 * 1024);
+    append_many_kernel<T, D, kInterleaved, 2><<<grid, threads / 2, smem, st>>>(P);
   }
   return launch_status();
 }

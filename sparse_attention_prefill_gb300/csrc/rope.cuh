@@ -127,6 +127,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // the 16 channels of a thread's two units; every product is rounded, so that a
 // rotation has the same bits wherever it is computed
 template <bool kInterleaved>
@@ -140,9 +146,9 @@ __device__ __forceinline__ void turn16(float (&x)[2 * kUnit], const Place &at,
 #pragma unroll
     for (int i = 0; i < kUnit; i += 2) {
       const uint64_t a = pack2(x[i], x[i + 1]), b = pack2(x[kUnit + i], x[kUnit + i + 1]);
-      const uint64_t co = pack2(c[i], c[i + 1]);
-      const float2 u = unpack2(add2(mul2(a, co), mul2(b, pack2(-s[i], -s[i + 1]))));
-      const float2 w = unpack2(add2(mul2(b, co), mul2(a, pack2(s[i], s[i + 1]))));
+      const uint64_t co = pack2(c[i], c[i + 1]), si = pack2(s[i], s[i + 1]);
+      const float2 u = unpack2(sub2(mul2(a, co), mul2(b, si)));
+      const float2 w = unpack2(add2(mul2(b, co), mul2(a, si)));
       x[i] = u.x, x[i + 1] = u.y, x[kUnit + i] = w.x, x[kUnit + i + 1] = w.y;
     }
   } else {
