@@ -770,6 +770,8 @@ CSA2_API int csa2_page_append(const csa2_packed *b, int32_t n_kv_heads, int32_t 
  * f16, which keeps their bits unless they lie 2^28 below the row's largest; codes
  * are exact in f16; the weights, times their block's scale, are rounded to f16 for
  * the product with V (2^-11 each; their sum is not rounded).
+ * Where requests lie over one another (a descent in cu_q) and have more than num_q rows
+ * together, some of them may be left out; the same holds for csa2_page_append.
  * Supported as csa2_prompt_attn. */
 CSA2_API int csa2_page_attn_workspace(int32_t num_q, int32_t num_req, int32_t n_heads,
                                       int32_t n_kv_heads, int32_t dim, int64_t max_kv,

@@ -188,13 +188,17 @@ struct Found {
 };
 
 // Calls f(found) for each page of a request that has one of `places` places from `place`
-// on (in a malformed batch places may be several requests').
+// on.  In a malformed batch places may be several requests'; of more than kMost the first
+// are served, or a batch whose requests all lie over one another would take requests times
+// pages of time.
+constexpr int kMost = 32;
+
 template <typename F>
 __device__ __forceinline__ void each_page(const AppendParams &P, int64_t place, int places,
                                           int &err, const F &f) {
   __shared__ Touched held;
   __shared__ int found, matches;
-  for (int from = 0;;) {
+  for (int from = 0, served = 0; served < kMost; ++served) {
     if (threadIdx.x == 0) found = 0x7fffffff, matches = 0;
     __syncthreads();
     int mine = 0x7fffffff;

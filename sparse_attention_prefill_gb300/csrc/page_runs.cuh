@@ -17,10 +17,12 @@ struct Run {
   int lo, n;                             // (n = 0: none, or skipped)
   int64_t m;
 };
-// A point of the row: unit i of run `run`, its head, and how far into the item.
+// A point of the row: unit i of run `run`, its head, and how far into the item; the query
+// rows of the runs in front.
 struct Place {
   int run, i, h, off;
   Run u;
+  int64_t rows;
 };
 
 __device__ __forceinline__ Run run_at(const Seqs &S, int r, int &err) {
@@ -70,7 +72,7 @@ __device__ __forceinline__ int64_t cost_of(const U &rule, const Run &u) {
 template <typename U>
 __device__ __forceinline__ Place place_in(const U &rule, const Run &u, int run, int n_kv,
                                           int64_t at) {
-  Place p{run, 0, 0, 0, u};
+  Place p{run, 0, 0, 0, u, 0};
   for (int64_t c; at >= (c = U::kFixed + rule.steps(u, p.i)) * n_kv; ++p.i) at -= c * n_kv;
   const int c = U::kFixed + rule.steps(u, p.i);
   for (; at >= c; ++p.h) at -= c;
@@ -78,47 +80,73 @@ __device__ __forceinline__ Place place_in(const U &rule, const Run &u, int run, 
   return p;
 }
 
-// The shares, and the place of the CTA's own, by the whole CTA of kThreads threads.
-template <int kThreads, typename U>
-__device__ Plan find_share(const U &rule, const Seqs &S, int n_kv,
-                           int64_t (&scan)[kThreads / 32], Place &place, int &err) {
+// Sum of the threads' values in front of this one's, and of all, by the whole CTA.
+template <int kThreads>
+__device__ __forceinline__ int64_t sum_before(int64_t own, int64_t (&scan)[kThreads / 32],
+                                              int64_t &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (S.count + kThreads - 1) / kThreads;
-  const int r0 = min(S.count, (int)threadIdx.x * per), r1 = min(S.count, r0 + per);
-  int64_t own = 0;
-  Run u{0, 0, 0};
-#pragma unroll 4
-  for (int r = r0; r < r1; ++r) {
-    u = run_at(S, r, err);
-    own += cost_of(rule, u) * n_kv;
-  }
   int64_t upto = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += v;
   }
+  __syncthreads();
   if (lane == 31) scan[warp] = upto;
   __syncthreads();
-  int64_t total = 0;
+  total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) upto += scan[w];
     total += scan[w];
   }
+  return upto - own;
+}
+
+// The shares, and the place of the CTA's own, by the whole CTA of kThreads threads.
+//
+// In a malformed batch requests may lie over one another and have any number of rows
+// together; they are served in order as long as that is num_q at most.
+template <int kThreads, typename U>
+__device__ Plan find_share(const U &rule, const Seqs &S, int n_kv,
+                           int64_t (&scan)[kThreads / 32], Place &place, int &err) {
+  const int per = (S.count + kThreads - 1) / kThreads;
+  const int r0 = min(S.count, (int)threadIdx.x * per), r1 = min(S.count, r0 + per);
+  int64_t own = 0, rows = 0;
+  Run u{0, 0, 0};
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) {
+    u = run_at(S, r, err);
+    rows += u.n;
+    if (rows <= S.num_q) own += cost_of(rule, u) * n_kv;
+  }
+  int64_t total, all;
+  int64_t before = sum_before<kThreads>(rows, scan, all);      // query rows in front
+  if (all > S.num_q) {                   // (the same in every thread)
+    own = 0;
+    int64_t upto = before;
+    int ignored = 0;
+    for (int r = r0; r < r1; ++r) {
+      u = run_at(S, r, ignored);
+      upto += u.n;
+      if (upto <= S.num_q) own += cost_of(rule, u) * n_kv;
+    }
+  }
+  int64_t base = sum_before<kThreads>(own, scan, total);       // of this thread's first run
   const Plan plan = plan_of(total, U::kLeast);
   const int64_t begin = share_begin(plan, (int)blockIdx.x);
-  int64_t base = upto - own;             // of this thread's first run
-  if (base <= begin && begin < upto) {
+  if (base <= begin && begin < base + own) {
     int ignored = 0;
     for (int r = r0; r < r1; ++r) {
       if (per > 1) u = run_at(S, r, ignored);
       const int64_t c = cost_of(rule, u) * n_kv;
       if (begin < base + c) {
         place = place_in(rule, u, r, n_kv, begin - base);
+        place.rows = before;
         break;
       }
       base += c;
+      before += u.n;
     }
   }
   __syncthreads();
@@ -135,12 +163,15 @@ __device__ __forceinline__ bool next_item(const U &rule, const Seqs &S, int n_kv
   if (++p.i < rule.units(p.u)) return true;
   p.i = 0;
   int ignored = 0;
+  p.rows += p.u.n;
   for (++p.run; p.run < S.count; p.run += 32) {
     int lo = 0, c = 0;
     if (p.run + lane < S.count) seq_rows(S, p.run + lane, lo, c, ignored);
     const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
     if (some) {
-      p.run += __ffs(some) - 1;
+      const int src = __ffs(some) - 1;
+      if (p.rows + __shfl_sync(0xffffffffu, c, src) > S.num_q) return false;
+      p.run += src;
       p.u = run_at(S, p.run, ignored);
       return true;
     }

@@ -248,3 +248,30 @@ def test_many_key_heads_and_requests():
                        torch.tensor([rows[r] - 1], device=DEV))
         R.check_attention(out[r:r + 1], lse[r:r + 1], ref, BF, rows[r],
                           float(c["v_scale"].max()))
+
+
+@pytest.mark.parametrize("single", [True, False])
+def test_requests_all_over_one_another(single):
+    """Every other request has all query rows: the calls end in the time of a few batches,
+    say so, and touch nothing but these rows."""
+    n, heads, kv, dim, page = 2000, 4, 1, 64, 16
+    r = n if single else 300
+    cu = torch.tensor(([2, n] * r)[:r + 1], dtype=torch.int32, device=DEV)
+    b = dict(num_q=n, num_req=r, cu_q=cu, kv_len=torch.full((r,), n, device=DEV))
+    c = R.make_cache([n], kv, dim, page, seed=1)
+    c["table"] = c["table"].expand(r, -1).contiguous()
+    q = _normal((n, heads, dim), HF, 2)
+    out = torch.full_like(q, 7.0)
+    k = _normal((n, kv, dim), HF, 3)
+    a, z = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    d = _derr()
+    S.rotate(b, q, S.rope_freqs(64), d_err=d)
+    a.record()
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device=DEV)):
+        S.page_attn(b, q, c, max_kv=n, out=out, workspace=ws, d_err=d)
+    S.page_append(b, k, k, c, rope=S.rope_freqs(64), d_err=d)
+    z.record()
+    z.synchronize()
+    assert int(d.item()) == S.DERR_BAD_EXTEND
+    assert (out[:2] == 7).all() and (out[2:] != 7).any(2).all()
+    assert a.elapsed_time(z) < 500
