@@ -21,7 +21,7 @@ frequencies), ``page_append`` and ``page_attn``.  They take the same batch witho
 ``kv_start``; the cache as a dict of ``k`` and ``v`` [pages, kv heads, page, dim]
 (uint8 or float8_e4m3fn codes), ``k_scale`` and ``v_scale`` [pages, kv heads] fp32 and
 ``table`` [R, width] int32; and the rotation as a dict of ``freq`` [rot / 2] float64,
-``interleaved`` and ``amplitude``.
+``interleaved`` and ``amplitude``.  ``rotate`` takes part in autograd; no other call does.
 """
 from __future__ import annotations
 
@@ -998,13 +998,65 @@ def rope_freqs(rot, base=10000.0, scaling=None, factor=1.0, original=None, low=1
     return dict(freq=f.to(device), amplitude=amplitude)
 
 
+class _Rotate(torch.autograd.Function):
+    """The rotation out of place with its gradient, the rotation by -a, on the stream that
+    is current.  Rows that are not rotated are zeros here, both ways: unset ones would go
+    into the sums over rows that gradients of weights are."""
+
+    @staticmethod
+    def forward(ctx, x, packed, rope, pos, inverse, d_err):
+        n = int(packed["num_q"])
+        if pos is None:
+            ctx.save_for_backward(rope["freq"], None, packed["cu_q"], packed["kv_len"])
+        else:
+            ctx.save_for_backward(rope["freq"], pos)
+        ctx.batch = dict(num_q=n, num_req=int(packed["num_req"]) if pos is None else 0)
+        ctx.rope = {k: rope[k] for k in ("interleaved", "amplitude") if k in rope}
+        ctx.inverse = bool(inverse)
+        make = torch.empty if pos is not None and n == x.shape[0] else torch.zeros
+        out = make(x.shape, dtype=x.dtype, device=x.device)
+        _check(csa2_rotate(packed, x, rope, pos, inverse, out, d_err), "csa2_rotate")
+        return out
+
+    @staticmethod
+    def backward(ctx, g):
+        freq, pos, *lens = ctx.saved_tensors
+        for t in (freq, pos, *lens):
+            if t is not None and t.is_cuda:      # this may be what holds it last
+                t.record_stream(torch.cuda.current_stream(t.device))
+        batch = dict(ctx.batch, **dict(zip(("cu_q", "kv_len"), lens)))
+        if not g.is_contiguous() or g.data_ptr() % 16:
+            g = g.clone(memory_format=torch.contiguous_format)
+        return (_Rotate.apply(g, batch, dict(ctx.rope, freq=freq), pos, not ctx.inverse, None),
+                None, None, None, None, None)
+
+
 def rotate(packed, x, rope, pos=None, inverse=False, out=None, d_err=None, stream=None):
     """Rotary positions of rows [num_q, heads, dim]: at ``pos`` (int64 [num_q]) if given,
     else each at its row of its request's cache.  ``inverse`` takes the gradient of the
     rotated rows to that of the rows.  ``out`` may be ``x``; rows of no request are
-    left as they were (unset, where it is allocated here)."""
+    left as they were (unset, where it is allocated here).
+
+    Autograd: where ``x`` requires a gradient, so does the result (rows of no request
+    are zeros then, as is their gradient); ``out`` is refused, and the batch, frequencies
+    and positions have to stay as they are until the gradient is there.  No gradient
+    reaches the frequencies, and ones that require it are refused."""
+    if torch.is_grad_enabled() and (x.requires_grad or rope["freq"].requires_grad
+                                    or (out is not None and out.requires_grad)):
+        if rope["freq"].requires_grad:
+            raise Csa2Error("rotate: there is no gradient of the frequencies")
+        if out is not None:
+            raise Csa2Error("rotate: no gradient goes through out=; leave it out, or call under "
+                            "torch.no_grad()")
+        with torch.cuda.stream(stream):
+            y = _Rotate.apply(x, packed, rope, pos, inverse, d_err)
+        if stream is not None:
+            y.record_stream(torch.cuda.current_stream(y.device))
+        return y
     if out is None:
         out = _new(torch.empty, x.shape, x.dtype, x.device, stream)
+    else:                                # it may be saved for a gradient
+        torch.autograd.graph.increment_version(out)
     _check(csa2_rotate(packed, x, rope, pos, inverse, out, d_err, stream), "csa2_rotate")
     return out
 
