@@ -673,9 +673,10 @@ CSA2_API int csa2_evict_rows(int32_t num_req, int32_t n_heads, const int32_t *id
  *   (x, y) -> amplitude * (x cos a - y sin a, y cos a + x sin a),  a = p * freq[i]
  * and the other channels stay as they are.
  *   freq        [rot / 2] radians per position, float64, 8-byte aligned: scaled
- *               for a longer context by whoever made it.  A position times a
- *               frequency is reduced to a turn exactly (in 2^-64 turns), so that
- *               far positions lose nothing; frequencies are finite
+ *               for a longer context by whoever made it.  A frequency is taken to
+ *               2^-64 of a turn, and its product with a position, less whole
+ *               turns, is exact: position p is off by p 2^-64 turns at most;
+ *               frequencies are finite, of at most 2^40
  *   pos         [num_q] position of each query row, or NULL: its row in the
  *               request's cache, kv_len - n + i for query i of n
  *   interleaved 0: pair i is channels i and i + rot / 2; else 2 i and 2 i + 1

@@ -3,8 +3,8 @@
 // A position p and a frequency f (radians per position) make p f / 2 pi turns, of
 // which only the fraction counts.  A frequency is held as the fraction of a turn in
 // units of 2^-64, so that p times it, modulo 2^64, is the fraction with no rounding
-// but the frequency's own 2^-65: a product in fp32 would be a whole turn off at
-// positions of 2^24, and one in fp64 costs its SM 32 cycles a warp.
+// but the frequency's own, 2^-64 of a turn at most: a product in fp32 would be a whole
+// turn off at positions of 2^24, and one in fp64 costs its SM 32 cycles a warp.
 #pragma once
 #include "dense.cuh"
 
@@ -30,13 +30,26 @@ inline int check_rope(const csa2_rope *r, int dim) {
   return CSA2_OK;
 }
 
-// fractions of a turn per position, in 2^-64, of the table's pairs, by a block
+// The fraction of a turn that a frequency makes per position, in 2^-64, from its bits: the
+// mantissa times 1 / 2 pi in 2^-128, shifted by the exponent (below 2^52).  (Times 1 / 2 pi
+// in fp64 frequencies near 1 are 2^-56 of a turn off, which positions of 2^31 make 1.9e-7
+// radians; with a second double for the rest a decode step's append takes 8.5 us instead of
+// 7.9: fp64 is slow.)
+__device__ __forceinline__ uint64_t turn_per_position(double freq) {
+  constexpr uint64_t kHigh = 0x28be60db9391054aull, kLow = 0x7f09d5f47d4d3770ull;
+  const uint64_t bits = (uint64_t)__double_as_longlong(freq);
+  const uint64_t m = (bits & 0xfffffffffffffull) | (1ull << 52);     // times 2^(exponent - 1075)
+  const uint64_t carry = __umul64hi(m, kLow), mid = m * kHigh + carry;
+  const uint64_t high = __umul64hi(m, kHigh) + (mid < carry);
+  const int right = 1011 - (int)((bits >> 52) & 0x7ff);
+  const uint64_t t = right >= 0 ? high >> min(right, 63)             // (high has 51 bits)
+                                : high << (-right & 63) | mid >> (right & 63);
+  return bits >> 63 ? 0 - t : t;
+}
+
+// of the table's pairs, by a block
 __device__ __forceinline__ void load_turns(const Rope &R, uint64_t *turn) {
-  for (int i = threadIdx.x; i < R.rot / 2; i += blockDim.x) {
-    double t = R.freq[i] * 0.15915494309189535;     // 1 / 2 pi
-    t -= floor(t);
-    turn[i] = __double2ull_rn(t * 18446744073709551616.0);
-  }
+  for (int i = threadIdx.x; i < R.rot / 2; i += blockDim.x) turn[i] = turn_per_position(R.freq[i]);
 }
 
 // Thread t of a row and head (dim / 16 of them) has two units of 8 channels, each
