@@ -262,7 +262,8 @@ __device__ bool softmax_item(const AttnParams &P, M *ms, const Item &it, int t, 
     const float2 part2 = unpack2(add2(part[0], part[1]));
     sum = part2.x + part2.y;
   }
-  return ok && finish_item<T, C, kNarrow>(P, ms, it, t, i, valid, rows_here, ref, sum, to, po, pst);
+  return finish_item<T, C, kNarrow>(P, ms, it, t, i, ok, steps > 0, valid, rows_here, ref, sum, to,
+                                    po, pst);
 }
 
 // Items one after another, as the producer publishes them.

@@ -510,8 +510,8 @@ __device__ bool softmax_item(const AttnParams &P, Misc<D> *ms, const Item &it, u
       }
     }
   }
-  return ok && finish_item<T, C, kNarrow, true>(P, ms, it, t, i, valid, rows_here, ref, sum, to,
-                                               po, pst);
+  return finish_item<T, C, kNarrow, true>(P, ms, it, t, i, ok, steps > 0, valid, rows_here, ref,
+                                          sum, to, po, pst);
 }
 
 template <typename T, int D, bool kNarrow, int kG>
