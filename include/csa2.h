@@ -716,7 +716,8 @@ CSA2_API int csa2_rotate(const csa2_packed *b, int32_t n_heads, int32_t dim, int
  *             table[r, j / page].  Entries behind a request's last page are not read;
  *             one that names no page (negative, or num_pages and above) sets
  *             CSA2_DERR_RANGE_ROW, and its rows are neither written nor seen
- * A request of more than table_ld * page rows has none (CSA2_DERR_RANGE_ROW).
+ * A request of more than table_ld * page rows has none (CSA2_DERR_RANGE_ROW); the
+ * length of one without query rows is not looked at.
  * table_ld * page < 2^31 - 256 (CSA2_ERR_UNSUPPORTED). */
 typedef struct csa2_pages {
   int32_t num_pages;

@@ -80,7 +80,10 @@ __device__ void find_item(const AttnParams &P, uint32_t cta, const Shares &s, It
       seq_rows(P.seqs, i0 + lane, a, c, err);
       if (kPaged) {
         m = P.seqs.kv_len[i0 + lane];
-        if (m < 0 || m > P.seqs.kv_rows) m = 0, err |= CSA2_DERR_RANGE_ROW;
+        if (m < 0 || m > P.seqs.kv_rows) {
+          m = 0;
+          if (c) err |= CSA2_DERR_RANGE_ROW;     // (without query rows nobody looks at it)
+        }
       } else {
         seq_keys(P.seqs, i0 + lane, start, m, err);
       }
