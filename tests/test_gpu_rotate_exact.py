@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import sparse_attention_prefill_gb300 as S
+from tests import page_ref as R
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -98,3 +99,57 @@ def test_far_positions(inverse):
     """Frequencies near 1, held to 2^-56 of a turn, would be some ten units off at 2^33."""
     pos = [2 ** 31 + 7, 2 ** 33 + 1, -(2 ** 33) - 5, 2 ** 34 - 3, 3 * 2 ** 33 + 11, 2 ** 35]
     check(pos, FREQS, inverse, 1.0, inverse, seed=1)
+
+
+@pytest.mark.parametrize("interleaved,amplitude", [(False, 1.0), (True, 1.0),
+                                                   (False, 0.1 * np.log(8.0) + 1), (True, 0.6)])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_positions_of_long_contexts(interleaved, amplitude, inverse):
+    """Within one unit of cosine and sine, where two would show."""
+    rng = np.random.default_rng(5)
+    pos = [int(p) for p in rng.integers(1, 1 << 20, 150)] + [0, 1, 2, 3]
+    freq = [10000.0 ** (-2 * i / 64) for i in range(32)]
+    check(pos, freq, interleaved, amplitude, inverse, seed=2)
+
+
+@pytest.mark.parametrize("new,interleaved,dtype", [([4000, 96], False, torch.bfloat16),
+                                                   ([1] * 300, True, torch.float16)])
+def test_codes_of_rotated_keys_are_those_of_64_bits(new, interleaved, dtype):
+    """An appended key's code is another one than the 64-bit rotation's only where that lies
+    as near to the middle of two codes as the error of the fp32 rotation allows."""
+    kv, dim, page = 8, 128, 64
+    rows = [n + (0 if n > 1 else 64 * (3 + i % 50)) for i, n in enumerate(new)]
+    c = R.make_cache(new, kv, dim, page, seed=3)
+    if new[0] == 1:                      # the first rows of pages further on
+        table = torch.zeros((len(new), 60), dtype=torch.int32, device=DEV)
+        table[torch.arange(len(new)), torch.tensor(rows) // page] = c["table"][:, 0]
+        c["table"] = table
+    g = torch.Generator(device=DEV).manual_seed(4)
+    b, cu = R.batch(new, rows, DEV)
+    k = torch.randn((b["num_q"], kv, dim), generator=g, device=DEV).to(dtype)
+    rope = dict(S.rope_freqs(dim), interleaved=interleaved)
+    S.page_append(b, k, k, c, rope=rope)
+    pos = torch.cat([torch.arange(m - n, m, device=DEV) for n, m in zip(new, rows)])
+    u = R.rotate(k, pos, rope)
+    z = R.rotation(pos, rope)
+    h = dim // 2
+    x = k.double().abs()
+    p, q = (x[..., 0::2], x[..., 1::2]) if interleaved else (x[..., :h], x[..., h:])
+    co, si = z.real.abs()[:, None], z.imag.abs()[:, None]
+    # (the turn's 2^-64 a position, and the reference's angles, half a step of 64 bits)
+    angle = (2.0 ** -48 + pos.double()[:, None] * (2.0 ** -61 + rope["freq"] * 2.0 ** -52))[:, None]
+    e0 = (p * co + q * si) * 1.33 * 2.0 ** -23 + (p + q) * angle
+    e1 = (q * co + p * si) * 1.33 * 2.0 ** -23 + (p + q) * angle
+    err = (torch.stack([e0, e1], 3).flatten(2) if interleaved else torch.cat([e0, e1], 2)) \
+        + u.abs() * 2.0 ** -24
+    req = torch.repeat_interleave(torch.arange(len(new), device=DEV), torch.tensor(new, device=DEV))
+    block, slot = c["table"].long()[req, pos // page], pos % page
+    scale = c["k_scale"].double()[block][..., None]
+    got = R.values(c["k"][block, :, slot].contiguous())
+    want = R.e4m3(u / scale)
+    differ = got != want
+    middle = (got + want) / 2 * scale
+    assert ((u - middle).abs() <= err)[differ].all()
+    assert ((got - want).abs() * 8 <= torch.maximum(got.abs(), want.abs()).clamp_min(2.0 ** -6)
+            )[differ].all()
+    assert int(differ.sum()) <= differ.numel() * 1e-4
