@@ -423,6 +423,25 @@ bool outputs_meet(const csa2_packed *b, const csa2_prefix_groups *g, const Shape
                  (lse && overlap(ws, (uint64_t)ws_bytes, lse, nl))));
 }
 
+struct PartPlan {
+  int tpt, splits;
+  Kind kind;
+};
+
+PartPlan plan_part(const Shape &s, int64_t num_q, int64_t runs, int64_t most, bool single) {
+  PartPlan p;
+  p.tpt = tile_tokens(num_q, runs, s.group);
+  p.kind = kind_of(num_q, runs, p.tpt, s.group, single);
+  const int64_t tok = p.kind == kWideItems ? 2 * p.tpt : p.tpt;
+  const int64_t items = (num_q / tok > runs ? num_q / tok : runs) * s.n_kv;
+  const int64_t tiles = most / kTile + (most % kTile != 0);
+  if (p.kind == kSingleTokens)       // three CTAs to an SM, 64 keys a step
+    p.splits = plan_splits(items, 3 * kSms, 2 * tiles, 4.0);
+  else
+    p.splits = plan_splits(items, kSms, p.kind == kNarrowItems ? (tiles + 1) / 2 : tiles, 3.0);
+  return p;
+}
+
 struct PrefixPlan {
   PartPlan pre, own;
 };

@@ -4,7 +4,6 @@
 #include <type_traits>
 
 #include "dense.cuh"
-#include "dense_join.cuh"
 
 namespace csa2 {
 namespace dense {
@@ -490,25 +489,6 @@ enum Kind { kWideItems, kNarrowItems, kSingleTokens };
 Kind kind_of(int64_t num_q, int64_t runs, int tpt, int group, bool single) {
   if (single && tpt == 1 && group <= kDecodeGroup) return kSingleTokens;
   return num_q <= runs * tpt ? kNarrowItems : kWideItems;
-}
-
-struct PartPlan {
-  int tpt, splits;
-  Kind kind;
-};
-
-PartPlan plan_part(const Shape &s, int64_t num_q, int64_t runs, int64_t most, bool single) {
-  PartPlan p;
-  p.tpt = tile_tokens(num_q, runs, s.group);
-  p.kind = kind_of(num_q, runs, p.tpt, s.group, single);
-  const int64_t tok = p.kind == kWideItems ? 2 * p.tpt : p.tpt;
-  const int64_t items = (num_q / tok > runs ? num_q / tok : runs) * s.n_kv;
-  const int64_t tiles = most / kTile + (most % kTile != 0);
-  if (p.kind == kSingleTokens)       // three CTAs to an SM, 64 keys a step
-    p.splits = plan_splits(items, 3 * kSms, 2 * tiles, 4.0);
-  else
-    p.splits = plan_splits(items, kSms, p.kind == kNarrowItems ? (tiles + 1) / 2 : tiles, 3.0);
-  return p;
 }
 
 }  // namespace

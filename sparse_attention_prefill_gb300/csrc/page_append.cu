@@ -195,7 +195,7 @@ constexpr int kMost = 32;
 
 template <typename F>
 __device__ __forceinline__ void each_page(const AppendParams &P, int64_t place, int places,
-                                          int &err, const F &f) {
+                                          const F &f) {
   __shared__ Touched held;
   __shared__ int found, matches;
   for (int from = 0, served = 0; served < kMost; ++served) {
@@ -318,7 +318,7 @@ append_few_kernel(const __grid_constant__ AppendParams P) {
   if (blockIdx.x == gridDim.x - 1) return check_batch(P);
   int err = 0;
   if (P.rope.freq) rope::load_turns(P.rope, turn);       // (a barrier follows)
-  each_page(P, 2 * (int64_t)blockIdx.x, 2, err, [&](const Found &F) {
+  each_page(P, 2 * (int64_t)blockIdx.x, 2, [&](const Found &F) {
     for (int i = threadIdx.x >> 5; i < 2 * P.n_kv; i += kWarps)
       append_block<T, D, kInterleaved>(P, turn, F, i >> 1, i & 1, err);
   });
@@ -355,7 +355,7 @@ append_many_kernel(const __grid_constant__ AppendParams P) {
   const bool rot = side == 0 && P.rope.freq;
   if (rot) rope::load_turns(P.rope, turn);               // (a barrier follows)
   if (threadIdx.x < 3) top[threadIdx.x] = 0;
-  each_page(P, blockIdx.x, 1, err, [&](const Found &F) {
+  each_page(P, blockIdx.x, 1, [&](const Found &F) {
     if (!is_page(P, F.id, err)) return;
     const Touched &t = F.t;
     const int64_t base = F.p << C.shift;

@@ -64,17 +64,6 @@ __device__ __forceinline__ uint32_t f16x2_of_high(uint32_t four) {
   return h;
 }
 
-// two fp32 to E4M3 (x0 in the low byte), to nearest even, saturating
-__device__ __forceinline__ uint32_t e4m3x2_of(float x0, float x1) {
-  uint32_t r;
-  asm("{ .reg .b16 h;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 h, %2, %1;\n\t"
-      "cvt.u32.u16 %0, h; }"
-      : "=r"(r)
-      : "f"(x0), "f"(x1));
-  return r;
-}
-
 // [pages, lines of 128 bytes] of one side, as boxes of `rows` rows of a page (a row
 // of 64 channels is half a line) in the 128-byte swizzle
 inline bool make_pages_map(CUtensorMap *map, const void *base, int64_t num_pages, int n_kv,
