@@ -171,9 +171,9 @@ extern "C" CSA2_API int csa2_rotate(const csa2_packed *b, int32_t n_heads, int32
   P.d_err = d_err;
   // all heads of a row in one block, unless there are too few rows to fill the GPU
   const int rows = dim == 128 ? rope::kRows<128> : rope::kRows<64>;
-  const int blocks = (b->num_q + rows - 1) / rows;
+  const int64_t blocks = ((int64_t)b->num_q + rows - 1) / rows;
   int chunks = 1;
-  while (chunks * rope::kSlots < n_heads && (int64_t)blocks * chunks < 4 * dense::kSms) chunks *= 2;
+  while (chunks * rope::kSlots < n_heads && blocks * chunks < 4 * dense::kSms) chunks *= 2;
   P.each = (n_heads + chunks - 1) / chunks;
   const dim3 grid((unsigned)blocks, (unsigned)((n_heads + P.each - 1) / P.each));
   const cudaStream_t cs = as_stream(stream);
