@@ -3,9 +3,10 @@
 // A block (page, head, side) has one scale s, the smallest power of two with |x| <=
 // 448 s, so that rescaling older rows by old / new is exact but below 2^-6.
 //
-// Bound by memory in the end, two bytes read and one written for each channel, but near it
-// by instructions: eight prompts of 8192 rows, 8 heads x 128, take 81.5 us (4.9 TB/s; one
-// row to a thread 87.6, of which the rotation was 15), 256 single rows 8.2.
+// Bound by memory in the end, two bytes read and one written for each channel, but short of
+// it by what 16 warps to an SM cover (126 registers): eight prompts of 8192 rows, 8 heads x
+// 128, take 82 us (4.9 TB/s; one row to a thread 87.6, of which the rotation was 15) with
+// issue slots 58 % busy; 256 single rows 8.0, in two waves of CTAs of 512 threads.
 //
 // Which page a block of the grid has: the pages that request r's new rows touch
 // take the places from floor(cu_q[r] / page) + 2 r on.  (n rows touch at most
