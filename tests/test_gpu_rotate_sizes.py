@@ -27,7 +27,7 @@ def test_most_query_rows_of_a_batch(dim):
     rope = S.rope_freqs(rot)
     freq = part(0, rope["freq"])
     cu_q, kv_len = part(1024, torch.tensor([0, n], dtype=torch.int32)), part(2048, torch.tensor([m]))
-    d_err = part(3072, torch.zeros(1, dtype=torch.int32))
+    d_err = part(3200, torch.zeros(1, dtype=torch.int32))
     g = torch.Generator(device=DEV).manual_seed(1)
     x = torch.randn((n, 1, dim), generator=g, device=DEV).half()
     rows = part(4096, x.flatten())
